@@ -14,6 +14,11 @@ Public API (all calls run in libbea.so's CUDA kernels on the current stream):
   the library's one-call form of the same replay).
 * ``flash_attention / ring_attention``: the same as torch.autograd functions
   (the backward recomputed from the saved log-sum-exp).
+* ``rope_axes`` (``rotary_axes`` for autograd): rotary positions with one or
+  several axes, q and k in one launch.
+* ``paged_plan / paged_write / paged_decode`` (and ``PagedKVCache``, which
+  holds their state): a paged K/V cache, from request lengths to the attention
+  of one new token per request.
 
 The seeded input generators live in ``workloads`` and import nothing else.
 """
@@ -35,4 +40,13 @@ from .ops import (  # noqa: F401
     selftest_inject_abort,
 )
 from .ring import chunk_schedule, ring_attention_bwd, ring_attention_fwd  # noqa: F401
+from .rotary import rope_axes, rotary_axes  # noqa: F401
+from .paged import (  # noqa: F401
+    PagedKVCache,
+    PagedPlan,
+    paged_decode,
+    paged_decode_workspace_bytes,
+    paged_plan,
+    paged_write,
+)
 from .autograd import flash_attention, ring_attention  # noqa: F401,E402

@@ -10,12 +10,14 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbea.so")
 
 BEA_BF16 = 0
 BEA_F32 = 1
+BEA_I32 = 2
 
 STATUS = {
     0: "BEA_OK",
@@ -27,6 +29,7 @@ STATUS = {
     -6: "BEA_ERR_CUDA",
     -7: "BEA_ERR_TIMEOUT",
     -8: "BEA_ERR_WORKSPACE",
+    -9: "BEA_ERR_PAGES",
 }
 
 # every symbol include/bea.h declares
@@ -49,6 +52,11 @@ EXPORTS = (
     "bea_ring_attention_fwd",
     "bea_ring_attention_bwd_workspace_size",
     "bea_ring_attention_bwd",
+    "bea_rope_axes",
+    "bea_paged_plan",
+    "bea_paged_write",
+    "bea_paged_decode_workspace_size",
+    "bea_paged_decode",
 )
 
 
@@ -118,6 +126,18 @@ def load() -> ctypes.CDLL:
     lib.bea_ring_attention_bwd_workspace_size.restype = sz
     lib.bea_ring_attention_bwd.argtypes = [P, P, P, P, P, P, P, P, P, i, f, i, i, i, vp, sz, vp]
     lib.bea_ring_attention_bwd.restype = i
+    # these take packed tensor records (see `record`) instead of BeaTensor structures
+    R = ctypes.c_char_p
+    lib.bea_rope_axes.argtypes = [R, R, R, vp, vp, i, R, R, vp]
+    lib.bea_rope_axes.restype = i
+    lib.bea_paged_plan.argtypes = [R, R, R, R, R, i64, R, R, R, R, R, R, vp]
+    lib.bea_paged_plan.restype = i
+    lib.bea_paged_write.argtypes = [R, R, R, R, R, vp]
+    lib.bea_paged_write.restype = i
+    lib.bea_paged_decode_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.bea_paged_decode_workspace_size.restype = sz
+    lib.bea_paged_decode.argtypes = [R, R, R, R, R, R, R, f, i, vp, sz, vp]
+    lib.bea_paged_decode.restype = i
     _LIB = lib
     return lib
 
@@ -131,6 +151,20 @@ def describe(data_ptr: int, dtype_code: int, shape, strides) -> BeaTensor:
         t.shape[k] = int(s)
         t.stride[k] = int(st)
     return t
+
+
+_pack = struct.Struct("=Qii8q").pack  # the layout of bea_tensor
+_PAD = ((0,) * 4, (0,) * 3, (0,) * 2, (0,), ())
+
+
+def record(data_ptr: int, dtype_code: int, shape, strides) -> bytes:
+    """A bea_tensor as packed bytes: what `describe` fills field by field, in one
+    call (0.5 us instead of 3, which is most of a single-token call's host time)."""
+    n = len(shape)
+    if n > 4:  # no call takes such a rank: the library refuses it by its ndim
+        return _pack(data_ptr, dtype_code, n, *_PAD[0], *_PAD[0])
+    pad = _PAD[n]
+    return _pack(data_ptr, dtype_code, n, *shape, *pad, *strides, *pad)
 
 
 def check(code: int, where: str) -> None:

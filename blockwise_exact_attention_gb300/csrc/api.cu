@@ -366,6 +366,7 @@ const char* bea_status_string(int code) {
     case BEA_ERR_CUDA: return "CUDA runtime or driver call failed";
     case BEA_ERR_TIMEOUT: return "a kernel wait ran past its time limit";
     case BEA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case BEA_ERR_PAGES: return "a page, slot or length of a paged call is out of range";
     default: return "unknown status";
   }
 }
@@ -648,6 +649,7 @@ int bea_get_device_status(void* stream) {
   if (cudaDeviceSynchronize() != cudaSuccess) return BEA_ERR_CUDA;
   if (word & bea::BEA_STATUS_TIMEOUT) return BEA_ERR_TIMEOUT;
   if (word & bea::BEA_STATUS_CONFIG) return BEA_ERR_UNSUPPORTED;
+  if (word & bea::BEA_STATUS_PAGES) return BEA_ERR_PAGES;
   return BEA_OK;
 }
 

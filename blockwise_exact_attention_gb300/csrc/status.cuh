@@ -13,6 +13,7 @@ namespace bea {
 enum : uint32_t {
   BEA_STATUS_TIMEOUT = 1u,  // an mbarrier wait ran past its limit
   BEA_STATUS_CONFIG = 2u,   // a kernel was launched with a configuration it cannot run
+  BEA_STATUS_PAGES = 4u,    // a paged call met a page, slot or length out of range
 };
 
 __device__ __forceinline__ void report_status(uint32_t* status, uint32_t code) {

@@ -70,7 +70,8 @@ extern "C" {
 
 typedef enum bea_dtype {
   BEA_BF16 = 0, /* bfloat16 */
-  BEA_F32 = 1   /* float32 */
+  BEA_F32 = 1,  /* float32 */
+  BEA_I32 = 2   /* int32: lengths, tables, slots and positions of the paged and rotary calls only */
 } bea_dtype;
 
 typedef enum bea_status {
@@ -82,13 +83,14 @@ typedef enum bea_status {
   BEA_ERR_UNSUPPORTED = -5, /* valid request this build does not implement (e.g. head dim) */
   BEA_ERR_CUDA = -6,        /* a CUDA runtime/driver call failed */
   BEA_ERR_TIMEOUT = -7,     /* a kernel wait ran past its limit (from bea_get_device_status) */
-  BEA_ERR_WORKSPACE = -8    /* workspace missing, misaligned or too small */
+  BEA_ERR_WORKSPACE = -8,   /* workspace missing, misaligned or too small */
+  BEA_ERR_PAGES = -9        /* a paged call met a page, slot or length out of range (from bea_get_device_status) */
 } bea_status;
 
 typedef struct bea_tensor {
   void* data;        /* device pointer to element [0,0,0,0] */
   int32_t dtype;     /* bea_dtype */
-  int32_t ndim;      /* 4 for [n,l,h,d] tensors, 3 for [n,h,l] lse tensors */
+  int32_t ndim;      /* 4 for [n,l,h,d] tensors, 3 for [n,h,l] lse tensors, 1 to 3 for int32 tensors */
   int64_t shape[4];  /* first ndim entries used */
   int64_t stride[4]; /* in elements; first ndim entries used */
 } bea_tensor;
@@ -320,10 +322,130 @@ int bea_ring_merge(const bea_tensor* out_acc, const bea_tensor* lse_acc, const b
                    const bea_tensor* lse_blk, const bea_tensor* out_final, void* stream);
 
 /*
+ * Rotary positions with one or several axes (time, height, width ...), q and k
+ * in one launch. Pair p of a row is (x_p, x_{p + d/2}), the rotate-half pairs;
+ * its angle at batch b, position i is
+ *   angle = positions[axis_of_pair[p], b, i] * freq[p]
+ * and y_p = x_p cos - x_{p+d/2} sin, y_{p+d/2} = x_{p+d/2} cos + x_p sin. With
+ * `inverse` the angle is negated: the rotation's adjoint, hence its gradient
+ * (dx from dy), and its inverse.
+ *
+ *   q          [n, l, h, d]    bf16 or f32
+ *   k          NULL, or [n, l, h_k, d], q's dtype
+ *   positions  [axes, n, l]    i32, any sign, 1 <= axes <= 8; outer strides may
+ *              be 0 (one row of positions for the whole batch)
+ *   axis_of_pair, freq   HOST arrays of d/2 entries: axis index in [0, axes)
+ *              and radians per position (finite); read during the call only
+ *   q_out, k_out   shapes and dtype of q, k (written); k_out NULL iff k is.
+ *              Each may be its input itself (same pointer, same strides), and
+ *              must not overlap the inputs otherwise; not broadcast.
+ *   d: bf16 a multiple of 16, f32 a multiple of 8, at most 256.
+ * The angle is reduced modulo a whole turn in 64-bit integer arithmetic, so a
+ * far position loses nothing: it is off by at most |position| * 2^-53 times
+ * the frequency's whole turns, as in fp64. Products in fp32, one rounding.
+ */
+int bea_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* positions, const int32_t* axis_of_pair,
+                  const double* freq, int inverse, const bea_tensor* q_out, const bea_tensor* k_out, void* stream);
+
+/*
+ * Paged K/V cache. A cache is [num_pages, page_size, h_kv, d] (any 16-byte
+ * aligned outer strides, so a [num_pages, h_kv, page_size, d] cache is passed
+ * as its permuted view). Request r owns the pages block_table[r, 0 ..
+ * ceil(len_r / page_size)), and its token at position p lives in page
+ * block_table[r, p / page_size] at offset p % page_size; its SLOT is page *
+ * page_size + offset. Free pages are a stack: free_pages[0 .. n_free), the top
+ * at n_free - 1. Pages may be shared between rows of a table for reading.
+ *
+ * What the device finds out of range (a length beyond the table, a page or a
+ * slot outside the cache) is never accessed: it is left out as described at
+ * each call, and bea_get_device_status then reads BEA_ERR_PAGES.
+ */
+
+/*
+ * One scheduling step of a paged cache from request lengths, on the GPU: ends
+ * requests, hands pages to the tokens that are added, and lists where those
+ * tokens go.
+ *
+ *   lens        [n] i32   tokens request r holds now
+ *   new_lens    [n] i32   tokens it adds (>= 0), or -1: the request ends
+ *   block_table [n, max_pages] i32, read and written: entries of new pages
+ *   free_pages  [F] i32, read and written: the stack; ended requests' pages are
+ *               pushed in row order, a row's pages in table order; then new
+ *               pages are popped in row order
+ *   n_free      [1] i32   height of the stack
+ *   slot_map    [capacity] i32, written: the slot of every added token, requests
+ *               in row order, tokens in sequence order; -1 behind the last
+ *   positions   [capacity] i32, written: each added token's position in its
+ *               request; 0 behind the last
+ *   cu_new      [n + 1] i32, written: added tokens before row r; [n] is their number
+ *   cu_pages    [n + 1] i32, written: pages popped before row r
+ *   lens_out    [n] i32, written: the new lengths (0 for ended requests); may be `lens`
+ *   n_free_out  [1] i32, written; may be `n_free`
+ * All or nothing: if a length or new length is negative (other than -1 as new
+ * length) or passes max_pages * page_size, if the added tokens pass the
+ * capacity, or if the stack would run empty or pass F, the step changes
+ * nothing (lens_out = lens, n_free_out = n_free, slot_map all -1, positions
+ * and the cu arrays all 0) and the device status reads BEA_ERR_PAGES. A slot
+ * that is not in [0, 2^31) is written as -1, with the same status.
+ * No two arrays may overlap other than as said. page_size in [1, 2^20].
+ */
+int bea_paged_plan(const bea_tensor* lens, const bea_tensor* new_lens, const bea_tensor* block_table,
+                   const bea_tensor* free_pages, const bea_tensor* n_free, int64_t page_size,
+                   const bea_tensor* slot_map, const bea_tensor* positions, const bea_tensor* cu_new,
+                   const bea_tensor* cu_pages, const bea_tensor* lens_out, const bea_tensor* n_free_out,
+                   void* stream);
+
+/*
+ * Writes new keys and values into a paged cache: token t (t = i * l + j for
+ * k[i, j]) goes to slot slot_map[t].
+ *
+ *   k, v              [n, l, h_kv, d] bf16 or f32
+ *   slot_map          [n * l] i32; -1: the token is not written. Two tokens must
+ *                     not have the same slot (which of them stays would depend
+ *                     on timing, 16 bytes at a time).
+ *   k_cache, v_cache  [num_pages, page_size, h_kv, d], k's dtype (written); same
+ *                     shape, own strides; num_pages * page_size < 2^31
+ *   d * element size must be a multiple of 16 bytes.
+ * A slot below -1 or past the cache is skipped and reported.
+ */
+int bea_paged_write(const bea_tensor* k, const bea_tensor* v, const bea_tensor* slot_map, const bea_tensor* k_cache,
+                    const bea_tensor* v_cache, void* stream);
+
+/*
+ * Attention of one new token per request over a paged cache: the forward of
+ * this library for lq = 1, with keys and values read through the block table.
+ * The new token is the request's last key (write it first): with len =
+ * lens[r], query r sees the keys j with j >= len - 1 - window_left (all of
+ * them for window_left = -1) and j < len.
+ *
+ *   q                 [n, 1, h, d]  bf16 (d 64 or 128) or f32 (4 <= d <= 128, d % 4 == 0)
+ *   k_cache, v_cache  [num_pages, page_size, h_kv, d], q's dtype, h % h_kv == 0;
+ *                     same shape, own strides
+ *   block_table       [n, max_pages] i32, outer stride any
+ *   lens              [n] i32
+ *   out               [n, 1, h, d]  bf16 q: bf16 or f32; f32 q: f32 (written)
+ *   lse               [n, h, 1]     f32, natural log, scale included (written)
+ *   workspace         bea_paged_decode_workspace_size() bytes, 256-byte aligned;
+ *                     may be NULL when that is 0. Contents on entry irrelevant;
+ *                     calls that may run concurrently need separate workspaces.
+ * A request of length 0 gets out = 0 and lse = -inf. A length past max_pages *
+ * page_size counts as that, a negative one as 0, and the keys of a page
+ * outside the cache as masked; each is reported. num_pages * page_size < 2^31;
+ * max_pages * page_size < 2^30 (16-key tiles of the table times h_kv times
+ * ceil(h / h_kv / 16) must stay below 2^31).
+ */
+size_t bea_paged_decode_workspace_size(int64_t h, int64_t h_kv, int64_t d, int64_t max_keys);
+int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_tensor* v_cache,
+                     const bea_tensor* block_table, const bea_tensor* lens, const bea_tensor* out,
+                     const bea_tensor* lse, float softmax_scale, int window_left, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, reads the device status word of the current device
  * and clears it. Returns BEA_OK, BEA_ERR_TIMEOUT if any kernel since the last
  * read gave up a wait, BEA_ERR_UNSUPPORTED if a kernel met a configuration it
- * cannot run, or BEA_ERR_CUDA.
+ * cannot run, BEA_ERR_PAGES if a paged call met a page, slot or length out of
+ * range, or BEA_ERR_CUDA.
  */
 int bea_get_device_status(void* stream);
 
