@@ -4,8 +4,9 @@ Bounds of paged_decode against fp64. With u = 2^-23 (a unit in the last place,
 which also covers sums that truncate) a score, a sum of d products of exact
 inputs in fp32, is within (d + 2) u S of the true one, S = scale * sum |q_i k_i|
 at its largest; the exponential adds 2^-21 relative, and weights that are split
-into two bf16 terms 2^-16 (each rounding leaves at most 2^-8 of what it rounds).
-So every weight is within e = (d + 2) u S + 2^-21 + 2^-16 of the true one,
+into two bf16 terms 2^-15 (the first is cut to 8 bits and leaves at most 2^-7, of
+which rounding the second to 8 bits leaves at most 2^-8).
+So every weight is within e = (d + 2) u S + 2^-21 + 2^-15 of the true one,
 relative, numerator and denominator alike, and a sum over L keys adds L u: the
 output is within (2 e + 2 L u) A, A = sum_j p_j |v_j|, the log-sum-exp within e +
 L u + u |lse|. A bf16 output adds half a step, 2^-8 of its value."""
@@ -77,7 +78,7 @@ def check(out, lse, q, k, v, table, lens, scale, left=-1):
     ref_o, ref_l, a, s = op.decode(f64(q), f64(k), f64(v), table.cpu().numpy(), lens.cpu().numpy(), scale, left)
     u = 2.0 ** -23
     keys = max(int(lens.max()), 0)
-    e = (q.shape[3] + 2) * u * s + 2 ** -21 + 2 ** -16
+    e = (q.shape[3] + 2) * u * s + 2 ** -21 + 2 ** -15
     o, l = f64(out), f64(lse)
     empty = np.isneginf(ref_l)
     assert np.array_equal(np.isneginf(l), empty)
