@@ -8,21 +8,22 @@
 // Work. A UNIT is one (request, K/V head, block of up to kRows of the group's
 // query heads); its visible keys are cut into tiles of kKeys. The tiles of all
 // units, request by request, make one list, and CTA c of G takes the c-th of G
-// equal runs of it, whatever the lengths are: nothing about them is known on the
-// host. Every CTA finds its run from the lengths alone (a scan of tiles per
-// request in shared memory). A unit that one CTA covers is written by it; of a
-// unit that is cut, each CTA leaves (O, m, l) in the workspace and a second
-// kernel joins them in a fixed order (no atomics: the same call gives the same
-// bits). If no unit is longer than kWholeTiles the runs' ends are moved to
-// unit borders instead, and if the host can see that from the table's width
-// the second kernel is not launched.
+// runs of it, each warp of the CTA an eighth of that, whatever the lengths are:
+// nothing about them is known on the host. Every CTA finds its run from the
+// lengths alone (a scan of tiles per request in shared memory). The runs cost
+// the same: a unit counts as its tiles and kUnitCost more, for its queries and
+// its output. A warp that covers a unit writes it; parts of a unit in several
+// warps of a CTA are merged through shared memory when the warps are done, and
+// parts in several CTAs go to the workspace as (O, m, l), which a second kernel
+// joins in a fixed order (no atomics: the same call gives the same bits). If no
+// unit is longer than kWholeTiles the CTAs' runs end at unit borders instead, and
+// where the host sees that from the table's width it launches no second kernel.
 //
-// Inside a CTA each of the four warps takes every fourth tile of the run and
-// streams it by cp.async into a ring of its own, running ahead over unit borders,
-// so no barrier stands in the loop; at the end of a unit the warps' (O, m, l) are
-// merged through shared memory. Rows of a tile that no key of the request fills
-// (behind its length, before its window, in a bad page) arrive as zeros and their
-// scores are masked, so what those places hold in memory does not matter.
+// A warp streams its tiles by cp.async into a ring of its own, running ahead over
+// unit borders, so no barrier stands before the end. Rows of a tile that no key
+// of the request fills (behind its length, before its window, in a bad page)
+// arrive as zeros and their scores are masked, so what those places hold in
+// memory does not matter.
 #include <cuda_bf16.h>
 
 #include "launch_cache.cuh"
@@ -32,12 +33,13 @@
 namespace bea {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCtas = 304;       // two per SM
+constexpr int kMaxCtas = 160;       // one per SM
 constexpr int kMaxRequests = 1024;  // per launch: their tile counts are scanned in shared memory
 constexpr int kWholeTiles = 32;     // units up to this long are not cut
-constexpr int kMinTiles = 2 * kWarps;  // of a CTA's run, as long as there are fewer than G such runs
+constexpr int kUnitCost = 2;        // of a unit, in tiles, besides its tiles
+constexpr int kMinCost = 2 * kWarps;  // of a CTA's run, as long as there are fewer than G such runs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -47,14 +49,20 @@ struct Cfg {
   static constexpr int kRows = kF32 ? 8 : 16;  // query heads of a unit
   static constexpr int kEs = kF32 ? 4 : 2;
   static constexpr int kRowBytes = kD * kEs;
-  static constexpr int kStages = kF32 ? 2 : (kD == 64 ? 4 : 2);
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // K then V
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
-  static constexpr int kPitch = kD + 8;  // floats a row of the merge buffer: 8 rows x 4 lanes fall on different banks
-  static constexpr int kMerge = kWarps * kRows * kPitch * 4;
+  static constexpr int kStages = 16384 / kStageBytes;       // 16 KB in flight or in use per warp
+  static constexpr int kWarpRing = kStages * kStageBytes;
+  static constexpr int kRing = kWarps * kWarpRing;
+  static constexpr int kPitch = kD + 8;  // floats a row of a part: 8 rows x 4 lanes fall on different banks
+  static constexpr int kPart = kRows * kPitch * 4;
+  static constexpr int kHeads = kWarps * kPart;  // a warp's first part; its last one takes its ring's place
   static constexpr int kQ = kF32 ? kWarps * kRows * kD * 4 : 0;
   static constexpr int kP = kF32 ? kWarps * kKeys * kRows * 4 : 0;
-  static constexpr int kSmem = kRing + kMerge + kQ + kP;
+  static constexpr int kSmem = kRing + kHeads + kQ + kP;
+  // The 16-byte pieces of row r are stored at piece ^ swizzle(r): the eight rows an ldmatrix reads (bf16), the two
+  // rows by four pieces a quarter-warp reads (f32) fall on different banks.
+  __host__ __device__ static constexpr int swizzle(int r) { return kF32 ? ((r & 1) << 2) | ((r & 7) >> 1) : r & 7; }
+  static_assert(kPart <= kWarpRing, "a part takes the place of its warp's ring");
 };
 
 // Workspace: [kMaxCtas] descriptors | [kMaxCtas][2][16] (m, l) | [kMaxCtas][2][rows][D] O. Entry 0 of a CTA is a
@@ -114,110 +122,141 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // The first visible key of a request of `len` keys.
 __device__ __forceinline__ int first_key(int len, int left) { return left >= len ? 0 : len - 1 - left; }
 
-// The request of tile t: pre[b] * units <= t < pre[b + 1] * units.
-__device__ __forceinline__ int request_of(const int* pre, int n, int units, int t) {
-  const int x = t / units;
+// The last index with key(index) <= x, key rising, key(0) <= x.
+template <typename F>
+__device__ __forceinline__ int last_below(int n, int64_t x, F key) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid + 1] > x)
-      hi = mid;
+    const int mid = (lo + hi + 1) >> 1;
+    if (key(mid) <= x)
+      lo = mid;
     else
-      lo = mid + 1;
+      hi = mid - 1;
   }
   return lo;
 }
 
 template <bool kF32, int kD>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Launch a) {
   using C = Cfg<kF32, kD>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int pre[kMaxRequests + 1];  // tiles of a unit, summed over the requests before
-  __shared__ int lens[kMaxRequests];
-  __shared__ int warp_sum[kWarps], warp_max[kWarps];
+  // requests with a visible key, in order: tiles of a unit summed over those before, number, length
+  __shared__ int pre[kMaxRequests + 1], who[kMaxRequests], lens[kMaxRequests];
+  __shared__ int warp_tiles[kWarps], warp_some[kWarps], warp_max[kWarps];
   __shared__ uint32_t masks[kWarps][C::kStages];
-  __shared__ float2 ml[kWarps][16];
+  __shared__ float2 ml[kWarps][2][16];  // of a warp's first and last part
+  __shared__ int2 part_of[kWarps][2];   // (request, unit) of these parts, -1: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_launch_dependents();
 
   // ---- tiles per request, their sums, and this CTA's run [t0, t1) -----------------
-  const int most = p.max_pages * p.page;
-  int run = 0, longest = 0;
-  for (int base = 0; base < a.n; base += kThreads) {
-    const int r = base + tid;
-    int tiles = 0;
-    if (r < a.n) {
-      int len = p.lens[a.r0 + r];
-      if (len < 0 || len > most) {
-        if (blockIdx.x == 0) report_status(p.status, BEA_STATUS_PAGES);
-        len = len < 0 ? 0 : most;
-      }
-      lens[r] = len;
-      if (len > 0) tiles = (len + C::kKeys - 1) / C::kKeys - first_key(len, p.left) / C::kKeys;
-      longest = max(longest, tiles);
-    }
-    int inc = tiles;
+  const int most = p.max_pages * p.page, units = a.units, grid = gridDim.x, cta = blockIdx.x;
+  constexpr int kPer = kMaxRequests / kThreads;  // consecutive requests of a thread
+  int len_of[kPer], tiles_of[kPer];
+  int tiles_sum = 0, some = 0, longest = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(~0u, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = run;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += warp_sum[w];
-      run += warp_sum[w];
-    }
-    if (r < a.n) pre[r + 1] = before + inc;
-    __syncthreads();
+  for (int i = 0; i < kPer; ++i) {
+    const int r = tid * kPer + i;
+    len_of[i] = r < a.n ? p.lens[a.r0 + r] : 0;
   }
-  if (tid == 0) pre[0] = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    int len = len_of[i];
+    if (len < 0 || len > most) {
+      if (cta == 0) report_status(p.status, BEA_STATUS_PAGES);
+      len = len_of[i] = len < 0 ? 0 : most;
+    }
+    tiles_of[i] = len > 0 ? (len + C::kKeys - 1) / C::kKeys - first_key(len, p.left) / C::kKeys : 0;
+    tiles_sum += tiles_of[i];
+    some += tiles_of[i] > 0;
+    longest = max(longest, tiles_of[i]);
+  }
+  int tiles_inc = tiles_sum, some_inc = some;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(~0u, tiles_inc, o), y = __shfl_up_sync(~0u, some_inc, o);
+    if (lane >= o) tiles_inc += x, some_inc += y;
+  }
   longest = __reduce_max_sync(~0u, longest);
-  if (lane == 0) warp_max[warp] = longest;
+  if (lane == 31) warp_tiles[warp] = tiles_inc, warp_some[warp] = some_inc, warp_max[warp] = longest;
+  if (lane < 2) part_of[warp][lane] = make_int2(-1, -1);
   __syncthreads();
-  for (int w = 0; w < kWarps; ++w) longest = max(longest, warp_max[w]);
-
-  const int units = a.units, total = run * units, grid = gridDim.x, cta = blockIdx.x;
-  const int ctas = min(grid, max(1, total / kMinTiles));
-  const bool whole = longest <= kWholeTiles;
-  auto border = [&](int c) {
-    if (c >= ctas) return total;
-    int t = (int)((int64_t)total * c / ctas);
-    if (whole && t > 0) {
-      const int b = request_of(pre, a.n, units, t);
-      const int cnt = pre[b + 1] - pre[b], begin = pre[b] * units;
-      t = begin + (t - begin) / cnt * cnt;
-    }
-    return t;
-  };
-  const int t0 = border(min(cta, ctas)), t1 = border(min(cta + 1, ctas));
-
-  // requests without a visible key
-  for (int r = cta; r < a.n; r += grid) {
-    if (pre[r + 1] != pre[r]) continue;
-    const int64_t b = a.r0 + r;
-    for (int i = tid; i < p.h * p.d; i += kThreads) {
-      const int hh = i / p.d;
-      const int64_t at = b * p.out.sn + hh * p.out.sh + (i - hh * p.d);
-      if (p.out_is_f32)
-        static_cast<float*>(p.out.ptr)[at] = 0.f;
-      else
-        static_cast<__nv_bfloat16*>(p.out.ptr)[at] = __float2bfloat16(0.f);
-    }
-    for (int i = tid; i < p.h; i += kThreads) p.lse.ptr[b * p.lse.sn + i * p.lse.sh] = -INFINITY;
+  int run = 0, count = 0, at_tiles = tiles_inc - tiles_sum, at = some_inc - some;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at_tiles += warp_tiles[w], at += warp_some[w];
+    run += warp_tiles[w];
+    count += warp_some[w];
+    longest = max(longest, warp_max[w]);
   }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (tiles_of[i] == 0) continue;
+    pre[at] = at_tiles;
+    who[at] = a.r0 + tid * kPer + i;
+    lens[at++] = len_of[i];
+    at_tiles += tiles_of[i];
+  }
+  if (tid == 0) pre[count] = run;
+  // requests without a visible key
+  if (count < a.n) {
+    for (int r = cta; r < a.n; r += grid) {
+      const int len = p.lens[a.r0 + r];
+      if (len > 0 && most > 0) continue;
+      const int64_t b = a.r0 + r;
+      for (int i = tid; i < p.h * p.d; i += kThreads) {
+        const int hh = i / p.d;
+        const int64_t to = b * p.out.sn + hh * p.out.sh + (i - hh * p.d);
+        if (p.out_is_f32)
+          static_cast<float*>(p.out.ptr)[to] = 0.f;
+        else
+          static_cast<__nv_bfloat16*>(p.out.ptr)[to] = __float2bfloat16(0.f);
+      }
+      for (int i = tid; i < p.h; i += kThreads) p.lse.ptr[b * p.lse.sn + i * p.lse.sh] = -INFINITY;
+    }
+  }
+  __syncthreads();
+
+  // Costs. Unit u of the k-th request costs its tiles and kUnitCost before them.
+  const int64_t cost = (int64_t)(run + kUnitCost * count) * units;
+  const int ctas = (int)min((int64_t)grid, max((int64_t)1, cost / kMinCost));
+  const bool whole = longest <= kWholeTiles;
+  auto begin_cost = [&](int k) { return (int64_t)(pre[k] + kUnitCost * k) * units; };
+  // where CTA c's run begins, as a cost
+  auto border = [&](int c) {
+    if (c >= ctas) return cost;
+    int64_t v = cost * c / ctas;
+    if (whole && v > 0) {
+      const int k = last_below(count, v, begin_cost);
+      const int each = pre[k + 1] - pre[k] + kUnitCost;
+      const int64_t in = v - begin_cost(k);
+      v += (in % each) * 2 < each ? -(in % each) : each - in % each;
+    }
+    return v;
+  };
+  // the first tile that is not before cost v
+  auto tile_at = [&](int64_t v) {
+    if (v >= cost) return run * units;
+    const int k = last_below(count, v, begin_cost);
+    const int cnt = pre[k + 1] - pre[k], in = (int)(v - begin_cost(k)), unit = in / (cnt + kUnitCost);
+    return pre[k] * units + unit * cnt + max(0, in - unit * (cnt + kUnitCost) - kUnitCost);
+  };
   const WsLayout wl = ws_layout(C::kRows, kD);
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   if (a.split && tid == 0) reinterpret_cast<Split*>(ws)[cta] = Split{0, 0, -1, 0};
-  if (t0 >= t1) return;
+  if (cta >= ctas || count == 0) return;
+  const int64_t v0 = border(cta), v1 = border(cta + 1);
+  if (v0 >= v1) return;
+  const int t0 = tile_at(v0), t1 = tile_at(v1);
+  const int w0 = tile_at(v0 + (v1 - v0) * warp / kWarps), w1 = tile_at(v0 + (v1 - v0) * (warp + 1) / kWarps);
 
-  // ---- loads: the i-th tile of this warp is tile t0 + warp + 4 i ---------------------
-  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+  // ---- loads: the i-th tile of this warp is tile w0 + i -------------------------------
+  auto first_tile = [&](int k) { return (int64_t)pre[k] * units; };
+  const uint32_t ring = smem_u32(smem) + warp * C::kWarpRing;
   const int group = p.h / p.hkv;
-  const int mine = (t1 - t0 - warp + kWarps - 1) / kWarps;  // may be <= 0
-  const bool paged16 = p.page % C::kKeys == 0;              // a tile lies in one page
+  const int mine = w1 - w0;
+  const bool one_page = p.page % C::kKeys == 0;  // a tile lies in one page
   // Descriptors of this warp's next 32 tiles, one per lane.
   int d_b = 0, d_hk = 0, d_key = 0;
   int64_t d_k = 0, d_v = 0;
@@ -226,17 +265,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     d_mask = 0;
     d_k = d_v = 0;
     if (i >= mine) return;
-    const int t = t0 + warp + kWarps * i;
-    const int r = request_of(pre, a.n, units, t);
-    const int cnt = pre[r + 1] - pre[r], in = t - pre[r] * units, unit = in / cnt;
-    const int len = lens[r], first = first_key(len, p.left);
-    d_b = a.r0 + r;
+    const int t = w0 + i;
+    const int k = last_below(count, t, first_tile);
+    const int cnt = pre[k + 1] - pre[k], in = t - pre[k] * units, unit = in / cnt;
+    const int len = lens[k], first = first_key(len, p.left);
+    d_b = who[k];
     d_hk = unit / a.mtiles;
     d_key = (first / C::kKeys + (in - unit * cnt)) * C::kKeys;
     // rows of the tile that are visible
     const int lo = max(first - d_key, 0), hi = min(len - d_key, C::kKeys);
     d_mask = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
-    if (paged16) {
+    if (one_page) {
       const int pg = d_key / p.page, off = d_key - pg * p.page;
       const int id = p.table[d_b * p.table_stride + pg];
       if (id < 0 || id >= p.num_pages) {
@@ -248,78 +287,87 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   };
+  // Where tiles lie in several pages, lane r looks up the page of the tile's row r one tile ahead of its load.
+  int n_id = -1, n_off = 0;
+  auto look_up = [&](int i) {
+    if (i >= mine) return;
+    const int j = i & 31;
+    if (j == 0) describe(i + lane);
+    const int b = __shfl_sync(~0u, d_b, j), key = __shfl_sync(~0u, d_key, j) + lane;
+    const uint32_t mask = __shfl_sync(~0u, d_mask, j);
+    n_id = INT32_MIN;  // not visible
+    if (lane < C::kKeys && ((mask >> lane) & 1u)) {
+      const int pg = key / p.page;
+      n_off = key - pg * p.page;
+      n_id = max(p.table[b * p.table_stride + pg], -1);
+    }
+  };
   auto load = [&](int i) {
     if (i < mine) {
-      const int j = i & 31;
-      if (j == 0) describe(i + lane);
-      const int stage = i % C::kStages;
+      const int j = i & 31, stage = i % C::kStages;
       const uint32_t kd = ring + stage * C::kStageBytes, vd = kd + C::kKeys * C::kRowBytes;
-      uint32_t mask = __shfl_sync(~0u, d_mask, j);
-      int64_t k_at = __shfl_sync(~0u, d_k, j), v_at = __shfl_sync(~0u, d_v, j);
-      int64_t k_row = 0, v_row = 0;
-      if (!paged16) {  // each row's own place
-        const int b = __shfl_sync(~0u, d_b, j), hk = __shfl_sync(~0u, d_hk, j), key = __shfl_sync(~0u, d_key, j) + lane;
-        bool ok = lane < C::kKeys && ((mask >> (lane & 15)) & 1u);
+      uint32_t mask;
+      int64_t k_at = 0, v_at = 0, k_row = 0, v_row = 0;
+      if (one_page) {
+        if (j == 0) describe(i + lane);
+        mask = __shfl_sync(~0u, d_mask, j);
+        k_at = __shfl_sync(~0u, d_k, j);
+        v_at = __shfl_sync(~0u, d_v, j);
+      } else {
+        const int hk = __shfl_sync(~0u, d_hk, j);
+        const bool ok = n_id >= 0 && n_id < p.num_pages;
         if (ok) {
-          const int pg = key / p.page, off = key - pg * p.page;
-          const int id = p.table[b * p.table_stride + pg];
-          ok = id >= 0 && id < p.num_pages;
-          if (ok) {
-            k_row = id * p.kc.sn + off * p.kc.sl + hk * p.kc.sh;
-            v_row = id * p.vc.sn + off * p.vc.sl + hk * p.vc.sh;
-          } else {
-            report_status(p.status, BEA_STATUS_PAGES);
-          }
+          k_row = n_id * p.kc.sn + n_off * p.kc.sl + hk * p.kc.sh;
+          v_row = n_id * p.vc.sn + n_off * p.vc.sl + hk * p.vc.sh;
+        } else if (n_id != INT32_MIN) {
+          report_status(p.status, BEA_STATUS_PAGES);
         }
         mask = __ballot_sync(~0u, ok);
       }
       if (lane == 0) masks[warp][stage] = mask;
-      if constexpr (kF32) {
+      constexpr int kChunks = kD * C::kEs / 16;                 // 16-byte pieces of a row
+      constexpr int kStep = 32 / kChunks;                       // rows per instruction
+      const int chunk = lane % kChunks, sub = lane / kChunks;
+      const bool in_row = !kF32 || chunk * 4 < p.d;
 #pragma unroll
-        for (int row = 0; row < C::kKeys; ++row) {
-          const bool read = (mask >> row) & 1u;
-          int64_t ka = k_at + row * p.kc.sl, va = v_at + row * p.vc.sl;
-          if (!paged16) ka = __shfl_sync(~0u, k_row, row), va = __shfl_sync(~0u, v_row, row);
-          if (lane * 4 < p.d) {
-            const uint32_t at = row * C::kRowBytes + ((lane ^ (((row & 1) << 2) | (row >> 1))) << 4);
-            cp_async16(kd + at, read ? static_cast<const float*>(p.kc.ptr) + ka + lane * 4 : p.q.ptr, read);
-            cp_async16(vd + at, read ? static_cast<const float*>(p.vc.ptr) + va + lane * 4 : p.q.ptr, read);
-          }
-        }
-      } else {
-        constexpr int kChunks = kD / 8, kStep = 32 / kChunks;  // rows per instruction
-        const int chunk = lane % kChunks, sub = lane / kChunks;
-#pragma unroll
-        for (int it = 0; it < C::kKeys / kStep; ++it) {
-          const int row = it * kStep + sub;
-          const bool read = (mask >> row) & 1u;
-          int64_t ka = k_at + row * p.kc.sl, va = v_at + row * p.vc.sl;
-          if (!paged16) ka = __shfl_sync(~0u, k_row, row), va = __shfl_sync(~0u, v_row, row);
-          const uint32_t at = row * C::kRowBytes + ((chunk ^ (row & 7)) << 4);
-          cp_async16(kd + at, read ? static_cast<const __nv_bfloat16*>(p.kc.ptr) + ka + chunk * 8 : p.q.ptr, read);
-          cp_async16(vd + at, read ? static_cast<const __nv_bfloat16*>(p.vc.ptr) + va + chunk * 8 : p.q.ptr, read);
+      for (int it = 0; it < C::kKeys / kStep; ++it) {
+        const int row = it * kStep + sub;
+        const bool read = (mask >> row) & 1u;
+        int64_t ka = k_at + row * p.kc.sl, va = v_at + row * p.vc.sl;
+        if (!one_page) ka = __shfl_sync(~0u, k_row, row), va = __shfl_sync(~0u, v_row, row);
+        const uint32_t to = row * C::kRowBytes + ((chunk ^ C::swizzle(row)) << 4);
+        const char* ks = static_cast<const char*>(p.kc.ptr) + ka * C::kEs + chunk * 16;
+        const char* vs = static_cast<const char*>(p.vc.ptr) + va * C::kEs + chunk * 16;
+        if (in_row) {
+          cp_async16(kd + to, read ? ks : p.q.ptr, read);
+          cp_async16(vd + to, read ? vs : p.q.ptr, read);
         }
       }
+      if (!one_page) look_up(i + 1);
     }
     cp_async_commit();  // an empty group where there is no tile, so that groups count tiles
   };
+  if (!one_page) look_up(0);
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) load(i);
 
   // ---- unit by unit ----------------------------------------------------------------
-  float* merge = reinterpret_cast<float*>(smem + C::kRing);
-  float* q_smem = reinterpret_cast<float*>(smem + C::kRing + C::kMerge) + warp * C::kRows * kD;
-  float* p_smem = reinterpret_cast<float*>(smem + C::kRing + C::kMerge + C::kQ) + warp * C::kKeys * C::kRows;
-  int done = 0;  // tiles of this warp
-  int r = request_of(pre, a.n, units, t0);
-  int unit = (t0 - pre[r] * units) / (pre[r + 1] - pre[r]);
-  for (int t = t0; t < t1;) {
-    const int cnt = pre[r + 1] - pre[r], begin = pre[r] * units + unit * cnt, end = begin + cnt;
-    const int stop = min(end, t1);
-    const int todo = max(0, (stop - t0 - warp + kWarps - 1) / kWarps);  // this warp's tiles up to here
-    const int64_t b = a.r0 + r;
+  float* head = reinterpret_cast<float*>(smem + C::kRing + warp * C::kPart);
+  float* tail = reinterpret_cast<float*>(smem + warp * C::kWarpRing);
+  float* q_smem = reinterpret_cast<float*>(smem + C::kRing + C::kHeads) + warp * C::kRows * kD;
+  float* p_smem = reinterpret_cast<float*>(smem + C::kRing + C::kHeads + C::kQ) + warp * C::kKeys * C::kRows;
+  int done = 0;
+  int k = last_below(count, w0, first_tile);
+  int unit = (w0 - pre[k] * units) / (pre[k + 1] - pre[k]);
+  while (done < mine) {
+    const int cnt = pre[k + 1] - pre[k], begin = pre[k] * units + unit * cnt, end = begin + cnt;
+    const int todo = min(end, w1) - w0;  // this warp's tiles up to the unit's end
+    const int64_t b = who[k];
     const int hk = unit / a.mtiles, mi = unit - hk * a.mtiles;
     const int h0 = hk * group + mi * C::kRows, rows = min(C::kRows, group - mi * C::kRows);
+    const bool covered = begin >= w0 && end <= w1;
+    const int which = begin < w0 ? 0 : 1;
+    float* part = which == 0 ? head : tail;
 
     if constexpr (kF32) {
       // Scores: lane (key, quarter) takes every fourth 16-byte piece of its key's row. Output: lane owns 4 columns.
@@ -329,18 +377,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < C::kRows; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       const float* q = static_cast<const float*>(p.q.ptr) + b * p.q.sn + h0 * p.q.sh;
       __syncwarp();
-      if (done < todo)
-        for (int i = 0; i < rows; ++i)
-          if (lane * 4 < p.d)
-            *reinterpret_cast<float4*>(q_smem + i * kD + lane * 4) = *reinterpret_cast<const float4*>(q + i * p.q.sh + lane * 4);
+      for (int i = 0; i < rows; ++i)
+        if (lane * 4 < p.d)
+          *reinterpret_cast<float4*>(q_smem + i * kD + lane * 4) =
+              *reinterpret_cast<const float4*>(q + i * p.q.sh + lane * 4);
       __syncwarp();
-      const int key = lane >> 2, quarter = lane & 3, sw = ((key & 1) << 2) | (key >> 1), pieces = p.d >> 2;
+      const int key = lane >> 2, quarter = lane & 3, sw = C::swizzle(key), pieces = p.d >> 2;
+      const bool column = lane * 4 < kD;
       for (; done < todo; ++done) {
         const int stage = done % C::kStages;
         load(done + C::kStages - 1);
         cp_async_wait<C::kStages - 1>();
         __syncwarp();
-        const uint8_t* kt = smem + (warp * C::kStages + stage) * C::kStageBytes;
+        const uint8_t* kt = smem + warp * C::kWarpRing + stage * C::kStageBytes;
         const uint8_t* vt = kt + C::kKeys * C::kRowBytes;
         const bool see = (masks[warp][stage] >> key) & 1u;
         float s[C::kRows];
@@ -380,14 +429,16 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         __syncwarp();
+        if (column) {
 #pragma unroll
-        for (int j = 0; j < C::kKeys; ++j) {
-          const float4 v = *reinterpret_cast<const float4*>(vt + j * C::kRowBytes + ((lane ^ (((j & 1) << 2) | (j >> 1))) << 4));
+          for (int j = 0; j < C::kKeys; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(vt + j * C::kRowBytes + ((lane ^ C::swizzle(j)) << 4));
 #pragma unroll
-          for (int i = 0; i < C::kRows; ++i) {
-            if (i < rows) {
-              const float e = p_smem[j * C::kRows + i];
-              o[i] = make_float4(fmaf(e, v.x, o[i].x), fmaf(e, v.y, o[i].y), fmaf(e, v.z, o[i].z), fmaf(e, v.w, o[i].w));
+            for (int i = 0; i < C::kRows; ++i) {
+              if (i < rows) {
+                const float e = p_smem[j * C::kRows + i];
+                o[i] = make_float4(fmaf(e, v.x, o[i].x), fmaf(e, v.y, o[i].y), fmaf(e, v.z, o[i].z), fmaf(e, v.w, o[i].w));
+              }
             }
           }
         }
@@ -399,8 +450,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           l[i] += __shfl_xor_sync(~0u, l[i], 4);
           l[i] += __shfl_xor_sync(~0u, l[i], 8);
           l[i] += __shfl_xor_sync(~0u, l[i], 16);
-          if (lane == 0) ml[warp][i] = make_float2(m[i], l[i]);
-          if (lane * 4 < p.d) *reinterpret_cast<float4*>(merge + (warp * C::kRows + i) * C::kPitch + lane * 4) = o[i];
+          l[i] = __shfl_sync(~0u, l[i], 0);
+          if (covered) {
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+            if (lane * 4 < p.d)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + b * p.out.sn + (h0 + i) * p.out.sh + lane * 4) =
+                  make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+            if (lane == 0)
+              p.lse.ptr[b * p.lse.sn + (h0 + i) * p.lse.sh] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+          } else {
+            if (lane == 0) ml[warp][which][i] = make_float2(m[i], l[i]);
+            if (lane * 4 < p.d) *reinterpret_cast<float4*>(part + i * C::kPitch + lane * 4) = o[i];
+          }
         }
       }
     } else {
@@ -411,16 +472,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       const int row = lane >> 2, col = (lane & 3) * 2;
       uint32_t qf[kD / 16][4];
-      if (done < todo) {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q.ptr) + b * p.q.sn + h0 * p.q.sh;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q.ptr) + b * p.q.sn + h0 * p.q.sh;
 #pragma unroll
-        for (int ks = 0; ks < kD / 16; ++ks)
+      for (int ks = 0; ks < kD / 16; ++ks)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int i = row + (x & 1) * 8, c = ks * 16 + (x >> 1) * 8 + col;
-            qf[ks][x] = i < rows ? *reinterpret_cast<const uint32_t*>(q + i * p.q.sh + c) : 0u;
-          }
-      }
+        for (int x = 0; x < 4; ++x) {
+          const int i = row + (x & 1) * 8, c = ks * 16 + (x >> 1) * 8 + col;
+          qf[ks][x] = i < rows ? *reinterpret_cast<const uint32_t*>(q + i * p.q.sh + c) : 0u;
+        }
       for (; done < todo; ++done) {
         const int stage = done % C::kStages;
         load(done + C::kStages - 1);
@@ -433,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int ks = 0; ks < kD / 16; ++ks) {
           uint32_t kf[4];
           const int kr = (lane & 7) + ((lane >> 4) << 3), chunk = 2 * ks + ((lane >> 3) & 1);
-          ldsm4(kt + kr * C::kRowBytes + ((chunk ^ (kr & 7)) << 4), kf);
+          ldsm4(kt + kr * C::kRowBytes + ((chunk ^ C::swizzle(kr)) << 4), kf);
           mma_bf16(s[0], qf[ks], kf[0], kf[1]);
           mma_bf16(s[1], qf[ks], kf[2], kf[3]);
         }
@@ -484,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int dp = 0; dp < kD / 16; ++dp) {
           uint32_t vf[4];
           const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), chunk = 2 * dp + (lane >> 4);
-          ldsm4_t(vt + vr * C::kRowBytes + ((chunk ^ (vr & 7)) << 4), vf);
+          ldsm4_t(vt + vr * C::kRowBytes + ((chunk ^ C::swizzle(vr)) << 4), vf);
           mma_bf16(o[2 * dp], hi, vf[0], vf[1]);
           mma_bf16(o[2 * dp + 1], hi, vf[2], vf[3]);
           mma_bf16(o[2 * dp], lo, vf[0], vf[1]);
@@ -497,45 +556,76 @@ __global__ void __launch_bounds__(kThreads, 2)
         l[x] += __shfl_xor_sync(~0u, l[x], 1);
         l[x] += __shfl_xor_sync(~0u, l[x], 2);
         const int i = row + 8 * x;
-        if (i < rows) {
-          if ((lane & 3) == 0) ml[warp][i] = make_float2(m[x], l[x]);
-          float* to = merge + (warp * C::kRows + i) * C::kPitch + col;
+        if (i >= rows) continue;
+        if (covered) {
+          const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
+          const int64_t to = b * p.out.sn + (h0 + i) * p.out.sh + col;
+#pragma unroll
+          for (int c = 0; c < kD / 8; ++c) {
+            if (p.out_is_f32)
+              *reinterpret_cast<float2*>(static_cast<float*>(p.out.ptr) + to + c * 8) =
+                  make_float2(o[c][2 * x] * inv, o[c][2 * x + 1] * inv);
+            else
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out.ptr) + to + c * 8) =
+                  pack_bf16x2(o[c][2 * x] * inv, o[c][2 * x + 1] * inv);
+          }
+          if ((lane & 3) == 0)
+            p.lse.ptr[b * p.lse.sn + (h0 + i) * p.lse.sh] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * kLn2;
+        } else {
+          if ((lane & 3) == 0) ml[warp][which][i] = make_float2(m[x], l[x]);
 #pragma unroll
           for (int c = 0; c < kD / 8; ++c)
-            *reinterpret_cast<float2*>(to + c * 8) = make_float2(o[c][2 * x], o[c][2 * x + 1]);
+            *reinterpret_cast<float2*>(part + i * C::kPitch + col + c * 8) = make_float2(o[c][2 * x], o[c][2 * x + 1]);
         }
       }
     }
+    if (!covered && lane == 0) part_of[warp][which] = make_int2(k, unit);
+    if (++unit == units) unit = 0, ++k;
+  }
 
-    // ---- the unit's, or its part's, (O, m, l) out of the four warps' ------------------
-    __syncthreads();
+  // ---- units in several warps: merge their parts, in order ----------------------------
+  __syncthreads();
+  const int quads = p.d >> 2;
+  const int2* parts = &part_of[0][0];
+  for (int x = 0; x < 2 * kWarps;) {
+    const int2 of = parts[x];
+    if (of.x < 0) {
+      ++x;
+      continue;
+    }
+    int y = x + 1;  // parts [x, y) are this unit's
+    while (y < 2 * kWarps && (parts[y].x < 0 || (parts[y].x == of.x && parts[y].y == of.y))) ++y;
+    const int cnt = pre[of.x + 1] - pre[of.x], begin = pre[of.x] * units + of.y * cnt, end = begin + cnt;
+    const int64_t b = who[of.x];
+    const int hk = of.y / a.mtiles, mi = of.y - hk * a.mtiles;
+    const int h0 = hk * group + mi * C::kRows, rows = min(C::kRows, group - mi * C::kRows);
     const bool complete = begin >= t0 && end <= t1;
     const int slot = cta * 2 + (begin < t0 ? 0 : 1);
-    const int quads = p.d >> 2;
     for (int i = tid; i < rows * quads; i += kThreads) {
       const int row = i / quads, c = (i - row * quads) * 4;
       float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][row].x);
+      for (int z = x; z < y; ++z)
+        if (parts[z].x >= 0) top = fmaxf(top, ml[z >> 1][z & 1][row].x);
       const float ref = top == -INFINITY ? 0.f : top;
       float sum = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 x = ml[w][row];
-        const float f = ex2_approx(x.x - ref);
-        const float4 y = *reinterpret_cast<const float4*>(merge + (w * C::kRows + row) * C::kPitch + c);
-        sum = fmaf(f, x.y, sum);
-        o = make_float4(fmaf(f, y.x, o.x), fmaf(f, y.y, o.y), fmaf(f, y.z, o.z), fmaf(f, y.w, o.w));
+      for (int z = x; z < y; ++z) {
+        if (parts[z].x < 0) continue;
+        const float2 e = ml[z >> 1][z & 1][row];
+        const float f = ex2_approx(e.x - ref);
+        const float* from = reinterpret_cast<const float*>(smem + ((z & 1) ? (z >> 1) * C::kWarpRing : C::kRing + (z >> 1) * C::kPart));
+        const float4 u = *reinterpret_cast<const float4*>(from + row * C::kPitch + c);
+        sum = fmaf(f, e.y, sum);
+        o = make_float4(fmaf(f, u.x, o.x), fmaf(f, u.y, o.y), fmaf(f, u.z, o.z), fmaf(f, u.w, o.w));
       }
       if (complete) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t at = b * p.out.sn + (h0 + row) * p.out.sh + c;
+        const int64_t to = b * p.out.sn + (h0 + row) * p.out.sh + c;
         if (p.out_is_f32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + at) =
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + to) =
               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         } else {
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out.ptr) + at) =
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out.ptr) + to) =
               make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         }
         if (c == 0)
@@ -546,19 +636,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (!complete && begin >= t0 && tid == 0) {
-      // the CTA whose run holds the unit's last tile
-      int last = (int)(((int64_t)(end - 1) * ctas) / total);
-      while ((int64_t)total * (last + 1) / ctas < end) ++last;
-      while ((int64_t)total * last / ctas >= end) --last;
-      reinterpret_cast<Split*>(ws)[cta] = Split{r, unit, last, 0};
+      // the CTA whose run holds the unit's last tile, at cost v: the last one that begins there or before
+      const int64_t v = begin_cost(of.x) + (int64_t)(of.y + 1) * (cnt + kUnitCost) - 1;
+      int last = (int)(v * ctas / cost);
+      while (last + 1 < ctas && cost * (last + 1) / ctas <= v) ++last;
+      while (cost * last / ctas > v) --last;
+      reinterpret_cast<Split*>(ws)[cta] = Split{(int)b, of.y, last, 0};
     }
-    __syncthreads();
-    t = stop;
-    if (++unit == units) {
-      unit = 0;
-      do ++r;
-      while (r < a.n && pre[r + 1] == pre[r]);
-    }
+    x = y;
   }
 }
 
@@ -619,7 +704,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
     o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t b = a.r0 + sp.b;
+  const int64_t b = sp.b;
   const int hh = hk * group + mi * C::kRows + row;
   if (lane == 0) p.lse.ptr[b * p.lse.sn + hh * p.lse.sh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   if (!mine) return;
@@ -633,6 +718,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   }
 }
 
+// The most that one request's units can cost.
+int64_t request_cost(int64_t keys, int64_t units, int tile) { return ((keys + tile - 1) / tile + 1 + kUnitCost) * units; }
+
 template <bool kF32, int kD>
 cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   using C = Cfg<kF32, kD>;
@@ -643,11 +731,9 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
         cudaError_t r = cudaFuncSetAttribute(paged_decode_kernel<kF32, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmem);
         if (r != cudaSuccess) return r;
-        int sms = 0, per_sm = 0;
+        int sms = 0;
         if ((r = device_sm_count(&sms)) != cudaSuccess) return r;
-        r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, paged_decode_kernel<kF32, kD>, kThreads, C::kSmem);
-        const int64_t n = (int64_t)sms * (per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm);
-        *v = n < kMaxCtas ? (int)n : kMaxCtas;
+        *v = sms < kMaxCtas ? sms : kMaxCtas;
         return r;
       },
       &ctas);
@@ -659,10 +745,8 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   a.sl2 = p.scale * kLog2e;
   const int64_t keys = (int64_t)p.max_pages * p.page;
   a.split = keys > kWholeTiles * C::kKeys;
-  // Requests per launch: their tiles have to stay countable in 31 bits.
-  const int64_t per_request = ((keys + C::kKeys - 1) / C::kKeys + 1) * a.units;
-  int64_t at_once = per_request > 0 ? ((int64_t(1) << 31) - 1) / per_request : kMaxRequests;
-  if (at_once < 1) return cudaErrorInvalidConfiguration;
+  // Requests per launch: their tiles and unit costs have to stay countable in 31 bits.
+  int64_t at_once = ((int64_t(1) << 31) - 1) / request_cost(keys, a.units, C::kKeys);
   if (at_once > kMaxRequests) at_once = kMaxRequests;
   for (int64_t r0 = 0; r0 < p.n; r0 += at_once) {
     a.r0 = (int)r0;
@@ -691,12 +775,17 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
 size_t paged_decode_workspace(int64_t, int64_t, int64_t d, int64_t max_keys) {
   // Without the type: the larger of the two kernels' needs, for the shorter of their uncut lengths.
   if (max_keys <= kWholeTiles * Cfg<true, 128>::kKeys) return 0;
-  return ws_layout(16, d <= 64 ? 64 : 128).total > ws_layout(8, 128).total ? ws_layout(16, d <= 64 ? 64 : 128).total
-                                                                          : ws_layout(8, 128).total;
+  return ws_layout(16, d <= 64 ? 64 : 128).total;
+}
+
+bool paged_decode_fits(int64_t h, int64_t hkv, bool is_f32, int64_t max_keys) {
+  const int rows = is_f32 ? Cfg<true, 128>::kRows : Cfg<false, 128>::kRows;
+  const int64_t units = hkv * ((h / hkv + rows - 1) / rows);
+  return request_cost(max_keys, units, is_f32 ? Cfg<true, 128>::kKeys : Cfg<false, 128>::kKeys) < (int64_t(1) << 31);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
-  if (p.is_f32) return launch<true, 128>(p, s, nlaunch);
+  if (p.is_f32) return p.d <= 64 ? launch<true, 64>(p, s, nlaunch) : launch<true, 128>(p, s, nlaunch);
   return p.d == 64 ? launch<false, 64>(p, s, nlaunch) : launch<false, 128>(p, s, nlaunch);
 }
 
