@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbea.so")
@@ -78,6 +77,19 @@ class BeaError(RuntimeError):
 
 
 _LIB = None
+_BIND = None
+
+
+def bind():
+    """The binding of the short calls (csrc/binding.cpp, `_bind.so`), which reaches
+    the same libbea.so without building a structure per tensor in Python."""
+    global _BIND
+    if _BIND is None:
+        load()
+        from . import _bind, ops
+        _bind.setup(check, ops._count)
+        _BIND = _bind
+    return _BIND
 
 
 def load() -> ctypes.CDLL:
@@ -126,17 +138,15 @@ def load() -> ctypes.CDLL:
     lib.bea_ring_attention_bwd_workspace_size.restype = sz
     lib.bea_ring_attention_bwd.argtypes = [P, P, P, P, P, P, P, P, P, i, f, i, i, i, vp, sz, vp]
     lib.bea_ring_attention_bwd.restype = i
-    # these take packed tensor records (see `record`) instead of BeaTensor structures
-    R = ctypes.c_char_p
-    lib.bea_rope_axes.argtypes = [R, R, R, vp, vp, i, R, R, vp]
+    lib.bea_rope_axes.argtypes = [P, P, P, vp, vp, i, P, P, vp]
     lib.bea_rope_axes.restype = i
-    lib.bea_paged_plan.argtypes = [R, R, R, R, R, i64, R, R, R, R, R, R, vp]
+    lib.bea_paged_plan.argtypes = [P, P, P, P, P, i64, P, P, P, P, P, P, vp]
     lib.bea_paged_plan.restype = i
-    lib.bea_paged_write.argtypes = [R, R, R, R, R, vp]
+    lib.bea_paged_write.argtypes = [P, P, P, P, P, vp]
     lib.bea_paged_write.restype = i
     lib.bea_paged_decode_workspace_size.argtypes = [i64, i64, i64, i64]
     lib.bea_paged_decode_workspace_size.restype = sz
-    lib.bea_paged_decode.argtypes = [R, R, R, R, R, R, R, f, i, vp, sz, vp]
+    lib.bea_paged_decode.argtypes = [P, P, P, P, P, P, P, f, i, vp, sz, vp]
     lib.bea_paged_decode.restype = i
     _LIB = lib
     return lib
@@ -151,20 +161,6 @@ def describe(data_ptr: int, dtype_code: int, shape, strides) -> BeaTensor:
         t.shape[k] = int(s)
         t.stride[k] = int(st)
     return t
-
-
-_pack = struct.Struct("=Qii8q").pack  # the layout of bea_tensor
-_PAD = ((0,) * 4, (0,) * 3, (0,) * 2, (0,), ())
-
-
-def record(data_ptr: int, dtype_code: int, shape, strides) -> bytes:
-    """A bea_tensor as packed bytes: what `describe` fills field by field, in one
-    call (0.5 us instead of 3, which is most of a single-token call's host time)."""
-    n = len(shape)
-    if n > 4:  # no call takes such a rank: the library refuses it by its ndim
-        return _pack(data_ptr, dtype_code, n, *_PAD[0], *_PAD[0])
-    pad = _PAD[n]
-    return _pack(data_ptr, dtype_code, n, *shape, *pad, *strides, *pad)
 
 
 def check(code: int, where: str) -> None:

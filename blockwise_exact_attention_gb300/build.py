@@ -6,6 +6,10 @@ to this file (CUDA runtime linked statically; the driver API is reached at
 run time through the runtime's entry-point query, so loading the library
 needs no GPU). Rebuilds only when a source or header is newer than the
 library.
+
+``csrc/binding.cpp``, the Python binding of the short calls, is compiled by the
+host compiler against torch's headers (in parallel with the CUDA units) and
+linked into ``_bind.so``, which finds libbea.so next to itself.
 """
 
 from __future__ import annotations
@@ -15,12 +19,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbea.so")
+BIND_SRC = os.path.join(CSRC, "binding.cpp")
+BIND = os.path.join(HERE, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -39,13 +46,13 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    return _sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(f) <= t for f in _deps() + [__file__])
 
 
@@ -58,13 +65,33 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _torch_paths() -> tuple[list[str], str]:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    return ["-I" + i for i in include], os.path.join(root, "lib")
+
+
+def _compile_binding() -> str:
+    obj = os.path.join(BUILD, "binding.o")
+    include, _ = _torch_paths()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *include, "-c", BIND_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libbea.so; returns its path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(_sources())) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(_sources()) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, _sources()))
+        binding = binding.result()
     log = "".join(err for _obj, err in results)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write(log)
@@ -76,6 +103,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, binding, "-L" + HERE, "-l:libbea.so", "-Wl,-rpath,$ORIGIN", "-L" + _torch_paths()[1], "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-L" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64"), "-lcudart"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
     return LIB
 
 

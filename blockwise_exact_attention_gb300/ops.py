@@ -53,30 +53,6 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-_DT_ALL = {**_DT, torch.int32: _lib.BEA_I32}
-
-
-def _records(*tensors):
-    """Packed records of the tensors (None where one is) and the current stream, for the calls whose
-    own run time is of the order of the host's: (records, stream). The tensors
-    have to live on the current device, whose stream the call uses."""
-    dev = tensors[0].get_device()
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev or dev < 0:
-            raise ValueError(f"tensors on {t.device} and {tensors[0].device}: all must live on one CUDA device")
-        code = _DT_ALL.get(t.dtype)
-        if code is None:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        out.append(_lib.record(t.data_ptr(), code, t.shape, t.stride()))
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return out, torch.cuda.current_stream().cuda_stream
-
-
 def flash_mha_fwd(q, k, v, softmax_scale=None, is_causal=False, window_size=(-1, -1), out=None, lse=None,
                   out_dtype=None):
     """Exact attention forward. q [n,l,h,d], k/v [n,lk,h_kv,d] -> (out [n,l,h,d], lse [n,h,l] fp32)."""

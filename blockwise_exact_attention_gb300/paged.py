@@ -15,7 +15,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _lib, ops
+from . import _lib
 
 
 class PagedPlan(NamedTuple):
@@ -36,25 +36,13 @@ def paged_plan(lens, new_lens, block_table, free_pages, n_free, page_size, capac
     ``n_free`` are not, unless ``out`` (a PagedPlan) holds them as its own.
     ``capacity``: places for added tokens. A step that cannot be done in full
     changes nothing and is reported by ``device_status``."""
-    if out is None:
-        n = lens.shape[0]
-        out = PagedPlan(*torch.empty(2 * capacity + 3 * n + 3, dtype=torch.int32, device=lens.device).split(
-            (capacity, capacity, n + 1, n + 1, n, 1)))
-    (a, b, c, d, e, *o), stream = ops._records(lens, new_lens, block_table, free_pages, n_free, *out)
-    rc = _lib.load().bea_paged_plan(a, b, c, d, e, page_size, *o, stream)
-    _lib.check(rc, "paged_plan")
-    ops._count()
-    return out
+    return PagedPlan._make(_lib.bind().paged_plan(lens, new_lens, block_table, free_pages, n_free, page_size, capacity, out))
 
 
 def paged_write(k, v, slot_map, k_cache, v_cache):
     """Write k, v [n, l, h_kv, d] to the slots ``slot_map`` [n * l] (int32, -1:
     not written) of the caches [num_pages, page_size, h_kv, d], in place."""
-    r, stream = ops._records(k, v, slot_map, k_cache, v_cache)
-    rc = _lib.load().bea_paged_write(*r, stream)
-    _lib.check(rc, "paged_write")
-    ops._count()
-    return k_cache, v_cache
+    return _lib.bind().paged_write(k, v, slot_map, k_cache, v_cache)
 
 
 def paged_decode_workspace_bytes(q, k_cache, block_table) -> int:
@@ -68,24 +56,12 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, softmax_scale=None, win
     and values of request r's first ``lens[r]`` slots (the new token's own among
     them) -> (out [n, 1, h, d], lse [n, h, 1] fp32). ``window_left`` >= 0 lets
     the token see only that many keys before its own."""
-    lib = _lib.load()
-    n, _, h, d = q.shape
     if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-    if lse is None:
-        lse = torch.empty((n, h, 1), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        need = paged_decode_workspace_bytes(q, k_cache, block_table)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    r, stream = ops._records(q, k_cache, v_cache, block_table, lens, out, lse)
-    rc = lib.bea_paged_decode(*r, softmax_scale, window_left, ws, nbytes, stream)
-    _lib.check(rc, "paged_decode")
-    ops._count()
-    return out, lse
+        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
+    if out_dtype is not None and out_dtype not in (q.dtype, torch.float32):
+        raise TypeError(f"out_dtype {out_dtype}: {q.dtype} or float32")
+    return _lib.bind().paged_decode(q, k_cache, v_cache, block_table, lens, softmax_scale, window_left, out, lse,
+                                    out_dtype is torch.float32, workspace)
 
 
 class PagedKVCache:

@@ -111,19 +111,11 @@ def T(shape, dtype=BF16, ptr=FAKE, strides=None):
         for s in reversed(shape):
             strides.insert(0, acc)
             acc *= s
-    return _lib.record(ptr, dtype, shape, strides)
+    return _lib.describe(ptr, dtype, shape, strides)
 
 
 def I(*shape, **kw):
     return T(shape, I32, **kw)
-
-
-def test_record_is_the_c_structure():
-    for shape, strides in (((2, 3, 4, 8), (96, 32, 8, 1)), ((2, 3, 4), (12, 4, 1)), ((7,), (1,)), ((), ())):
-        want = bytes(_lib.describe(0x1230, 1, shape, strides))
-        assert _lib.record(0x1230, 1, shape, strides) == want
-    assert ctypes.sizeof(_lib.BeaTensor) == len(_lib.record(0, 0, (1,) * 6, (1,) * 6))
-    assert _lib.BeaTensor.from_buffer_copy(_lib.record(0, 0, (1,) * 6, (1,) * 6)).ndim == 6
 
 
 def test_status_strings(lib):
