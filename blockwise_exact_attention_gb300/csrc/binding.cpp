@@ -269,12 +269,14 @@ PyObject* py_paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(capacity >= 0 && capacity <= INT32_MAX, "paged_plan: capacity ", capacity);
     const int64_t rows = in[0].dim() == 1 ? in[0].size(0) : 0;
     const int64_t sizes[6] = {capacity, capacity, rows + 1, rows + 1, rows, 1};
+    const int64_t one = 1;
     int64_t total = 0, at = 0;
-    for (int64_t s : sizes) total += s;
+    for (int64_t s : sizes) total += (s + 3) / 4 * 4;  // each on a 16-byte boundary
     const Tensor all = at::empty({total}, in[0].options());
-    for (int i = 0; i < 6; ++i) {
-      out[i] = all.narrow(0, at, sizes[i]);
-      at += sizes[i];
+    for (int i = 0; i < 6; ++i) {  // views of one allocation
+      out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+      out[i].unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(&sizes[i], 1), at::IntArrayRef(&one, 1), at);
+      at += (sizes[i] + 3) / 4 * 4;
     }
   }
   Call c;

@@ -12,6 +12,23 @@
 
 namespace bea {
 
+// Launch with programmatic stream serialisation: the kernel may be set up while the one before it on the stream still
+// runs, so it has to call grid_dependency_wait() in every thread before it touches anything in memory.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // ---- rotary positions ----------------------------------------------------------
 constexpr int kRopeMaxPairs = 128;  // d <= 256
 constexpr int kRopeMaxAxes = 8;
@@ -53,7 +70,9 @@ cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t s, int* n
 
 struct PagedDecodeParams {
   int n, h, hkv, d;
-  int num_pages, page, max_pages, left;  // left: keys before the last one that are visible (kUnbounded: all)
+  int num_pages, page, max_pages;
+  int page_shift;  // log2(page), -1 where page is not a power of two
+  int left;        // keys before the last one that are visible (kUnbounded: all)
   int is_f32, out_is_f32;
   float scale;
   Seq4 q, out;  // sl unused (one query per request)
@@ -67,7 +86,7 @@ struct PagedDecodeParams {
 };
 size_t paged_decode_workspace(int64_t h, int64_t hkv, int64_t d, int64_t max_keys);
 // Whether a request's tiles can be counted in 31 bits.
-bool paged_decode_fits(int64_t h, int64_t hkv, bool is_f32, int64_t max_keys);
+bool paged_decode_fits(int64_t h, int64_t hkv, int64_t d, bool is_f32, int64_t max_keys);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch);
 
 }  // namespace bea

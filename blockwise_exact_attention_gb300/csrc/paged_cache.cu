@@ -2,15 +2,19 @@
 // positions from request lengths, and new keys and values scattered to their
 // slots.
 //
-// paged_plan. One CTA scans the requests (three exclusive sums: pages given
-// back, pages taken, tokens added), checks the whole step before it changes
-// anything, pushes the pages of ended requests and writes the per-request
-// arrays. The places of the added tokens are then independent of one another:
-// token i of row r (the row is found by bisection of cu_new) has position p =
-// len_r + i and lives in page p / page of its row, which is either an old entry
-// of the table or the page popped for it, pool[top - 1 - (cu_pages[r] + k)].
-// The token that opens a page also writes the table's entry, so no thread reads
-// an entry that this step writes.
+// paged_plan. One CTA scans the requests (exclusive sums of pages given back,
+// pages taken, tokens added), checks the whole step before it changes anything,
+// pushes the pages of ended requests and writes the per-request arrays. The
+// places of the added tokens are then independent of one another: token i of row
+// r has position p = len_r + i and lives in page p / page of its row, which is
+// either an old entry of the table or the page popped for it, pool[top - 1 -
+// (cu_pages[r] + k)]. The token that opens a page also writes the table's entry,
+// so no thread reads an entry that this step writes. Up to kFuseCapacity places
+// the same CTA fills them row by row; above, a second launch spreads them over
+// the GPU and finds their rows in cu_new.
+//
+// Latency-bound: a decode step moves some KB, in a chain of dependent reads
+// (lengths, then table or stack) with a block-wide scan between them.
 #include "launch_cache.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -19,113 +23,95 @@ namespace bea {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kFillThreads = 256;
+constexpr int kFillRun = 4;  // consecutive places of a thread
 // Up to this many places the scanning CTA fills them itself.
 constexpr int kFuseCapacity = 4096;
 
 __device__ __forceinline__ int pages_of(int tokens, int page) { return (int)(((int64_t)tokens + page - 1) / page); }
 
-// Inclusive sum over the block of a pair of values; *total gets the block's sum.
-__device__ __forceinline__ int2 block_scan(int2 x, int2* warp_sums, int2* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Pages given back, pages taken, tokens added.
+struct Sums {
+  long long back, need, add;
+  __device__ __forceinline__ Sums operator+(const Sums& o) const { return {back + o.back, need + o.need, add + o.add}; }
+};
+__device__ __forceinline__ Sums shfl_up(const Sums& s, int o) {
+  return {__shfl_up_sync(~0u, s.back, o), __shfl_up_sync(~0u, s.need, o), __shfl_up_sync(~0u, s.add, o)};
+}
+__device__ __forceinline__ Sums warp_inclusive(Sums x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(~0u, x.x, o), b = __shfl_up_sync(~0u, x.y, o);
-    if (lane >= o) x.x += a, x.y += b;
+    const Sums y = shfl_up(x, o);
+    if ((threadIdx.x & 31) >= o) x = x + y;
   }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int2 w = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(~0u, w.x, o), b = __shfl_up_sync(~0u, w.y, o);
-      if (lane >= o) w.x += a, w.y += b;
-    }
-    warp_sums[lane] = w;
-  }
-  __syncthreads();
-  if (warp > 0) x.x += warp_sums[warp - 1].x, x.y += warp_sums[warp - 1].y;
-  *total = warp_sums[31];
-  __syncthreads();
   return x;
 }
 
-// Places [first, capacity) in steps of `stride`.
-__device__ __forceinline__ void fill_places(const PlanParams& p, int64_t first, int64_t stride) {
-  const int total = p.cu_new[p.n];
-  const int top = p.n_free_out[0] + p.cu_pages[p.n];
-  for (int64_t i = first; i < p.capacity; i += stride) {
-    int slot = -1, pos = 0;
-    if (i < total) {
-      int lo = 0, hi = p.n - 1;  // the row with cu_new[row] <= i < cu_new[row + 1]
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu_new[mid + 1] > i)
-          hi = mid;
-        else
-          lo = mid + 1;
-      }
-      const int start = p.cu_new[lo];
-      const int old = p.lens_out[lo] - (p.cu_new[lo + 1] - start);
-      pos = old + (int)(i - start);
-      const int j = pos / p.page, off = pos - j * p.page;
-      const int had = pages_of(old, p.page);
-      int32_t* entry = p.table + lo * p.table_stride + j;
-      const int id = j < had ? *entry : p.pool[top - 1 - (p.cu_pages[lo] + j - had)];
-      if (off == 0) *entry = id;
-      const int64_t at = (int64_t)id * p.page + off;
-      if (id >= 0 && at <= INT32_MAX)
-        slot = (int)at;
-      else
-        report_status(p.status, BEA_STATUS_PAGES);
-    }
-    p.slot_map[i] = slot;
-    p.positions[i] = pos;
+// One row of the step.
+struct Row {
+  int len, add, back, had, need;
+  bool wrong;
+};
+__device__ __forceinline__ Row row_of(const PlanParams& p, int len, int a) {
+  Row r{len, 0, 0, 0, 0, false};
+  if (len < 0 || a < -1 || (int64_t)len + max(a, 0) > (int64_t)p.max_pages * p.page) {
+    r.wrong = true;
+    return r;
   }
+  r.had = pages_of(len, p.page);
+  if (a < 0) {
+    r.back = r.had;
+  } else {
+    r.add = a;
+    r.need = pages_of(len + a, p.page) - r.had;
+  }
+  return r;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, int fill) {
-  __shared__ int2 warp_sums[32];
-  __shared__ long long sums[3];  // given back, taken, added
-  __shared__ int bad;
-  __shared__ int give_at[kPlanThreads], give_n[kPlanThreads];
-  const int tid = threadIdx.x;
-  if (tid < 3) sums[tid] = 0;
-  if (tid == 0) bad = 0;
+// The place of token i of a row that held `old` tokens: writes the slot, the position and, for a page's first token,
+// the table's entry. `taken`: pages popped before the row.
+__device__ __forceinline__ int2 place_of(const PlanParams& p, int row, int old, int i, int taken, int top) {
+  const int pos = old + i, j = pos / p.page, off = pos - j * p.page, had = pages_of(old, p.page);
+  int32_t* entry = p.table + row * p.table_stride + j;
+  const int id = j < had ? *entry : p.pool[top - 1 - (taken + j - had)];
+  if (off == 0) *entry = id;
+  const int64_t at = (int64_t)id * p.page + off;
+  if (id >= 0 && at <= INT32_MAX) return make_int2((int)at, pos);
+  report_status(p.status, BEA_STATUS_PAGES);
+  return make_int2(-1, pos);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p, int fill) {
+  __shared__ Sums warp_sums[kPlanWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_launch_dependents();
-  __syncthreads();
-  // 1. totals and checks, before anything is changed
-  const int64_t most = (int64_t)p.max_pages * p.page;
-  long long back = 0, need = 0, add = 0;
-  bool wrong = false;
-  for (int r = tid; r < p.n; r += kPlanThreads) {
-    const int len = p.lens[r], a = p.new_lens[r];
-    if (len < 0 || a < -1 || (int64_t)len + max(a, 0) > most) {
-      wrong = true;
-    } else if (a < 0) {
-      back += pages_of(len, p.page);
-    } else {
-      need += pages_of(len + a, p.page) - pages_of(len, p.page);
-      add += a;
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    back += __shfl_xor_sync(~0u, back, o);
-    need += __shfl_xor_sync(~0u, need, o);
-    add += __shfl_xor_sync(~0u, add, o);
-  }
-  if ((tid & 31) == 0) {
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sums[0]), (unsigned long long)back);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sums[1]), (unsigned long long)need);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sums[2]), (unsigned long long)add);
-  }
-  if (wrong) bad = 1;
-  __syncthreads();
+  grid_dependency_wait();
+  // 1. Totals and checks, before anything is changed. A thread has `per` consecutive rows.
+  const int per = (p.n + kPlanThreads - 1) / kPlanThreads, r0 = tid * per;
   const int have = p.n_free[0];
-  const bool ok = !bad && have >= 0 && have + sums[0] <= p.n_pool && sums[1] <= have + sums[0] && sums[2] <= p.capacity;
-  __syncthreads();  // n_free has been read by all threads (n_free_out may be the same word)
+  Sums mine{0, 0, 0};
+  bool wrong = false;
+  int len = 0, a = 0;  // of the thread's only row, where it has one
+  for (int x = 0; x < per; ++x) {
+    if (r0 + x >= p.n) break;
+    len = p.lens[r0 + x];
+    a = p.new_lens[r0 + x];
+    const Row r = row_of(p, len, a);
+    wrong = wrong || r.wrong;
+    mine = mine + Sums{r.back, r.need, r.add};
+  }
+  const Sums inc = warp_inclusive(mine);
+  if (lane == 31) warp_sums[warp] = inc;
+  const bool bad = __syncthreads_or(wrong);
+  const Sums w = warp_inclusive(warp_sums[lane]);  // by every warp for itself
+  const Sums all{__shfl_sync(~0u, w.back, 31), __shfl_sync(~0u, w.need, 31), __shfl_sync(~0u, w.add, 31)};
+  const int prev = max(warp - 1, 0);
+  Sums at{__shfl_sync(~0u, w.back, prev), __shfl_sync(~0u, w.need, prev), __shfl_sync(~0u, w.add, prev)};
+  if (warp == 0) at = Sums{0, 0, 0};
+  at = Sums{at.back + inc.back - mine.back, at.need + inc.need - mine.need, at.add + inc.add - mine.add};
+  const bool ok = !bad && have >= 0 && have + all.back <= p.n_pool && all.need <= have + all.back && all.add <= p.capacity;
+  const int top = have + (int)all.back;
   if (!ok) {
     if (tid == 0) report_status(p.status, BEA_STATUS_PAGES);
     for (int r = tid; r <= p.n; r += kPlanThreads) {
@@ -133,85 +119,192 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, int fi
       p.cu_pages[r] = 0;
       if (r < p.n) p.lens_out[r] = p.lens[r];
     }
+    __syncthreads();
     if (tid == 0) p.n_free_out[0] = have;
   } else {
-    // 2. exclusive sums, 1024 rows at a time; ended rows' pages go on the stack
-    int2 base = make_int2(0, 0);  // taken, added
-    int given = 0;
-    for (int r0 = 0; r0 < p.n; r0 += kPlanThreads) {
-      const int r = r0 + tid;
-      int len = 0, a = 0;
-      if (r < p.n) len = p.lens[r], a = p.new_lens[r];
-      const int ends = a < 0 ? pages_of(len, p.page) : 0;
-      const int takes = a < 0 ? 0 : pages_of(len + a, p.page) - pages_of(len, p.page);
-      const int adds = max(a, 0);
-      int2 tot, tot_given;
-      const int2 inc = block_scan(make_int2(takes, adds), warp_sums, &tot);
-      const int2 inc_given = block_scan(make_int2(ends, 0), warp_sums, &tot_given);
-      if (r < p.n) {
-        p.cu_pages[r] = base.x + inc.x - takes;
-        p.cu_new[r] = base.y + inc.y - adds;
-        p.lens_out[r] = a < 0 ? 0 : len + a;
+    // 2. The arrays, and ended rows' pages onto the stack (by the whole warp, row after row).
+    for (int x = 0; x < per; ++x) {
+      const int row = r0 + x;
+      Row r{0, 0, 0, 0, 0, false};
+      if (row < p.n) {
+        if (per > 1) len = p.lens[row], a = p.new_lens[row];
+        r = row_of(p, len, a);
+        p.cu_pages[row] = (int)at.need;
+        p.cu_new[row] = (int)at.add;
+        p.lens_out[row] = a < 0 ? 0 : len + a;
       }
-      give_at[tid] = have + given + inc_given.x - ends;
-      give_n[tid] = ends;
-      base.x += tot.x;
-      base.y += tot.y;
-      given += tot_given.x;
-      __syncthreads();
-      if (tot_given.x > 0) {
-        const int rows = min(kPlanThreads, p.n - r0);
-        for (int w = tid >> 5; w < rows; w += kPlanThreads / 32) {
-          const int m = give_n[w], at = give_at[w];
-          const int32_t* row = p.table + (r0 + w) * p.table_stride;
-          for (int j = tid & 31; j < m; j += 32) p.pool[at + j] = row[j];
+      for (uint32_t ends = __ballot_sync(~0u, r.back > 0); ends != 0; ends &= ends - 1) {
+        const int from = __ffs(ends) - 1;
+        const int m = __shfl_sync(~0u, r.back, from), to = have + __shfl_sync(~0u, (int)at.back, from);
+        const int32_t* entries = p.table + __shfl_sync(~0u, row, from) * p.table_stride;
+        for (int j = lane; j < m; j += 32 * 8) {
+          int32_t id[8];
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            if (j + 32 * z < m) id[z] = entries[j + 32 * z];
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            if (j + 32 * z < m) p.pool[to + j + 32 * z] = id[z];
         }
       }
-      __syncthreads();
+      at = at + Sums{r.back, r.need, r.add};
     }
+    __syncthreads();  // the stack is complete, and n_free has been read by all (n_free_out may be the same word)
     if (tid == 0) {
-      p.cu_pages[p.n] = base.x;
-      p.cu_new[p.n] = base.y;
-      p.n_free_out[0] = have + given - base.x;
+      p.cu_pages[p.n] = (int)all.need;
+      p.cu_new[p.n] = (int)all.add;
+      p.n_free_out[0] = top - (int)all.need;
     }
   }
-  if (fill) {
-    __syncthreads();
-    fill_places(p, tid, kPlanThreads);
+  if (!fill) return;
+  // 3. The places, row after row: short rows by their thread, long ones by its warp.
+  const int total = ok ? (int)all.add : 0;
+  for (int i = total + tid; i < p.capacity; i += kPlanThreads) {
+    p.slot_map[i] = -1;
+    p.positions[i] = 0;
+  }
+  if (total == 0) return;
+  constexpr int kShort = 2;
+  at = Sums{at.back - mine.back, at.need - mine.need, at.add - mine.add};
+  for (int x = 0; x < per; ++x) {
+    const int row = r0 + x;
+    Row r{0, 0, 0, 0, 0, false};
+    int old = len;
+    if (row < p.n) {
+      if (per > 1) {  // the row's numbers as written above
+        a = p.new_lens[row];
+        old = p.lens_out[row] - a;
+        at.add = p.cu_new[row];
+        at.need = p.cu_pages[row];
+      }
+      r.add = max(a, 0);
+    }
+    if (r.add <= kShort)
+      for (int i = 0; i < r.add; ++i) {
+        const int2 s = place_of(p, row, old, i, (int)at.need, top);
+        p.slot_map[at.add + i] = s.x;
+        p.positions[at.add + i] = s.y;
+      }
+    for (uint32_t rows = __ballot_sync(~0u, r.add > kShort); rows != 0; rows &= rows - 1) {
+      const int from = __ffs(rows) - 1;
+      const int m = __shfl_sync(~0u, r.add, from), to = __shfl_sync(~0u, (int)at.add, from);
+      const int w_row = __shfl_sync(~0u, row, from), w_old = __shfl_sync(~0u, old, from);
+      const int w_taken = __shfl_sync(~0u, (int)at.need, from);
+      for (int i = lane; i < m; i += 32) {
+        const int2 s = place_of(p, w_row, w_old, i, w_taken, top);
+        p.slot_map[to + i] = s.x;
+        p.positions[to + i] = s.y;
+      }
+    }
   }
 }
 
-__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PlanParams p) {
+// The last row with cu[row] <= i among [lo, hi].
+__device__ __forceinline__ int row_of_token(const int32_t* cu, int lo, int hi, int i) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= i)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_constant__ PlanParams p) {
+  grid_launch_dependents();
   grid_dependency_wait();
-  fill_places(p, (int64_t)blockIdx.x * kFillThreads + threadIdx.x, (int64_t)gridDim.x * kFillThreads);
+  constexpr int kWarpRun = 32 * kFillRun;
+  const int lane = threadIdx.x & 31;
+  const int total = p.cu_new[p.n], top = p.n_free_out[0] + p.cu_pages[p.n];
+  const bool vec = ((reinterpret_cast<uintptr_t>(p.slot_map) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+  const int64_t warps = (int64_t)gridDim.x * (kFillThreads / 32);
+  for (int64_t w = (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5); w * kWarpRun < p.capacity; w += warps) {
+    const int first = (int)(w * kWarpRun), last = min(first + kWarpRun, total) - 1;
+    // The rows of the warp's first and last token, by 32 probes at a time; each lane searches between them.
+    int lo = 0, hi = 0;
+    if (first < total) {
+#pragma unroll
+      for (int end = 0; end < 2; ++end) {
+        const int i = end ? last : first;
+        int x = end ? lo : 0, y = p.n - 1;  // the row is in [x, y]
+        while (x < y) {
+          const int step = (y - x + 32) / 32, at = x + step * lane;
+          const uint32_t below = __ballot_sync(~0u, at <= y && p.cu_new[at] <= i);
+          x += step * (31 - __clz(below));  // lane 0 is always below
+          y = min(y, x + step - 1);
+        }
+        if (end == 0)
+          lo = x;
+        else
+          hi = x;
+      }
+    }
+    const int64_t i0 = (int64_t)first + lane * kFillRun;
+    int32_t slot[kFillRun], pos[kFillRun];
+    int row = i0 < total ? row_of_token(p.cu_new, lo, hi, (int)i0) : 0;
+    int begin = 0, next = 0, old = 0, taken = 0;
+    bool fresh = true;
+#pragma unroll
+    for (int z = 0; z < kFillRun; ++z) {
+      slot[z] = -1;
+      pos[z] = 0;
+      if (i0 + z < total) {
+        while (fresh || i0 + z >= next) {  // rows without tokens are passed over
+          if (!fresh) ++row;
+          fresh = false;
+          begin = p.cu_new[row];
+          next = p.cu_new[row + 1];
+          old = p.lens_out[row] - (next - begin);
+          taken = p.cu_pages[row];
+        }
+        const int2 s = place_of(p, row, old, (int)(i0 + z) - begin, taken, top);
+        slot[z] = s.x;
+        pos[z] = s.y;
+      }
+    }
+    if (vec && i0 + kFillRun <= p.capacity) {
+      *reinterpret_cast<int4*>(p.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int z = 0; z < kFillRun; ++z)
+        if (i0 + z < p.capacity) p.slot_map[i0 + z] = slot[z], p.positions[i0 + z] = pos[z];
+    }
+  }
 }
 
 // ---- write ---------------------------------------------------------------------
 
+// HBM-bound copy of rows of some hundred bytes to places of their own: a thread
+// moves 16 bytes of K and 16 of V.
 constexpr int kWriteThreads = 256;
 
 __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int per_token = p.hkv * p.row_vecs;
   const int64_t total = (int64_t)p.n * p.l * per_token;
   for (int64_t it = (int64_t)blockIdx.x * kWriteThreads + threadIdx.x; it < total;
        it += (int64_t)gridDim.x * kWriteThreads) {
     const int64_t t = it / per_token;
     const int in = (int)(it - t * per_token);
-    const int hh = in / p.row_vecs, c = in - hh * p.row_vecs;
     const int slot = p.slot_map[t];
+    const int64_t b = t / p.l;
+    const int i = (int)(t - b * p.l);
+    const int hh = in / p.row_vecs, c = in - hh * p.row_vecs;
+    // read before the slot is known
+    const uint4 kx = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k.ptr) +
+                                                           (b * p.k.sn + i * p.k.sl + hh * p.k.sh) * p.es + c * 16));
+    const uint4 vx = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v.ptr) +
+                                                           (b * p.v.sn + i * p.v.sl + hh * p.v.sh) * p.es + c * 16));
     if (slot < 0 || slot >= p.num_slots) {
       if (slot != -1 && in == 0) report_status(p.status, BEA_STATUS_PAGES);
       continue;
     }
-    const int64_t b = t / p.l;
-    const int i = (int)(t - b * p.l);
     const int pg = slot / p.page, off = slot - pg * p.page;
-    const int64_t ks = (b * p.k.sn + i * p.k.sl + hh * p.k.sh) * p.es + c * 16;
-    const int64_t vs = (b * p.v.sn + i * p.v.sl + hh * p.v.sh) * p.es + c * 16;
     const int64_t kd = (pg * p.k_cache.sn + off * p.k_cache.sl + hh * p.k_cache.sh) * p.es + c * 16;
     const int64_t vd = (pg * p.v_cache.sn + off * p.v_cache.sl + hh * p.v_cache.sh) * p.es + c * 16;
-    const uint4 kx = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.k.ptr) + ks);
-    const uint4 vx = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.v.ptr) + vs);
     *reinterpret_cast<uint4*>(static_cast<char*>(p.k_cache.ptr) + kd) = kx;
     *reinterpret_cast<uint4*>(static_cast<char*>(p.v_cache.ptr) + vd) = vx;
   }
@@ -221,28 +314,17 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid
 
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t s, int* nlaunch) {
   const int fill = p.capacity <= kFuseCapacity;
-  plan_kernel<<<1, kPlanThreads, 0, s>>>(p, fill);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(plan_kernel, dim3(1), kPlanThreads, 0, s, p, fill);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
   if (fill) return cudaSuccess;
   static PerContext<int> cache;
   int cap = 0;
   if ((e = wave_cap(cache, plan_fill_kernel, kFillThreads, 0, &cap)) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  const int blocks = (p.capacity + kFillThreads - 1) / kFillThreads;
-  cfg.gridDim = dim3((unsigned)(blocks < cap ? blocks : cap));
-  cfg.blockDim = dim3(kFillThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, plan_fill_kernel, p);
-  if (e != cudaSuccess) return e;
-  *nlaunch += 1;
-  return cudaSuccess;
+  const int blocks = (p.capacity + kFillThreads * kFillRun - 1) / (kFillThreads * kFillRun);
+  e = launch_dependent(plan_fill_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), kFillThreads, 0, s, p);
+  if (e == cudaSuccess) *nlaunch += 1;
+  return e;
 }
 
 cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t s, int* nlaunch) {
@@ -250,9 +332,9 @@ cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t s, int* n
   if (total == 0) return cudaSuccess;
   int64_t blocks = (total + kWriteThreads - 1) / kWriteThreads;
   if (blocks > (int64_t(1) << 30)) blocks = int64_t(1) << 30;
-  paged_write_kernel<<<(unsigned)blocks, kWriteThreads, 0, s>>>(p);
-  *nlaunch += 1;
-  return cudaGetLastError();
+  const cudaError_t e = launch_dependent(paged_write_kernel, dim3((unsigned)blocks), kWriteThreads, 0, s, p);
+  if (e == cudaSuccess) *nlaunch += 1;
+  return e;
 }
 
 }  // namespace bea

@@ -43,14 +43,15 @@ constexpr int kMinCost = 2 * kWarps;  // of a CTA's run, as long as there are fe
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <bool kF32, int kD>
+// kHd: query heads a unit has at most (bf16: 16, the rows of an mma).
+template <bool kF32, int kD, int kHd>
 struct Cfg {
-  static constexpr int kKeys = kF32 ? 8 : 16;  // keys of a tile
-  static constexpr int kRows = kF32 ? 8 : 16;  // query heads of a unit
+  static constexpr int kRows = kHd;
   static constexpr int kEs = kF32 ? 4 : 2;
   static constexpr int kRowBytes = kD * kEs;
-  static constexpr int kStageBytes = 2 * kKeys * kRowBytes;  // K then V
-  static constexpr int kStages = 16384 / kStageBytes;       // 16 KB in flight or in use per warp
+  static constexpr int kKeys = 4096 / kRowBytes;  // of a tile: K and V 4 KB each
+  static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
+  static constexpr int kStages = 2;
   static constexpr int kWarpRing = kStages * kStageBytes;
   static constexpr int kRing = kWarps * kWarpRing;
   static constexpr int kPitch = kD + 8;  // floats a row of a part: 8 rows x 4 lanes fall on different banks
@@ -119,12 +120,52 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A row of kRows floats in shared memory, 16 bytes at a time where it can be.
+template <int kRows>
+__device__ __forceinline__ void store_rows(float* to, const float (&x)[kRows]) {
+  if constexpr (kRows % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < kRows; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) to[i] = x[i];
+  }
+}
+template <int kRows>
+__device__ __forceinline__ void load_rows(const float* from, float (&x)[kRows]) {
+  if constexpr (kRows % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < kRows; i += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(from + i);
+      x[i] = y.x, x[i + 1] = y.y, x[i + 2] = y.z, x[i + 3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) x[i] = from[i];
+  }
+}
+
 // The first visible key of a request of `len` keys.
 __device__ __forceinline__ int first_key(int len, int left) { return left >= len ? 0 : len - 1 - left; }
 
+// m: in units of log2.
+__device__ __forceinline__ void write_lse(const PagedDecodeParams& p, int64_t b, int hh, float m, float l) {
+  p.lse.ptr[b * p.lse.sn + hh * p.lse.sh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+__device__ __forceinline__ void write_out4(const PagedDecodeParams& p, int64_t b, int hh, int c, float4 o, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t to = b * p.out.sn + hh * p.out.sh + c;
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (p.out_is_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + to) = o;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out.ptr) + to) =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+
 // The last index with key(index) <= x, key rising, key(0) <= x.
 template <typename F>
-__device__ __forceinline__ int last_below(int n, int64_t x, F key) {
+__device__ __forceinline__ int last_below(int n, int x, F key) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -136,10 +177,10 @@ __device__ __forceinline__ int last_below(int n, int64_t x, F key) {
   return lo;
 }
 
-template <bool kF32, int kD>
+template <bool kF32, int kD, int kHd>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Launch a) {
-  using C = Cfg<kF32, kD>;
+  using C = Cfg<kF32, kD, kHd>;
   extern __shared__ __align__(128) uint8_t smem[];
   // requests with a visible key, in order: tiles of a unit summed over those before, number, length
   __shared__ int pre[kMaxRequests + 1], who[kMaxRequests], lens[kMaxRequests];
@@ -149,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int2 part_of[kWarps][2];   // (request, unit) of these parts, -1: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_launch_dependents();
+  grid_dependency_wait();
 
   // ---- tiles per request, their sums, and this CTA's run [t0, t1) -----------------
   const int most = p.max_pages * p.page, units = a.units, grid = gridDim.x, cta = blockIdx.x;
@@ -218,45 +260,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  // Costs. Unit u of the k-th request costs its tiles and kUnitCost before them.
-  const int64_t cost = (int64_t)(run + kUnitCost * count) * units;
-  const int ctas = (int)min((int64_t)grid, max((int64_t)1, cost / kMinCost));
+  // Costs (below 2^31, which the host sees to). Unit u of the k-th request costs its tiles and kUnitCost before them.
+  const int cost = (run + kUnitCost * count) * units;
+  const int ctas = min(grid, max(1, cost / kMinCost));
   const bool whole = longest <= kWholeTiles;
-  auto begin_cost = [&](int k) { return (int64_t)(pre[k] + kUnitCost * k) * units; };
-  // where CTA c's run begins, as a cost
+  const int share = cost / ctas, over = cost - share * ctas;  // the first `over` runs cost one more
+  auto begin_cost = [&](int k) { return (pre[k] + kUnitCost * k) * units; };
+  struct Place {
+    int v, k, unit, in;  // a cost, its request and unit, and how far into the unit
+  };
+  auto place = [&](int v) {
+    const int k = last_below(count, v, begin_cost);
+    const int each = pre[k + 1] - pre[k] + kUnitCost, in = v - begin_cost(k), unit = in / each;
+    return Place{v, k, unit, in - unit * each};
+  };
+  // where CTA c's run begins
   auto border = [&](int c) {
-    if (c >= ctas) return cost;
-    int64_t v = cost * c / ctas;
-    if (whole && v > 0) {
-      const int k = last_below(count, v, begin_cost);
-      const int each = pre[k + 1] - pre[k] + kUnitCost;
-      const int64_t in = v - begin_cost(k);
-      v += (in % each) * 2 < each ? -(in % each) : each - in % each;
+    int v = share * c + min(c, over);
+    if (whole && v > 0 && v < cost) {
+      const Place at = place(v);
+      const int each = pre[at.k + 1] - pre[at.k] + kUnitCost;
+      v += at.in * 2 < each ? -at.in : each - at.in;
     }
     return v;
   };
   // the first tile that is not before cost v
-  auto tile_at = [&](int64_t v) {
+  auto tile_at = [&](int v) {
     if (v >= cost) return run * units;
-    const int k = last_below(count, v, begin_cost);
-    const int cnt = pre[k + 1] - pre[k], in = (int)(v - begin_cost(k)), unit = in / (cnt + kUnitCost);
-    return pre[k] * units + unit * cnt + max(0, in - unit * (cnt + kUnitCost) - kUnitCost);
+    const Place at = place(v);
+    return pre[at.k] * units + at.unit * (pre[at.k + 1] - pre[at.k]) + max(0, at.in - kUnitCost);
   };
   const WsLayout wl = ws_layout(C::kRows, kD);
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   if (a.split && tid == 0) reinterpret_cast<Split*>(ws)[cta] = Split{0, 0, -1, 0};
   if (cta >= ctas || count == 0) return;
-  const int64_t v0 = border(cta), v1 = border(cta + 1);
+  // Searches and divisions side by side: lanes 0, 1 the CTA's run, then lanes 2, 3 this warp's eighth of it. The first
+  // unit's own cost is left out of the split, it has no tiles.
+  int mark = border(cta + (lane & 1));
+  const int v0 = __shfl_sync(~0u, mark, 0), v1 = __shfl_sync(~0u, mark, 1);
   if (v0 >= v1) return;
-  const int t0 = tile_at(v0), t1 = tile_at(v1);
-  const int w0 = tile_at(v0 + (v1 - v0) * warp / kWarps), w1 = tile_at(v0 + (v1 - v0) * (warp + 1) / kWarps);
+  const Place start = place(v0);
+  const int s0 = min(v1, v0 + max(0, kUnitCost - start.in));
+  const int step = (v1 - s0) / kWarps, rest = v1 - s0 - step * kWarps, part_no = warp + (lane & 1);
+  mark = tile_at((lane & 2) == 0 ? (lane == 0 ? v0 : v1) : s0 + step * part_no + min(part_no, rest));
+  const int t0 = __shfl_sync(~0u, mark, 0), t1 = __shfl_sync(~0u, mark, 1);
+  const int w0 = __shfl_sync(~0u, mark, 2), w1 = __shfl_sync(~0u, mark, 3);
 
   // ---- loads: the i-th tile of this warp is tile w0 + i -------------------------------
-  auto first_tile = [&](int k) { return (int64_t)pre[k] * units; };
+  auto first_tile = [&](int k) { return pre[k] * units; };
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpRing;
   const int group = p.h / p.hkv;
   const int mine = w1 - w0;
   const bool one_page = p.page % C::kKeys == 0;  // a tile lies in one page
+  auto page_of = [&](int key) { return p.page_shift >= 0 ? key >> p.page_shift : key / p.page; };
   // Descriptors of this warp's next 32 tiles, one per lane.
   int d_b = 0, d_hk = 0, d_key = 0;
   int64_t d_k = 0, d_v = 0;
@@ -270,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cnt = pre[k + 1] - pre[k], in = t - pre[k] * units, unit = in / cnt;
     const int len = lens[k], first = first_key(len, p.left);
     d_b = who[k];
-    d_hk = unit / a.mtiles;
+    d_hk = a.mtiles == 1 ? unit : unit / a.mtiles;
     d_key = (first / C::kKeys + (in - unit * cnt)) * C::kKeys;
     // rows of the tile that are visible
     const int lo = max(first - d_key, 0), hi = min(len - d_key, C::kKeys);
-    d_mask = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+    d_mask = (0xFFFFFFFFu >> (32 - hi)) & (0xFFFFFFFFu << lo);
     if (one_page) {
-      const int pg = d_key / p.page, off = d_key - pg * p.page;
+      const int pg = page_of(d_key), off = d_key - pg * p.page;
       const int id = p.table[d_b * p.table_stride + pg];
       if (id < 0 || id >= p.num_pages) {
         report_status(p.status, BEA_STATUS_PAGES);
@@ -297,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t mask = __shfl_sync(~0u, d_mask, j);
     n_id = INT32_MIN;  // not visible
     if (lane < C::kKeys && ((mask >> lane) & 1u)) {
-      const int pg = key / p.page;
+      const int pg = page_of(key);
       n_off = key - pg * p.page;
       n_id = max(p.table[b * p.table_stride + pg], -1);
     }
@@ -305,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto load = [&](int i) {
     if (i < mine) {
       const int j = i & 31, stage = i % C::kStages;
+      if (!one_page && i == 0) look_up(0);
       const uint32_t kd = ring + stage * C::kStageBytes, vd = kd + C::kKeys * C::kRowBytes;
       uint32_t mask;
       int64_t k_at = 0, v_at = 0, k_row = 0, v_row = 0;
@@ -347,23 +404,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     cp_async_commit();  // an empty group where there is no tile, so that groups count tiles
   };
-  if (!one_page) look_up(0);
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) load(i);
 
   // ---- unit by unit ----------------------------------------------------------------
   float* head = reinterpret_cast<float*>(smem + C::kRing + warp * C::kPart);
   float* tail = reinterpret_cast<float*>(smem + warp * C::kWarpRing);
   float* q_smem = reinterpret_cast<float*>(smem + C::kRing + C::kHeads) + warp * C::kRows * kD;
   float* p_smem = reinterpret_cast<float*>(smem + C::kRing + C::kHeads + C::kQ) + warp * C::kKeys * C::kRows;
-  int done = 0;
+  int done = 0, sent = 0;
   int k = last_below(count, w0, first_tile);
   int unit = (w0 - pre[k] * units) / (pre[k + 1] - pre[k]);
   while (done < mine) {
     const int cnt = pre[k + 1] - pre[k], begin = pre[k] * units + unit * cnt, end = begin + cnt;
     const int todo = min(end, w1) - w0;  // this warp's tiles up to the unit's end
     const int64_t b = who[k];
-    const int hk = unit / a.mtiles, mi = unit - hk * a.mtiles;
+    const int hk = a.mtiles == 1 ? unit : unit / a.mtiles, mi = unit - hk * a.mtiles;
     const int h0 = hk * group + mi * C::kRows, rows = min(C::kRows, group - mi * C::kRows);
     const bool covered = begin >= w0 && end <= w1;
     const int which = begin < w0 ? 0 : 1;
@@ -377,91 +431,109 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < C::kRows; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       const float* q = static_cast<const float*>(p.q.ptr) + b * p.q.sn + h0 * p.q.sh;
       __syncwarp();
-      for (int i = 0; i < rows; ++i)
-        if (lane * 4 < p.d)
-          *reinterpret_cast<float4*>(q_smem + i * kD + lane * 4) =
-              *reinterpret_cast<const float4*>(q + i * p.q.sh + lane * 4);
+      float4 qr[C::kRows];  // rows the unit does not have are zeros: computed along, never written
+#pragma unroll
+      for (int i = 0; i < C::kRows; ++i)
+        qr[i] = i < rows && lane * 4 < p.d ? *reinterpret_cast<const float4*>(q + i * p.q.sh + lane * 4)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < C::kRows; ++i)
+        if (lane * 4 < kD) *reinterpret_cast<float4*>(q_smem + i * kD + lane * 4) = qr[i];
       __syncwarp();
       const int key = lane >> 2, quarter = lane & 3, sw = C::swizzle(key), pieces = p.d >> 2;
       const bool column = lane * 4 < kD;
       for (; done < todo; ++done) {
         const int stage = done % C::kStages;
-        load(done + C::kStages - 1);
+        while (sent < done + C::kStages) load(sent++);
         cp_async_wait<C::kStages - 1>();
         __syncwarp();
         const uint8_t* kt = smem + warp * C::kWarpRing + stage * C::kStageBytes;
         const uint8_t* vt = kt + C::kKeys * C::kRowBytes;
-        const bool see = (masks[warp][stage] >> key) & 1u;
-        float s[C::kRows];
+        const uint32_t mask = masks[warp][stage];
+        constexpr int kGroups = C::kKeys / 8;  // keys key, key + 8, ... of this lane
+        float s[kGroups][C::kRows];
 #pragma unroll
-        for (int i = 0; i < C::kRows; ++i) s[i] = 0.f;
+        for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+          for (int i = 0; i < C::kRows; ++i) s[g][i] = 0.f;
+#pragma unroll 2
         for (int c = quarter; c < pieces; c += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(kt + key * C::kRowBytes + ((c ^ sw) << 4));
+          float4 x[kGroups];
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g)
+            x[g] = *reinterpret_cast<const float4*>(kt + (key + 8 * g) * C::kRowBytes + ((c ^ sw) << 4));
 #pragma unroll
           for (int i = 0; i < C::kRows; ++i) {
-            if (i < rows) {
-              const float4 y = *reinterpret_cast<const float4*>(q_smem + i * kD + c * 4);
-              s[i] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[i]))));
-            }
+            const float4 y = *reinterpret_cast<const float4*>(q_smem + i * kD + c * 4);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+              s[g][i] = fmaf(x[g].x, y.x, fmaf(x[g].y, y.y, fmaf(x[g].z, y.z, fmaf(x[g].w, y.w, s[g][i]))));
           }
         }
 #pragma unroll
         for (int i = 0; i < C::kRows; ++i) {
-          if (i < rows) {
-            s[i] += __shfl_xor_sync(~0u, s[i], 1);
-            s[i] += __shfl_xor_sync(~0u, s[i], 2);
-            s[i] = see ? s[i] * a.sl2 : -INFINITY;
-            float top = s[i];
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-            if (top > m[i]) {
-              const float w = ex2_approx(m[i] - top);
-              m[i] = top;
-              l[i] *= w;
-              o[i] = make_float4(o[i].x * w, o[i].y * w, o[i].z * w, o[i].w * w);
-            }
-            const float e = ex2_approx(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
-            if (quarter == 0) {
-              l[i] += e;
-              p_smem[key * C::kRows + i] = e;
-            }
+          float top = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            s[g][i] += __shfl_xor_sync(~0u, s[g][i], 1);
+            s[g][i] += __shfl_xor_sync(~0u, s[g][i], 2);
+            s[g][i] = (mask >> (key + 8 * g)) & 1u ? s[g][i] * a.sl2 : -INFINITY;
+            top = fmaxf(top, s[g][i]);
           }
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+          const float mn = fmaxf(m[i], top), w = mn == -INFINITY ? 1.f : ex2_approx(m[i] - mn);
+          m[i] = mn;
+          l[i] *= w;
+          o[i] = make_float4(o[i].x * w, o[i].y * w, o[i].z * w, o[i].w * w);
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            s[g][i] = ex2_approx(s[g][i] - (mn == -INFINITY ? 0.f : mn));
+            if (quarter == 0) l[i] += s[g][i];
+          }
+        }
+        if (quarter == 0) {
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) store_rows<C::kRows>(p_smem + (key + 8 * g) * C::kRows, s[g]);
         }
         __syncwarp();
         if (column) {
 #pragma unroll
           for (int j = 0; j < C::kKeys; ++j) {
             const float4 v = *reinterpret_cast<const float4*>(vt + j * C::kRowBytes + ((lane ^ C::swizzle(j)) << 4));
+            float e[C::kRows];
+            load_rows<C::kRows>(p_smem + j * C::kRows, e);
 #pragma unroll
-            for (int i = 0; i < C::kRows; ++i) {
-              if (i < rows) {
-                const float e = p_smem[j * C::kRows + i];
-                o[i] = make_float4(fmaf(e, v.x, o[i].x), fmaf(e, v.y, o[i].y), fmaf(e, v.z, o[i].z), fmaf(e, v.w, o[i].w));
-              }
-            }
+            for (int i = 0; i < C::kRows; ++i)
+              o[i] = make_float4(fmaf(e[i], v.x, o[i].x), fmaf(e[i], v.y, o[i].y), fmaf(e[i], v.z, o[i].z),
+                                 fmaf(e[i], v.w, o[i].w));
           }
         }
         __syncwarp();
       }
 #pragma unroll
       for (int i = 0; i < C::kRows; ++i) {
-        if (i < rows) {
-          l[i] += __shfl_xor_sync(~0u, l[i], 4);
-          l[i] += __shfl_xor_sync(~0u, l[i], 8);
-          l[i] += __shfl_xor_sync(~0u, l[i], 16);
-          l[i] = __shfl_sync(~0u, l[i], 0);
-          if (covered) {
-            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-            if (lane * 4 < p.d)
-              *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + b * p.out.sn + (h0 + i) * p.out.sh + lane * 4) =
-                  make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
-            if (lane == 0)
-              p.lse.ptr[b * p.lse.sn + (h0 + i) * p.lse.sh] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
-          } else {
-            if (lane == 0) ml[warp][which][i] = make_float2(m[i], l[i]);
-            if (lane * 4 < p.d) *reinterpret_cast<float4*>(part + i * C::kPitch + lane * 4) = o[i];
-          }
+        l[i] += __shfl_xor_sync(~0u, l[i], 4);
+        l[i] += __shfl_xor_sync(~0u, l[i], 8);
+        l[i] += __shfl_xor_sync(~0u, l[i], 16);
+        l[i] = __shfl_sync(~0u, l[i], 0);
+      }
+      if (covered) {
+#pragma unroll
+        for (int i = 0; i < C::kRows; ++i) {
+          if (i >= rows) break;
+          const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+          if (lane * 4 < p.d)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + b * p.out.sn + (h0 + i) * p.out.sh + lane * 4) =
+                make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+          if (lane == 0) write_lse(p, b, h0 + i, m[i], l[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kRows; ++i) {
+          if (lane == 0) ml[warp][which][i] = make_float2(m[i], l[i]);
+          if (lane * 4 < p.d) *reinterpret_cast<float4*>(part + i * C::kPitch + lane * 4) = o[i];
         }
       }
     } else {
@@ -482,23 +554,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       for (; done < todo; ++done) {
         const int stage = done % C::kStages;
-        load(done + C::kStages - 1);
+        while (sent < done + C::kStages) load(sent++);
         cp_async_wait<C::kStages - 1>();
         __syncwarp();
         const uint32_t kt = ring + stage * C::kStageBytes, vt = kt + C::kKeys * C::kRowBytes;
         const uint32_t mask = masks[warp][stage];
-        float s[2][4] = {};
+        constexpr int kSub = C::kKeys / 16;  // blocks of 16 keys
+        float s[2 * kSub][4] = {};
 #pragma unroll
         for (int ks = 0; ks < kD / 16; ++ks) {
-          uint32_t kf[4];
-          const int kr = (lane & 7) + ((lane >> 4) << 3), chunk = 2 * ks + ((lane >> 3) & 1);
-          ldsm4(kt + kr * C::kRowBytes + ((chunk ^ C::swizzle(kr)) << 4), kf);
-          mma_bf16(s[0], qf[ks], kf[0], kf[1]);
-          mma_bf16(s[1], qf[ks], kf[2], kf[3]);
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            uint32_t kf[4];
+            const int kr = u * 16 + (lane & 7) + ((lane >> 4) << 3), chunk = 2 * ks + ((lane >> 3) & 1);
+            ldsm4(kt + kr * C::kRowBytes + ((chunk ^ C::swizzle(kr)) << 4), kf);
+            mma_bf16(s[2 * u], qf[ks], kf[0], kf[1]);
+            mma_bf16(s[2 * u + 1], qf[ks], kf[2], kf[3]);
+          }
         }
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+        for (int nb = 0; nb < 2 * kSub; ++nb)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const bool see = (mask >> (nb * 8 + col + (x & 1))) & 1u;
@@ -525,29 +601,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // P as two bf16 terms: the first 8 bits truncated, the rest rounded (2^-15 of P left over, where one term
         // would leave 2^-8). The second term is kept above 0, so that an infinite value stays infinite.
-        uint32_t hi[4], lo[4];
+        uint32_t hi[kSub][4], lo[kSub][4];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+        for (int nb = 0; nb < 2 * kSub; ++nb)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float ref = m[x] == -INFINITY ? 0.f : m[x];
             const float p0 = ex2_approx(s[nb][2 * x] - ref), p1 = ex2_approx(s[nb][2 * x + 1] - ref);
             l[x] += p0 + p1;
             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-            hi[nb * 2 + x] = __byte_perm(u0, u1, 0x7632);
+            hi[nb / 2][(nb & 1) * 2 + x] = __byte_perm(u0, u1, 0x7632);
             const float r0 = fmaxf(p0 - __uint_as_float(u0 & 0xFFFF0000u), p0 * 0x1p-20f);
             const float r1 = fmaxf(p1 - __uint_as_float(u1 & 0xFFFF0000u), p1 * 0x1p-20f);
-            lo[nb * 2 + x] = pack_bf16x2(r0, r1);
+            lo[nb / 2][(nb & 1) * 2 + x] = pack_bf16x2(r0, r1);
           }
 #pragma unroll
         for (int dp = 0; dp < kD / 16; ++dp) {
-          uint32_t vf[4];
-          const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), chunk = 2 * dp + (lane >> 4);
-          ldsm4_t(vt + vr * C::kRowBytes + ((chunk ^ C::swizzle(vr)) << 4), vf);
-          mma_bf16(o[2 * dp], hi, vf[0], vf[1]);
-          mma_bf16(o[2 * dp + 1], hi, vf[2], vf[3]);
-          mma_bf16(o[2 * dp], lo, vf[0], vf[1]);
-          mma_bf16(o[2 * dp + 1], lo, vf[2], vf[3]);
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            uint32_t vf[4];
+            const int vr = u * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), chunk = 2 * dp + (lane >> 4);
+            ldsm4_t(vt + vr * C::kRowBytes + ((chunk ^ C::swizzle(vr)) << 4), vf);
+            mma_bf16(o[2 * dp], hi[u], vf[0], vf[1]);
+            mma_bf16(o[2 * dp + 1], hi[u], vf[2], vf[3]);
+            mma_bf16(o[2 * dp], lo[u], vf[0], vf[1]);
+            mma_bf16(o[2 * dp + 1], lo[u], vf[2], vf[3]);
+          }
         }
         __syncwarp();
       }
@@ -569,8 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out.ptr) + to + c * 8) =
                   pack_bf16x2(o[c][2 * x] * inv, o[c][2 * x + 1] * inv);
           }
-          if ((lane & 3) == 0)
-            p.lse.ptr[b * p.lse.sn + (h0 + i) * p.lse.sh] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * kLn2;
+          if ((lane & 3) == 0) write_lse(p, b, h0 + i, m[x], l[x]);
         } else {
           if ((lane & 3) == 0) ml[warp][which][i] = make_float2(m[x], l[x]);
 #pragma unroll
@@ -585,65 +663,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- units in several warps: merge their parts, in order ----------------------------
   __syncthreads();
-  const int quads = p.d >> 2;
-  const int2* parts = &part_of[0][0];
-  for (int x = 0; x < 2 * kWarps;) {
-    const int2 of = parts[x];
-    if (of.x < 0) {
-      ++x;
-      continue;
-    }
-    int y = x + 1;  // parts [x, y) are this unit's
-    while (y < 2 * kWarps && (parts[y].x < 0 || (parts[y].x == of.x && parts[y].y == of.y))) ++y;
+  const int2 own = (&part_of[0][0])[lane & (2 * kWarps - 1)];  // lane z: part z & 1 of warp z >> 1
+  uint32_t left = __ballot_sync(~0u, lane < 2 * kWarps && own.x >= 0);
+  while (left != 0) {
+    const int x = __ffs(left) - 1;
+    const int2 of = make_int2(__shfl_sync(~0u, own.x, x), __shfl_sync(~0u, own.y, x));
+    const bool one = ((left >> lane) & 1u) && own.x == of.x && own.y == of.y;  // of this unit's parts
+    const uint32_t these = __ballot_sync(~0u, one);
+    left &= ~these;
     const int cnt = pre[of.x + 1] - pre[of.x], begin = pre[of.x] * units + of.y * cnt, end = begin + cnt;
     const int64_t b = who[of.x];
-    const int hk = of.y / a.mtiles, mi = of.y - hk * a.mtiles;
+    const int hk = a.mtiles == 1 ? of.y : of.y / a.mtiles, mi = of.y - hk * a.mtiles;
     const int h0 = hk * group + mi * C::kRows, rows = min(C::kRows, group - mi * C::kRows);
     const bool complete = begin >= t0 && end <= t1;
     const int slot = cta * 2 + (begin < t0 ? 0 : 1);
-    for (int i = tid; i < rows * quads; i += kThreads) {
-      const int row = i / quads, c = (i - row * quads) * 4;
-      float top = -INFINITY;
-      for (int z = x; z < y; ++z)
-        if (parts[z].x >= 0) top = fmaxf(top, ml[z >> 1][z & 1][row].x);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
+    // A warp per row, lane c four columns; lane z works out the weight of part z.
+    for (int row = warp; row < rows; row += kWarps) {
+      const float2 e = one ? ml[lane >> 1][lane & 1][row] : make_float2(-INFINITY, 0.f);
+      float top = e.x;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      top = __shfl_sync(~0u, top, 0);
+      const float f = one ? ex2_approx(e.x - (top == -INFINITY ? 0.f : top)) : 0.f;
+      float sum = one ? f * e.y : 0.f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      sum = __shfl_sync(~0u, sum, 0);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int z = x; z < y; ++z) {
-        if (parts[z].x < 0) continue;
-        const float2 e = ml[z >> 1][z & 1][row];
-        const float f = ex2_approx(e.x - ref);
-        const float* from = reinterpret_cast<const float*>(smem + ((z & 1) ? (z >> 1) * C::kWarpRing : C::kRing + (z >> 1) * C::kPart));
-        const float4 u = *reinterpret_cast<const float4*>(from + row * C::kPitch + c);
-        sum = fmaf(f, e.y, sum);
-        o = make_float4(fmaf(f, u.x, o.x), fmaf(f, u.y, o.y), fmaf(f, u.z, o.z), fmaf(f, u.w, o.w));
+      const int c = min(lane * 4, kD - 4);
+#pragma unroll 4
+      for (int z = 0; z < 2 * kWarps; ++z) {
+        const float g = __shfl_sync(~0u, f, z);
+        if ((these >> z) & 1u) {
+          const float4 u = *reinterpret_cast<const float4*>(
+              smem + (z % 2 ? (z / 2) * C::kWarpRing : C::kRing + (z / 2) * C::kPart) + (row * C::kPitch + c) * 4);
+          o = make_float4(fmaf(g, u.x, o.x), fmaf(g, u.y, o.y), fmaf(g, u.z, o.z), fmaf(g, u.w, o.w));
+        }
       }
       if (complete) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t to = b * p.out.sn + (h0 + row) * p.out.sh + c;
-        if (p.out_is_f32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + to) =
-              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        } else {
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out.ptr) + to) =
-              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        }
-        if (c == 0)
-          p.lse.ptr[b * p.lse.sn + (h0 + row) * p.lse.sh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        if (lane * 4 < p.d) write_out4(p, b, h0 + row, lane * 4, o, sum);
+        if (lane == 0) write_lse(p, b, h0 + row, top, sum);
       } else {
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(ws + wl.o) + ((int64_t)slot * C::kRows + row) * kD + c) = o;
-        if (c == 0) reinterpret_cast<float2*>(ws + wl.ml)[slot * 16 + row] = make_float2(top, sum);
+        if (lane * 4 < p.d)
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(ws + wl.o) + ((int64_t)slot * C::kRows + row) * kD + lane * 4) = o;
+        if (lane == 0) reinterpret_cast<float2*>(ws + wl.ml)[slot * 16 + row] = make_float2(top, sum);
       }
     }
     if (!complete && begin >= t0 && tid == 0) {
-      // the CTA whose run holds the unit's last tile, at cost v: the last one that begins there or before
-      const int64_t v = begin_cost(of.x) + (int64_t)(of.y + 1) * (cnt + kUnitCost) - 1;
-      int last = (int)(v * ctas / cost);
-      while (last + 1 < ctas && cost * (last + 1) / ctas <= v) ++last;
-      while (cost * last / ctas > v) --last;
+      // the CTA whose run holds the unit's last tile, at cost v: runs up to the `over`-th are one longer
+      const int v = begin_cost(of.x) + (of.y + 1) * (cnt + kUnitCost) - 1;
+      const int last = v < over * (share + 1) ? v / (share + 1) : over + (v - over * (share + 1)) / share;
       reinterpret_cast<Split*>(ws)[cta] = Split{(int)b, of.y, last, 0};
     }
-    x = y;
   }
 }
 
@@ -651,13 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // block's warps, each lane 4 columns, then the warps' results are summed in order.
 constexpr int kJoinWarps = 8;
 
-template <bool kF32, int kD>
+template <bool kF32, int kD, int kHd>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedDecodeParams p,
                                                                       const __grid_constant__ Launch a) {
-  using C = Cfg<kF32, kD>;
+  using C = Cfg<kF32, kD, kHd>;
   __shared__ float4 part[kJoinWarps][32];
   __shared__ float sums[kJoinWarps], tops[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y, cta = blockIdx.x;
+  grid_launch_dependents();
   grid_dependency_wait();
   const uint8_t* ws = static_cast<const uint8_t*>(p.ws);
   const WsLayout wl = ws_layout(C::kRows, kD);
@@ -703,32 +775,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
     sum += sums[w];
     o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t b = sp.b;
   const int hh = hk * group + mi * C::kRows + row;
-  if (lane == 0) p.lse.ptr[b * p.lse.sn + hh * p.lse.sh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-  if (!mine) return;
-  const int64_t at = b * p.out.sn + hh * p.out.sh + lane * 4;
-  if (p.out_is_f32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out.ptr) + at) =
-        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  } else {
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out.ptr) + at) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  }
+  if (lane == 0) write_lse(p, sp.b, hh, top, sum);
+  if (mine) write_out4(p, sp.b, hh, lane * 4, o, sum);
 }
 
 // The most that one request's units can cost.
 int64_t request_cost(int64_t keys, int64_t units, int tile) { return ((keys + tile - 1) / tile + 1 + kUnitCost) * units; }
 
-template <bool kF32, int kD>
+template <bool kF32, int kD, int kHd>
 cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
-  using C = Cfg<kF32, kD>;
+  using C = Cfg<kF32, kD, kHd>;
   static PerContext<int> cache;
   int ctas = 0;
   cudaError_t e = cache.get(
       [](int* v) {
-        cudaError_t r = cudaFuncSetAttribute(paged_decode_kernel<kF32, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t r = cudaFuncSetAttribute(paged_decode_kernel<kF32, kD, kHd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmem);
         if (r != cudaSuccess) return r;
         int sms = 0;
@@ -751,20 +813,14 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   for (int64_t r0 = 0; r0 < p.n; r0 += at_once) {
     a.r0 = (int)r0;
     a.n = (int)(p.n - r0 < at_once ? p.n - r0 : at_once);
-    paged_decode_kernel<kF32, kD><<<ctas, kThreads, C::kSmem, s>>>(p, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_dependent(paged_decode_kernel<kF32, kD, kHd>, dim3((unsigned)ctas), kThreads, C::kSmem, s, p, a)) !=
+        cudaSuccess)
+      return e;
     *nlaunch += 1;
     if (!a.split) continue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(group < C::kRows ? group : C::kRows));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, paged_join_kernel<kF32, kD>, p, a)) != cudaSuccess) return e;
+    const dim3 grid((unsigned)ctas, (unsigned)(group < C::kRows ? group : C::kRows));
+    if ((e = launch_dependent(paged_join_kernel<kF32, kD, kHd>, grid, kJoinWarps * 32, 0, s, p, a)) != cudaSuccess)
+      return e;
     *nlaunch += 1;
   }
   return cudaSuccess;
@@ -772,21 +828,30 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
 
 }  // namespace
 
+// The tile of rows of `bytes` bytes; the kernels' rows are 64 or 128 elements.
+static int tile_keys(int64_t d, bool is_f32) { return 4096 / ((d <= 64 ? 64 : 128) * (is_f32 ? 4 : 2)); }
+
 size_t paged_decode_workspace(int64_t, int64_t, int64_t d, int64_t max_keys) {
-  // Without the type: the larger of the two kernels' needs, for the shorter of their uncut lengths.
-  if (max_keys <= kWholeTiles * Cfg<true, 128>::kKeys) return 0;
+  // Without the type: of the shorter of their uncut lengths.
+  if (max_keys <= kWholeTiles * tile_keys(d, true)) return 0;
   return ws_layout(16, d <= 64 ? 64 : 128).total;
 }
 
-bool paged_decode_fits(int64_t h, int64_t hkv, bool is_f32, int64_t max_keys) {
-  const int rows = is_f32 ? Cfg<true, 128>::kRows : Cfg<false, 128>::kRows;
-  const int64_t units = hkv * ((h / hkv + rows - 1) / rows);
-  return request_cost(max_keys, units, is_f32 ? Cfg<true, 128>::kKeys : Cfg<false, 128>::kKeys) < (int64_t(1) << 31);
+// Query heads of a unit.
+static int unit_heads(int64_t group, bool is_f32) { return !is_f32 ? 16 : group <= 1 ? 1 : group <= 4 ? 4 : 8; }
+
+bool paged_decode_fits(int64_t h, int64_t hkv, int64_t d, bool is_f32, int64_t max_keys) {
+  const int64_t group = h / hkv, heads = unit_heads(group, is_f32);
+  return request_cost(max_keys, hkv * ((group + heads - 1) / heads), tile_keys(d, is_f32)) < (int64_t(1) << 31);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
-  if (p.is_f32) return p.d <= 64 ? launch<true, 64>(p, s, nlaunch) : launch<true, 128>(p, s, nlaunch);
-  return p.d == 64 ? launch<false, 64>(p, s, nlaunch) : launch<false, 128>(p, s, nlaunch);
+  if (!p.is_f32) return p.d == 64 ? launch<false, 64, 16>(p, s, nlaunch) : launch<false, 128, 16>(p, s, nlaunch);
+  switch (unit_heads(p.h / p.hkv, true)) {
+    case 1: return p.d <= 64 ? launch<true, 64, 1>(p, s, nlaunch) : launch<true, 128, 1>(p, s, nlaunch);
+    case 4: return p.d <= 64 ? launch<true, 64, 4>(p, s, nlaunch) : launch<true, 128, 4>(p, s, nlaunch);
+    default: return p.d <= 64 ? launch<true, 64, 8>(p, s, nlaunch) : launch<true, 128, 8>(p, s, nlaunch);
+  }
 }
 
 }  // namespace bea
