@@ -86,7 +86,7 @@ struct PagedDecodeParams {
 };
 size_t paged_decode_workspace(int64_t h, int64_t hkv, int64_t d, int64_t max_keys);
 // Whether a request's tiles can be counted in 31 bits.
-bool paged_decode_fits(int64_t h, int64_t hkv, int64_t d, bool is_f32, int64_t max_keys);
+bool paged_decode_fits(int64_t hkv, int64_t d, bool is_f32, int64_t max_keys);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch);
 
 }  // namespace bea

@@ -226,7 +226,7 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
   const int64_t page = k_cache->shape[1], max_pages = block_table->shape[1];
   const int64_t max_keys = max_pages * page;
   if (max_keys >= bea::kUnbounded) return BEA_ERR_SHAPE;
-  if (!bea::paged_decode_fits(h, hkv, d, q->dtype == BEA_F32, max_keys)) return BEA_ERR_SHAPE;
+  if (!bea::paged_decode_fits(hkv, d, q->dtype == BEA_F32, max_keys)) return BEA_ERR_SHAPE;
   const size_t need = bea::paged_decode_workspace(h, hkv, d, max_keys);
   if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < need))
     return BEA_ERR_WORKSPACE;

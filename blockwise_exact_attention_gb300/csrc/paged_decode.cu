@@ -5,10 +5,11 @@
 // and value read once. HBM-bound: 2 d (K and V) elements a key and K/V head
 // against 4 d g flops, g = h / h_kv query heads reading the same key.
 //
-// Work. A UNIT is one (request, K/V head, block of up to kRows of the group's
-// query heads); its visible keys are cut into tiles of kKeys. The tiles of all
-// units, request by request, make one list, and CTA c of G takes the c-th of G
-// runs of it, each warp of the CTA an eighth of that, whatever the lengths are:
+// Work. A UNIT is one (request, K/V head); its visible keys are cut into tiles of
+// kKeys. The tiles of all units, request by request, make one list, and CTA c of
+// G takes the c-th of G runs of it, each warp of the CTA an eighth of that (with
+// more than kRows query heads to a K/V head, neighbouring CTAs take the same run
+// for a block of kRows each, so that the second reads from L2), whatever the lengths are:
 // nothing about them is known on the host. Every CTA finds its run from the
 // lengths alone (a scan of tiles per request in shared memory). The runs cost
 // the same: a unit counts as its tiles and kUnitCost more, for its queries and
@@ -43,7 +44,7 @@ constexpr int kMinCost = 2 * kWarps;  // of a CTA's run, as long as there are fe
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// kHd: query heads a unit has at most (bf16: 16, the rows of an mma).
+// kHd: query heads of a K/V head that a CTA takes at most (bf16: 8 or 16 of an mma's 16 rows).
 template <bool kF32, int kD, int kHd>
 struct Cfg {
   static constexpr int kRows = kHd;
@@ -63,13 +64,14 @@ struct Cfg {
   // The 16-byte pieces of row r are stored at piece ^ swizzle(r): the eight rows an ldmatrix reads (bf16), the two
   // rows by four pieces a quarter-warp reads (f32) fall on different banks.
   __host__ __device__ static constexpr int swizzle(int r) { return kF32 ? ((r & 1) << 2) | ((r & 7) >> 1) : r & 7; }
+  static_assert(!kF32 || kKeys <= 32, "a tile's rows are bits of a mask");
   static_assert(kPart <= kWarpRing, "a part takes the place of its warp's ring");
 };
 
 // Workspace: [kMaxCtas] descriptors | [kMaxCtas][2][16] (m, l) | [kMaxCtas][2][rows][D] O. Entry 0 of a CTA is a
 // unit that began before its run, entry 1 one that begins in the run and goes on after it.
 struct Split {
-  int b, unit, last, pad;  // last: the CTA that ends the unit; -1: nothing begins here that goes on
+  int b, hk, last, pad;  // last: the CTA that ends the unit; -1: nothing begins here that goes on
 };
 struct WsLayout {
   size_t ml, o, total;
@@ -85,8 +87,8 @@ __host__ __device__ inline WsLayout ws_layout(int rows, int d) {
 // The part of a launch that is not in PagedDecodeParams.
 struct Launch {
   int r0, n;     // requests [r0, r0 + n)
-  int mtiles;    // blocks of query heads per K/V head
-  int units;     // per request: h_kv * mtiles
+  int planes;    // blocks of kRows query heads per K/V head in this launch
+  int head0;     // of a group, the first head of the first plane
   float sl2;     // scale * log2(e)
   int split;     // units may be cut: the workspace is there
 };
@@ -193,7 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   // ---- tiles per request, their sums, and this CTA's run [t0, t1) -----------------
-  const int most = p.max_pages * p.page, units = a.units, grid = gridDim.x, cta = blockIdx.x;
+  // an empty cache has no page to read from: every length is past it
+  const int most = p.num_pages > 0 ? p.max_pages * p.page : 0, units = p.hkv;
+  // every plane has `grid` CTAs; cta: this one's place among its plane's
+  const int grid = gridDim.x / a.planes, cta = blockIdx.x / a.planes, plane = blockIdx.x % a.planes;
   constexpr int kPer = kMaxRequests / kThreads;  // consecutive requests of a thread
   int len_of[kPer], tiles_of[kPer];
   int tiles_sum = 0, some = 0, longest = 0;
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = 0; i < kPer; ++i) {
     int len = len_of[i];
     if (len < 0 || len > most) {
-      if (cta == 0) report_status(p.status, BEA_STATUS_PAGES);
+      if (blockIdx.x == 0) report_status(p.status, BEA_STATUS_PAGES);
       len = len_of[i] = len < 0 ? 0 : most;
     }
     tiles_of[i] = len > 0 ? (len + C::kKeys - 1) / C::kKeys - first_key(len, p.left) / C::kKeys : 0;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) pre[count] = run;
   // requests without a visible key
   if (count < a.n) {
-    for (int r = cta; r < a.n; r += grid) {
+    for (int r = blockIdx.x; r < a.n; r += gridDim.x) {
       const int len = p.lens[a.r0 + r];
       if (len > 0 && most > 0) continue;
       const int64_t b = a.r0 + r;
@@ -284,32 +289,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return v;
   };
-  // the first tile that is not before cost v
-  auto tile_at = [&](int v) {
-    if (v >= cost) return run * units;
-    const Place at = place(v);
-    return pre[at.k] * units + at.unit * (pre[at.k + 1] - pre[at.k]) + max(0, at.in - kUnitCost);
-  };
+  // the first tile of the place's unit
+  auto first_tile = [&](const Place& at) { return pre[at.k] * units + at.unit * (pre[at.k + 1] - pre[at.k]); };
   const WsLayout wl = ws_layout(C::kRows, kD);
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
-  if (a.split && tid == 0) reinterpret_cast<Split*>(ws)[cta] = Split{0, 0, -1, 0};
+  if (a.split && tid == 0) reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{0, 0, -1, 0};
   if (cta >= ctas || count == 0) return;
-  // Searches and divisions side by side: lanes 0, 1 the CTA's run, then lanes 2, 3 this warp's eighth of it. The first
-  // unit's own cost is left out of the split, it has no tiles.
+  // Searches and divisions side by side: lanes 0, 1 the CTA's run, then lanes 2, 3 this warp's eighth of it. (Of a
+  // whole first unit the cost before its tiles is left out, so that no warp goes without tiles.)
   int mark = border(cta + (lane & 1));
   const int v0 = __shfl_sync(~0u, mark, 0), v1 = __shfl_sync(~0u, mark, 1);
   if (v0 >= v1) return;
-  const Place start = place(v0);
-  const int s0 = min(v1, v0 + max(0, kUnitCost - start.in));
+  const int s0 = whole ? v0 + kUnitCost : v0;
   const int step = (v1 - s0) / kWarps, rest = v1 - s0 - step * kWarps, part_no = warp + (lane & 1);
-  mark = tile_at((lane & 2) == 0 ? (lane == 0 ? v0 : v1) : s0 + step * part_no + min(part_no, rest));
+  const int at_cost = (lane & 2) == 0 ? (lane == 0 ? v0 : v1) : s0 + step * part_no + min(part_no, rest);
+  const Place at_place = place(min(at_cost, cost - 1));
+  mark = at_cost >= cost ? run * units : first_tile(at_place) + max(0, at_place.in - kUnitCost);
   const int t0 = __shfl_sync(~0u, mark, 0), t1 = __shfl_sync(~0u, mark, 1);
   const int w0 = __shfl_sync(~0u, mark, 2), w1 = __shfl_sync(~0u, mark, 3);
 
   // ---- loads: the i-th tile of this warp is tile w0 + i -------------------------------
-  auto first_tile = [&](int k) { return pre[k] * units; };
+  auto tiles_before = [&](int k) { return pre[k] * units; };
   const uint32_t ring = smem_u32(smem) + warp * C::kWarpRing;
-  const int group = p.h / p.hkv;
+  const int group = p.h / p.hkv, head0 = a.head0 + plane * C::kRows, rows = min(C::kRows, group - head0);
   const int mine = w1 - w0;
   const bool one_page = p.page % C::kKeys == 0;  // a tile lies in one page
   auto page_of = [&](int key) { return p.page_shift >= 0 ? key >> p.page_shift : key / p.page; };
@@ -322,11 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     d_k = d_v = 0;
     if (i >= mine) return;
     const int t = w0 + i;
-    const int k = last_below(count, t, first_tile);
+    const int k = last_below(count, t, tiles_before);
     const int cnt = pre[k + 1] - pre[k], in = t - pre[k] * units, unit = in / cnt;
     const int len = lens[k], first = first_key(len, p.left);
     d_b = who[k];
-    d_hk = a.mtiles == 1 ? unit : unit / a.mtiles;
+    d_hk = unit;
     d_key = (first / C::kKeys + (in - unit * cnt)) * C::kKeys;
     // rows of the tile that are visible
     const int lo = max(first - d_key, 0), hi = min(len - d_key, C::kKeys);
@@ -338,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         report_status(p.status, BEA_STATUS_PAGES);
         d_mask = 0;
       } else {
-        d_k = id * p.kc.sn + off * p.kc.sl + d_hk * p.kc.sh;
-        d_v = id * p.vc.sn + off * p.vc.sl + d_hk * p.vc.sh;
+        d_k = (id * p.kc.sn + off * p.kc.sl + d_hk * p.kc.sh) * C::kEs;
+        d_v = (id * p.vc.sn + off * p.vc.sl + d_hk * p.vc.sh) * C::kEs;
       }
     }
   };
@@ -358,6 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       n_id = max(p.table[b * p.table_stride + pg], -1);
     }
   };
+  // This lane's 16-byte piece of a tile's rows sub, sub + kStep, ...
+  constexpr int kChunks = kD * C::kEs / 16, kStep = 32 / kChunks;
+  const int chunk = lane % kChunks, sub = lane / kChunks;
+  const bool in_row = !kF32 || chunk * 4 < p.d;
+  const int64_t k_lane = sub * p.kc.sl * C::kEs + chunk * 16, v_lane = sub * p.vc.sl * C::kEs + chunk * 16;
+  const int64_t k_step = kStep * p.kc.sl * C::kEs, v_step = kStep * p.vc.sl * C::kEs;
   auto load = [&](int i) {
     if (i < mine) {
       const int j = i & 31, stage = i % C::kStages;
@@ -374,30 +382,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = __shfl_sync(~0u, d_hk, j);
         const bool ok = n_id >= 0 && n_id < p.num_pages;
         if (ok) {
-          k_row = n_id * p.kc.sn + n_off * p.kc.sl + hk * p.kc.sh;
-          v_row = n_id * p.vc.sn + n_off * p.vc.sl + hk * p.vc.sh;
+          k_row = (n_id * p.kc.sn + n_off * p.kc.sl + hk * p.kc.sh) * C::kEs;
+          v_row = (n_id * p.vc.sn + n_off * p.vc.sl + hk * p.vc.sh) * C::kEs;
         } else if (n_id != INT32_MIN) {
           report_status(p.status, BEA_STATUS_PAGES);
         }
         mask = __ballot_sync(~0u, ok);
       }
       if (lane == 0) masks[warp][stage] = mask;
-      constexpr int kChunks = kD * C::kEs / 16;                 // 16-byte pieces of a row
-      constexpr int kStep = 32 / kChunks;                       // rows per instruction
-      const int chunk = lane % kChunks, sub = lane / kChunks;
-      const bool in_row = !kF32 || chunk * 4 < p.d;
+      // A row that is not visible is not read: its address only has to be one (in the page, or in page 0).
 #pragma unroll
       for (int it = 0; it < C::kKeys / kStep; ++it) {
         const int row = it * kStep + sub;
         const bool read = (mask >> row) & 1u;
-        int64_t ka = k_at + row * p.kc.sl, va = v_at + row * p.vc.sl;
-        if (!one_page) ka = __shfl_sync(~0u, k_row, row), va = __shfl_sync(~0u, v_row, row);
         const uint32_t to = row * C::kRowBytes + ((chunk ^ C::swizzle(row)) << 4);
-        const char* ks = static_cast<const char*>(p.kc.ptr) + ka * C::kEs + chunk * 16;
-        const char* vs = static_cast<const char*>(p.vc.ptr) + va * C::kEs + chunk * 16;
+        int64_t ka = k_at + k_lane + it * k_step, va = v_at + v_lane + it * v_step;
+        if (!one_page) ka = __shfl_sync(~0u, k_row, row) + chunk * 16, va = __shfl_sync(~0u, v_row, row) + chunk * 16;
         if (in_row) {
-          cp_async16(kd + to, read ? ks : p.q.ptr, read);
-          cp_async16(vd + to, read ? vs : p.q.ptr, read);
+          cp_async16(kd + to, static_cast<const char*>(p.kc.ptr) + ka, read);
+          cp_async16(vd + to, static_cast<const char*>(p.vc.ptr) + va, read);
         }
       }
       if (!one_page) look_up(i + 1);
@@ -411,20 +414,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* q_smem = reinterpret_cast<float*>(smem + C::kRing + C::kHeads) + warp * C::kRows * kD;
   float* p_smem = reinterpret_cast<float*>(smem + C::kRing + C::kHeads + C::kQ) + warp * C::kKeys * C::kRows;
   int done = 0, sent = 0;
-  int k = last_below(count, w0, first_tile);
-  int unit = (w0 - pre[k] * units) / (pre[k + 1] - pre[k]);
+  int k = __shfl_sync(~0u, at_place.k, 2), unit = __shfl_sync(~0u, at_place.unit, 2);
   while (done < mine) {
     const int cnt = pre[k + 1] - pre[k], begin = pre[k] * units + unit * cnt, end = begin + cnt;
     const int todo = min(end, w1) - w0;  // this warp's tiles up to the unit's end
     const int64_t b = who[k];
-    const int hk = a.mtiles == 1 ? unit : unit / a.mtiles, mi = unit - hk * a.mtiles;
-    const int h0 = hk * group + mi * C::kRows, rows = min(C::kRows, group - mi * C::kRows);
+    const int h0 = unit * group + head0;
     const bool covered = begin >= w0 && end <= w1;
     const int which = begin < w0 ? 0 : 1;
     float* part = which == 0 ? head : tail;
 
     if constexpr (kF32) {
-      // Scores: lane (key, quarter) takes every fourth 16-byte piece of its key's row. Output: lane owns 4 columns.
+      // Scores: lane (key, quarter) takes every fourth 16-byte piece of its key's row.
       float m[C::kRows], l[C::kRows];  // l: this lane's keys only, quarter 0 counts
       float4 o[C::kRows];
 #pragma unroll
@@ -441,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane * 4 < kD) *reinterpret_cast<float4*>(q_smem + i * kD + lane * 4) = qr[i];
       __syncwarp();
       const int key = lane >> 2, quarter = lane & 3, sw = C::swizzle(key), pieces = p.d >> 2;
-      const bool column = lane * 4 < kD;
+      constexpr int kCols = kD / 4, kParts = 32 / kCols;  // output: kParts lanes to 4 columns, each every kParts-th key
+      const int col = lane % kCols, share_of = lane / kCols;
       for (; done < todo; ++done) {
         const int stage = done % C::kStages;
         while (sent < done + C::kStages) load(sent++);
@@ -498,20 +500,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < kGroups; ++g) store_rows<C::kRows>(p_smem + (key + 8 * g) * C::kRows, s[g]);
         }
         __syncwarp();
-        if (column) {
 #pragma unroll
-          for (int j = 0; j < C::kKeys; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(vt + j * C::kRowBytes + ((lane ^ C::swizzle(j)) << 4));
-            float e[C::kRows];
-            load_rows<C::kRows>(p_smem + j * C::kRows, e);
+        for (int jj = 0; jj < C::kKeys / kParts; ++jj) {
+          const int j = jj * kParts + share_of;
+          const float4 v = *reinterpret_cast<const float4*>(vt + j * C::kRowBytes + ((col ^ C::swizzle(j)) << 4));
+          float e[C::kRows];
+          load_rows<C::kRows>(p_smem + j * C::kRows, e);
 #pragma unroll
-            for (int i = 0; i < C::kRows; ++i)
-              o[i] = make_float4(fmaf(e[i], v.x, o[i].x), fmaf(e[i], v.y, o[i].y), fmaf(e[i], v.z, o[i].z),
-                                 fmaf(e[i], v.w, o[i].w));
-          }
+          for (int i = 0; i < C::kRows; ++i)
+            o[i] = make_float4(fmaf(e[i], v.x, o[i].x), fmaf(e[i], v.y, o[i].y), fmaf(e[i], v.z, o[i].z),
+                               fmaf(e[i], v.w, o[i].w));
         }
         __syncwarp();
       }
+#pragma unroll
+      for (int off = kCols; off < 32; off *= 2)
+#pragma unroll
+        for (int i = 0; i < C::kRows; ++i) {
+          o[i].x += __shfl_xor_sync(~0u, o[i].x, off);
+          o[i].y += __shfl_xor_sync(~0u, o[i].y, off);
+          o[i].z += __shfl_xor_sync(~0u, o[i].z, off);
+          o[i].w += __shfl_xor_sync(~0u, o[i].w, off);
+        }
 #pragma unroll
       for (int i = 0; i < C::kRows; ++i) {
         l[i] += __shfl_xor_sync(~0u, l[i], 4);
@@ -541,7 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float o[kD / 8][4];
 #pragma unroll
       for (int i = 0; i < kD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      // rows 8-15 of the products stay empty where a unit has at most 8 heads
+      constexpr int kHalves = C::kRows / 8;
+      float m[kHalves], l[kHalves];
+#pragma unroll
+      for (int x = 0; x < kHalves; ++x) m[x] = -INFINITY, l[x] = 0.f;
       const int row = lane >> 2, col = (lane & 3) * 2;
       uint32_t qf[kD / 16][4];
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q.ptr) + b * p.q.sn + h0 * p.q.sh;
@@ -550,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int i = row + (x & 1) * 8, c = ks * 16 + (x >> 1) * 8 + col;
-          qf[ks][x] = i < rows ? *reinterpret_cast<const uint32_t*>(q + i * p.q.sh + c) : 0u;
+          qf[ks][x] = (x & 1) < kHalves && i < rows ? *reinterpret_cast<const uint32_t*>(q + i * p.q.sh + c) : 0u;
         }
       for (; done < todo; ++done) {
         const int stage = done % C::kStages;
@@ -572,25 +586,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_bf16(s[2 * u + 1], qf[ks], kf[2], kf[3]);
           }
         }
-        float top[2] = {-INFINITY, -INFINITY};
+        if (mask != (0xFFFFFFFFu >> (32 - C::kKeys))) {
 #pragma unroll
-        for (int nb = 0; nb < 2 * kSub; ++nb)
+          for (int nb = 0; nb < 2 * kSub; ++nb)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const bool see = (mask >> (nb * 8 + col + (x & 1))) & 1u;
-            s[nb][x] = see ? s[nb][x] * a.sl2 : -INFINITY;
-            top[x >> 1] = fmaxf(top[x >> 1], s[nb][x]);
-          }
+            for (int x = 0; x < 2 * kHalves; ++x)
+              if (!((mask >> (nb * 8 + col + (x & 1))) & 1u)) s[nb][x] = -INFINITY;
+        }
+        float top[kHalves];  // in units of log2, like m
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kHalves; ++x) {
+          top[x] = fmaxf(s[0][2 * x], s[0][2 * x + 1]);
+#pragma unroll
+          for (int nb = 1; nb < 2 * kSub; ++nb) top[x] = fmax3(top[x], s[nb][2 * x], s[nb][2 * x + 1]);
           top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 1));
-          top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 2));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], 2)) * a.sl2;
         }
         // O and l are rescaled only when a maximum grows by more than 2^8: the reference value then in use
         // cancels in the end, and P stays below 2^8.
-        if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+        bool grown = top[0] > m[0] + 8.f;
+        if constexpr (kHalves == 2) grown = grown || top[1] > m[1] + 8.f;
+        if (__any_sync(~0u, grown)) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < kHalves; ++x) {
             const float mn = fmaxf(m[x], top[x]);
             const float w = mn == -INFINITY ? 1.f : ex2_approx(m[x] - mn);
             m[x] = mn;
@@ -601,13 +619,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // P as two bf16 terms: the first 8 bits truncated, the rest rounded (2^-15 of P left over, where one term
         // would leave 2^-8). The second term is kept above 0, so that an infinite value stays infinite.
-        uint32_t hi[kSub][4], lo[kSub][4];
+        uint32_t hi[kSub][4] = {}, lo[kSub][4] = {};
 #pragma unroll
-        for (int nb = 0; nb < 2 * kSub; ++nb)
+        for (int x = 0; x < kHalves; ++x) {
+          const float ref = m[x] == -INFINITY ? 0.f : m[x];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float ref = m[x] == -INFINITY ? 0.f : m[x];
-            const float p0 = ex2_approx(s[nb][2 * x] - ref), p1 = ex2_approx(s[nb][2 * x + 1] - ref);
+          for (int nb = 0; nb < 2 * kSub; ++nb) {
+            const float p0 = ex2_approx(fmaf(s[nb][2 * x], a.sl2, -ref)), p1 = ex2_approx(fmaf(s[nb][2 * x + 1], a.sl2, -ref));
             l[x] += p0 + p1;
             const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
             hi[nb / 2][(nb & 1) * 2 + x] = __byte_perm(u0, u1, 0x7632);
@@ -615,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float r1 = fmaxf(p1 - __uint_as_float(u1 & 0xFFFF0000u), p1 * 0x1p-20f);
             lo[nb / 2][(nb & 1) * 2 + x] = pack_bf16x2(r0, r1);
           }
+        }
 #pragma unroll
         for (int dp = 0; dp < kD / 16; ++dp) {
 #pragma unroll
@@ -631,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < kHalves; ++x) {
         l[x] += __shfl_xor_sync(~0u, l[x], 1);
         l[x] += __shfl_xor_sync(~0u, l[x], 2);
         const int i = row + 8 * x;
@@ -673,10 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     left &= ~these;
     const int cnt = pre[of.x + 1] - pre[of.x], begin = pre[of.x] * units + of.y * cnt, end = begin + cnt;
     const int64_t b = who[of.x];
-    const int hk = a.mtiles == 1 ? of.y : of.y / a.mtiles, mi = of.y - hk * a.mtiles;
-    const int h0 = hk * group + mi * C::kRows, rows = min(C::kRows, group - mi * C::kRows);
+    const int h0 = of.y * group + head0;
     const bool complete = begin >= t0 && end <= t1;
-    const int slot = cta * 2 + (begin < t0 ? 0 : 1);
+    const int slot = blockIdx.x * 2 + (begin < t0 ? 0 : 1);
     // A warp per row, lane c four columns; lane z works out the weight of part z.
     for (int row = warp; row < rows; row += kWarps) {
       const float2 e = one ? ml[lane >> 1][lane & 1][row] : make_float2(-INFINITY, 0.f);
@@ -713,21 +731,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the CTA whose run holds the unit's last tile, at cost v: runs up to the `over`-th are one longer
       const int v = begin_cost(of.x) + (of.y + 1) * (cnt + kUnitCost) - 1;
       const int last = v < over * (share + 1) ? v / (share + 1) : over + (v - over * (share + 1)) / share;
-      reinterpret_cast<Split*>(ws)[cta] = Split{(int)b, of.y, last, 0};
+      reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{(int)b, of.y, last * a.planes + plane, 0};
     }
   }
 }
 
-// Joins the parts of unit that begins in CTA blockIdx.x's run, query head blockIdx.y of it: the parts are dealt to the
-// block's warps, each lane 4 columns, then the warps' results are summed in order.
-constexpr int kJoinWarps = 8;
+// Joins the parts of the unit that begins in CTA blockIdx.x's run and goes on after it, query head blockIdx.y of it. The
+// parts are dealt to the block's warps, a lane has 4 columns; then the warps' results are merged in order. A chain of
+// three memory latencies (which unit, its parts, the result); 128 threads of 32 registers, so that a block finds room
+// beside a CTA of the kernel before.
+constexpr int kJoinWarps = 4;
 
 template <bool kF32, int kD, int kHd>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedDecodeParams p,
-                                                                      const __grid_constant__ Launch a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 16)
+    paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Launch a) {
   using C = Cfg<kF32, kD, kHd>;
   __shared__ float4 part[kJoinWarps][32];
-  __shared__ float sums[kJoinWarps], tops[kJoinWarps];
+  __shared__ float2 part_ml[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y, cta = blockIdx.x;
   grid_launch_dependents();
   grid_dependency_wait();
@@ -735,47 +755,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   const WsLayout wl = ws_layout(C::kRows, kD);
   const Split sp = reinterpret_cast<const Split*>(ws)[cta];
   if (sp.last < 0) return;
-  const int group = p.h / p.hkv, hk = sp.unit / a.mtiles, mi = sp.unit - hk * a.mtiles;
-  if (row >= min(C::kRows, group - mi * C::kRows)) return;
-  const float2* ml = reinterpret_cast<const float2*>(ws + wl.ml);
-  const float* os = reinterpret_cast<const float*>(ws + wl.o);
-  // part 0 is this CTA's entry 1, part i the entry 0 of CTA + i
-  const int parts = sp.last - cta + 1;
-  auto slot = [&](int i) { return i == 0 ? cta * 2 + 1 : (cta + i) * 2; };
-  float top = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += kJoinWarps * 32) top = fmaxf(top, ml[slot(i) * 16 + row].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (lane == 0) tops[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, tops[w]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int group = p.h / p.hkv, head = a.head0 + cta % a.planes * C::kRows + row;
+  if (head >= group) return;
+  // part 0 is this CTA's entry 1, part i the entry 0 of its plane's i-th CTA from here
+  const int parts = (sp.last - cta) / a.planes + 1;
   const bool mine = lane * 4 < p.d;
-#pragma unroll 8
+  float top = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float2 e, float4 y) {
+    const float mn = fmaxf(top, e.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2_approx(top - ref), g = ex2_approx(e.x - ref);
+    top = mn;
+    sum = fmaf(sum, f, e.y * g);
+    o = make_float4(fmaf(o.x, f, y.x * g), fmaf(o.y, f, y.y * g), fmaf(o.z, f, y.z * g), fmaf(o.w, f, y.w * g));
+  };
   for (int i = warp; i < parts; i += kJoinWarps) {
-    const float2 x = ml[slot(i) * 16 + row];
+    const int slot = i == 0 ? cta * 2 + 1 : (cta + i * a.planes) * 2;
+    const float2 e = reinterpret_cast<const float2*>(ws + wl.ml)[slot * 16 + row];
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mine) y = *reinterpret_cast<const float4*>(os + ((int64_t)slot(i) * C::kRows + row) * kD + lane * 4);
-    const float f = ex2_approx(x.x - ref);
-    sum = fmaf(f, x.y, sum);
-    o = make_float4(fmaf(f, y.x, o.x), fmaf(f, y.y, o.y), fmaf(f, y.z, o.z), fmaf(f, y.w, o.w));
+    if (mine) y = *reinterpret_cast<const float4*>(ws + wl.o + (((int64_t)slot * C::kRows + row) * kD + lane * 4) * 4);
+    add(e, y);
   }
-  part[warp][lane] = o;
-  if (lane == 0) sums[warp] = sum;
+  if (warp > 0) {
+    part[warp][lane] = o;
+    if (lane == 0) part_ml[warp] = make_float2(top, sum);
+  }
   __syncthreads();
-  if (warp != 0) return;
-  sum = sums[0];
-  o = part[0][lane];
-#pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) {
-    const float4 y = part[w][lane];
-    sum += sums[w];
-    o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
-  }
-  const int hh = hk * group + mi * C::kRows + row;
+  if (warp > 0) return;
+  for (int w = 1; w < min(kJoinWarps, parts); ++w) add(part_ml[w], part[w][lane]);
+  const int hh = sp.hk * group + head;
   if (lane == 0) write_lse(p, sp.b, hh, top, sum);
   if (mine) write_out4(p, sp.b, hh, lane * 4, o, sum);
 }
@@ -802,34 +810,38 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   if (e != cudaSuccess) return e;
   const int group = p.h / p.hkv;
   Launch a;
-  a.mtiles = (group + C::kRows - 1) / C::kRows;
-  a.units = p.hkv * a.mtiles;
   a.sl2 = p.scale * kLog2e;
   const int64_t keys = (int64_t)p.max_pages * p.page;
   a.split = keys > kWholeTiles * C::kKeys;
   // Requests per launch: their tiles and unit costs have to stay countable in 31 bits.
-  int64_t at_once = ((int64_t(1) << 31) - 1) / request_cost(keys, a.units, C::kKeys);
+  int64_t at_once = ((int64_t(1) << 31) - 1) / request_cost(keys, p.hkv, C::kKeys);
   if (at_once > kMaxRequests) at_once = kMaxRequests;
-  for (int64_t r0 = 0; r0 < p.n; r0 += at_once) {
-    a.r0 = (int)r0;
-    a.n = (int)(p.n - r0 < at_once ? p.n - r0 : at_once);
-    if ((e = launch_dependent(paged_decode_kernel<kF32, kD, kHd>, dim3((unsigned)ctas), kThreads, C::kSmem, s, p, a)) !=
-        cudaSuccess)
-      return e;
-    *nlaunch += 1;
-    if (!a.split) continue;
-    const dim3 grid((unsigned)ctas, (unsigned)(group < C::kRows ? group : C::kRows));
-    if ((e = launch_dependent(paged_join_kernel<kF32, kD, kHd>, grid, kJoinWarps * 32, 0, s, p, a)) != cudaSuccess)
-      return e;
-    *nlaunch += 1;
+  constexpr int kMaxPlanes = 16;
+  for (a.head0 = 0; a.head0 < group; a.head0 += kMaxPlanes * C::kRows) {
+    const int left = (group - a.head0 + C::kRows - 1) / C::kRows;
+    a.planes = left < kMaxPlanes ? left : kMaxPlanes;
+    const unsigned grid = (unsigned)(ctas / a.planes * a.planes);
+    for (int64_t r0 = 0; r0 < p.n; r0 += at_once) {
+      a.r0 = (int)r0;
+      a.n = (int)(p.n - r0 < at_once ? p.n - r0 : at_once);
+      if ((e = launch_dependent(paged_decode_kernel<kF32, kD, kHd>, dim3(grid), kThreads, C::kSmem, s, p, a)) != cudaSuccess)
+        return e;
+      *nlaunch += 1;
+      if (!a.split) continue;
+      const dim3 join(grid, (unsigned)(group < C::kRows ? group : C::kRows));
+      if ((e = launch_dependent(paged_join_kernel<kF32, kD, kHd>, join, kJoinWarps * 32, 0, s, p, a)) != cudaSuccess)
+        return e;
+      *nlaunch += 1;
+    }
   }
   return cudaSuccess;
 }
 
 }  // namespace
 
-// The tile of rows of `bytes` bytes; the kernels' rows are 64 or 128 elements.
-static int tile_keys(int64_t d, bool is_f32) { return 4096 / ((d <= 64 ? 64 : 128) * (is_f32 ? 4 : 2)); }
+// The elements of a row in the kernels, and the tile of such rows.
+static int row_elements(int64_t d, bool is_f32) { return is_f32 && d <= 32 ? 32 : d <= 64 ? 64 : 128; }
+static int tile_keys(int64_t d, bool is_f32) { return 4096 / (row_elements(d, is_f32) * (is_f32 ? 4 : 2)); }
 
 size_t paged_decode_workspace(int64_t, int64_t, int64_t d, int64_t max_keys) {
   // Without the type: of the shorter of their uncut lengths.
@@ -837,20 +849,28 @@ size_t paged_decode_workspace(int64_t, int64_t, int64_t d, int64_t max_keys) {
   return ws_layout(16, d <= 64 ? 64 : 128).total;
 }
 
-// Query heads of a unit.
-static int unit_heads(int64_t group, bool is_f32) { return !is_f32 ? 16 : group <= 1 ? 1 : group <= 4 ? 4 : 8; }
+bool paged_decode_fits(int64_t hkv, int64_t d, bool is_f32, int64_t max_keys) {
+  return request_cost(max_keys, hkv, tile_keys(d, is_f32)) < (int64_t(1) << 31);
+}
 
-bool paged_decode_fits(int64_t h, int64_t hkv, int64_t d, bool is_f32, int64_t max_keys) {
-  const int64_t group = h / hkv, heads = unit_heads(group, is_f32);
-  return request_cost(max_keys, hkv * ((group + heads - 1) / heads), tile_keys(d, is_f32)) < (int64_t(1) << 31);
+template <bool kF32, int kD>
+static cudaError_t launch_heads(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
+  const int group = p.h / p.hkv;
+  if constexpr (!kF32) {
+    return group <= 8 ? launch<false, kD, 8>(p, s, nlaunch) : launch<false, kD, 16>(p, s, nlaunch);
+  } else {
+    return group == 1   ? launch<true, kD, 1>(p, s, nlaunch)
+           : group <= 4 ? launch<true, kD, 4>(p, s, nlaunch)
+                        : launch<true, kD, 8>(p, s, nlaunch);
+  }
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
-  if (!p.is_f32) return p.d == 64 ? launch<false, 64, 16>(p, s, nlaunch) : launch<false, 128, 16>(p, s, nlaunch);
-  switch (unit_heads(p.h / p.hkv, true)) {
-    case 1: return p.d <= 64 ? launch<true, 64, 1>(p, s, nlaunch) : launch<true, 128, 1>(p, s, nlaunch);
-    case 4: return p.d <= 64 ? launch<true, 64, 4>(p, s, nlaunch) : launch<true, 128, 4>(p, s, nlaunch);
-    default: return p.d <= 64 ? launch<true, 64, 8>(p, s, nlaunch) : launch<true, 128, 8>(p, s, nlaunch);
+  if (!p.is_f32) return p.d == 64 ? launch_heads<false, 64>(p, s, nlaunch) : launch_heads<false, 128>(p, s, nlaunch);
+  switch (row_elements(p.d, true)) {
+    case 32: return launch_heads<true, 32>(p, s, nlaunch);
+    case 64: return launch_heads<true, 64>(p, s, nlaunch);
+    default: return launch_heads<true, 128>(p, s, nlaunch);
   }
 }
 

@@ -431,7 +431,7 @@ int bea_paged_write(const bea_tensor* k, const bea_tensor* v, const bea_tensor* 
  * A request of length 0 gets out = 0 and lse = -inf. A length past max_pages *
  * page_size counts as that, a negative one as 0, and the keys of a page
  * outside the cache as masked; each is reported. num_pages * page_size < 2^31;
- * max_pages * page_size < 2^30, and (max_pages * page_size / 8 + 4) * h < 2^31
+ * max_pages * page_size < 2^30, and (max_pages * page_size / 8 + 4) * h_kv < 2^31
  * is always enough for the kernels' 32-bit counts (BEA_ERR_SHAPE past them).
  */
 size_t bea_paged_decode_workspace_size(int64_t h, int64_t h_kv, int64_t d, int64_t max_keys);
