@@ -86,8 +86,8 @@ def bind():
     global _BIND
     if _BIND is None:
         load()
-        from . import _bind, ops
-        _bind.setup(check, ops._count)
+        from . import _bind
+        _bind.setup(check)
         _BIND = _bind
     return _BIND
 

@@ -33,7 +33,7 @@ using torch::autograd::Node;
 using torch::autograd::variable_list;
 
 PyObject* g_check = nullptr;  // _lib.check(code, where): raises BeaError
-PyObject* g_count = nullptr;  // ops._count(): adds the call's launches
+long long g_launches = 0;     // kernels launched through here since the last reset
 
 // The tensors of one call, described; all on the current device.
 class Call {
@@ -101,7 +101,11 @@ void arguments(const char* name, Py_ssize_t got, Py_ssize_t want) {
 
 // What every call ends with, back in Python.
 void finish(int rc, const char* where) {
-  PyObject* r = rc != BEA_OK ? PyObject_CallFunction(g_check, "is", rc, where) : PyObject_CallNoArgs(g_count);
+  if (rc == BEA_OK) {
+    g_launches += bea_last_launch_count();
+    return;
+  }
+  PyObject* r = PyObject_CallFunction(g_check, "is", rc, where);
   if (r == nullptr) throw python_error();
   Py_DECREF(r);
 }
@@ -209,8 +213,14 @@ std::pair<Tensor, Tensor> rotary(const Tensor& q, const Tensor& k, const Tensor&
   return {qo, ko};
 }
 
-// The tables as Python hands them over: bytes of int32 and of double, one entry a pair.
-Turn turn_of(PyObject* axis, PyObject* freq, const Tensor& q) {
+// The tables as Python hands them over: bytes of int32 and of double, one entry a pair; and the number of axes, which
+// positions have to be of.
+Turn turn_of(PyObject* table, const Tensor& q, const Tensor& positions) {
+  TORCH_CHECK_TYPE(PyTuple_Check(table) && PyTuple_GET_SIZE(table) == 3, "the rotation's tables");
+  PyObject *axis = PyTuple_GET_ITEM(table, 0), *freq = PyTuple_GET_ITEM(table, 1);
+  const long long axes = integer(PyTuple_GET_ITEM(table, 2));
+  TORCH_CHECK_VALUE(positions.dim() == 3 && positions.size(0) == axes, "positions ", positions.sizes(), ": [", axes,
+                    ", n, l] for ", axes, " sections");
   TORCH_CHECK_TYPE(PyBytes_Check(axis) && PyBytes_Check(freq) && PyBytes_GET_SIZE(axis) * 2 == PyBytes_GET_SIZE(freq),
                    "the rotation's tables");
   const auto* a = reinterpret_cast<const int32_t*>(PyBytes_AS_STRING(axis));
@@ -223,14 +233,14 @@ Turn turn_of(PyObject* axis, PyObject* freq, const Tensor& q) {
   return t;
 }
 
-// rope_axes(q, k, positions, axis, freq, inverse, q_out, k_out) -> (q_out, k_out)
+// rope_axes(q, k, positions, table, inverse, q_out, k_out) -> (q_out, k_out)
 PyObject* py_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments("rope_axes", n, 8);
+  arguments("rope_axes", n, 7);
   const Tensor q = tensor(a[0]), k = tensor(a[1], true), pos = tensor(a[2]);
-  Tensor qo = tensor(a[6], true), ko = tensor(a[7], true);
-  Turn turn = turn_of(a[3], a[4], q);
-  turn.inverse = integer(a[5]) != 0;
+  Tensor qo = tensor(a[5], true), ko = tensor(a[6], true);
+  Turn turn = turn_of(a[3], q, pos);
+  turn.inverse = integer(a[4]) != 0;
   if (!qo.defined()) qo = like(q);
   if (!ko.defined()) ko = like(k);
   finish(rope(q, k, pos, turn, qo, ko), "rope_axes");
@@ -238,13 +248,13 @@ PyObject* py_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// rotary_axes(q, k, positions, axis, freq) -> (q_out, k_out)
+// rotary_axes(q, k, positions, table) -> (q_out, k_out)
 PyObject* py_rotary_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments("rotary_axes", n, 5);
+  arguments("rotary_axes", n, 4);
   const Tensor q = tensor(a[0]), k = tensor(a[1], true), pos = tensor(a[2]);
   int rc = 0;
-  const auto out = rotary(q, k, pos, turn_of(a[3], a[4], q), &rc);
+  const auto out = rotary(q, k, pos, turn_of(a[3], q, pos), &rc);
   finish(rc, "rotary_axes");
   return tuple({out.first, out.second});
   END_HANDLE_TH_ERRORS
@@ -334,15 +344,23 @@ PyObject* py_paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// setup(check, count): the package's functions that raise a status code and count launches
+// setup(check): the package's function that raises a status code
 PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments("setup", n, 2);
+  arguments("setup", n, 1);
   Py_INCREF(a[0]);
-  Py_INCREF(a[1]);
   Py_XSETREF(g_check, a[0]);
-  Py_XSETREF(g_count, a[1]);
   Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// launches(reset) -> kernels launched since the last reset
+PyObject* py_launches(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("launches", n, 1);
+  const long long count = g_launches;
+  if (integer(a[0]) != 0) g_launches = 0;
+  return PyLong_FromLongLong(count);
   END_HANDLE_TH_ERRORS
 }
 
@@ -352,6 +370,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<py_setup>("setup"),
+                           method<py_launches>("launches"),
                            method<py_rope_axes>("rope_axes"),
                            method<py_rotary_axes>("rotary_axes"),
                            method<py_paged_plan>("paged_plan"),

@@ -98,7 +98,7 @@ int bea_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* po
     // The fraction of a turn as a 64-bit fixed-point number. Below 0 the difference can round up to 1: a whole turn.
     const double turns = freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     const double fraction = turns - std::floor(turns);
-    p.turn[i] = fraction < 1.0 ? static_cast<uint64_t>(std::ldexp(fraction, 64)) : 0;
+    p.turn[i] = fraction < 1.0 ? static_cast<uint64_t>(fraction * 0x1p64) : 0;
     p.axis[i] = static_cast<uint8_t>(axis_of_pair[i]);
   }
   p.n = (int)q->shape[0];

@@ -22,8 +22,6 @@
 namespace bea {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kFillThreads = 256;
 constexpr int kFillRun = 4;  // consecutive places of a thread
 // Up to this many places the scanning CTA fills them itself.
@@ -82,7 +80,10 @@ __device__ __forceinline__ int2 place_of(const PlanParams& p, int row, int old, 
   return make_int2(-1, pos);
 }
 
+// kPlanThreads: 256 for up to as many requests (a block of a quarter the size starts and meets sooner), else 1024.
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p, int fill) {
+  constexpr int kPlanWarps = kPlanThreads / 32;
   __shared__ Sums warp_sums[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_launch_dependents();
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   const Sums inc = warp_inclusive(mine);
   if (lane == 31) warp_sums[warp] = inc;
   const bool bad = __syncthreads_or(wrong);
-  const Sums w = warp_inclusive(warp_sums[lane]);  // by every warp for itself
+  const Sums w = warp_inclusive(lane < kPlanWarps ? warp_sums[lane] : Sums{0, 0, 0});  // by every warp for itself
   const Sums all{__shfl_sync(~0u, w.back, 31), __shfl_sync(~0u, w.need, 31), __shfl_sync(~0u, w.add, 31)};
   const int prev = max(warp - 1, 0);
   Sums at{__shfl_sync(~0u, w.back, prev), __shfl_sync(~0u, w.need, prev), __shfl_sync(~0u, w.add, prev)};
@@ -277,21 +278,22 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_co
 // ---- write ---------------------------------------------------------------------
 
 // HBM-bound copy of rows of some hundred bytes to places of their own: a thread
-// moves 16 bytes of K and 16 of V.
+// moves 16 bytes of K and 16 of V. Index: of these pieces; 32 bits where they are
+// enough, divisions by run-time numbers stand before every load.
 constexpr int kWriteThreads = 256;
 
+template <typename Index>
 __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int per_token = p.hkv * p.row_vecs;
-  const int64_t total = (int64_t)p.n * p.l * per_token;
-  for (int64_t it = (int64_t)blockIdx.x * kWriteThreads + threadIdx.x; it < total;
-       it += (int64_t)gridDim.x * kWriteThreads) {
-    const int64_t t = it / per_token;
-    const int in = (int)(it - t * per_token);
+  const unsigned per_token = p.hkv * p.row_vecs;
+  const Index total = (Index)p.n * p.l * per_token;
+  for (Index it = (Index)blockIdx.x * kWriteThreads + threadIdx.x; it < total; it += (Index)gridDim.x * kWriteThreads) {
+    const Index t = it / per_token;
+    const unsigned in = (unsigned)(it - t * per_token);
     const int slot = p.slot_map[t];
     const int64_t b = t / p.l;
-    const int i = (int)(t - b * p.l);
+    const int i = (int)(t - (Index)b * p.l);
     const int hh = in / p.row_vecs, c = in - hh * p.row_vecs;
     // read before the slot is known
     const uint4 kx = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k.ptr) +
@@ -314,7 +316,8 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid
 
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t s, int* nlaunch) {
   const int fill = p.capacity <= kFuseCapacity;
-  cudaError_t e = launch_dependent(plan_kernel, dim3(1), kPlanThreads, 0, s, p, fill);
+  cudaError_t e = p.n <= 256 ? launch_dependent(plan_kernel<256>, dim3(1), 256, 0, s, p, fill)
+                             : launch_dependent(plan_kernel<1024>, dim3(1), 1024, 0, s, p, fill);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
   if (fill) return cudaSuccess;
@@ -332,7 +335,9 @@ cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t s, int* n
   if (total == 0) return cudaSuccess;
   int64_t blocks = (total + kWriteThreads - 1) / kWriteThreads;
   if (blocks > (int64_t(1) << 30)) blocks = int64_t(1) << 30;
-  const cudaError_t e = launch_dependent(paged_write_kernel, dim3((unsigned)blocks), kWriteThreads, 0, s, p);
+  const bool narrow = blocks * kWriteThreads * 2 < (int64_t(1) << 32);
+  const cudaError_t e = launch_dependent(narrow ? paged_write_kernel<uint32_t> : paged_write_kernel<uint64_t>,
+                                         dim3((unsigned)blocks), kWriteThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }

@@ -40,7 +40,7 @@ constexpr int kMaxCtas = 160;       // one per SM
 constexpr int kMaxRequests = 1024;  // per launch: their tile counts are scanned in shared memory
 constexpr int kWholeTiles = 32;     // units up to this long are not cut
 constexpr int kUnitCost = 2;        // of a unit, in tiles, besides its tiles
-constexpr int kMinCost = 2 * kWarps;  // of a CTA's run, as long as there are fewer than G such runs
+constexpr int kMinCost = kWarps;   // of a CTA's run, as long as there are fewer than G such runs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -738,12 +738,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the unit that begins in CTA blockIdx.x's run and goes on after it, query head blockIdx.y of it. The
 // parts are dealt to the block's warps, a lane has 4 columns; then the warps' results are merged in order. A chain of
-// three memory latencies (which unit, its parts, the result); 128 threads of 32 registers, so that a block finds room
-// beside a CTA of the kernel before.
-constexpr int kJoinWarps = 4;
+// three memory latencies (which unit, its parts, the result) as long as a warp has at most kJoinBatch parts.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinBatch = 4;
 
 template <bool kF32, int kD, int kHd>
-__global__ void __launch_bounds__(kJoinWarps * 32, 16)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     paged_join_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Launch a) {
   using C = Cfg<kF32, kD, kHd>;
   __shared__ float4 part[kJoinWarps][32];
@@ -769,12 +769,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 16)
     sum = fmaf(sum, f, e.y * g);
     o = make_float4(fmaf(o.x, f, y.x * g), fmaf(o.y, f, y.y * g), fmaf(o.z, f, y.z * g), fmaf(o.w, f, y.w * g));
   };
-  for (int i = warp; i < parts; i += kJoinWarps) {
-    const int slot = i == 0 ? cta * 2 + 1 : (cta + i * a.planes) * 2;
-    const float2 e = reinterpret_cast<const float2*>(ws + wl.ml)[slot * 16 + row];
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mine) y = *reinterpret_cast<const float4*>(ws + wl.o + (((int64_t)slot * C::kRows + row) * kD + lane * 4) * 4);
-    add(e, y);
+  for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kJoinBatch) {
+    float2 e[kJoinBatch];
+    float4 y[kJoinBatch];
+#pragma unroll
+    for (int z = 0; z < kJoinBatch; ++z) {
+      const int i = i0 + z * kJoinWarps, slot = i == 0 ? cta * 2 + 1 : (cta + i * a.planes) * 2;
+      e[z] = make_float2(-INFINITY, 0.f);
+      y[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < parts) {
+        e[z] = reinterpret_cast<const float2*>(ws + wl.ml)[slot * 16 + row];
+        if (mine) y[z] = *reinterpret_cast<const float4*>(ws + wl.o + (((int64_t)slot * C::kRows + row) * kD + lane * 4) * 4);
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < kJoinBatch; ++z) add(e[z], y[z]);
   }
   if (warp > 0) {
     part[warp][lane] = o;

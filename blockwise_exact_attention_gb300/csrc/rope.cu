@@ -17,6 +17,8 @@
 // with 4. Where 8 heads would leave the GPU's threads unfilled it takes 4: 17.0
 // against 22.4 us for [3, 1369, 12 + 12, 64] f32, 4.3 against 5.5 us for 256
 // tokens.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "launch_cache.cuh"
@@ -65,7 +67,8 @@ struct Piece<false> {
   }
 };
 
-template <bool kF32, int kHeads>
+// Index: of a thread's work item; 32 bits where they are enough, three divisions by run-time numbers start each item.
+template <bool kF32, int kHeads, typename Index>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   using P = Piece<kF32>;
   __shared__ uint64_t turn[kRopeMaxPairs];
@@ -79,17 +82,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   __syncthreads();
   grid_dependency_wait();
   constexpr int es = kF32 ? 4 : 2;
-  const int pieces = half / P::kN;  // per half row
+  const unsigned pieces = half / P::kN;  // per half row
   const int heads = p.hq + p.hk;
-  const int groups = (heads + kHeads - 1) / kHeads;
-  const int64_t total = (int64_t)p.n * p.l * groups * pieces;
-  for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < total; it += (int64_t)gridDim.x * kThreads) {
-    const int64_t tg = it / pieces;
+  const unsigned groups = (heads + kHeads - 1) / kHeads;
+  const Index total = (Index)p.n * p.l * groups * pieces;
+  for (Index it = (Index)blockIdx.x * kThreads + threadIdx.x; it < total; it += (Index)gridDim.x * kThreads) {
+    const Index tg = it / pieces, t = tg / groups;
     const int c = (int)(it - tg * pieces) * P::kN;
-    const int64_t t = tg / groups;
     const int first = (int)(tg - t * groups) * kHeads;
     const int64_t b = t / p.l;
-    const int i = (int)(t - b * p.l);
+    const int i = (int)(t - (Index)b * p.l);
     uint4 ru[kHeads], rv[kHeads];
 #pragma unroll
     for (int x = 0; x < kHeads; ++x) {
@@ -143,10 +145,19 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t s, int* nlaunch) {
   auto threads = [&](int heads) { return tokens * ((p.hq + p.hk + heads - 1) / heads) * pieces; };
   if (threads(1) == 0) return cudaSuccess;
   const bool wide = threads(8) >= kFull;
-  int64_t blocks = (threads(wide ? 8 : 4) + kThreads - 1) / kThreads;
+  const int64_t total = threads(wide ? 8 : 4);
+  int64_t blocks = (total + kThreads - 1) / kThreads;
   if (blocks > (int64_t(1) << 30)) blocks = int64_t(1) << 30;  // the kernel strides over the rest
-  auto kern = p.is_f32 ? (wide ? rope_kernel<true, 8> : rope_kernel<true, 4>)
-                       : (wide ? rope_kernel<false, 8> : rope_kernel<false, 4>);
+  const bool narrow = blocks * kThreads * 2 < (int64_t(1) << 32);
+  auto pick = [&](auto f32, auto heads) {
+    constexpr bool kF32 = decltype(f32)::value;
+    constexpr int kHeads = decltype(heads)::value;
+    return narrow ? rope_kernel<kF32, kHeads, uint32_t> : rope_kernel<kF32, kHeads, uint64_t>;
+  };
+  using Four = std::integral_constant<int, 4>;
+  using Eight = std::integral_constant<int, 8>;
+  auto kern = p.is_f32 ? (wide ? pick(std::true_type{}, Eight{}) : pick(std::true_type{}, Four{}))
+                       : (wide ? pick(std::false_type{}, Eight{}) : pick(std::false_type{}, Four{}));
   const cudaError_t e = launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;

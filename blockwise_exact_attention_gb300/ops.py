@@ -18,12 +18,12 @@ from . import _lib
 
 _DT = {torch.bfloat16: _lib.BEA_BF16, torch.float32: _lib.BEA_F32}
 
-_launches = 0  # kernels launched through this module since the last reset
+_launches = 0  # kernels launched through this module since the last reset (the binding counts its own)
 
 
 def launches_since_reset(reset: bool = False) -> int:
     global _launches
-    n = _launches
+    n = _launches + _lib.bind().launches(reset)
     if reset:
         _launches = 0
     return n

@@ -16,8 +16,8 @@ from . import _lib
 
 
 @functools.lru_cache(maxsize=128)
-def _table(sections: tuple, base: float, spectrum: str, d: int) -> tuple[bytes, bytes]:
-    """(axis, frequency) of every pair, as the int32 and double arrays the library reads."""
+def _table(sections: tuple, base: float, spectrum: str, d: int) -> tuple[bytes, bytes, int]:
+    """(axis, frequency) of every pair, as the int32 and double arrays the library reads, and the number of axes."""
     half = d // 2
     if not all(isinstance(s, int) and s >= 0 for s in sections) or sum(sections) != half:
         raise ValueError(f"sections {sections} are not numbers of pairs that sum to d / 2 = {half}")
@@ -30,13 +30,7 @@ def _table(sections: tuple, base: float, spectrum: str, d: int) -> tuple[bytes, 
         for j in range(pairs):
             freq.append(base ** -(len(freq) / half if spectrum == "joint" else j / pairs))
             axis.append(a)
-    return struct.pack(f"={half}i", *axis), struct.pack(f"={half}d", *freq)
-
-
-def _arguments(q, positions, sections, base, spectrum):
-    if positions.ndim != 3 or positions.shape[0] != len(sections):
-        raise ValueError(f"positions {tuple(positions.shape)}: [{len(sections)}, n, l] for sections {tuple(sections)}")
-    return _table(tuple(sections), float(base), spectrum, q.shape[-1])
+    return struct.pack(f"={half}i", *axis), struct.pack(f"={half}d", *freq), len(sections)
 
 
 def rope_axes(q, k, positions, sections, base=10000.0, spectrum="joint", inverse=False, q_out=None, k_out=None):
@@ -48,8 +42,8 @@ def rope_axes(q, k, positions, sections, base=10000.0, spectrum="joint", inverse
     with s pairs have base**(-j/s), j = 0 .. s-1. One axis with all pairs is
     the ordinary rotary embedding. ``inverse`` turns back (the gradient).
     Returns (q_out, k_out); either may be its input, turned in place."""
-    axis, freq = _arguments(q, positions, sections, base, spectrum)
-    return _lib.bind().rope_axes(q, k, positions, axis, freq, inverse, q_out, k_out)
+    table = _table(tuple(sections), base, spectrum, q.shape[-1])
+    return _lib.bind().rope_axes(q, k, positions, table, inverse, q_out, k_out)
 
 
 def rotary_axes(q, k, positions, sections, base=10000.0, spectrum="joint"):
@@ -58,5 +52,4 @@ def rotary_axes(q, k, positions, sections, base=10000.0, spectrum="joint"):
     Captured into a CUDA graph, it refuses a leaf tensor on which a graph made on
     the default stream is still alive: autograd would wait for that stream in the
     middle of the capture. Delete the earlier outputs first."""
-    axis, freq = _arguments(q, positions, sections, base, spectrum)
-    return _lib.bind().rotary_axes(q, k, positions, axis, freq)
+    return _lib.bind().rotary_axes(q, k, positions, _table(tuple(sections), base, spectrum, q.shape[-1]))
