@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   constexpr int kPlanWarps = kPlanThreads / 32;
   __shared__ Sums warp_sums[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_launch_dependents();
+  if (fill) grid_launch_dependents();  // one CTA: the next kernel is set up beside it
   grid_dependency_wait();
   // 1. Totals and checks, before anything is changed. A thread has `per` consecutive rows.
   const int per = (p.n + kPlanThreads - 1) / kPlanThreads, r0 = tid * per;
@@ -213,7 +213,6 @@ __device__ __forceinline__ int row_of_token(const int32_t* cu, int lo, int hi, i
 }
 
 __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_constant__ PlanParams p) {
-  grid_launch_dependents();
   grid_dependency_wait();
   constexpr int kWarpRun = 32 * kFillRun;
   const int lane = threadIdx.x & 31;
@@ -284,7 +283,6 @@ constexpr int kWriteThreads = 256;
 
 template <typename Index>
 __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
-  grid_launch_dependents();
   grid_dependency_wait();
   const unsigned per_token = p.hkv * p.row_vecs;
   const Index total = (Index)p.n * p.l * per_token;

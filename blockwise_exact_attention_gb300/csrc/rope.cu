@@ -73,7 +73,6 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   using P = Piece<kF32>;
   __shared__ uint64_t turn[kRopeMaxPairs];
   __shared__ uint8_t axis[kRopeMaxPairs];
-  grid_launch_dependents();
   const int half = p.d >> 1;
   for (int i = threadIdx.x; i < half; i += kThreads) {
     turn[i] = p.turn[i];
