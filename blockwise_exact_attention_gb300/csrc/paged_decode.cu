@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto first_tile = [&](const Place& at) { return pre[at.k] * units + at.unit * (pre[at.k + 1] - pre[at.k]); };
   const WsLayout wl = ws_layout(C::kRows, kD);
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
-  if (a.split && tid == 0) reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{0, 0, -1, 0};
+  if (a.split && tid == 0) reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{0, 0, -1, 0};  // until a unit is cut
   if (cta >= ctas || count == 0) return;
   // Searches and divisions side by side: lanes 0, 1 the CTA's run, then lanes 2, 3 this warp's eighth of it. (Of a
   // whole first unit the cost before its tiles is left out, so that no warp goes without tiles.)
@@ -682,56 +682,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- units in several warps: merge their parts, in order ----------------------------
   __syncthreads();
-  const int2 own = (&part_of[0][0])[lane & (2 * kWarps - 1)];  // lane z: part z & 1 of warp z >> 1
-  uint32_t left = __ballot_sync(~0u, lane < 2 * kWarps && own.x >= 0);
-  while (left != 0) {
-    const int x = __ffs(left) - 1;
-    const int2 of = make_int2(__shfl_sync(~0u, own.x, x), __shfl_sync(~0u, own.y, x));
-    const bool one = ((left >> lane) & 1u) && own.x == of.x && own.y == of.y;  // of this unit's parts
-    const uint32_t these = __ballot_sync(~0u, one);
-    left &= ~these;
-    const int cnt = pre[of.x + 1] - pre[of.x], begin = pre[of.x] * units + of.y * cnt, end = begin + cnt;
-    const int64_t b = who[of.x];
-    const int h0 = of.y * group + head0;
-    const bool complete = begin >= t0 && end <= t1;
-    const int slot = blockIdx.x * 2 + (begin < t0 ? 0 : 1);
-    // A warp per row, lane c four columns; lane z works out the weight of part z.
-    for (int row = warp; row < rows; row += kWarps) {
-      const float2 e = one ? ml[lane >> 1][lane & 1][row] : make_float2(-INFINITY, 0.f);
-      float top = e.x;
+  // Lane z: part z & 1 of warp z >> 1. A unit's parts follow one another; the first one leads.
+  const int2 own = (&part_of[0][0])[lane & (2 * kWarps - 1)];
+  const uint32_t valid = __ballot_sync(~0u, lane < 2 * kWarps && own.x >= 0);
+  const uint32_t before = valid & ((1u << lane) - 1u);
+  const int prev = before != 0 ? 31 - __clz(before) : 0;
+  const int prev_x = __shfl_sync(~0u, own.x, prev), prev_y = __shfl_sync(~0u, own.y, prev);
+  const bool follows = before != 0 && prev_x == own.x && prev_y == own.y;
+  const uint32_t leads = __ballot_sync(~0u, ((valid >> lane) & 1u) && !follows);
+  // A warp per (unit, row), lane c four columns; lane z works out the weight of part z.
+  const int items = __popc(leads) * rows;
+  for (int item = warp; item < items; item += kWarps) {
+    const int nth = item / rows, row = item - nth * rows;
+    uint32_t rest_of = leads;
+    for (int i = 0; i < nth; ++i) rest_of &= rest_of - 1;
+    const int x = __ffs(rest_of) - 1;
+    rest_of &= rest_of - 1;
+    const uint32_t these = valid & ~((1u << x) - 1u) & (rest_of != 0 ? (1u << (__ffs(rest_of) - 1)) - 1u : ~0u);
+    const bool one = (these >> lane) & 1u;
+    const float2 e = one ? ml[lane >> 1][lane & 1][row] : make_float2(-INFINITY, 0.f);
+    float top = e.x;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      top = __shfl_sync(~0u, top, 0);
-      const float f = one ? ex2_approx(e.x - (top == -INFINITY ? 0.f : top)) : 0.f;
-      float sum = one ? f * e.y : 0.f;
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    top = __shfl_sync(~0u, top, 0);
+    const float f = one ? ex2_approx(e.x - (top == -INFINITY ? 0.f : top)) : 0.f;
+    float sum = one ? f * e.y : 0.f;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      sum = __shfl_sync(~0u, sum, 0);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int c = min(lane * 4, kD - 4);
-#pragma unroll 4
-      for (int z = 0; z < 2 * kWarps; ++z) {
-        const float g = __shfl_sync(~0u, f, z);
-        if ((these >> z) & 1u) {
-          const float4 u = *reinterpret_cast<const float4*>(
-              smem + (z % 2 ? (z / 2) * C::kWarpRing : C::kRing + (z / 2) * C::kPart) + (row * C::kPitch + c) * 4);
-          o = make_float4(fmaf(g, u.x, o.x), fmaf(g, u.y, o.y), fmaf(g, u.z, o.z), fmaf(g, u.w, o.w));
-        }
-      }
-      if (complete) {
-        if (lane * 4 < p.d) write_out4(p, b, h0 + row, lane * 4, o, sum);
-        if (lane == 0) write_lse(p, b, h0 + row, top, sum);
-      } else {
-        if (lane * 4 < p.d)
-          *reinterpret_cast<float4*>(reinterpret_cast<float*>(ws + wl.o) + ((int64_t)slot * C::kRows + row) * kD + lane * 4) = o;
-        if (lane == 0) reinterpret_cast<float2*>(ws + wl.ml)[slot * 16 + row] = make_float2(top, sum);
-      }
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    sum = __shfl_sync(~0u, sum, 0);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int c = min(lane * 4, kD - 4);
+    for (uint32_t zs = these; zs != 0; zs &= zs - 1) {
+      const int z = __ffs(zs) - 1;
+      const float g = __shfl_sync(~0u, f, z);
+      const float4 u = *reinterpret_cast<const float4*>(
+          smem + (z % 2 ? (z / 2) * C::kWarpRing : C::kRing + (z / 2) * C::kPart) + (row * C::kPitch + c) * 4);
+      o = make_float4(fmaf(g, u.x, o.x), fmaf(g, u.y, o.y), fmaf(g, u.z, o.z), fmaf(g, u.w, o.w));
     }
-    if (!complete && begin >= t0 && tid == 0) {
+    const int k_of = __shfl_sync(~0u, own.x, x), unit_of = __shfl_sync(~0u, own.y, x);
+    const int cnt = pre[k_of + 1] - pre[k_of], begin = pre[k_of] * units + unit_of * cnt, end = begin + cnt;
+    const int64_t b = who[k_of];
+    const int hh = unit_of * group + head0 + row;
+    if (begin >= t0 && end <= t1) {
+      if (lane * 4 < p.d) write_out4(p, b, hh, lane * 4, o, sum);
+      if (lane == 0) write_lse(p, b, hh, top, sum);
+      continue;
+    }
+    const int slot = blockIdx.x * 2 + (begin < t0 ? 0 : 1);
+    if (lane * 4 < p.d)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(ws + wl.o) + ((int64_t)slot * C::kRows + row) * kD + lane * 4) = o;
+    if (lane == 0) reinterpret_cast<float2*>(ws + wl.ml)[slot * 16 + row] = make_float2(top, sum);
+    if (begin >= t0 && row == 0 && lane == 0) {
       // the CTA whose run holds the unit's last tile, at cost v: runs up to the `over`-th are one longer
-      const int v = begin_cost(of.x) + (of.y + 1) * (cnt + kUnitCost) - 1;
+      const int v = begin_cost(k_of) + (unit_of + 1) * (cnt + kUnitCost) - 1;
       const int last = v < over * (share + 1) ? v / (share + 1) : over + (v - over * (share + 1)) / share;
-      reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{(int)b, of.y, last * a.planes + plane, 0};
+      reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{(int)b, unit_of, last * a.planes + plane, 0};
     }
   }
 }
