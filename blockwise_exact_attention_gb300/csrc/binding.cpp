@@ -9,6 +9,7 @@
 // pass does not enter the interpreter.
 #include <Python.h>
 
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -77,6 +78,15 @@ Tensor tensor(PyObject* o, bool or_none = false) {
   if (or_none && o == Py_None) return Tensor();
   TORCH_CHECK_TYPE(THPVariable_Check(o), "a tensor is expected, got ", Py_TYPE(o)->tp_name);
   return THPVariable_Unpack(o);
+}
+
+// A tensor that the caller gives to be written: autograd must learn that it changed, and may not be recording it.
+Tensor written(const Tensor& t) {
+  if (!t.defined()) return t;
+  TORCH_CHECK_VALUE(!(at::GradMode::is_enabled() && t.requires_grad()),
+                    "a tensor to be written requires grad: detach it, or call under torch.no_grad()");
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return t;
 }
 
 long long integer(PyObject* o) {
@@ -149,7 +159,10 @@ struct RotaryBackward : public Node {
   at::ScalarType dtype = at::kFloat;
 
   std::string name() const override { return "RotaryAxesBackward"; }
-  void release_variables() override { positions.reset_data(); }
+  void release_variables() override {
+    std::lock_guard<std::mutex> lock(mutex_);
+    positions.reset_data();
+  }
 
   // A gradient that autograd hands over may be of another dtype, expanded or not aligned.
   Tensor ready(const Tensor& g) const {
@@ -167,9 +180,14 @@ struct RotaryBackward : public Node {
     if (!g[0].defined() && !g[1].defined()) return out;
     Turn back = turn;
     back.inverse = !turn.inverse;
+    Tensor at;
+    {
+      std::lock_guard<std::mutex> lock(mutex_);
+      at = positions.unpack();
+    }
     const bool first = g[0].defined();
     int rc = 0;
-    const auto r = rotary(first ? g[0] : g[1], first ? g[1] : Tensor(), positions.unpack(), std::move(back), &rc);
+    const auto r = rotary(first ? g[0] : g[1], first ? g[1] : Tensor(), at, std::move(back), &rc);
     if (rc != BEA_OK) throw std::runtime_error(std::string("rotary_axes, backward: ") + bea_status_string(rc));
     out[first ? 0 : 1] = r.first;
     if (first && out.size() > 1) out[1] = r.second;
@@ -192,6 +210,8 @@ void check_capture(const Tensor& x) {
 }
 
 std::pair<Tensor, Tensor> rotary(const Tensor& q, const Tensor& k, const Tensor& positions, Turn turn, int* rc) {
+  for (const Tensor* t : {&q, &k})
+    TORCH_CHECK_NOT_IMPLEMENTED(!t->defined() || !t->_fw_grad(0).defined(), "rotary_axes has no forward-mode derivative");
   const bool grad = at::GradMode::is_enabled() && (q.requires_grad() || (k.defined() && k.requires_grad()));
   if (grad) {
     if (q.is_cuda() && c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
@@ -238,7 +258,7 @@ PyObject* py_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments("rope_axes", n, 7);
   const Tensor q = tensor(a[0]), k = tensor(a[1], true), pos = tensor(a[2]);
-  Tensor qo = tensor(a[5], true), ko = tensor(a[6], true);
+  Tensor qo = written(tensor(a[5], true)), ko = written(tensor(a[6], true));
   Turn turn = turn_of(a[3], q, pos);
   turn.inverse = integer(a[4]) != 0;
   if (!qo.defined()) qo = like(q);
@@ -268,11 +288,11 @@ PyObject* py_paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments("paged_plan", n, 8);
   Tensor in[5], out[6];
-  for (int i = 0; i < 5; ++i) in[i] = tensor(a[i]);
+  for (int i = 0; i < 5; ++i) in[i] = i == 2 || i == 3 ? written(tensor(a[i])) : tensor(a[i]);
   const long long page = integer(a[5]), capacity = integer(a[6]);
   if (a[7] != Py_None) {
     TORCH_CHECK_TYPE(PyTuple_Check(a[7]) && PyTuple_GET_SIZE(a[7]) == 6, "paged_plan: out is a PagedPlan");
-    for (int i = 0; i < 6; ++i) out[i] = tensor(PyTuple_GET_ITEM(a[7], i));
+    for (int i = 0; i < 6; ++i) out[i] = written(tensor(PyTuple_GET_ITEM(a[7], i)));
     TORCH_CHECK_VALUE(out[0].dim() != 1 || out[0].size(0) == capacity, "paged_plan: out has ", out[0].size(0),
                       " places, capacity is ", capacity);
   } else {
@@ -305,7 +325,7 @@ PyObject* py_paged_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor t[5];
   Call c;
   const bea_tensor* r[5];
-  for (int i = 0; i < 5; ++i) r[i] = c.add(t[i] = tensor(a[i]));
+  for (int i = 0; i < 5; ++i) r[i] = c.add(t[i] = i >= 3 ? written(tensor(a[i])) : tensor(a[i]));
   finish(bea_paged_write(r[0], r[1], r[2], r[3], r[4], c.stream()), "paged_write");
   return PyTuple_Pack(2, a[3], a[4]);
   END_HANDLE_TH_ERRORS
@@ -322,7 +342,7 @@ PyObject* py_paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     "paged_decode: q [n, 1, h, d], caches [pages, page_size, h_kv, d], block_table [n, max_pages]");
   const float scale = static_cast<float>(real(a[5]));
   const int left = clamp_int(integer(a[6]));
-  Tensor out = tensor(a[7], true), lse = tensor(a[8], true), ws = tensor(a[10], true);
+  Tensor out = written(tensor(a[7], true)), lse = written(tensor(a[8], true)), ws = tensor(a[10], true);
   const auto options = q.options().requires_grad(false);
   if (!out.defined()) out = at::empty(q.sizes(), integer(a[9]) != 0 ? options.dtype(at::kFloat) : options);
   if (!lse.defined()) lse = at::empty({q.size(0), q.size(2), 1}, options.dtype(at::kFloat));

@@ -306,6 +306,80 @@ def test_decode_in_two_graphs_and_on_two_streams():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_captured_behind_other_nodes():
+    """The calls' launches behind a memset, a copy and a fork of the captured stream."""
+    import blockwise_exact_attention_gb300 as bea
+    x = make([3000, 70], 8, 2, 128, 16, BF16, seed=90)
+    q, k, v, table, lens = x
+    bea.paged_decode(*x, 0.1)
+    junk, q2 = torch.ones(1000, device="cuda"), torch.empty_like(q)
+    slots = i32([5, -1])
+    new = draw((2, 1, 2, 128), BF16, 91)
+    kc, vc = torch.zeros_like(k), torch.zeros_like(v)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        junk.zero_()
+        a = bea.paged_decode(*x, 0.1)
+        q2.copy_(q)
+        b = bea.paged_decode(q2, k, v, table, lens, 0.1)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            bea.paged_write(new, new, slots, kc, vc)
+            c = bea.paged_decode(q2, k, v, table, lens, 0.1)
+        d = bea.paged_decode(q2, k, v, table, lens, 0.1)
+        torch.cuda.current_stream().wait_stream(side)
+        e = bea.paged_decode(q2, k, v, table, lens, 0.1)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    check(*a, *x, 0.1)
+    for y in (b, c, d, e):
+        assert torch.equal(a[0], y[0]) and torch.equal(a[1], y[1])
+    assert torch.equal(kc.view(-1, 2, 128)[5], new[0, 0])
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first calls are captured ones (no warm-up)."""
+    import subprocess
+    import sys
+    code = """
+import torch, blockwise_exact_attention_gb300 as bea
+q = torch.randn(2, 1, 4, 64, device="cuda").bfloat16()
+k, v = torch.randn(2, 9, 16, 2, 64, device="cuda").bfloat16().unbind(0)
+table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+lens = torch.tensor([60, 3], dtype=torch.int32, device="cuda")
+pos = lens.view(1, 2, 1)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    turned, _ = bea.rope_axes(q, None, pos, (32,))
+    out, lse = bea.paged_decode(turned, k, v, table, lens, 0.1)
+g.replay()
+ref, ref_lse = bea.paged_decode(bea.rope_axes(q, None, pos, (32,))[0], k, v, table, lens, 0.1)
+assert torch.equal(out, ref) and torch.equal(lse, ref_lse) and bea.device_status() == 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert r.stdout.strip() == "captured", r.stderr[-2000:]
+
+
+def test_written_tensors_are_known_to_autograd():
+    import blockwise_exact_attention_gb300 as bea
+    x = make([30, 20], 4, 2, 64, 16, BF16, seed=92)
+    q, k, v, table, lens = x
+    new = draw((2, 1, 2, 64), BF16, 93)
+    leaf = k.clone().requires_grad_()
+    with pytest.raises(ValueError, match="requires grad"):
+        bea.paged_write(new, new, lens, leaf, v)
+    w = torch.ones_like(k, requires_grad=True)
+    y = (w * k).sum()
+    bea.paged_write(new, new, lens, k, v)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with pytest.raises(ValueError, match="requires grad"):
+        bea.paged_decode(*x, out=torch.zeros_like(q, requires_grad=True))
+
+
 def test_decode_workspace_is_checked():
     import blockwise_exact_attention_gb300 as bea
     x = make([5000], 8, 2, 128, 16, BF16, seed=11)
@@ -445,6 +519,17 @@ def test_plan_refuses_whole_steps():
                    dict(new=[2 ** 31 - 1, 0, 0]), dict(lens=[2 ** 31 - 1, 16, 0], new=[-1, 0, 0]), dict(new=[0, 0, 2 ** 31 - 1], capacity=5000),
                    dict(new=[1, 1, 3], capacity=0)):
         expect(**{**base, **change}, status=PAGES)
+
+
+def test_plan_without_requests_or_places():
+    import blockwise_exact_attention_gb300 as bea
+    none = i32([])
+    for capacity in (0, 7, 5000):
+        p = bea.paged_plan(none, none, i32([]).reshape(0, 3), i32([4, 5]), i32([2]), 16, capacity)
+        assert p.slot_map.tolist() == [-1] * capacity and p.positions.tolist() == [0] * capacity
+        assert p.cu_new.tolist() == p.cu_pages.tolist() == [0] and p.lens.tolist() == [] and p.n_free.tolist() == [2]
+    expect([20, 0, 3], [0, 0, -1], [[1, 2], [-1, -1], [0, -1]], [7, 8, -1, -1], 2, 16, 0)
+    assert bea.device_status() == 0
 
 
 def test_plan_ends_feed_the_new():

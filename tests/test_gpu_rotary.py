@@ -206,6 +206,59 @@ def test_captured_forward_and_backward_replay():
         assert torch.equal(dq, bea.rope_axes(g, None, p, (32,), inverse=True)[0])
 
 
+def test_capture_over_a_live_eager_graph_is_refused():
+    """Its backward pass would end the process: the forward call refuses."""
+    import blockwise_exact_attention_gb300 as bea
+    q = draw((1, 4, 2, 32), BF16, 25).requires_grad_()
+    p = torch.arange(4, dtype=torch.int32, device="cuda").expand(1, 1, 4)
+    out, _ = bea.rotary_axes(q, None, p, (16,))           # on the default stream, kept alive
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="captured"):
+            bea.rotary_axes(q, None, p, (16,))
+        inside, _ = bea.rope_axes(q, None, p, (16,))      # the plain call has no such tie
+    del out
+    again = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(again):
+        out, _ = bea.rotary_axes(q, None, p, (16,))
+    again.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, inside)
+
+
+def test_written_tensors_are_known_to_autograd():
+    import blockwise_exact_attention_gb300 as bea
+    q = draw((1, 3, 2, 16), F32, 26).requires_grad_()
+    p = torch.arange(3, dtype=torch.int32, device="cuda").expand(1, 1, 3)
+    with pytest.raises(ValueError, match="requires grad"):
+        bea.rope_axes(q, None, p, (8,), q_out=q)
+    x = q * 1.0
+    y = (x * x).sum()                                     # keeps x for its gradient
+    with torch.no_grad():
+        bea.rope_axes(x, None, p, (8,), q_out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    out, _ = bea.rotary_axes(q, None, p2 := p.contiguous(), (8,))
+    p2.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    with torch.inference_mode():
+        z = q.clone()
+        bea.rope_axes(z, None, p, (8,), q_out=z)
+    assert torch.equal(z, bea.rope_axes(q.detach(), None, p, (8,))[0])
+
+
+def test_no_forward_mode():
+    import blockwise_exact_attention_gb300 as bea
+    from torch.autograd import forward_ad
+    q = draw((1, 3, 2, 16), F32, 27)
+    p = torch.arange(3, dtype=torch.int32, device="cuda").expand(1, 1, 3)
+    with forward_ad.dual_level():
+        with pytest.raises(NotImplementedError):
+            bea.rotary_axes(forward_ad.make_dual(q, q), None, p, (8,))
+
+
 def test_another_stream():
     import blockwise_exact_attention_gb300 as bea
     q = draw((1, 500, 8, 128), BF16, 23)
