@@ -222,7 +222,7 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f) || window_left < -1) return BEA_ERR_ARG;
   if (broadcast(out) || broadcast(lse)) return BEA_ERR_ARG;
   if (q->dtype == BEA_BF16 ? (d != 64 && d != 128) : (d < 4 || d > 128 || d % 4 != 0)) return BEA_ERR_UNSUPPORTED;
-  if (n * h > (int64_t(1) << 31) - 1) return BEA_ERR_SHAPE;
+  if (n * h > (int64_t(1) << 31) - 1 || h * d > (int64_t(1) << 31) - 1) return BEA_ERR_SHAPE;
   const int64_t page = k_cache->shape[1], max_pages = block_table->shape[1];
   const int64_t max_keys = max_pages * page;
   if (max_keys >= bea::kUnbounded) return BEA_ERR_SHAPE;

@@ -2,29 +2,44 @@
 //
 // out = sum_j p_j v_j / sum_j p_j with p_j = exp(scale q.k_j - m): one pass over
 // the visible keys with a running maximum m and sum (online softmax), every key
-// and value read once. HBM-bound: 2 d (K and V) elements a key and K/V head
-// against 4 d g flops, g = h / h_kv query heads reading the same key.
+// and value read once. HBM-bound: 2 d elements (K and V) a key and K/V head
+// against 4 d g flops, g = h / h_kv query heads reading the same key. At 7 TB/s
+// that is 28 TFLOP/s for g = 8 in bf16: too much for the CUDA cores beside the
+// conversions, little for mma.sync with its 16 rows (112 TFLOP/s with the empty
+// ones, of which the loop keeps a quarter of the issue slots busy). A tcgen05
+// product has 64 rows at least, which 8 heads would leave empty, and its operands
+// would have to meet in shared memory CTA-wide; here a warp goes through its keys
+// alone. fp32 inputs stay exact: CUDA cores.
 //
 // Work. A UNIT is one (request, K/V head); its visible keys are cut into tiles of
 // kKeys. The tiles of all units, request by request, make one list, and CTA c of
-// G takes the c-th of G runs of it, each warp of the CTA an eighth of that (with
+// G takes the c-th of G runs of it, each warp of the CTA an eighth of that. (With
 // more than kRows query heads to a K/V head, neighbouring CTAs take the same run
-// for a block of kRows each, so that the second reads from L2), whatever the lengths are:
-// nothing about them is known on the host. Every CTA finds its run from the
-// lengths alone (a scan of tiles per request in shared memory). The runs cost
-// the same: a unit counts as its tiles and kUnitCost more, for its queries and
-// its output. A warp that covers a unit writes it; parts of a unit in several
-// warps of a CTA are merged through shared memory when the warps are done, and
-// parts in several CTAs go to the workspace as (O, m, l), which a second kernel
-// joins in a fixed order (no atomics: the same call gives the same bits). If no
-// unit is longer than kWholeTiles the CTAs' runs end at unit borders instead, and
-// where the host sees that from the table's width it launches no second kernel.
+// for kRows of them each, so that all but the first read from L2.) Nothing about
+// the lengths is known on the host: every CTA finds its run from them, by a scan
+// of tiles per request in shared memory. The runs cost the same, where a unit
+// counts as its tiles and kUnitCost more for its queries and its output. A warp
+// that covers a unit writes it; parts of a unit in several warps of a CTA are
+// merged through shared memory when the warps are done, and parts in several CTAs
+// go to the workspace as (O, m, l), which a second kernel joins in a fixed order
+// (no atomics: the same call gives the same bits). If no unit is longer than
+// kWholeTiles the CTAs' runs end at unit borders instead, and where the host sees
+// that from the table's width it launches no second kernel.
 //
 // A warp streams its tiles by cp.async into a ring of its own, running ahead over
 // unit borders, so no barrier stands before the end. Rows of a tile that no key
 // of the request fills (behind its length, before its window, in a bad page)
 // arrive as zeros and their scores are masked, so what those places hold in
 // memory does not matter.
+//
+// Measured (GPU time, three sets of inputs in turn): 48 requests of 16k-32k keys,
+// 32 / 8 heads of 128, bf16: 680-702 us, 6.9-7.1 TB/s (a copy reaches 6.8); one of
+// 130k keys 83-85 us, 6.4 TB/s; 64 requests of 1-8192 keys 59-60 us, 5.7 TB/s: 2.5
+// us pass before the first load is sent (the lengths, their scan, the page table)
+// and 5 at the end (the longest warp, the merge, the join); one request of 159
+// keys 5.9 us, all of it latency.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "launch_cache.cuh"
@@ -38,11 +53,22 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 160;       // one per SM
 constexpr int kMaxRequests = 1024;  // per launch: their tile counts are scanned in shared memory
-constexpr int kWholeTiles = 32;     // units up to this long are not cut
-constexpr int kUnitCost = 2;        // of a unit, in tiles, besides its tiles
-constexpr int kMinCost = kWarps;   // of a CTA's run, as long as there are fewer than G such runs
+// Units up to this long are not cut between CTAs. 16: one request of 159 keys 8.3 instead of 7.3 us, 256 requests of
+// 20-300 keys 39.8 instead of 37.1 us; 64: within 1% either way.
+constexpr int kWholeTiles = 32;
+// Of a unit, in tiles, besides its tiles. 1, 4, 6: within 1% on large batches, 4 and 6 2-5% slower on 73 requests of 32
+// K/V heads.
+constexpr int kUnitCost = 2;
+// Of a CTA's run, as long as there are fewer than G such runs. 16, 32: one request of 159 keys 7.3, 9.6 instead of 5.4
+// us.
+constexpr int kMinCost = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Keys of a tile of rows of `d` elements (32, 64 or 128): K and V 4 KB each. (bf16, d = 64, with tiles of 16 keys, not
+// 32: 66.0 against 68.6 us where pages of 16 tokens then hold a tile each, 82.6 against 64.7 us with pages of 20,
+// whose rows are looked up one by one either way.)
+__host__ __device__ constexpr int tile_keys(int d, bool is_f32) { return 4096 / (d * (is_f32 ? 4 : 2)); }
 
 // kHd: query heads of a K/V head that a CTA takes at most (bf16: 8 or 16 of an mma's 16 rows).
 template <bool kF32, int kD, int kHd>
@@ -50,21 +76,23 @@ struct Cfg {
   static constexpr int kRows = kHd;
   static constexpr int kEs = kF32 ? 4 : 2;
   static constexpr int kRowBytes = kD * kEs;
-  static constexpr int kKeys = 4096 / kRowBytes;  // of a tile: K and V 4 KB each
+  static constexpr int kKeys = tile_keys(kD, kF32);  // of a tile
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
-  static constexpr int kStages = 2;
-  static constexpr int kWarpRing = kStages * kStageBytes;
-  static constexpr int kRing = kWarps * kWarpRing;
   static constexpr int kPitch = kD + 8;  // floats a row of a part: 8 rows x 4 lanes fall on different banks
   static constexpr int kPart = kRows * kPitch * 4;
   static constexpr int kHeads = kWarps * kPart;  // a warp's first part; its last one takes its ring's place
   static constexpr int kQ = kF32 ? kWarps * kRows * kD * 4 : 0;
   static constexpr int kP = kF32 ? kWarps * kKeys * kRows * 4 : 0;
+  // Tiles in a warp's ring. A third is slower (48 long requests 742 instead of 702 us, one of 130k keys 89.6 instead of
+  // 85.1 us): the further the warps' streams run ahead, the less the memory sees of each row at a time.
+  static constexpr int kStages = 2;
+  static constexpr int kWarpRing = kStages * kStageBytes;
+  static constexpr int kRing = kWarps * kWarpRing;
   static constexpr int kSmem = kRing + kHeads + kQ + kP;
   // The 16-byte pieces of row r are stored at piece ^ swizzle(r): the eight rows an ldmatrix reads (bf16), the two
   // rows by four pieces a quarter-warp reads (f32) fall on different banks.
   __host__ __device__ static constexpr int swizzle(int r) { return kF32 ? ((r & 1) << 2) | ((r & 7) >> 1) : r & 7; }
-  static_assert(!kF32 || kKeys <= 32, "a tile's rows are bits of a mask");
+  static_assert(kKeys <= 32, "a tile's rows are bits of a mask");
   static_assert(kPart <= kWarpRing, "a part takes the place of its warp's ring");
 };
 
@@ -552,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       // rows 8-15 of the products stay empty where a unit has at most 8 heads
-      constexpr int kHalves = C::kRows / 8;
+      constexpr int kHalves = C::kRows > 8 ? 2 : 1;
       float m[kHalves], l[kHalves];
 #pragma unroll
       for (int x = 0; x < kHalves; ++x) m[x] = -INFINITY, l[x] = 0.f;
@@ -853,18 +881,18 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
 
 }  // namespace
 
-// The elements of a row in the kernels, and the tile of such rows.
+// The elements of a row in the kernels.
 static int row_elements(int64_t d, bool is_f32) { return is_f32 && d <= 32 ? 32 : d <= 64 ? 64 : 128; }
-static int tile_keys(int64_t d, bool is_f32) { return 4096 / (row_elements(d, is_f32) * (is_f32 ? 4 : 2)); }
 
 size_t paged_decode_workspace(int64_t, int64_t, int64_t d, int64_t max_keys) {
   // Without the type: of the shorter of their uncut lengths.
-  if (max_keys <= kWholeTiles * tile_keys(d, true)) return 0;
+  if (max_keys <= kWholeTiles * std::min(tile_keys(row_elements(d, true), true), tile_keys(row_elements(d, false), false)))
+    return 0;
   return ws_layout(16, d <= 64 ? 64 : 128).total;
 }
 
 bool paged_decode_fits(int64_t hkv, int64_t d, bool is_f32, int64_t max_keys) {
-  return request_cost(max_keys, hkv, tile_keys(d, is_f32)) < (int64_t(1) << 31);
+  return request_cost(max_keys, hkv, tile_keys(row_elements(d, is_f32), is_f32)) < (int64_t(1) << 31);
 }
 
 template <bool kF32, int kD>

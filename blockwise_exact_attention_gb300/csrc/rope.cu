@@ -13,10 +13,10 @@
 // kHeads heads of one token: it sends all its loads, computes the pieces'
 // cosines and sines while they are under way, turns and stores. With 8 heads the
 // cosines and sines cost half as much and the stores are streamed past L2: 206 us
-// for a gradient step of [1, 32768, 32 + 8, 128] bf16 (6.5 TB/s) against 229 us
-// with 4. Where 8 heads would leave the GPU's threads unfilled it takes 4: 17.0
-// against 22.4 us for [3, 1369, 12 + 12, 64] f32, 4.3 against 5.5 us for 256
-// tokens.
+// for forward and gradient of [1, 32768, 32 + 8, 128] bf16 against 229 us with 4
+// (now 204 us, 6.6 TB/s). Where 8 heads would leave the GPU's threads unfilled it
+// takes 4: 17.0 against 22.4 us for [3, 1369, 12 + 12, 64] f32 (now 16 us), 4.3
+// against 5.5 us for 256 tokens of 32 + 8 heads (now 3.0 us).
 #include <type_traits>
 
 #include <cuda_bf16.h>
