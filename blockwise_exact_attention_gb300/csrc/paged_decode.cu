@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(128) uint8_t smem[];
   // requests with a visible key, in order: tiles of a unit summed over those before, number, length
   __shared__ int pre[kMaxRequests + 1], who[kMaxRequests], lens[kMaxRequests];
-  __shared__ int warp_tiles[kWarps], warp_some[kWarps], warp_max[kWarps];
+  __shared__ int4 warp_sums[kWarps];  // of a warp's requests: tiles, how many have some, the most
   __shared__ uint32_t masks[kWarps][C::kStages];
   __shared__ float2 ml[kWarps][2][16];  // of a warp's first and last part
   __shared__ int2 part_of[kWarps][2];   // (request, unit) of these parts, -1: none
@@ -227,51 +227,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int most = p.num_pages > 0 ? p.max_pages * p.page : 0, units = p.hkv;
   // every plane has `grid` CTAs; cta: this one's place among its plane's
   const int grid = gridDim.x / a.planes, cta = blockIdx.x / a.planes, plane = blockIdx.x % a.planes;
-  constexpr int kPer = kMaxRequests / kThreads;  // consecutive requests of a thread
-  int len_of[kPer], tiles_of[kPer];
-  int tiles_sum = 0, some = 0, longest = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = tid * kPer + i;
-    len_of[i] = r < a.n ? p.lens[a.r0 + r] : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    int len = len_of[i];
+  if (lane < 2) part_of[warp][lane] = make_int2(-1, -1);
+  int run = 0, count = 0, longest = 0;
+  for (int r0 = 0; r0 < a.n; r0 += kThreads) {
+    const int r = r0 + tid;
+    int len = r < a.n ? p.lens[a.r0 + r] : 0;
     if (len < 0 || len > most) {
       if (blockIdx.x == 0) report_status(p.status, BEA_STATUS_PAGES);
-      len = len_of[i] = len < 0 ? 0 : most;
+      len = len < 0 ? 0 : most;
     }
-    tiles_of[i] = len > 0 ? (len + C::kKeys - 1) / C::kKeys - first_key(len, p.left) / C::kKeys : 0;
-    tiles_sum += tiles_of[i];
-    some += tiles_of[i] > 0;
-    longest = max(longest, tiles_of[i]);
-  }
-  int tiles_inc = tiles_sum, some_inc = some;
+    const int tiles = len > 0 ? (len + C::kKeys - 1) / C::kKeys - first_key(len, p.left) / C::kKeys : 0;
+    const uint32_t some = __ballot_sync(~0u, tiles > 0);
+    const int most_tiles = __reduce_max_sync(~0u, tiles);
+    int inc = tiles;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(~0u, tiles_inc, o), y = __shfl_up_sync(~0u, some_inc, o);
-    if (lane >= o) tiles_inc += x, some_inc += y;
-  }
-  longest = __reduce_max_sync(~0u, longest);
-  if (lane == 31) warp_tiles[warp] = tiles_inc, warp_some[warp] = some_inc, warp_max[warp] = longest;
-  if (lane < 2) part_of[warp][lane] = make_int2(-1, -1);
-  __syncthreads();
-  int run = 0, count = 0, at_tiles = tiles_inc - tiles_sum, at = some_inc - some;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) warp_sums[warp] = make_int4(inc, __popc(some), most_tiles, 0);
+    __syncthreads();
+    int at_tiles = run + inc - tiles, at = count + __popc(some & ((1u << lane) - 1u));
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) at_tiles += warp_tiles[w], at += warp_some[w];
-    run += warp_tiles[w];
-    count += warp_some[w];
-    longest = max(longest, warp_max[w]);
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (tiles_of[i] == 0) continue;
-    pre[at] = at_tiles;
-    who[at] = a.r0 + tid * kPer + i;
-    lens[at++] = len_of[i];
-    at_tiles += tiles_of[i];
+    for (int w = 0; w < kWarps; ++w) {
+      const int4 x = warp_sums[w];
+      if (w < warp) at_tiles += x.x, at += x.y;
+      run += x.x;
+      count += x.y;
+      longest = max(longest, x.z);
+    }
+    if (tiles > 0) {
+      pre[at] = at_tiles;
+      who[at] = a.r0 + r;
+      lens[at] = len;
+    }
+    if (r0 + kThreads < a.n) __syncthreads();  // before warp_sums is written again
   }
   if (tid == 0) pre[count] = run;
   // requests without a visible key
