@@ -9,6 +9,7 @@
 // pass does not enter the interpreter.
 #include <Python.h>
 
+#include <atomic>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -34,7 +35,7 @@ using torch::autograd::Node;
 using torch::autograd::variable_list;
 
 PyObject* g_check = nullptr;  // _lib.check(code, where): raises BeaError
-long long g_launches = 0;     // kernels launched through here since the last reset
+std::atomic<long long> g_launches{0};  // kernels launched through here since the last reset
 
 // The tensors of one call, described; all on the current device.
 class Call {
@@ -42,6 +43,7 @@ class Call {
   const bea_tensor* add(const Tensor& t) {
     if (!t.defined()) return nullptr;
     TORCH_CHECK_VALUE(t.is_cuda(), "tensors must live on a CUDA device");
+    TORCH_CHECK_VALUE(!t.is_neg(), "a tensor whose negation is pending (torch.resolve_neg carries it out)");
     const int dev = t.get_device();
     if (n_ == 0) dev_ = dev;
     TORCH_CHECK_VALUE(dev == dev_, "tensors on cuda:", dev_, " and cuda:", dev, ": all must live on one device");
@@ -80,13 +82,15 @@ Tensor tensor(PyObject* o, bool or_none = false) {
   return THPVariable_Unpack(o);
 }
 
-// A tensor that the caller gives to be written: autograd must learn that it changed, and may not be recording it.
-Tensor written(const Tensor& t) {
-  if (!t.defined()) return t;
-  TORCH_CHECK_VALUE(!(at::GradMode::is_enabled() && t.requires_grad()),
+// A tensor that the caller gives to be written: autograd may not be recording it, and learns that it changed.
+Tensor to_write(const Tensor& t) {
+  TORCH_CHECK_VALUE(!t.defined() || !(at::GradMode::is_enabled() && t.requires_grad()),
                     "a tensor to be written requires grad: detach it, or call under torch.no_grad()");
-  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
   return t;
+}
+void written(std::initializer_list<Tensor> ts) {
+  for (const Tensor& t : ts)
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 long long integer(PyObject* o) {
@@ -109,12 +113,14 @@ void arguments(const char* name, Py_ssize_t got, Py_ssize_t want) {
   TORCH_CHECK_TYPE(got == want, name, ": ", got, " arguments, ", want, " expected");
 }
 
+int counted(int rc) {
+  if (rc == BEA_OK) g_launches += bea_last_launch_count();
+  return rc;
+}
+
 // What every call ends with, back in Python.
 void finish(int rc, const char* where) {
-  if (rc == BEA_OK) {
-    g_launches += bea_last_launch_count();
-    return;
-  }
+  if (rc == BEA_OK) return;
   PyObject* r = PyObject_CallFunction(g_check, "is", rc, where);
   if (r == nullptr) throw python_error();
   Py_DECREF(r);
@@ -147,7 +153,8 @@ int rope(const Tensor& q, const Tensor& k, const Tensor& positions, const Turn& 
          const Tensor& k_out) {
   Call c;
   const bea_tensor *a = c.add(q), *b = c.add(k), *p = c.add(positions), *x = c.add(q_out), *y = c.add(k_out);
-  return bea_rope_axes(a, b, p, turn.axis.data(), turn.freq.data(), turn.inverse ? 1 : 0, x, y, c.stream());
+  return counted(
+      bea_rope_axes(a, b, p, turn.axis.data(), turn.freq.data(), turn.inverse ? 1 : 0, x, y, c.stream()));
 }
 
 std::pair<Tensor, Tensor> rotary(const Tensor& q, const Tensor& k, const Tensor& positions, Turn turn, int* rc);
@@ -258,12 +265,13 @@ PyObject* py_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments("rope_axes", n, 7);
   const Tensor q = tensor(a[0]), k = tensor(a[1], true), pos = tensor(a[2]);
-  Tensor qo = written(tensor(a[5], true)), ko = written(tensor(a[6], true));
+  Tensor qo = to_write(tensor(a[5], true)), ko = to_write(tensor(a[6], true));
   Turn turn = turn_of(a[3], q, pos);
   turn.inverse = integer(a[4]) != 0;
   if (!qo.defined()) qo = like(q);
   if (!ko.defined()) ko = like(k);
   finish(rope(q, k, pos, turn, qo, ko), "rope_axes");
+  written({qo, ko});
   return tuple({qo, ko});
   END_HANDLE_TH_ERRORS
 }
@@ -288,11 +296,11 @@ PyObject* py_paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments("paged_plan", n, 8);
   Tensor in[5], out[6];
-  for (int i = 0; i < 5; ++i) in[i] = i == 2 || i == 3 ? written(tensor(a[i])) : tensor(a[i]);
+  for (int i = 0; i < 5; ++i) in[i] = i == 2 || i == 3 ? to_write(tensor(a[i])) : tensor(a[i]);
   const long long page = integer(a[5]), capacity = integer(a[6]);
   if (a[7] != Py_None) {
     TORCH_CHECK_TYPE(PyTuple_Check(a[7]) && PyTuple_GET_SIZE(a[7]) == 6, "paged_plan: out is a PagedPlan");
-    for (int i = 0; i < 6; ++i) out[i] = written(tensor(PyTuple_GET_ITEM(a[7], i)));
+    for (int i = 0; i < 6; ++i) out[i] = to_write(tensor(PyTuple_GET_ITEM(a[7], i)));
     TORCH_CHECK_VALUE(out[0].dim() != 1 || out[0].size(0) == capacity, "paged_plan: out has ", out[0].size(0),
                       " places, capacity is ", capacity);
   } else {
@@ -313,7 +321,9 @@ PyObject* py_paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bea_tensor* r[11];
   for (int i = 0; i < 5; ++i) r[i] = c.add(in[i]);
   for (int i = 0; i < 6; ++i) r[5 + i] = c.add(out[i]);
-  finish(bea_paged_plan(r[0], r[1], r[2], r[3], r[4], page, r[5], r[6], r[7], r[8], r[9], r[10], c.stream()), "paged_plan");
+  finish(counted(bea_paged_plan(r[0], r[1], r[2], r[3], r[4], page, r[5], r[6], r[7], r[8], r[9], r[10], c.stream())),
+         "paged_plan");
+  written({in[2], in[3], out[0], out[1], out[2], out[3], out[4], out[5]});
   return tuple({out[0], out[1], out[2], out[3], out[4], out[5]});
   END_HANDLE_TH_ERRORS
 }
@@ -325,8 +335,9 @@ PyObject* py_paged_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor t[5];
   Call c;
   const bea_tensor* r[5];
-  for (int i = 0; i < 5; ++i) r[i] = c.add(t[i] = i >= 3 ? written(tensor(a[i])) : tensor(a[i]));
-  finish(bea_paged_write(r[0], r[1], r[2], r[3], r[4], c.stream()), "paged_write");
+  for (int i = 0; i < 5; ++i) r[i] = c.add(t[i] = i >= 3 ? to_write(tensor(a[i])) : tensor(a[i]));
+  finish(counted(bea_paged_write(r[0], r[1], r[2], r[3], r[4], c.stream())), "paged_write");
+  written({t[3], t[4]});
   return PyTuple_Pack(2, a[3], a[4]);
   END_HANDLE_TH_ERRORS
 }
@@ -342,7 +353,7 @@ PyObject* py_paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     "paged_decode: q [n, 1, h, d], caches [pages, page_size, h_kv, d], block_table [n, max_pages]");
   const float scale = static_cast<float>(real(a[5]));
   const int left = clamp_int(integer(a[6]));
-  Tensor out = written(tensor(a[7], true)), lse = written(tensor(a[8], true)), ws = tensor(a[10], true);
+  Tensor out = to_write(tensor(a[7], true)), lse = to_write(tensor(a[8], true)), ws = tensor(a[10], true);
   const auto options = q.options().requires_grad(false);
   if (!out.defined()) out = at::empty(q.sizes(), integer(a[9]) != 0 ? options.dtype(at::kFloat) : options);
   if (!lse.defined()) lse = at::empty({q.size(0), q.size(2), 1}, options.dtype(at::kFloat));
@@ -357,9 +368,10 @@ PyObject* py_paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r[6] = c.add(lse);
   TORCH_CHECK_VALUE(!ws.defined() || (ws.is_cuda() && ws.get_device() == q.get_device() && ws.is_contiguous()),
                     "paged_decode: the workspace has to be contiguous and on the tensors' device");
-  finish(bea_paged_decode(r[0], r[1], r[2], r[3], r[4], r[5], r[6], scale, left, ws.defined() ? ws.data_ptr() : nullptr,
-                          ws.defined() ? ws.nbytes() : 0, c.stream()),
+  finish(counted(bea_paged_decode(r[0], r[1], r[2], r[3], r[4], r[5], r[6], scale, left,
+                                  ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, c.stream())),
          "paged_decode");
+  written({out, lse});
   return tuple({out, lse});
   END_HANDLE_TH_ERRORS
 }
@@ -378,9 +390,7 @@ PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* py_launches(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments("launches", n, 1);
-  const long long count = g_launches;
-  if (integer(a[0]) != 0) g_launches = 0;
-  return PyLong_FromLongLong(count);
+  return PyLong_FromLongLong(integer(a[0]) != 0 ? g_launches.exchange(0) : g_launches.load());
   END_HANDLE_TH_ERRORS
 }
 

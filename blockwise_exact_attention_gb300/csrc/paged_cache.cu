@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_co
   const bool vec = ((reinterpret_cast<uintptr_t>(p.slot_map) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
   const int64_t warps = (int64_t)gridDim.x * (kFillThreads / 32);
   for (int64_t w = (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5); w * kWarpRun < p.capacity; w += warps) {
-    const int first = (int)(w * kWarpRun), last = min(first + kWarpRun, total) - 1;
+    const int first = (int)(w * kWarpRun), last = (int)min((int64_t)first + kWarpRun, (int64_t)total) - 1;
     // The rows of the warp's first and last token, by 32 probes at a time; each lane searches between them.
     int lo = 0, hi = 0;
     if (first < total) {
@@ -328,7 +328,7 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t s, int* nlaunch)
   static PerContext<int> cache;
   int cap = 0;
   if ((e = wave_cap(cache, plan_fill_kernel, kFillThreads, 0, &cap)) != cudaSuccess) return e;
-  const int blocks = (p.capacity + kFillThreads * kFillRun - 1) / (kFillThreads * kFillRun);
+  const int64_t blocks = ((int64_t)p.capacity + kFillThreads * kFillRun - 1) / (kFillThreads * kFillRun);
   e = launch_dependent(plan_fill_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), kFillThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;

@@ -55,7 +55,7 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, softmax_scale=None, win
     """Attention of one new token per request: q [n, 1, h, d] against the keys
     and values of request r's first ``lens[r]`` slots (the new token's own among
     them) -> (out [n, 1, h, d], lse [n, h, 1] fp32). ``window_left`` >= 0 lets
-    the token see only that many keys before its own."""
+    the token see only that many keys before its own. No gradient."""
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(q.shape[-1])
     if out_dtype is not None and out_dtype not in (q.dtype, torch.float32):

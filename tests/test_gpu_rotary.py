@@ -243,6 +243,10 @@ def test_written_tensors_are_known_to_autograd():
     p2.add_(1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.sum().backward()
+    before = x._version
+    with torch.no_grad(), pytest.raises(RuntimeError, match="SHAPE"):   # a refused call writes nothing
+        bea.rope_axes(x[:, :2], None, p, (8,), q_out=x)
+    assert x._version == before
     with torch.inference_mode():
         z = q.clone()
         bea.rope_axes(z, None, p, (8,), q_out=z)
@@ -257,6 +261,25 @@ def test_no_forward_mode():
     with forward_ad.dual_level():
         with pytest.raises(NotImplementedError):
             bea.rotary_axes(forward_ad.make_dual(q, q), None, p, (8,))
+
+
+def test_launches_are_counted():
+    import blockwise_exact_attention_gb300 as bea
+    q = draw((1, 3, 2, 16), F32, 28).requires_grad_()
+    p = torch.arange(3, dtype=torch.int32, device="cuda").expand(1, 1, 3)
+    bea.launches_since_reset(reset=True)
+    out, _ = bea.rotary_axes(q, None, p, (8,))
+    assert bea.launches_since_reset() == 1
+    torch.autograd.grad(out.sum(), q)
+    assert bea.launches_since_reset(reset=True) == 2 and bea.launches_since_reset() == 0
+
+
+def test_pending_negation_is_refused():
+    import blockwise_exact_attention_gb300 as bea
+    q = torch._neg_view(draw((1, 3, 2, 16), F32, 29))
+    p = torch.arange(3, dtype=torch.int32, device="cuda").expand(1, 1, 3)
+    with pytest.raises(ValueError, match="resolve_neg"):
+        bea.rope_axes(q, None, p, (8,))
 
 
 def test_another_stream():
