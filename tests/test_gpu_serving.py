@@ -127,3 +127,40 @@ def test_train_through_rotation_and_attention():
     assert torch.equal(k.grad, dk) and torch.equal(v.grad, dv)
     assert (q.grad.float() - dq.float()).abs().max() <= 1e-2     # the backward sums dQ in any order
     assert bea.device_status() == 0
+
+
+def test_inputs_from_another_stream():
+    """Keys, lengths and tables that a slow kernel on another stream writes last, read right after an event, behind an
+    early-launched call on this stream; and results read by another stream behind an event."""
+    import blockwise_exact_attention_gb300 as bea
+    torch.manual_seed(3)
+    n, h, h_kv, d, page = 3, 4, 2, 64, 16
+    k, v = torch.randn(2, 200, page, h_kv, d, device="cuda").to(BF16)
+    q = torch.randn(n, 1, h, d, device="cuda").to(BF16)
+    table = torch.arange(198, dtype=I32, device="cuda").view(n, 66)
+    big = torch.randn(3000, 3000, device="cuda")
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    small = torch.zeros(1, 1, 2, 64, dtype=BF16, device="cuda")
+    pos = torch.zeros(1, 1, 1, dtype=I32, device="cuda")
+    for t in range(20):
+        want_lens = i32([1000 - t, 3 + t, 0 if t % 2 else 500])
+        want_k = k * (1.0 + 0.125 * (t % 4))
+        want = bea.paged_decode(q, want_k, v, table, want_lens, 0.1)
+        lens, kk = torch.zeros_like(want_lens), torch.zeros_like(k)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                big = big @ big * 1e-3
+            kk.copy_(want_k + 0 * big.sum().nan_to_num(0, 0, 0).to(BF16))
+            lens.copy_(want_lens)
+            ready = side.record_event()
+        bea.rope_axes(small, None, pos, (32,))
+        here.wait_event(ready)
+        got = bea.paged_decode(q, kk, v, table, lens, 0.1)
+        done = here.record_event()
+        with torch.cuda.stream(side):
+            side.wait_event(done)
+            copies = [x.clone() for x in got]
+        torch.cuda.synchronize()
+        for a, b in zip(copies, want):
+            assert torch.equal(a, b), t
