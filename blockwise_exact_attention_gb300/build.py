@@ -105,7 +105,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     tmp = BIND + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, binding, "-L" + HERE, "-l:libbea.so", "-Wl,-rpath,$ORIGIN", "-L" + _torch_paths()[1], "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_python", "-L" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64"), "-lcudart"]
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64"), "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

@@ -15,7 +15,7 @@
 #include <vector>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
@@ -141,13 +141,19 @@ PyObject* tuple(std::initializer_list<Tensor> ts) {
 
 // ---- rotary ----------------------------------------------------------------------
 
+// A new tensor on the device of a tensor of the call, past the dispatcher (0.8 instead of 1.6 us).
+Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const Tensor& beside) {
+  TORCH_CHECK_VALUE(beside.is_cuda(), "tensors must live on a CUDA device");
+  return at::detail::empty_cuda(shape, dtype, beside.device(), std::nullopt);
+}
+
 struct Turn {
   std::vector<int32_t> axis;  // of every pair
   std::vector<double> freq;
   bool inverse = false;
 };
 
-Tensor like(const Tensor& x) { return x.defined() ? at::empty(x.sizes(), x.options().requires_grad(false)) : Tensor(); }
+Tensor like(const Tensor& x) { return x.defined() ? empty(x.sizes(), x.scalar_type(), x) : Tensor(); }
 
 int rope(const Tensor& q, const Tensor& k, const Tensor& positions, const Turn& turn, const Tensor& q_out,
          const Tensor& k_out) {
@@ -310,7 +316,7 @@ PyObject* py_paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t one = 1;
     int64_t total = 0, at = 0;
     for (int64_t s : sizes) total += (s + 3) / 4 * 4;  // each on a 16-byte boundary
-    const Tensor all = at::empty({total}, in[0].options());
+    const Tensor all = empty({total}, at::kInt, in[0]);
     for (int i = 0; i < 6; ++i) {  // views of one allocation
       out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
       out[i].unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(&sizes[i], 1), at::IntArrayRef(&one, 1), at);
@@ -354,12 +360,11 @@ PyObject* py_paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float scale = static_cast<float>(real(a[5]));
   const int left = clamp_int(integer(a[6]));
   Tensor out = to_write(tensor(a[7], true)), lse = to_write(tensor(a[8], true)), ws = tensor(a[10], true);
-  const auto options = q.options().requires_grad(false);
-  if (!out.defined()) out = at::empty(q.sizes(), integer(a[9]) != 0 ? options.dtype(at::kFloat) : options);
-  if (!lse.defined()) lse = at::empty({q.size(0), q.size(2), 1}, options.dtype(at::kFloat));
+  if (!out.defined()) out = empty(q.sizes(), integer(a[9]) != 0 ? at::kFloat : q.scalar_type(), q);
+  if (!lse.defined()) lse = empty({q.size(0), q.size(2), 1}, at::kFloat, q);
   if (!ws.defined()) {
     const size_t need = bea_paged_decode_workspace_size(q.size(2), kc.size(2), q.size(3), table.size(1) * kc.size(1));
-    if (need > 0) ws = at::empty({static_cast<int64_t>(need)}, options.dtype(at::kByte));
+    if (need > 0) ws = empty({static_cast<int64_t>(need)}, at::kByte, q);
   }
   Call c;
   const bea_tensor* r[7];
