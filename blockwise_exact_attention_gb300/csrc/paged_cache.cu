@@ -15,8 +15,8 @@
 //
 // Latency-bound: a decode step moves some KB, in a chain of dependent reads
 // (lengths, then table or stack) with a block-wide scan between them. A step of
-// 256 requests takes 3.9 us of GPU time, one of 1024 requests that ends 50 of up
-// to 16k tokens and adds 0.5 M tokens 13.8 us, 8.2 of them in the scanning CTA.
+// 256 requests takes 3.6 us of GPU time, one of 1024 requests that ends 50 of up
+// to 16k tokens and adds 0.5 M tokens 13.2 us, more than half in the scanning CTA.
 #include "launch_cache.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -25,25 +25,27 @@ namespace bea {
 namespace {
 
 constexpr int kFillThreads = 256;
-constexpr int kFillRun = 4;  // consecutive places of a thread
+constexpr int kFillRun = 4;      // consecutive places of a thread
+constexpr int kFillRows = 2048;  // up to as many rows' cu_new are searched in shared memory
 // Up to this many places the scanning CTA fills them itself: 772 requests of a token each 6.2 us, 10.7 with the second
 // launch; 64 requests and 1024 places 6.1 against 6.8 us, but 4000 places 7.5 against 6.6 us.
 constexpr int kFuseCapacity = 2048;
 
 __device__ __forceinline__ int pages_of(int tokens, int page) { return (int)(((int64_t)tokens + page - 1) / page); }
 
-// Pages given back, pages taken, tokens added.
+// Pages given back, pages taken, tokens added. A sum that reaches kMany stays there; no step is done with such a sum, and
+// below it sums are exact.
+constexpr uint32_t kMany = (1u << 31) - 1;
 struct Sums {
-  long long back, need, add;
-  __device__ __forceinline__ Sums operator+(const Sums& o) const { return {back + o.back, need + o.need, add + o.add}; }
+  uint32_t back, need, add;
+  __device__ __forceinline__ Sums operator+(const Sums& o) const {
+    return {min(back + o.back, kMany), min(need + o.need, kMany), min(add + o.add, kMany)};
+  }
 };
-__device__ __forceinline__ Sums shfl_up(const Sums& s, int o) {
-  return {__shfl_up_sync(~0u, s.back, o), __shfl_up_sync(~0u, s.need, o), __shfl_up_sync(~0u, s.add, o)};
-}
 __device__ __forceinline__ Sums warp_inclusive(Sums x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Sums y = shfl_up(x, o);
+    const Sums y{__shfl_up_sync(~0u, x.back, o), __shfl_up_sync(~0u, x.need, o), __shfl_up_sync(~0u, x.add, o)};
     if ((threadIdx.x & 31) >= o) x = x + y;
   }
   return x;
@@ -53,6 +55,7 @@ __device__ __forceinline__ Sums warp_inclusive(Sums x) {
 struct Row {
   int len, add, back, had, need;
   bool wrong;
+  __device__ __forceinline__ Sums sums() const { return {(uint32_t)back, (uint32_t)need, (uint32_t)add}; }
 };
 __device__ __forceinline__ Row row_of(const PlanParams& p, int len, int a) {
   Row r{len, 0, 0, 0, 0, false};
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     a = p.new_lens[r0 + x];
     const Row r = row_of(p, len, a);
     wrong = wrong || r.wrong;
-    mine = mine + Sums{r.back, r.need, r.add};
+    mine = mine + r.sums();
   }
   const Sums inc = warp_inclusive(mine);
   if (lane == 31) warp_sums[warp] = inc;
@@ -115,8 +118,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   Sums at{__shfl_sync(~0u, w.back, prev), __shfl_sync(~0u, w.need, prev), __shfl_sync(~0u, w.add, prev)};
   if (warp == 0) at = Sums{0, 0, 0};
   at = Sums{at.back + inc.back - mine.back, at.need + inc.need - mine.need, at.add + inc.add - mine.add};
-  const bool ok = !bad && have >= 0 && have + all.back <= p.n_pool && all.need <= have + all.back && all.add <= p.capacity;
-  const int top = have + (int)all.back;
+  const int64_t top64 = (int64_t)have + all.back;
+  const bool ok = !bad && have >= 0 && top64 <= p.n_pool && all.need <= top64 && all.add <= (uint32_t)p.capacity &&
+                  max(all.back, max(all.need, all.add)) < kMany;
+  const int top = (int)top64;
   if (!ok) {
     if (tid == 0) report_status(p.status, BEA_STATUS_PAGES);
     for (int r = tid; r <= p.n; r += kPlanThreads) {
@@ -142,17 +147,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int from = __ffs(ends) - 1;
         const int m = __shfl_sync(~0u, r.back, from), to = have + __shfl_sync(~0u, (int)at.back, from);
         const int32_t* entries = p.table + __shfl_sync(~0u, row, from) * p.table_stride;
-        for (int j = lane; j < m; j += 32 * 8) {
-          int32_t id[8];
+        constexpr int kBatch = 16;
+        for (int j = lane; j < m; j += 32 * kBatch) {
+          int32_t id[kBatch];
 #pragma unroll
-          for (int z = 0; z < 8; ++z)
+          for (int z = 0; z < kBatch; ++z)
             if (j + 32 * z < m) id[z] = entries[j + 32 * z];
 #pragma unroll
-          for (int z = 0; z < 8; ++z)
+          for (int z = 0; z < kBatch; ++z)
             if (j + 32 * z < m) p.pool[to + j + 32 * z] = id[z];
         }
       }
-      at = at + Sums{r.back, r.need, r.add};
+      at = at + r.sums();
     }
     __syncthreads();  // the stack is complete, and n_free has been read by all (n_free_out may be the same word)
     if (tid == 0) {
@@ -179,8 +185,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (per > 1) {  // the row's numbers as written above
         a = p.new_lens[row];
         old = p.lens_out[row] - a;
-        at.add = p.cu_new[row];
-        at.need = p.cu_pages[row];
+        at.add = (uint32_t)p.cu_new[row];
+        at.need = (uint32_t)p.cu_pages[row];
       }
       r.add = max(a, 0);
     }
@@ -219,8 +225,15 @@ __device__ __forceinline__ int row_of_token(const int32_t* cu, int lo, int hi, i
 __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_constant__ PlanParams p) {
   grid_dependency_wait();
   constexpr int kWarpRun = 32 * kFillRun;
+  __shared__ int32_t cu_shared[kFillRows + 1];
   const int lane = threadIdx.x & 31;
-  const int total = p.cu_new[p.n], top = p.n_free_out[0] + p.cu_pages[p.n];
+  const int32_t* cu = p.cu_new;  // searched: from shared memory where it fits
+  if (p.n <= kFillRows) {
+    for (int r = threadIdx.x; r <= p.n; r += kFillThreads) cu_shared[r] = p.cu_new[r];
+    __syncthreads();
+    cu = cu_shared;
+  }
+  const int total = cu[p.n], top = p.n_free_out[0] + p.cu_pages[p.n];
   const bool vec = ((reinterpret_cast<uintptr_t>(p.slot_map) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
   const int64_t warps = (int64_t)gridDim.x * (kFillThreads / 32);
   for (int64_t w = (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5); w * kWarpRun < p.capacity; w += warps) {
@@ -234,7 +247,7 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_co
         int x = end ? lo : 0, y = p.n - 1;  // the row is in [x, y]
         while (x < y) {
           const int step = (y - x + 32) / 32, at = x + step * lane;
-          const uint32_t below = __ballot_sync(~0u, at <= y && p.cu_new[at] <= i);
+          const uint32_t below = __ballot_sync(~0u, at <= y && cu[at] <= i);
           x += step * (31 - __clz(below));  // lane 0 is always below
           y = min(y, x + step - 1);
         }
@@ -246,7 +259,7 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_co
     }
     const int64_t i0 = (int64_t)first + lane * kFillRun;
     int32_t slot[kFillRun], pos[kFillRun];
-    int row = i0 < total ? row_of_token(p.cu_new, lo, hi, (int)i0) : 0;
+    int row = i0 < total ? row_of_token(cu, lo, hi, (int)i0) : 0;
     int begin = 0, next = 0, old = 0, taken = 0;
     bool fresh = true;
 #pragma unroll
@@ -257,8 +270,8 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_co
         while (fresh || i0 + z >= next) {  // rows without tokens are passed over
           if (!fresh) ++row;
           fresh = false;
-          begin = p.cu_new[row];
-          next = p.cu_new[row + 1];
+          begin = cu[row];
+          next = cu[row + 1];
           old = p.lens_out[row] - (next - begin);
           taken = p.cu_pages[row];
         }

@@ -885,6 +885,10 @@ bool paged_decode_fits(int64_t hkv, int64_t d, bool is_f32, int64_t max_keys) {
   return request_cost(max_keys, hkv, tile_keys(row_elements(d, is_f32), is_f32)) < (int64_t(1) << 31);
 }
 
+// The smallest kernel that holds the group. bf16, 4 heads: 8 rows against 16, one request of 159 keys 5.7, 6.1 us, one of
+// 8k keys 9.3, 9.8 us, large batches within 1%. f32: 1, 4, 8 rows for one head, 33 requests with a window 28.1, 31.5, 38.9
+// us; 4, 8 rows for 4 heads, a large batch 237, 360 us. (The row's elements: d = 32 in 32, 64 a large batch 77.6, 94.6 us;
+// d = 64 in 64, 128 121, 137 us.)
 template <bool kF32, int kD>
 static cudaError_t launch_heads(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   const int group = p.h / p.hkv;
