@@ -146,6 +146,17 @@ def test_decode_split_lengths(lens, dtype, d):
     check(out, lse, *x, 0.125, 1500)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (F32, 32)])
+@pytest.mark.parametrize("h,h_kv", [(40, 1), (66, 2), (300, 1), (150, 1)])
+def test_decode_wide_groups(h, h_kv, dtype, d):
+    """Query heads of a K/V head dealt to neighbouring CTAs, and past 16 such blocks to further launches."""
+    import blockwise_exact_attention_gb300 as bea
+    x = make([2500, 0, 3, 700], h, h_kv, d, 16, dtype, seed=h)
+    out, lse = bea.paged_decode(*x, 0.15)
+    check(out, lse, *x, 0.15)
+    assert bea.device_status() == 0
+
+
 def test_decode_more_requests_than_one_pass_takes():
     import blockwise_exact_attention_gb300 as bea
     n = 5003
