@@ -17,6 +17,7 @@ from __future__ import annotations
 import concurrent.futures
 import glob
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -65,11 +66,15 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _cuda_home() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(nvcc()) or nvcc())))
+
+
 def _torch_paths() -> tuple[list[str], str]:
     import torch
     root = os.path.dirname(torch.__file__)
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+               sysconfig.get_paths()["include"], os.path.join(_cuda_home(), "include")]
     return ["-I" + i for i in include], os.path.join(root, "lib")
 
 
@@ -105,7 +110,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     tmp = BIND + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, binding, "-L" + HERE, "-l:libbea.so", "-Wl,-rpath,$ORIGIN", "-L" + _torch_paths()[1], "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L" + os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64"), "-lcudart"]
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L" + os.path.join(_cuda_home(), "lib64"), "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
