@@ -150,6 +150,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first 8 bits of a float, and two such as the bf16 numbers they are.
+__device__ __forceinline__ float bf16_cut(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16x2_cut(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
 // A row of kRows floats in shared memory, 16 bytes at a time where it can be.
 template <int kRows>
 __device__ __forceinline__ void store_rows(float* to, const float (&x)[kRows]) {
@@ -635,9 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kD / 8; ++i) o[i][2 * x] *= w, o[i][2 * x + 1] *= w;
           }
         }
-        // P as two bf16 terms: the first 8 bits truncated, the rest rounded (2^-15 of P left over, where one term
-        // would leave 2^-8). The second term is kept above 0, so that an infinite value stays infinite.
-        uint32_t hi[kSub][4] = {}, lo[kSub][4] = {};
+        // P as three bf16 terms of 8 bits each: all 24 of it, so that the product with V loses nothing of the weights.
+        // The last two are kept above 0 (by 2^-24 of P at most), so that an infinite value stays infinite.
+        uint32_t hi[kSub][4] = {}, mid[kSub][4] = {}, lo[kSub][4] = {};
 #pragma unroll
         for (int x = 0; x < kHalves; ++x) {
           const float ref = m[x] == -INFINITY ? 0.f : m[x];
@@ -645,11 +651,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int nb = 0; nb < 2 * kSub; ++nb) {
             const float p0 = ex2_approx(fmaf(s[nb][2 * x], a.sl2, -ref)), p1 = ex2_approx(fmaf(s[nb][2 * x + 1], a.sl2, -ref));
             l[x] += p0 + p1;
-            const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-            hi[nb / 2][(nb & 1) * 2 + x] = __byte_perm(u0, u1, 0x7632);
-            const float r0 = fmaxf(p0 - __uint_as_float(u0 & 0xFFFF0000u), p0 * 0x1p-20f);
-            const float r1 = fmaxf(p1 - __uint_as_float(u1 & 0xFFFF0000u), p1 * 0x1p-20f);
-            lo[nb / 2][(nb & 1) * 2 + x] = pack_bf16x2(r0, r1);
+            const float least0 = p0 * 0x1p-24f, least1 = p1 * 0x1p-24f;
+            const float r0 = fmaxf(p0 - bf16_cut(p0), least0), r1 = fmaxf(p1 - bf16_cut(p1), least1);
+            const float t0 = fmaxf(r0 - bf16_cut(r0), least0), t1 = fmaxf(r1 - bf16_cut(r1), least1);
+            hi[nb / 2][(nb & 1) * 2 + x] = pack_bf16x2_cut(p0, p1);
+            mid[nb / 2][(nb & 1) * 2 + x] = pack_bf16x2_cut(r0, r1);
+            lo[nb / 2][(nb & 1) * 2 + x] = pack_bf16x2_cut(t0, t1);
           }
         }
 #pragma unroll
@@ -661,6 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ldsm4_t(vt + vr * C::kRowBytes + ((chunk ^ C::swizzle(vr)) << 4), vf);
             mma_bf16(o[2 * dp], hi[u], vf[0], vf[1]);
             mma_bf16(o[2 * dp + 1], hi[u], vf[2], vf[3]);
+            mma_bf16(o[2 * dp], mid[u], vf[0], vf[1]);
+            mma_bf16(o[2 * dp + 1], mid[u], vf[2], vf[3]);
             mma_bf16(o[2 * dp], lo[u], vf[0], vf[1]);
             mma_bf16(o[2 * dp + 1], lo[u], vf[2], vf[3]);
           }
