@@ -659,19 +659,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             lo[nb / 2][(nb & 1) * 2 + x] = pack_bf16x2_cut(t0, t1);
           }
         }
+        // A tile's products are summed from 0, small terms first, and added to O in fp32: the tensor core cuts its sums
+        // off, which in one accumulator over all keys draws O towards 0 (48 requests of 16k-32k keys: fp32 output off by
+        // 2.5e-5 of its size, so by 4.5e-7, and by 3.3e-6 and 2.7e-7 for one of 130k keys). With up to 8 heads the middle
+        // terms take the rows 8-15 of the small terms' product, which no head has: 5% of the time where pages end inside
+        // a tile, else within 1% of two terms in one accumulator; three products instead were 1-7%, 15% there. With 16
+        // heads a product for each term: 1%, but 24% where two CTAs share a K/V head (97 -> 121 us): there mma.sync is
+        // the bound.
 #pragma unroll
         for (int dp = 0; dp < kD / 16; ++dp) {
+          uint32_t vf[kSub][4];
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
-            uint32_t vf[4];
             const int vr = u * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), chunk = 2 * dp + (lane >> 4);
-            ldsm4_t(vt + vr * C::kRowBytes + ((chunk ^ C::swizzle(vr)) << 4), vf);
-            mma_bf16(o[2 * dp], hi[u], vf[0], vf[1]);
-            mma_bf16(o[2 * dp + 1], hi[u], vf[2], vf[3]);
-            mma_bf16(o[2 * dp], mid[u], vf[0], vf[1]);
-            mma_bf16(o[2 * dp + 1], mid[u], vf[2], vf[3]);
-            mma_bf16(o[2 * dp], lo[u], vf[0], vf[1]);
-            mma_bf16(o[2 * dp + 1], lo[u], vf[2], vf[3]);
+            ldsm4_t(vt + vr * C::kRowBytes + ((chunk ^ C::swizzle(vr)) << 4), vf[u]);
+          }
+          float sum[2][4] = {};
+          if constexpr (kHalves == 2) {
+#pragma unroll
+            for (int term = 0; term < 3; ++term)
+#pragma unroll
+              for (int u = 0; u < kSub; ++u) {
+                const uint32_t(&w)[4] = term == 0 ? lo[u] : term == 1 ? mid[u] : hi[u];
+                mma_bf16(sum[0], w, vf[u][0], vf[u][1]);
+                mma_bf16(sum[1], w, vf[u][2], vf[u][3]);
+              }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[2 * dp][x] += sum[0][x], o[2 * dp + 1][x] += sum[1][x];
+          } else {  // the middle terms take the rows 8-15, which no head has
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+              const uint32_t w[4] = {lo[u][0], mid[u][0], lo[u][2], mid[u][2]};
+              mma_bf16(sum[0], w, vf[u][0], vf[u][1]);
+              mma_bf16(sum[1], w, vf[u][2], vf[u][3]);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) sum[z][x] += sum[z][x + 2], sum[z][x + 2] = 0.f;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+              mma_bf16(sum[0], hi[u], vf[u][0], vf[u][1]);
+              mma_bf16(sum[1], hi[u], vf[u][2], vf[u][3]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) o[2 * dp][x] += sum[0][x], o[2 * dp + 1][x] += sum[1][x];
           }
         }
         __syncwarp();

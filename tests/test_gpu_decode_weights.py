@@ -105,3 +105,30 @@ def test_many_requests_some_of_them_cut():
     le = np.abs(lse.double().cpu().numpy() - ref_lse)[some]
     assert (le <= (e + length + u * np.abs(ref_lse))[some]).all()
     assert torch.isneginf(lse[torch.from_numpy(~some).cuda()]).all() and bea.device_status() == 0
+
+
+@pytest.mark.parametrize("h,d", [(1, 64), (2, 128), (9, 128), (16, 64)])
+def test_long_sums_keep_their_last_bits(h, d):
+    """18 million keys of value 1 (requests that share their pages for reading), so that each warp of a GPU of 152 SMs
+    adds up some 500 tiles. The output is 1; off by what sums of that length lose where each addition rounds to nearest:
+    with N additions of equal numbers, the k-th at most 2^-24 k / N of the sum and as often up as down, one standard
+    deviation is 2^-24 sqrt(N) / 3. N is 500 above and 2000 in each of four parts below, together 2^-24 * 11; six of
+    these are 2^-18. A tile's products, which the tensor core may cut off, add three units of 2^-23 at most, the
+    terms of a weight 2^-23, the merges 2^-21."""
+    import blockwise_exact_attention_gb300 as bea
+    page, pages = 64, 32
+    n, width = 560, (512 if d == 64 else 256)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(h)
+    k = torch.zeros((pages, page, 1, d), dtype=BF16, device="cuda")
+    k[..., 0] = -torch.rand((pages, page, 1), device="cuda", generator=g).to(BF16)
+    v = torch.ones_like(k)
+    q = torch.zeros((n, 1, h, d), dtype=BF16, device="cuda")
+    q[..., 0] = 1
+    table = (torch.arange(width, device="cuda") % pages).to(I32).expand(n, width).contiguous()
+    lens = torch.full((n,), width * page, dtype=I32, device="cuda")
+    out, lse = bea.paged_decode(q, k, v, table, lens, 1.0, out_dtype=F32)
+    assert (out.double() - 1).abs().max() <= 2 ** -18 + 4 * 2 ** -23 + 2 ** -21
+    ref = torch.log(torch.exp(k[..., 0].double()).sum() * (width // pages))
+    # the same below, the exponentials' 2^-22 and 2^-23 of their exponents; lse itself, up to 11, in fp32
+    assert (lse.double() - ref).abs().max() <= 2 ** -18 + 2 ** -21 + 2 ** -21 + 11 * 2 ** -22
