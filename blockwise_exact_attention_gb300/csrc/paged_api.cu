@@ -95,10 +95,11 @@ int bea_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* po
   std::memset(&p, 0, sizeof(p));
   for (int i = 0; i < d / 2; ++i) {
     if (axis_of_pair[i] < 0 || axis_of_pair[i] >= axes || !std::isfinite(freq[i])) return BEA_ERR_ARG;
-    // The fraction of a turn as a 64-bit fixed-point number. Below 0 the difference can round up to 1: a whole turn.
-    const double turns = freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    const double fraction = turns - std::floor(turns);
-    p.turn[i] = fraction < 1.0 ? static_cast<uint64_t>(fraction * 0x1p64) : 0;
+    // The fraction of a turn as a 64-bit fixed-point number, rounded; of a negative one's size, which loses no bits where
+    // it is small. It is at most 1 - 2^-53, so its product is below 2^64.
+    const double turns = std::fabs(freq[i]) * 0.15915494309189533577;  // 1 / (2 pi)
+    const uint64_t step = static_cast<uint64_t>(std::nearbyint((turns - std::floor(turns)) * 0x1p64));
+    p.turn[i] = freq[i] < 0 ? 0 - step : step;
     p.axis[i] = static_cast<uint8_t>(axis_of_pair[i]);
   }
   p.n = (int)q->shape[0];

@@ -340,9 +340,12 @@ int bea_ring_merge(const bea_tensor* out_acc, const bea_tensor* lse_acc, const b
  *              Each may be its input itself (same pointer, same strides), and
  *              must not overlap the inputs otherwise; not broadcast.
  *   d: bf16 a multiple of 16, f32 a multiple of 8, at most 256.
- * The angle is reduced modulo a whole turn in 64-bit integer arithmetic, so a
- * far position loses nothing: it is off by at most |position| * 2^-53 times
- * the frequency's whole turns, as in fp64. Products in fp32, one rounding.
+ * The angle is reduced modulo a whole turn in 64-bit fixed point, with the turns
+ * per position held as a multiple of 2^-64: it is off by at most |position| *
+ * (2^-65 + 2^-52 * |freq| / (2 pi)) turns, so a far position loses next to
+ * nothing. Less its nearest quarter turn it is rounded to fp32, off by at most
+ * 2^-28 turns. Cosine and sine are then within 2^-23.5 of the true ones; products
+ * in fp32, one rounding.
  */
 int bea_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* positions, const int32_t* axis_of_pair,
                   const double* freq, int inverse, const bea_tensor* q_out, const bea_tensor* k_out, void* stream);

@@ -1,9 +1,10 @@
 """The angles of rope_axes, and its kernels for many heads and many rows.
 
 u = 1, v = 0 turn to (cos, sin) as the kernel has them. The angle less its nearest quarter turn is at most a quarter of
-a half turn, so rounding it to fp32 is off by at most 2^-27 half turns, 2^-25.3 radians; sincospif is good to one unit
-in the last place, 2^-24 of values below 1; the fixed-point step is off by 2^-65 turns and 2^-52 of itself, which the
-positions here keep below 2^-30 with the oracle's own rounding: 2^-24 + 2^-25.3 + 2^-30 < 2^-23.5 in all."""
+a half turn, so rounding it to fp32 is off by at most 2^-27 half turns, 2^-25.34 radians, and its 32 bits before that by
+2^-31.3 radians; sincospif is good to one unit in the last place, 2^-24 of values below 1; the fixed-point step is off by
+2^-65 turns and 2^-52 of itself, which the positions here keep below 2^-36 with the oracle's own rounding: 2^-24 +
+2^-25.34 + 2^-31.3 + 2^-36 < 2^-23.5 in all."""
 
 import numpy as np
 import pytest
@@ -44,26 +45,46 @@ def test_cosines_and_sines(base, inverse):
     assert (y[0, 0, 0, :d // 2] == 1).all() and (y[0, 0, 0, d // 2:] == 0).all()     # position 0 turns nothing
 
 
-def test_whole_quarters_are_exact():
-    """Steps of an eighth of a turn: cosines and sines of the quarters without an error."""
-    import math
+def turned(pos, freqs, inverse=0):
+    """(cos, sin) of every position (rows) by every frequency, from the C entry point."""
     import ctypes
     import blockwise_exact_attention_gb300 as bea
     from blockwise_exact_attention_gb300 import _lib
-    x = torch.zeros((1, 17, 1, 8), dtype=F32, device="cuda")
-    x[..., :4] = 1
+    m, half = len(pos), len(freqs)
+    x = torch.zeros((1, m, 1, 2 * half), dtype=F32, device="cuda")
+    x[..., :half] = 1
     y = torch.empty_like(x)
-    pos = torch.arange(-8, 9, dtype=I32, device="cuda")[None, None]
+    p = torch.tensor(pos, dtype=I32, device="cuda")[None, None]
     t = lambda z, code: _lib.describe(z.data_ptr(), code, z.shape, z.stride())  # noqa: E731
-    # pi / 4 as a double is an eighth of a turn within 2^-54: its fixed-point step is exact
-    freq, axis = (ctypes.c_double * 4)(*[math.pi / 4] * 4), (ctypes.c_int32 * 4)()
-    rc = _lib.load().bea_rope_axes(t(x, 1), None, t(pos, 2), axis, freq, 0, t(y, 1), None,
-                                   torch.cuda.current_stream().cuda_stream)
+    rc = _lib.load().bea_rope_axes(t(x, 1), None, t(p, 2), (ctypes.c_int32 * half)(), (ctypes.c_double * half)(*freqs), inverse,
+                                   t(y, 1), None, torch.cuda.current_stream().cuda_stream)
     assert rc == 0 and bea.device_status() == 0
-    for i, p in enumerate(range(-8, 9)):
-        if p % 2 == 0:
-            c, s = [(1, 0), (0, 1), (-1, 0), (0, -1)][p // 2 % 4]
-            assert (y[0, i, 0, :4] == c).all() and (y[0, i, 0, 4:] == s).all(), p
+    y = y[0, :, 0].double().cpu().numpy()
+    return y[:, :half], y[:, half:]
+
+
+def test_whole_quarters_are_exact():
+    """Steps of an eighth of a turn (pi / 4 as a double is one within 2^-54: its fixed-point step is exact): cosines and
+    sines of the quarters without an error."""
+    for sign in (1, -1):
+        for inverse in (0, 1):
+            c, s = turned(range(-8, 9), [sign * np.pi / 4] * 4, inverse)
+            for i, p in enumerate(range(-8, 9)):
+                if p % 2 == 0:
+                    want = [(1, 0), (0, 1), (-1, 0), (0, -1)][p // 2 * sign * (-1) ** inverse % 4]
+                    assert (c[i] == want[0]).all() and (s[i] == want[1]).all(), p
+
+
+def test_small_frequencies_of_either_sign_at_far_positions():
+    """At 2^31 the fixed-point step's 2^-65 turns are 2^-31.3 radians, 2^-52 of an angle below 2^21 are 2^-31, and the fp64
+    product below is off by 2^-32: with the 2^-23.5 above less than 2^-23.4 in all."""
+    freqs = [1e-3, 1e-5, 3e-7, 2.0 ** -40] + [-1e-3, -1e-5, -3e-7, -2.0 ** -40]
+    pos = [2 ** 31 - 1, -(2 ** 31), 2 ** 30 + 12345, -123456789, 1, -1, 0]
+    ang = np.array(pos, dtype=np.float64)[:, None] * np.array(freqs)
+    for inverse in (0, 1):
+        c, s = turned(pos, freqs, inverse)
+        assert np.abs(c - np.cos(ang)).max() <= 2 ** -23.4
+        assert np.abs(s - np.sin(ang) * (-1) ** inverse).max() <= 2 ** -23.4
 
 
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 64), (BF16, 80), (F32, 24)])
@@ -135,16 +156,3 @@ def test_write_of_more_pieces_than_32_bits_count():
         hit[list(to.values())] = True
         assert (flat[hit] == new[0, 0]).all() and not flat[~hit].any()
     assert bea.device_status() == 0
-
-
-def test_a_gradient_with_a_pending_negation():
-    """Autograd may hand over a view whose negation is pending (the imaginary part of a conjugate)."""
-    import blockwise_exact_attention_gb300 as bea
-    q = draw((1, 5, 2, 16), F32, 6).requires_grad_()
-    p = torch.arange(5, dtype=I32, device="cuda")[None, None]
-    g = draw((1, 5, 2, 16), F32, 7)
-    (dq,) = torch.autograd.grad(bea.rotary_axes(q, None, p, (8,))[0], q, torch._neg_view(g))
-    assert torch.equal(dq, bea.rope_axes(-g, None, p, (8,), inverse=True)[0])
-    k = draw((1, 5, 1, 16), F32, 8).requires_grad_()
-    dq, dk = torch.autograd.grad(bea.rotary_axes(q, k, p, (8,)), (q, k), (g, torch._neg_view(g[:, :, :1])))
-    assert torch.equal(dk, bea.rope_axes(-g[:, :, :1], None, p, (8,), inverse=True)[0])
