@@ -177,9 +177,9 @@ struct RotaryBackward : public Node {
     positions.reset_data();
   }
 
-  // A gradient that autograd hands over may be of another dtype, expanded or not aligned.
+  // A gradient that autograd hands over may be of another dtype, expanded, not aligned or yet to be negated.
   Tensor ready(const Tensor& g) const {
-    Tensor x = g.scalar_type() == dtype ? g : g.to(dtype);
+    Tensor x = (g.scalar_type() == dtype ? g : g.to(dtype)).resolve_neg();
     bool fits = reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0 && x.stride(-1) == 1;
     for (int64_t i = 0; i + 1 < x.dim(); ++i) fits = fits && x.stride(i) * x.element_size() % 16 == 0;
     return fits ? x : x.clone(at::MemoryFormat::Contiguous);

@@ -156,3 +156,16 @@ def test_write_of_more_pieces_than_32_bits_count():
         hit[list(to.values())] = True
         assert (flat[hit] == new[0, 0]).all() and not flat[~hit].any()
     assert bea.device_status() == 0
+
+
+def test_a_gradient_with_a_pending_negation():
+    """Autograd may hand over a view whose negation is pending (the imaginary part of a conjugate)."""
+    import blockwise_exact_attention_gb300 as bea
+    q = draw((1, 5, 2, 16), F32, 6).requires_grad_()
+    p = torch.arange(5, dtype=I32, device="cuda")[None, None]
+    g = draw((1, 5, 2, 16), F32, 7)
+    (dq,) = torch.autograd.grad(bea.rotary_axes(q, None, p, (8,))[0], q, torch._neg_view(g))
+    assert torch.equal(dq, bea.rope_axes(-g, None, p, (8,), inverse=True)[0])
+    k = draw((1, 5, 1, 16), F32, 8).requires_grad_()
+    dq, dk = torch.autograd.grad(bea.rotary_axes(q, k, p, (8,)), (q, k), (g, torch._neg_view(g[:, :, :1])))
+    assert torch.equal(dk, bea.rope_axes(-g[:, :, :1], None, p, (8,), inverse=True)[0])
