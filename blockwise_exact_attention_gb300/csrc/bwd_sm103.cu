@@ -464,8 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the next kernel on the stream may start as soon as every CTA of this one is running
-  grid_launch_dependents();
+  // the next kernel on the stream may start as soon as every CTA of this one is running, where the last bulk writes
+  // below are then waited for in full
+  if (p.pdl_next) grid_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   // TMEM slot h: S_h^T at 128h (then P^T / dS^T, 16 + 16 columns per key warpgroup), dP_h^T / dQ_h^T at 128h + 64
   const uint32_t T_DP = 64, T_DV = 256, T_DK = 384;
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (rows past the last key are not touched)
           for (int x = 0; x < D / 32; ++x) tma_reduce_add_4d(tmap, stage + x * 16384, 32 * x, kvh, sc.k0, b);
           bulk_commit_group();
-          // (a launch that depends on this one programmatically also needs the additions done)
+          // (a launch let in early also needs the additions done; any other starts after this one's end, additions included)
           if (p.pdl_next) bulk_wait_group_all();
           else bulk_wait_group_read_all();
         }

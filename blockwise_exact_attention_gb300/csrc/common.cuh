@@ -77,7 +77,7 @@ struct FwdParams {
   Seq4 fin;   // merge only: bf16 copy of the merged rows, ptr may be null
   int fin_b0, fin_b1;  // merge only: fin is written for batch indices [fin_b0, fin_b1) only
   int pdl;    // launch with programmatic stream serialisation (see grid_dependency_wait)
-  int pdl_next;  // the next launch on the stream depends on this one programmatically
+  int pdl_next;  // let the next launch on the stream start early: it depends on this one programmatically
   uint32_t* status;
   int inject_abort;  // test hook, 0 = off: CTA 0's MMA warp aborts at tile inject_abort - 1
 };
@@ -100,7 +100,7 @@ struct BwdParams {
   float* lse2;    // workspace: [n, h, lq_pad] lse * log2(e), +inf for rows without keys / padding
   int lq_pad;
   int pdl;        // launch with programmatic stream serialisation (see grid_dependency_wait)
-  int pdl_next;   // the next launch on the stream depends on this one programmatically
+  int pdl_next;   // let the next launch on the stream start early: it depends on this one programmatically
   uint32_t* status;
   int inject_abort;  // test hook, 0 = off: CTA 0's MMA warp aborts at iteration inject_abort - 1
 };

@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the next kernel on the stream may start as soon as every CTA of this one is running
-  grid_launch_dependents();
+  // the next kernel on the stream may start as soon as every CTA of this one is running, where the last bulk writes
+  // below are then waited for in full
+  if (p.pdl_next) grid_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   // Fused ring step: subtile t's accumulator rows are staged in the K (t = 0) or V (t = 1)
   // stages, taken in the order their last tiles release them: stage i of the accumulator (boxes
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && r == 0) {
             for (int c = 0; c < D / 64; ++c) tma_store_4d(&tfin, stage + c * 16384, 64 * c, hq, qs, b);
             bulk_commit_group();
-            // (a launch that depends on this one programmatically also needs the writes done)
+            // (a launch let in early also needs the writes done; any other starts after this one's end, writes included)
             if (p.pdl_next) bulk_wait_group_all();
             else bulk_wait_group_read_all();
           }

@@ -173,7 +173,7 @@ __device__ __forceinline__ void tma_reduce_add_4d(const CUtensorMap* map, const 
 }
 __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until every committed bulk group of this thread has completed (its global writes included):
-// needed where a programmatically dependent launch may start before this grid has completed.
+// needed where this kernel lets a dependent launch start early (grid_launch_dependents).
 __device__ __forceinline__ void bulk_wait_group_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Wait until every committed bulk group of this thread has read its shared-memory source; the
 // global writes complete with the grid, before any stream-ordered successor starts.
@@ -206,7 +206,11 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes
 // serialisation may start while the kernel before it on the stream is still
 // running; it must call grid_dependency_wait() before it reads anything that
 // kernel writes or writes anything that kernel reads or writes. Both are
-// no-ops for a kernel launched the ordinary way.
+// no-ops for a kernel launched the ordinary way. What stands before it may be
+// any kernel of this library. So one that calls grid_launch_dependents() also
+// waits for its bulk writes in full (bulk_wait_group_all); one that ends with
+// bulk_wait_group_read_all() does not call it, and the next kernel then starts
+// when all of its CTAs have ended, and waits for its completion.
 // This CTA lets the next kernel on the stream start (once every CTA has said so or exited).
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
