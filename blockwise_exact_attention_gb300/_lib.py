@@ -9,6 +9,7 @@ kernels. The library is loaded on first use and a missing build raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -86,10 +87,21 @@ def bind():
     global _BIND
     if _BIND is None:
         load()
-        from . import _bind
-        _bind.setup(check)
-        _BIND = _bind
+        from . import build
+        if not os.path.exists(build.BIND):
+            raise RuntimeError(f"the Python binding {build.BIND} is not built; run `python -m {__package__}.build`, "
+                               "which says why where it cannot be")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._bind", build.BIND)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.setup(check)
+        _BIND = module
     return _BIND
+
+
+def bound_launches(reset: bool) -> int:
+    """Kernels that the binding launched since its last reset: none where it has not been loaded."""
+    return 0 if _BIND is None else _BIND.launches(reset)
 
 
 def load() -> ctypes.CDLL:

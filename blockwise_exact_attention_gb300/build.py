@@ -9,7 +9,9 @@ library.
 
 ``csrc/binding.cpp``, the Python binding of the short calls, is compiled by the
 host compiler against torch's headers (in parallel with the CUDA units) and
-linked into ``_bind.so``, which finds libbea.so next to itself.
+linked into ``_bind.so``, which finds libbea.so next to itself. The library does
+not need it: where it cannot be built, that is said on stderr, libbea.so is there
+all the same, and only the calls that go through the binding raise.
 """
 
 from __future__ import annotations
@@ -46,15 +48,25 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+def _headers():
+    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+        os.path.join(ROOT, "include", "*.h"))
+
+
+def _newer(target: str, files) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in files)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + _headers() + [__file__])
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BIND, [BIND_SRC] + _headers() + [__file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    return all(os.path.getmtime(f) <= t for f in _deps() + [__file__])
+    return library_up_to_date() and binding_up_to_date()
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -64,6 +76,10 @@ def _compile(src: str) -> tuple[str, str]:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
     return obj, r.stderr
+
+
+def _host_compiler() -> list[str]:
+    return ["g++"]
 
 
 def _cuda_home() -> str:
@@ -81,40 +97,50 @@ def _torch_paths() -> tuple[list[str], str]:
 def _compile_binding() -> str:
     obj = os.path.join(BUILD, "binding.o")
     include, _ = _torch_paths()
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *include, "-c", BIND_SRC, "-o", obj]
+    cmd = [*_host_compiler(), "-O2", "-std=c++17", "-fPIC", *include, "-c", BIND_SRC, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
     return obj
 
 
+def _link(cmd: list[str], target: str) -> None:
+    """Run a link command that writes `target`.tmp and put the result in place."""
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(target + ".tmp", target)
+
+
+def _link_binding(obj: str) -> None:
+    _link([*_host_compiler(), "-shared", "-o", BIND + ".tmp", obj, "-L" + os.path.dirname(LIB), "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN", "-L" + _torch_paths()[1], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python", "-L" + os.path.join(_cuda_home(), "lib64"), "-lcudart"], BIND)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libbea.so; returns its path."""
-    if not force and up_to_date():
+    """Compile and link libbea.so, and the binding where that can be done; returns the library's path."""
+    library, binding = force or not library_up_to_date(), force or not binding_up_to_date()
+    if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    if binding and os.path.exists(BIND):
+        os.remove(BIND)  # of other sources: not to be loaded if this build fails
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(_sources()) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        results = list(ex.map(_compile, _sources()))
-        binding = binding.result()
-    log = "".join(err for _obj, err in results)
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        f.write(log)
-    if verbose:
-        sys.stderr.write(log)
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = BIND + ".tmp"
-    cmd = ["g++", "-shared", "-o", tmp, binding, "-L" + HERE, "-l:libbea.so", "-Wl,-rpath,$ORIGIN", "-L" + _torch_paths()[1], "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L" + os.path.join(_cuda_home(), "lib64"), "-lcudart"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND)
+        bind_obj = ex.submit(_compile_binding) if binding else None
+        results = list(ex.map(_compile, _sources())) if library else []
+    if library:
+        log = "".join(err for _obj, err in results)
+        with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+            f.write(log)
+        if verbose:
+            sys.stderr.write(log)
+        _link([nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *[o for o, _ in results]], LIB)
+    if binding:
+        try:
+            _link_binding(bind_obj.result())
+        except Exception as e:  # no torch, no host compiler, an error of either: the library stands without it
+            sys.stderr.write(f"the Python binding of the rotary and paged calls was not built: {e}\n")
     return LIB
 
 

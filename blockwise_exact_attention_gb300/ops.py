@@ -23,7 +23,7 @@ _launches = 0  # kernels launched through this module since the last reset (the 
 
 def launches_since_reset(reset: bool = False) -> int:
     global _launches
-    n = _launches + _lib.bind().launches(reset)
+    n = _launches + _lib.bound_launches(reset)
     if reset:
         _launches = 0
     return n
