@@ -91,6 +91,10 @@ def bind():
         if not os.path.exists(build.BIND):
             raise RuntimeError(f"the Python binding {build.BIND} is not built; run `python -m {__package__}.build`, "
                                "which says why where it cannot be")
+        of, here = build.built_binding_stamp(), build.binding_stamp()
+        if of != here:
+            raise RuntimeError(f"the Python binding {build.BIND} was built for {of}, this is {here}; run "
+                               f"`python -m {__package__}.build`")
         spec = importlib.util.spec_from_file_location(f"{__package__}._bind", build.BIND)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -11,7 +11,9 @@ library.
 host compiler against torch's headers (in parallel with the CUDA units) and
 linked into ``_bind.so``, which finds libbea.so next to itself. The library does
 not need it: where it cannot be built, that is said on stderr, libbea.so is there
-all the same, and only the calls that go through the binding raise.
+all the same, and only the calls that go through the binding raise. Beside it
+stands what it was built for (torch, Python, flags): one built for another is
+neither loaded nor taken for up to date.
 """
 
 from __future__ import annotations
@@ -31,6 +33,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbea.so")
 BIND_SRC = os.path.join(CSRC, "binding.cpp")
 BIND = os.path.join(HERE, "_bind.so")
+BINDING_FLAGS = ["-O2", "-std=c++17", "-fPIC"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -61,8 +64,29 @@ def library_up_to_date() -> bool:
     return _newer(LIB, _sources() + _headers() + [__file__])
 
 
+def binding_stamp() -> str:
+    """What a binding built now is built for: it uses torch's and Python's C++ objects as they lie in memory."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}, {' '.join(_host_compiler() + BINDING_FLAGS)}"
+
+
+def _stamp_path() -> str:
+    return os.path.join(BUILD, os.path.basename(BIND) + ".stamp")
+
+
+def built_binding_stamp() -> str | None:
+    """What the binding that is there was built for."""
+    if not os.path.exists(BIND) or not os.path.exists(_stamp_path()):
+        return None
+    with open(_stamp_path()) as f:
+        return f.read()
+
+
 def binding_up_to_date() -> bool:
-    return _newer(BIND, [BIND_SRC] + _headers() + [__file__])
+    try:
+        return _newer(BIND, [BIND_SRC] + _headers() + [__file__]) and built_binding_stamp() == binding_stamp()
+    except ImportError:
+        return False
 
 
 def up_to_date() -> bool:
@@ -97,7 +121,7 @@ def _torch_paths() -> tuple[list[str], str]:
 def _compile_binding() -> str:
     obj = os.path.join(BUILD, "binding.o")
     include, _ = _torch_paths()
-    cmd = [*_host_compiler(), "-O2", "-std=c++17", "-fPIC", *include, "-c", BIND_SRC, "-o", obj]
+    cmd = [*_host_compiler(), *BINDING_FLAGS, *include, "-c", BIND_SRC, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
@@ -113,6 +137,8 @@ def _link(cmd: list[str], target: str) -> None:
 
 
 def _link_binding(obj: str) -> None:
+    with open(_stamp_path(), "w") as f:
+        f.write(binding_stamp())
     _link([*_host_compiler(), "-shared", "-o", BIND + ".tmp", obj, "-L" + os.path.dirname(LIB), "-l:" + os.path.basename(LIB),
            "-Wl,-rpath,$ORIGIN", "-L" + _torch_paths()[1], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch_python", "-L" + os.path.join(_cuda_home(), "lib64"), "-lcudart"], BIND)

@@ -84,3 +84,30 @@ def test_a_missing_binding_is_an_error_that_names_it(monkeypatch, tmp_path):
     monkeypatch.setattr(build, "BIND", str(tmp_path / "_bind.so"))
     with pytest.raises(RuntimeError, match="binding"):
         _lib.bind()
+
+
+def test_a_binding_of_another_torch_or_python_is_built_anew(monkeypatch):
+    import sysconfig
+    import torch
+    build.build()
+    assert build.binding_up_to_date() and build.up_to_date()
+    of = build.binding_stamp()
+    assert torch.__version__ in of and sysconfig.get_config_var("SOABI") in of
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0.0")
+        assert not build.binding_up_to_date() and not build.up_to_date() and build.library_up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(build, "BINDING_FLAGS", ["-O0"])
+        assert not build.binding_up_to_date()
+    assert build.binding_up_to_date()
+
+
+def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
+    import torch
+    build.build()
+    monkeypatch.setattr(_lib, "_BIND", None)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0.0")
+        with pytest.raises(RuntimeError, match="1.0.0"):
+            _lib.bind()
+    _lib.bind()
