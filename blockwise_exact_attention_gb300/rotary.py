@@ -15,9 +15,14 @@ import struct
 from . import _lib
 
 
-@functools.lru_cache(maxsize=128)
 def _table(sections: tuple, base: float, spectrum: str, d: int) -> tuple[bytes, bytes, int]:
     """(axis, frequency) of every pair, as the int32 and double arrays the library reads, and the number of axes."""
+    return _built_table(sections, (*map(type, sections),), base, spectrum, d)
+
+
+# To a cache 16.0 is 16, so the arguments' types are part of its key.
+@functools.lru_cache(maxsize=128, typed=True)
+def _built_table(sections: tuple, types: tuple, base: float, spectrum: str, d: int) -> tuple[bytes, bytes, int]:
     half = d // 2
     if not all(isinstance(s, int) and s >= 0 for s in sections) or sum(sections) != half:
         raise ValueError(f"sections {sections} are not numbers of pairs that sum to d / 2 = {half}")
