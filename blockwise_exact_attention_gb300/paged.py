@@ -35,7 +35,9 @@ def paged_plan(lens, new_lens, block_table, free_pages, n_free, page_size, capac
     ``free_pages`` (height ``n_free`` [1]) are updated in place; ``lens`` and
     ``n_free`` are not, unless ``out`` (a PagedPlan) holds them as its own.
     ``capacity``: places for added tokens. A step that cannot be done in full
-    changes nothing and is reported by ``device_status``."""
+    changes nothing and is reported by ``device_status``. Every page is taken to
+    be owned by one row: all pages of a row that ends go on the stack, also those
+    that another row shares for reading, which the caller has to prevent."""
     return PagedPlan._make(_lib.bind().paged_plan(lens, new_lens, block_table, free_pages, n_free, page_size, capacity, out))
 
 

@@ -357,7 +357,11 @@ int bea_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* po
  * ceil(len_r / page_size)), and its token at position p lives in page
  * block_table[r, p / page_size] at offset p % page_size; its SLOT is page *
  * page_size + offset. Free pages are a stack: free_pages[0 .. n_free), the top
- * at n_free - 1. Pages may be shared between rows of a table for reading.
+ * at n_free - 1. For reading (bea_paged_decode) pages may be shared between rows
+ * of a table. bea_paged_plan takes every page to be owned by one row: it does
+ * not count owners, so a row whose pages another row shares has to be kept from
+ * ending (or the shared entries taken out of one of the two) by the caller, and
+ * a row may not add tokens to a last page that it shares.
  *
  * What the device finds out of range (a length beyond the table, a page or a
  * slot outside the cache) is never accessed: it is left out as described at
