@@ -889,6 +889,8 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   // Requests per launch: their tiles and unit costs have to stay countable in 31 bits.
   int64_t at_once = ((int64_t(1) << 31) - 1) / request_cost(keys, p.hkv, C::kKeys);
   if (at_once > kMaxRequests) at_once = kMaxRequests;
+  // Of a launch, so that a plane keeps CTAs enough to cut its work among. 300 heads to a K/V head, 16 requests of 4k-8k
+  // keys: 155 us; 8: 161, 4: 183, 32: 136 us.
   constexpr int kMaxPlanes = 16;
   for (a.head0 = 0; a.head0 < group; a.head0 += kMaxPlanes * C::kRows) {
     const int left = (group - a.head0 + C::kRows - 1) / C::kRows;

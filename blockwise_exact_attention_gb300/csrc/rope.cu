@@ -32,7 +32,7 @@ namespace bea {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kFull = 152 * 2048;  // threads that fill the GPU
+constexpr int kSmThreads = 2048;  // that an SM holds
 
 template <bool kF32>
 struct Piece;  // 16 bytes of a row as fp32 values
@@ -151,7 +151,10 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t s, int* nlaunch) {
   const int64_t pieces = p.d / 2 / (p.is_f32 ? 4 : 8), tokens = (int64_t)p.n * p.l;
   auto threads = [&](int heads) { return tokens * ((p.hq + p.hk + heads - 1) / heads) * pieces; };
   if (threads(1) == 0) return cudaSuccess;
-  const bool wide = threads(8) >= kFull;
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const bool wide = threads(8) >= (int64_t)sms * kSmThreads;  // enough to fill the GPU
   const int64_t total = threads(wide ? 8 : 4);
   int64_t blocks = (total + kThreads - 1) / kThreads;
   if (blocks > (int64_t(1) << 30)) blocks = int64_t(1) << 30;  // the kernel strides over the rest
@@ -165,7 +168,7 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t s, int* nlaunch) {
   using Eight = std::integral_constant<int, 8>;
   auto kern = p.is_f32 ? (wide ? pick(std::true_type{}, Eight{}) : pick(std::true_type{}, Four{}))
                        : (wide ? pick(std::false_type{}, Eight{}) : pick(std::false_type{}, Four{}));
-  const cudaError_t e = launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, s, p);
+  e = launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }
