@@ -4,8 +4,9 @@
 // Argument marshalling only, like the ctypes binding of the other calls: torch
 // tensors are described to libbea.so's C entry points by pointer, dtype, shape
 // and strides, outputs that are not given are allocated, a status code becomes
-// the package's error. Described from C++, a call costs the host 2.2-5.5 us
-// instead of 12-25 us, and the rotation's gradient is a C++ node, so that a
+// the package's error. Described from C++, a call costs the host 2.3 us
+// (paged_write), 4.7 (paged_decode), 5.7 (paged_plan) and 5.9 (rope_axes), 2.7-3.7
+// us where its outputs are given, instead of 12-25 us, and the rotation's gradient is a C++ node, so that a
 // backward pass does not enter the interpreter.
 #include <Python.h>
 

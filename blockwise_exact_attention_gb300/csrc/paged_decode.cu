@@ -6,7 +6,8 @@
 // against 4 d g flops, g = h / h_kv query heads reading the same key. At 7 TB/s
 // that is 28 TFLOP/s for g = 8 in bf16: too much for the CUDA cores beside the
 // conversions, little for mma.sync with its 16 rows (112 TFLOP/s with the empty
-// ones, of which the loop keeps a quarter of the issue slots busy). A tcgen05
+// ones; with the weights in three terms the tensor pipe is a quarter and the issue
+// slots a third busy). A tcgen05
 // product has 64 rows at least, which 8 heads would leave empty, and its operands
 // would have to meet in shared memory CTA-wide; here a warp goes through its keys
 // alone. fp32 inputs stay exact: CUDA cores.
@@ -33,11 +34,11 @@
 // memory does not matter.
 //
 // Measured (GPU time, three sets of inputs in turn): 48 requests of 16k-32k keys,
-// 32 / 8 heads of 128, bf16: 680-702 us, 6.9-7.1 TB/s (a copy reaches 6.8); one of
-// 130k keys 83-85 us, 6.4 TB/s; 64 requests of 1-8192 keys 59-60 us, 5.7 TB/s: 2.5
-// us pass before the first load is sent (the lengths, their scan, the page table)
-// and 5 at the end (the longest warp, the merge, the join); one request of 159
-// keys 5.9 us, all of it latency.
+// 32 / 8 heads of 128, bf16: 682-704 us, 6.8-7.1 TB/s (a copy reaches 6.8); one of
+// 130k keys 83-85 us, 6.3-6.4 TB/s; 64 requests of 1-8192 keys 59-60 us, 5.7 TB/s:
+// 2.5 us pass before the first load is sent (the lengths, their scan, the page
+// table) and 5 at the end (the longest warp, the merge, the join); one request of
+// 159 keys 5.7 us, all of it latency.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -664,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 2.5e-5 of its size, so by 4.5e-7, and by 3.3e-6 and 2.7e-7 for one of 130k keys). With up to 8 heads the middle
         // terms take the rows 8-15 of the small terms' product, which no head has: 5% of the time where pages end inside
         // a tile, else within 1% of two terms in one accumulator; three products instead were 1-7%, 15% there. With 16
-        // heads a product for each term: 1%, but 24% where two CTAs share a K/V head (97 -> 121 us): there mma.sync is
-        // the bound.
+        // heads a product for each term: 1%, but 24% where two CTAs share a K/V head (97 -> 121 us) and a warp's own chain
+        // of products is the bound (no wait for memory, the tensor pipe 38% busy).
 #pragma unroll
         for (int dp = 0; dp < kD / 16; ++dp) {
           uint32_t vf[kSub][4];

@@ -17,8 +17,8 @@
 // cosines and sines while they are under way, turns and stores. With 8 heads the
 // cosines and sines cost half as much and the stores are streamed past L2: 206 us
 // for forward and gradient of [1, 32768, 32 + 8, 128] bf16 against 229 us with 4
-// (now 204 us, 6.6 TB/s). Where 8 heads would leave the GPU's threads unfilled it
-// takes 4: 17.0 against 22.4 us for [3, 1369, 12 + 12, 64] f32 (now 16 us), 4.3
+// (now 203 us, 6.6 TB/s). Where 8 heads would leave the GPU's threads unfilled it
+// takes 4: 17.0 against 22.4 us for [3, 1369, 12 + 12, 64] f32 (now 17.3 us), 4.3
 // against 5.5 us for 256 tokens of 32 + 8 heads (now 3.0 us).
 #include <type_traits>
 
