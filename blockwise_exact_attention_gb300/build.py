@@ -71,7 +71,7 @@ def binding_stamp() -> str:
 
 
 def _stamp_path() -> str:
-    return os.path.join(BUILD, os.path.basename(BIND) + ".stamp")
+    return BIND + ".stamp"
 
 
 def built_binding_stamp() -> str | None:
@@ -137,11 +137,11 @@ def _link(cmd: list[str], target: str) -> None:
 
 
 def _link_binding(obj: str) -> None:
-    with open(_stamp_path(), "w") as f:
-        f.write(binding_stamp())
     _link([*_host_compiler(), "-shared", "-o", BIND + ".tmp", obj, "-L" + os.path.dirname(LIB), "-l:" + os.path.basename(LIB),
            "-Wl,-rpath,$ORIGIN", "-L" + _torch_paths()[1], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch_python", "-L" + os.path.join(_cuda_home(), "lib64"), "-lcudart"], BIND)
+    with open(_stamp_path(), "w") as f:
+        f.write(binding_stamp())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -150,8 +150,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    if binding and os.path.exists(BIND):
-        os.remove(BIND)  # of other sources: not to be loaded if this build fails
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(_sources()) + 1) as ex:
         bind_obj = ex.submit(_compile_binding) if binding else None
         results = list(ex.map(_compile, _sources())) if library else []
@@ -167,6 +165,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             _link_binding(bind_obj.result())
         except Exception as e:  # no torch, no host compiler, an error of either: the library stands without it
             sys.stderr.write(f"the Python binding of the rotary and paged calls was not built: {e}\n")
+            if os.path.exists(BIND):
+                os.remove(BIND)  # of other sources
     return LIB
 
 

@@ -111,3 +111,12 @@ def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
         with pytest.raises(RuntimeError, match="1.0.0"):
             _lib.bind()
     _lib.bind()
+
+
+def test_the_binding_needs_no_intermediate_files(monkeypatch, tmp_path):
+    """Neither the objects nor the log of its build."""
+    build.build()
+    monkeypatch.setattr(_lib, "_BIND", None)
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "cleaned"))
+    assert build.up_to_date()
+    _lib.bind()
