@@ -102,8 +102,8 @@ def test_many_requests_some_of_them_cut():
     length = np.array(lens)[:, None, None] * u
     err = np.abs(out.double().cpu().numpy() - ref)
     assert (err <= ((2 * e + 2 * length)[:, None] * a + 1e-38)).all()
-    le = np.abs(lse.double().cpu().numpy() - ref_lse)[some]
-    assert (le <= (e + length + u * np.abs(ref_lse))[some]).all()
+    le = np.abs(lse.double().cpu().numpy()[some] - ref_lse[some])
+    assert (le <= (e + length)[some] + u * np.abs(ref_lse[some])).all()
     assert torch.isneginf(lse[torch.from_numpy(~some).cuda()]).all() and bea.device_status() == 0
 
 
@@ -132,3 +132,20 @@ def test_long_sums_keep_their_last_bits(h, d):
     ref = torch.log(torch.exp(k[..., 0].double()).sum() * (width // pages))
     # the same below, the exponentials' 2^-22 and 2^-23 of their exponents; lse itself, up to 11, in fp32
     assert (lse.double() - ref).abs().max() <= 2 ** -18 + 2 ** -21 + 2 ** -21 + 11 * 2 ** -22
+
+
+def test_long_tables_need_a_workspace_and_short_ones_none():
+    import blockwise_exact_attention_gb300 as bea
+    q = torch.zeros((1, 1, 8, 128), dtype=BF16, device="cuda")
+    cache = torch.zeros((400, 16, 2, 128), dtype=BF16, device="cuda")
+    table = torch.arange(400, dtype=I32, device="cuda")[None]
+    lens = torch.full((1,), 5000, dtype=I32, device="cuda")
+    need = bea.paged_decode_workspace_bytes(q, cache, table)
+    assert need > 0 and bea.paged_decode_workspace_bytes(q, cache, table[:, :4]) == 0
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    bea.paged_decode(q, cache, cache, table, lens, 0.1, workspace=ws[:need])
+    assert (ws[need:] == 255).all()
+    for bad in (ws[:need - 1], ws[16:], ws[:0]):
+        with pytest.raises(RuntimeError, match="WORKSPACE"):
+            bea.paged_decode(q, cache, cache, table, lens, 0.1, workspace=bad)
+    assert bea.device_status() == 0
