@@ -15,7 +15,9 @@ Public API (all calls run in libbea.so's CUDA kernels on the current stream):
 * ``flash_attention / ring_attention``: the same as torch.autograd functions
   (the backward recomputed from the saved log-sum-exp).
 * ``rope_axes`` (``rotary_axes`` for autograd): rotary positions with one or
-  several axes, q and k in one launch.
+  several axes, q and k in one launch; interleaved pairs, a part of the head and
+  scaled frequencies (``RopeScaling``) where asked for. ``norm_rope_axes``
+  (``norm_rotary_axes``): the RMS norm of every head before it, in the same pass.
 * ``paged_plan / paged_write / paged_decode`` (and ``PagedKVCache``, which
   holds their state): a paged K/V cache, from request lengths to the attention
   of one new token per request.
@@ -40,7 +42,13 @@ from .ops import (  # noqa: F401
     selftest_inject_abort,
 )
 from .ring import chunk_schedule, ring_attention_bwd, ring_attention_fwd  # noqa: F401
-from .rotary import rope_axes, rotary_axes  # noqa: F401
+from .rotary import (  # noqa: F401
+    RopeScaling,
+    norm_rope_axes,
+    norm_rotary_axes,
+    rope_axes,
+    rotary_axes,
+)
 from .paged import (  # noqa: F401
     PagedKVCache,
     PagedPlan,

@@ -53,6 +53,9 @@ EXPORTS = (
     "bea_ring_attention_bwd_workspace_size",
     "bea_ring_attention_bwd",
     "bea_rope_axes",
+    "bea_norm_rope_axes",
+    "bea_norm_rope_axes_bwd_workspace_size",
+    "bea_norm_rope_axes_bwd",
     "bea_paged_plan",
     "bea_paged_write",
     "bea_paged_decode_workspace_size",
@@ -156,6 +159,12 @@ def load() -> ctypes.CDLL:
     lib.bea_ring_attention_bwd.restype = i
     lib.bea_rope_axes.argtypes = [P, P, P, vp, vp, i, P, P, vp]
     lib.bea_rope_axes.restype = i
+    lib.bea_norm_rope_axes.argtypes = [P, P, P, vp, vp, i, i, f, i, P, P, i, f, P, P, vp]
+    lib.bea_norm_rope_axes.restype = i
+    lib.bea_norm_rope_axes_bwd_workspace_size.argtypes = [i64]
+    lib.bea_norm_rope_axes_bwd_workspace_size.restype = sz
+    lib.bea_norm_rope_axes_bwd.argtypes = [P, P, P, P, P, vp, vp, i, i, f, P, P, f, P, P, P, P, vp, sz, vp]
+    lib.bea_norm_rope_axes_bwd.restype = i
     lib.bea_paged_plan.argtypes = [P, P, P, P, P, i64, P, P, P, P, P, P, vp]
     lib.bea_paged_plan.restype = i
     lib.bea_paged_write.argtypes = [P, P, P, P, P, vp]

@@ -39,6 +39,18 @@ int make_seq_map(const bea_tensor* t, CUtensorMap* map);
 int make_acc_map(const bea_tensor* t, CUtensorMap* map);
 int make_grad_map(const bea_tensor* g, CUtensorMap* map);
 
+// An i32 tensor: rank, dtype, non-negative shape and strides, contiguous last dimension, 4-byte aligned.
+int check_ints(const bea_tensor* t, int ndim);
+// Whether several entries of a tensor lie on the same place; one that is written may not.
+bool broadcast(const bea_tensor* t);
+bool same_strides(const bea_tensor* a, const bea_tensor* b);
+// A [num_pages, page_size, h_kv, d] pair of caches.
+int check_caches(const bea_tensor* k, const bea_tensor* v);
+// An (input, output) pair of the rotary calls, of `like`'s dtype, batch, length and head dim.
+int check_rope_pair(const bea_tensor* x, const bea_tensor* y, const bea_tensor* like);
+// A frequency (radians per position) as the fraction of a turn per position, times 2^64.
+uint64_t fraction_of_turn(double freq);
+
 // Backward workspace: [dq_acc | D | lse2], each region [n, h, lq_pad(, d)] and 256-byte aligned.
 struct BwdWorkspace {
   size_t dq_off, d_off, l_off, total;

@@ -166,6 +166,14 @@ int rope(const Tensor& q, const Tensor& k, const Tensor& positions, const Turn& 
 
 std::pair<Tensor, Tensor> rotary(const Tensor& q, const Tensor& k, const Tensor& positions, Turn turn, int* rc);
 
+// A gradient that autograd hands over may be of another dtype, expanded, not aligned or yet to be negated.
+Tensor ready(const Tensor& g, at::ScalarType dtype) {
+  Tensor x = (g.scalar_type() == dtype ? g : g.to(dtype)).resolve_neg();
+  bool fits = reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0 && x.stride(-1) == 1;
+  for (int64_t i = 0; i + 1 < x.dim(); ++i) fits = fits && x.stride(i) * x.element_size() % 16 == 0;
+  return fits ? x : x.clone(at::MemoryFormat::Contiguous);
+}
+
 // The gradient of a rotation: the gradients of (q_out, k_out) turned back.
 struct RotaryBackward : public Node {
   torch::autograd::SavedVariable positions;
@@ -178,19 +186,11 @@ struct RotaryBackward : public Node {
     positions.reset_data();
   }
 
-  // A gradient that autograd hands over may be of another dtype, expanded, not aligned or yet to be negated.
-  Tensor ready(const Tensor& g) const {
-    Tensor x = (g.scalar_type() == dtype ? g : g.to(dtype)).resolve_neg();
-    bool fits = reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0 && x.stride(-1) == 1;
-    for (int64_t i = 0; i + 1 < x.dim(); ++i) fits = fits && x.stride(i) * x.element_size() % 16 == 0;
-    return fits ? x : x.clone(at::MemoryFormat::Contiguous);
-  }
-
   variable_list apply(variable_list&& grads) override {
     variable_list out(num_outputs());  // q's, and k's where there is one
     Tensor g[2];
     for (uint32_t i = 0; i < num_outputs(); ++i)
-      if (grads[i].defined() && task_should_compute_output(i)) g[i] = ready(grads[i]);
+      if (grads[i].defined() && task_should_compute_output(i)) g[i] = ready(grads[i], dtype);
     if (!g[0].defined() && !g[1].defined()) return out;
     Turn back = turn;
     back.inverse = !turn.inverse;
@@ -212,14 +212,15 @@ struct RotaryBackward : public Node {
 // A leaf's accumulation node is shared by all graphs that live on the leaf, and keeps the stream that was current
 // when it was made. If that is the legacy default stream, a backward pass captured on another stream makes autograd
 // wait there in the middle of the capture, which ends the process: the call is refused before that.
-void check_capture(const Tensor& x) {
+void check_capture(const Tensor& x, const char* name) {
   if (!x.defined() || !x.requires_grad() || !x.is_leaf()) return;
   const auto node = torch::autograd::impl::try_get_grad_accumulator(x);
   if (node == nullptr) return;
   const auto made = node->stream();
   if (made.has_value() && c10::cuda::CUDAStream(*made).stream() == nullptr)
     throw std::runtime_error(
-        "rotary_axes: captured into a CUDA graph while an earlier graph of the same leaf tensor, made on the default "
+        std::string(name) +
+        ": captured into a CUDA graph while an earlier graph of the same leaf tensor, made on the default "
         "stream, is alive; delete its outputs before the capture");
 }
 
@@ -229,8 +230,8 @@ std::pair<Tensor, Tensor> rotary(const Tensor& q, const Tensor& k, const Tensor&
   const bool grad = at::GradMode::is_enabled() && (q.requires_grad() || (k.defined() && k.requires_grad()));
   if (grad) {
     if (q.is_cuda() && c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
-      check_capture(q);
-      check_capture(k);
+      check_capture(q, "rotary_axes");
+      check_capture(k, "rotary_axes");
     }
   }
   Tensor qo = like(q), ko = like(k);
@@ -291,6 +292,187 @@ PyObject* py_rotary_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int rc = 0;
   const auto out = rotary(q, k, pos, turn_of(a[3], q, pos), &rc);
   finish(rc, "rotary_axes");
+  return tuple({out.first, out.second});
+  END_HANDLE_TH_ERRORS
+}
+
+// ---- rotary with other layouts, and norms ------------------------------------------
+
+struct Layout {
+  Turn turn;
+  bool interleaved = false, norm = false;
+  float amplitude = 1.f, eps = 0.f;
+  int pairs() const { return static_cast<int>(turn.axis.size()); }
+};
+
+int norm_rope(const Tensor& q, const Tensor& k, const Tensor& positions, const Layout& how, const Tensor& qw,
+              const Tensor& kw, const Tensor& q_out, const Tensor& k_out) {
+  Call c;
+  const bea_tensor *a = c.add(q), *b = c.add(k), *p = c.add(positions), *u = c.add(qw), *v = c.add(kw), *x = c.add(q_out),
+                   *y = c.add(k_out);
+  return counted(bea_norm_rope_axes(a, b, p, how.turn.axis.data(), how.turn.freq.data(), how.pairs(), how.interleaved,
+                                    how.amplitude, how.turn.inverse ? 1 : 0, u, v, how.norm, how.eps, x, y, c.stream()));
+}
+
+std::pair<Tensor, Tensor> norm_rotary(const Tensor& q, const Tensor& k, const Tensor& positions, Layout how,
+                                      const Tensor& qw, const Tensor& kw, int* rc);
+
+// The gradients of q, k and their weights; without the norm that of a rotation: its adjoint.
+struct NormRotaryBackward : public Node {
+  torch::autograd::SavedVariable positions, x[2], weight[2];  // x and weights: of the norm's gradient alone
+  Layout how;
+  bool has_k = false;
+  at::ScalarType dtype = at::kFloat;
+
+  std::string name() const override { return "NormRotaryAxesBackward"; }
+  void release_variables() override {
+    std::lock_guard<std::mutex> lock(mutex_);
+    positions.reset_data();
+    for (int i = 0; i < 2; ++i) x[i].reset_data(), weight[i].reset_data();
+  }
+
+  variable_list apply(variable_list&& grads) override {
+    variable_list out(4);  // of q, k, q_weight, k_weight
+    Tensor g[2], at, saved[2], w[2];
+    bool wanted[2];
+    for (uint32_t i = 0; i < 2; ++i) {
+      wanted[i] = (i == 0 || has_k) && i < grads.size() && grads[i].defined() &&
+                  (task_should_compute_output(i) || task_should_compute_output(2 + i));
+      if (wanted[i]) g[i] = ready(grads[i], dtype);
+    }
+    if (!wanted[0] && !wanted[1]) return out;
+    if (how.norm && at::GradMode::is_enabled())
+      throw std::runtime_error("norm_rotary_axes has no second derivative (backward with create_graph)");
+    {
+      std::lock_guard<std::mutex> lock(mutex_);
+      at = positions.unpack();
+      for (int i = 0; how.norm && i < 2; ++i)
+        if (wanted[i]) saved[i] = x[i].unpack(), w[i] = weight[i].unpack();
+    }
+    // what the library calls q is the first of the two that has a gradient
+    const int first = wanted[0] ? 0 : 1, second = first == 0 && wanted[1] ? 1 : -1;
+    int rc = 0;
+    if (!how.norm) {
+      Layout back = how;
+      back.turn.inverse = !how.turn.inverse;
+      const auto r = norm_rotary(g[first], second > 0 ? g[1] : Tensor(), at, std::move(back), Tensor(), Tensor(), &rc);
+      out[first] = r.first;
+      if (second > 0) out[1] = r.second;
+    } else {
+      Tensor dw[2], ws;
+      for (int i = 0; i < 2; ++i) {
+        if (!wanted[i]) continue;
+        out[i] = like(saved[i]);
+        if (w[i].defined() && task_should_compute_output(2 + i)) dw[i] = like(w[i]);
+      }
+      if (dw[0].defined() || dw[1].defined())
+        ws = empty({static_cast<int64_t>(bea_norm_rope_axes_bwd_workspace_size(saved[first].size(-1)))}, at::kByte, at);
+      Call c;
+      const int f = first, z = 1;
+      const bool two = second > 0;
+      const bea_tensor *q = c.add(saved[f]), *k = two ? c.add(saved[z]) : nullptr, *gq = c.add(g[f]),
+                       *gk = two ? c.add(g[z]) : nullptr, *p = c.add(at), *u = c.add(w[f]),
+                       *v = two ? c.add(w[z]) : nullptr, *dq = c.add(out[f]), *dk = two ? c.add(out[z]) : nullptr,
+                       *du = c.add(dw[f]), *dv = two ? c.add(dw[z]) : nullptr;
+      rc = counted(bea_norm_rope_axes_bwd(q, k, gq, gk, p, how.turn.axis.data(), how.turn.freq.data(), how.pairs(),
+                                          how.interleaved, how.amplitude, u, v, how.eps, dq, dk, du, dv,
+                                          ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
+                                          c.stream()));
+      for (int i = 0; i < 2; ++i) {
+        out[2 + i] = dw[i];
+        if (!task_should_compute_output(i)) out[i] = Tensor();
+      }
+    }
+    if (rc != BEA_OK) throw std::runtime_error(std::string("norm_rotary_axes, backward: ") + bea_status_string(rc));
+    return out;
+  }
+};
+
+std::pair<Tensor, Tensor> norm_rotary(const Tensor& q, const Tensor& k, const Tensor& positions, Layout how,
+                                      const Tensor& qw, const Tensor& kw, int* rc) {
+  const char* name = how.norm ? "norm_rotary_axes" : "rotary_axes";
+  bool grad = false;
+  for (const Tensor* t : {&q, &k, &qw, &kw}) {
+    if (!t->defined()) continue;
+    TORCH_CHECK_NOT_IMPLEMENTED(!t->_fw_grad(0).defined(), name, " has no forward-mode derivative");
+    grad = grad || t->requires_grad();
+  }
+  grad = grad && at::GradMode::is_enabled();
+  if (grad && q.is_cuda() && c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+    for (const Tensor* t : {&q, &k, &qw, &kw}) check_capture(*t, name);
+  Tensor qo = like(q), ko = like(k);
+  *rc = norm_rope(q, k, positions, how, qw, kw, qo, ko);
+  if (*rc == BEA_OK && grad) {
+    auto node = std::shared_ptr<NormRotaryBackward>(new NormRotaryBackward(), torch::autograd::deleteNode);
+    node->set_next_edges(torch::autograd::collect_next_edges(q, k, qw, kw));
+    node->positions = torch::autograd::SavedVariable(positions, false);
+    if (how.norm) {
+      node->x[0] = torch::autograd::SavedVariable(q, false);
+      node->x[1] = torch::autograd::SavedVariable(k, false);
+      node->weight[0] = torch::autograd::SavedVariable(qw, false);
+      node->weight[1] = torch::autograd::SavedVariable(kw, false);
+    }
+    node->has_k = k.defined();
+    node->dtype = q.scalar_type();
+    node->how = std::move(how);
+    torch::autograd::set_history(qo, node);
+    if (k.defined()) torch::autograd::set_history(ko, node);
+  }
+  return {qo, ko};
+}
+
+// (axes, frequencies, number of axes, amplitude, interleaved): the arrays' entries are the turned pairs.
+Layout layout_of(PyObject* table, const Tensor& positions) {
+  TORCH_CHECK_TYPE(PyTuple_Check(table) && PyTuple_GET_SIZE(table) == 5, "the rotation's tables");
+  PyObject *axis = PyTuple_GET_ITEM(table, 0), *freq = PyTuple_GET_ITEM(table, 1);
+  const long long axes = integer(PyTuple_GET_ITEM(table, 2));
+  TORCH_CHECK_VALUE(positions.dim() == 3 && positions.size(0) == axes, "positions ", positions.sizes(), ": [", axes,
+                    ", n, l] for ", axes, " sections");
+  TORCH_CHECK_TYPE(PyBytes_Check(axis) && PyBytes_Check(freq) && PyBytes_GET_SIZE(axis) * 2 == PyBytes_GET_SIZE(freq),
+                   "the rotation's tables");
+  const auto* a = reinterpret_cast<const int32_t*>(PyBytes_AS_STRING(axis));
+  const auto* f = reinterpret_cast<const double*>(PyBytes_AS_STRING(freq));
+  const size_t n = PyBytes_GET_SIZE(axis) / 4;
+  Layout how;
+  how.turn.axis.assign(a, a + n);
+  how.turn.freq.assign(f, f + n);
+  how.amplitude = static_cast<float>(real(PyTuple_GET_ITEM(table, 3)));
+  how.interleaved = integer(PyTuple_GET_ITEM(table, 4)) != 0;
+  return how;
+}
+
+// norm_rope_axes(q, k, positions, table, inverse, q_weight, k_weight, norm, eps, q_out, k_out) -> (q_out, k_out)
+PyObject* py_norm_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("norm_rope_axes", n, 11);
+  const Tensor q = tensor(a[0]), k = tensor(a[1], true), pos = tensor(a[2]);
+  const Tensor qw = tensor(a[5], true), kw = tensor(a[6], true);
+  Tensor qo = to_write(tensor(a[9], true)), ko = to_write(tensor(a[10], true));
+  Layout how = layout_of(a[3], pos);
+  how.turn.inverse = integer(a[4]) != 0;
+  how.norm = integer(a[7]) != 0;
+  how.eps = static_cast<float>(real(a[8]));
+  if (!qo.defined()) qo = like(q);
+  if (!ko.defined()) ko = like(k);
+  finish(norm_rope(q, k, pos, how, qw, kw, qo, ko), how.norm ? "norm_rope_axes" : "rope_axes");
+  written({qo, ko});
+  return tuple({qo, ko});
+  END_HANDLE_TH_ERRORS
+}
+
+// norm_rotary_axes(q, k, positions, table, q_weight, k_weight, norm, eps) -> (q_out, k_out)
+PyObject* py_norm_rotary_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("norm_rotary_axes", n, 8);
+  const Tensor q = tensor(a[0]), k = tensor(a[1], true), pos = tensor(a[2]);
+  const Tensor qw = tensor(a[4], true), kw = tensor(a[5], true);
+  Layout how = layout_of(a[3], pos);
+  how.norm = integer(a[6]) != 0;
+  how.eps = static_cast<float>(real(a[7]));
+  const bool norm = how.norm;
+  int rc = 0;
+  const auto out = norm_rotary(q, k, pos, std::move(how), qw, kw, &rc);
+  finish(rc, norm ? "norm_rotary_axes" : "rotary_axes");
   return tuple({out.first, out.second});
   END_HANDLE_TH_ERRORS
 }
@@ -409,6 +591,8 @@ PyMethodDef g_methods[] = {method<py_setup>("setup"),
                            method<py_launches>("launches"),
                            method<py_rope_axes>("rope_axes"),
                            method<py_rotary_axes>("rotary_axes"),
+                           method<py_norm_rope_axes>("norm_rope_axes"),
+                           method<py_norm_rotary_axes>("norm_rotary_axes"),
                            method<py_paged_plan>("paged_plan"),
                            method<py_paged_write>("paged_write"),
                            method<py_paged_decode>("paged_decode"),

@@ -7,9 +7,8 @@
 #include "abi_internal.h"
 #include "paged.cuh"
 
-using namespace bea::abi;
-
-namespace {
+namespace bea {
+namespace abi {
 
 // An i32 tensor: rank, dtype, non-negative shape and strides, contiguous last
 // dimension, 4-byte aligned.
@@ -46,6 +45,16 @@ bool same_strides(const bea_tensor* a, const bea_tensor* b) {
   return true;
 }
 
+// A [num_pages, page_size, h_kv, d] pair of caches.
+int check_caches(const bea_tensor* k, const bea_tensor* v) {
+  int rc;
+  if ((rc = check_tensor(k, 4)) || (rc = check_tensor(v, 4))) return rc;
+  if (k->dtype != v->dtype) return BEA_ERR_DTYPE;
+  if (!same_shape(k, v)) return BEA_ERR_SHAPE;
+  if (k->shape[1] < 1 || k->shape[0] * k->shape[1] > (int64_t(1) << 31) - 1) return BEA_ERR_SHAPE;
+  return BEA_OK;
+}
+
 // One of rope's (input, output) pairs.
 int check_rope_pair(const bea_tensor* x, const bea_tensor* y, const bea_tensor* like) {
   int rc;
@@ -59,15 +68,20 @@ int check_rope_pair(const bea_tensor* x, const bea_tensor* y, const bea_tensor* 
   return BEA_OK;
 }
 
-// A [num_pages, page_size, h_kv, d] pair of caches.
-int check_caches(const bea_tensor* k, const bea_tensor* v) {
-  int rc;
-  if ((rc = check_tensor(k, 4)) || (rc = check_tensor(v, 4))) return rc;
-  if (k->dtype != v->dtype) return BEA_ERR_DTYPE;
-  if (!same_shape(k, v)) return BEA_ERR_SHAPE;
-  if (k->shape[1] < 1 || k->shape[0] * k->shape[1] > (int64_t(1) << 31) - 1) return BEA_ERR_SHAPE;
-  return BEA_OK;
+uint64_t fraction_of_turn(double freq) {
+  // Rounded; of a negative one's size, which loses no bits where it is small. It is at most 1 - 2^-53, so its product is
+  // below 2^64.
+  const double turns = std::fabs(freq) * 0.15915494309189533577;  // 1 / (2 pi)
+  const uint64_t step = static_cast<uint64_t>(std::nearbyint((turns - std::floor(turns)) * 0x1p64));
+  return freq < 0 ? 0 - step : step;
 }
+
+}  // namespace abi
+}  // namespace bea
+
+using namespace bea::abi;
+
+namespace {
 
 const int32_t* ints(const bea_tensor* t) { return static_cast<const int32_t*>(t->data); }
 int32_t* ints_out(const bea_tensor* t) { return static_cast<int32_t*>(t->data); }
@@ -95,11 +109,7 @@ int bea_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* po
   std::memset(&p, 0, sizeof(p));
   for (int i = 0; i < d / 2; ++i) {
     if (axis_of_pair[i] < 0 || axis_of_pair[i] >= axes || !std::isfinite(freq[i])) return BEA_ERR_ARG;
-    // The fraction of a turn as a 64-bit fixed-point number, rounded; of a negative one's size, which loses no bits where
-    // it is small. It is at most 1 - 2^-53, so its product is below 2^64.
-    const double turns = std::fabs(freq[i]) * 0.15915494309189533577;  // 1 / (2 pi)
-    const uint64_t step = static_cast<uint64_t>(std::nearbyint((turns - std::floor(turns)) * 0x1p64));
-    p.turn[i] = freq[i] < 0 ? 0 - step : step;
+    p.turn[i] = fraction_of_turn(freq[i]);
     p.axis[i] = static_cast<uint8_t>(axis_of_pair[i]);
   }
   p.n = (int)q->shape[0];

@@ -22,53 +22,16 @@
 // against 5.5 us for 256 tokens of 32 + 8 heads (now 3.0 us).
 #include <type_traits>
 
-#include <cuda_bf16.h>
-
 #include "launch_cache.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
+#include "rotary.cuh"
 
 namespace bea {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kSmThreads = 2048;  // that an SM holds
-
-template <bool kF32>
-struct Piece;  // 16 bytes of a row as fp32 values
-
-template <>
-struct Piece<true> {
-  static constexpr int kN = 4;
-  __device__ static void load(const uint4& r, float* x) {
-    x[0] = __uint_as_float(r.x), x[1] = __uint_as_float(r.y), x[2] = __uint_as_float(r.z), x[3] = __uint_as_float(r.w);
-  }
-  __device__ static uint4 store(const float* x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-  }
-};
-
-template <>
-struct Piece<false> {
-  static constexpr int kN = 8;
-  __device__ static void load(const uint4& r, float* x) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  __device__ static uint4 store(const float* x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
 
 // Index: of a thread's work item; 32 bits where they are enough, three divisions by run-time numbers start each item.
 template <bool kF32, int kHeads, typename Index>
@@ -109,14 +72,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
     for (int j = 0; j < P::kN; ++j) {
       const int64_t pos = p.pos[axis[c + j] * p.pos_sa + b * p.pos_sn + i];
-      const uint64_t a = (uint64_t)pos * turn[c + j];
-      const uint32_t quarter = ((uint32_t)(a >> 32) + 0x20000000u) >> 30;  // the nearest; bit 61 of a is the rest's sign
-      float s, x;
-      sincospif((float)(int32_t)(a >> 30) * 0x1p-33f, &s, &x);
-      cs[j] = quarter & 1u ? s : x;
-      sn[j] = quarter & 1u ? x : s;
-      if ((quarter + 1u) & 2u) cs[j] = -cs[j];
-      if (((quarter >> 1) & 1u) != (uint32_t)p.inverse) sn[j] = -sn[j];
+      cos_sin(pos, turn[c + j], p.inverse, &cs[j], &sn[j]);
     }
 #pragma unroll
     for (int x = 0; x < kHeads; ++x) {

@@ -351,6 +351,50 @@ int bea_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* po
                   const double* freq, int inverse, const bea_tensor* q_out, const bea_tensor* k_out, void* stream);
 
 /*
+ * The rotation of bea_rope_axes with its other layouts, and the RMS norm that
+ * some models put before it, q and k in one launch. Of a row x (d elements):
+ *   norm 1: y = w * x / sqrt(mean(x^2) + eps), w the row of weights; norm 0: y = x
+ *   pair p < pairs is (y_p, y_{p + pairs}), or, interleaved, (y_{2p}, y_{2p + 1});
+ *   (a, b) becomes amplitude * (a cos - b sin, b cos + a sin), the angle as for
+ *   bea_rope_axes; what lies behind the 2 * pairs first elements is not turned.
+ *
+ *   q, k, positions, axis_of_pair, freq, q_out, k_out  as for bea_rope_axes, the
+ *              arrays of `pairs` entries (NULL where that is 0)
+ *   pairs      0 <= 2 * pairs <= d; not interleaved: a multiple of 8 (bf16) or 4
+ *              (f32), else BEA_ERR_UNSUPPORTED
+ *   amplitude  finite
+ *   inverse    1 (norm 0 only): the angles negated, which is the adjoint (and, at
+ *              amplitude 1, the inverse)
+ *   q_weight, k_weight   NULL (ones) or [d], bf16 or f32 whatever q is; norm 0: NULL
+ *   eps        >= 0, finite
+ * In fp32, rounded once. d as for bea_rope_axes.
+ */
+int bea_norm_rope_axes(const bea_tensor* q, const bea_tensor* k, const bea_tensor* positions,
+                       const int32_t* axis_of_pair, const double* freq, int pairs, int interleaved, float amplitude,
+                       int inverse, const bea_tensor* q_weight, const bea_tensor* k_weight, int norm, float eps,
+                       const bea_tensor* q_out, const bea_tensor* k_out, void* stream);
+
+/*
+ * The gradient of bea_norm_rope_axes with norm 1: from x (q, k) and the outputs'
+ * gradients those of x and of the weights (their sums over all rows in fp32, in a
+ * fixed order).
+ *   dq_out, dk_out   shapes and dtype of q, k
+ *   dq, dk           the same (written); dk, dk_out NULL iff k is. Each may be
+ *                    the output's gradient itself (same pointer, same strides).
+ *   dq_weight, dk_weight   NULL (not wanted), or [d] of the weight's dtype (written)
+ *   workspace        bea_norm_rope_axes_bwd_workspace_size(d) bytes, 256-byte
+ *                    aligned; may be NULL where no weight's gradient is wanted.
+ *                    Contents on entry irrelevant; calls that may run
+ *                    concurrently need separate workspaces.
+ */
+size_t bea_norm_rope_axes_bwd_workspace_size(int64_t d);
+int bea_norm_rope_axes_bwd(const bea_tensor* q, const bea_tensor* k, const bea_tensor* dq_out, const bea_tensor* dk_out,
+                           const bea_tensor* positions, const int32_t* axis_of_pair, const double* freq, int pairs,
+                           int interleaved, float amplitude, const bea_tensor* q_weight, const bea_tensor* k_weight,
+                           float eps, const bea_tensor* dq, const bea_tensor* dk, const bea_tensor* dq_weight,
+                           const bea_tensor* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Paged K/V cache. A cache is [num_pages, page_size, h_kv, d] (any 16-byte
  * aligned outer strides, so a [num_pages, h_kv, page_size, d] cache is passed
  * as its permuted view). Request r owns the pages block_table[r, 0 ..
