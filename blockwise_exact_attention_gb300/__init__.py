@@ -21,6 +21,7 @@ Public API (all calls run in libbea.so's CUDA kernels on the current stream):
 * ``paged_plan / paged_write / paged_decode`` (and ``PagedKVCache``, which
   holds their state): a paged K/V cache, from request lengths to the attention
   of one new token per request.
+* ``paged_fork / paged_free / paged_compact / paged_copy``: rows that share pages.
 
 The seeded input generators live in ``workloads`` and import nothing else.
 """
@@ -50,10 +51,17 @@ from .rotary import (  # noqa: F401
     rotary_axes,
 )
 from .paged import (  # noqa: F401
+    PagedCompaction,
+    PagedFork,
+    PagedFreed,
     PagedKVCache,
     PagedPlan,
+    paged_compact,
+    paged_copy,
     paged_decode,
     paged_decode_workspace_bytes,
+    paged_fork,
+    paged_free,
     paged_plan,
     paged_write,
 )

@@ -60,6 +60,10 @@ EXPORTS = (
     "bea_paged_write",
     "bea_paged_decode_workspace_size",
     "bea_paged_decode",
+    "bea_paged_fork",
+    "bea_paged_free",
+    "bea_paged_compact",
+    "bea_paged_copy",
 )
 
 
@@ -173,6 +177,14 @@ def load() -> ctypes.CDLL:
     lib.bea_paged_decode_workspace_size.restype = sz
     lib.bea_paged_decode.argtypes = [P, P, P, P, P, P, P, f, i, vp, sz, vp]
     lib.bea_paged_decode.restype = i
+    lib.bea_paged_fork.argtypes = [P, P, P, P, P, P, P, i64, P, P, P, P, vp]
+    lib.bea_paged_fork.restype = i
+    lib.bea_paged_free.argtypes = [P, P, P, P, P, P, i64, P, P, P, vp]
+    lib.bea_paged_free.restype = i
+    lib.bea_paged_compact.argtypes = [P, P, P, P, P, i64, P, P, P, P, P, vp]
+    lib.bea_paged_compact.restype = i
+    lib.bea_paged_copy.argtypes = [P, P, i, vp]
+    lib.bea_paged_copy.restype = i
     _LIB = lib
     return lib
 

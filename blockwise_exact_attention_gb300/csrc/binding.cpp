@@ -564,6 +564,111 @@ PyObject* py_paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---- shared pages ------------------------------------------------------------------
+
+// The i-th of a call's outputs: given, or new.
+Tensor ints_like(PyObject* o, const Tensor& x) {
+  Tensor t = to_write(tensor(o, true));
+  return t.defined() ? t : like(x);
+}
+
+// Records of several tensors, for the call that takes any number of them.
+bea_tensor record_of(const Tensor& t) {
+  Call c;
+  return *c.add(t);
+}
+
+// paged_fork(src, tokens, lens, block_table, shares, free_pages, n_free, page_size, lens_out, n_free_out, shares_out,
+// copies) -> (lens, n_free, shares, copies); outputs that are None are allocated
+PyObject* py_paged_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("paged_fork", n, 12);
+  Tensor in[7];
+  for (int i = 0; i < 7; ++i) in[i] = i == 3 ? to_write(tensor(a[i])) : tensor(a[i], i == 1);
+  const long long page = integer(a[7]);
+  const Tensor lens = ints_like(a[8], in[2]), height = ints_like(a[9], in[6]), shares = ints_like(a[10], in[4]);
+  Tensor copies = to_write(tensor(a[11], true));
+  if (!copies.defined()) copies = empty({in[2].dim() == 1 ? in[2].size(0) : 0, 3}, at::kInt, in[2]);
+  Call c;
+  const bea_tensor* r[11];
+  for (int i = 0; i < 7; ++i) r[i] = c.add(in[i]);
+  r[7] = c.add(lens), r[8] = c.add(height), r[9] = c.add(shares), r[10] = c.add(copies);
+  finish(counted(bea_paged_fork(r[0], r[1], r[2], r[3], r[4], r[5], r[6], page, r[7], r[8], r[9], r[10], c.stream())),
+         "paged_fork");
+  written({in[3], lens, height, shares, copies});
+  return tuple({lens, height, shares, copies});
+  END_HANDLE_TH_ERRORS
+}
+
+// paged_free(ends, lens, block_table, shares, free_pages, n_free, page_size, lens_out, n_free_out, shares_out) -> (lens,
+// n_free, shares)
+PyObject* py_paged_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("paged_free", n, 10);
+  Tensor in[6];
+  for (int i = 0; i < 6; ++i) in[i] = i == 4 ? to_write(tensor(a[i])) : tensor(a[i]);
+  const long long page = integer(a[6]);
+  const Tensor lens = ints_like(a[7], in[1]), height = ints_like(a[8], in[5]), shares = ints_like(a[9], in[3]);
+  Call c;
+  const bea_tensor* r[9];
+  for (int i = 0; i < 6; ++i) r[i] = c.add(in[i]);
+  r[6] = c.add(lens), r[7] = c.add(height), r[8] = c.add(shares);
+  finish(counted(bea_paged_free(r[0], r[1], r[2], r[3], r[4], r[5], page, r[6], r[7], r[8], c.stream())), "paged_free");
+  written({in[4], lens, height, shares});
+  return tuple({lens, height, shares});
+  END_HANDLE_TH_ERRORS
+}
+
+// paged_compact(lens, block_table, shares, free_pages, n_free, page_size, capacity, block_table_out, shares_out,
+// free_pages_out, page_map, copies) -> (block_table, shares, free_pages, page_map, copies)
+PyObject* py_paged_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("paged_compact", n, 12);
+  Tensor in[5];
+  for (int i = 0; i < 5; ++i) in[i] = tensor(a[i]);
+  const long long page = integer(a[5]), capacity = integer(a[6]);
+  TORCH_CHECK_VALUE(capacity >= 0 && capacity <= INT32_MAX, "paged_compact: capacity ", capacity);
+  const Tensor table = ints_like(a[7], in[1]), shares = ints_like(a[8], in[2]), pool = ints_like(a[9], in[3]),
+               map = ints_like(a[10], in[2]);
+  Tensor copies = to_write(tensor(a[11], true));
+  if (!copies.defined()) copies = empty({capacity, 3}, at::kInt, in[0]);
+  TORCH_CHECK_VALUE(copies.dim() != 2 || copies.size(0) == capacity, "paged_compact: copies has ", copies.size(0),
+                    " places, capacity is ", capacity);
+  Call c;
+  const bea_tensor* r[10];
+  for (int i = 0; i < 5; ++i) r[i] = c.add(in[i]);
+  r[5] = c.add(table), r[6] = c.add(shares), r[7] = c.add(pool), r[8] = c.add(map), r[9] = c.add(copies);
+  finish(counted(bea_paged_compact(r[0], r[1], r[2], r[3], r[4], page, r[5], r[6], r[7], r[8], r[9], c.stream())),
+         "paged_compact");
+  written({table, shares, pool, map, copies});
+  return tuple({table, shares, pool, map, copies});
+  END_HANDLE_TH_ERRORS
+}
+
+// paged_copy(copies, caches): a tuple or list of tensors, written
+PyObject* py_paged_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("paged_copy", n, 2);
+  const Tensor copies = tensor(a[0]);
+  TORCH_CHECK_TYPE(PyTuple_Check(a[1]) || PyList_Check(a[1]), "paged_copy: caches is a tuple or list of tensors");
+  const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[1]);
+  std::vector<Tensor> caches;
+  std::vector<bea_tensor> records;
+  Call c;
+  const bea_tensor* list = c.add(copies);
+  void* stream = c.stream();
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    caches.push_back(to_write(tensor(PySequence_Fast_GET_ITEM(a[1], i))));
+    TORCH_CHECK_VALUE(!caches.back().is_cuda() || caches.back().get_device() == copies.get_device(), "tensors on cuda:",
+                      copies.get_device(), " and cuda:", caches.back().get_device(), ": all must live on one device");
+    records.push_back(record_of(caches.back()));
+  }
+  finish(counted(bea_paged_copy(list, records.data(), clamp_int(count), stream)), "paged_copy");
+  for (const Tensor& t : caches) written({t});
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // setup(check): the package's function that raises a status code
 PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -596,6 +701,10 @@ PyMethodDef g_methods[] = {method<py_setup>("setup"),
                            method<py_paged_plan>("paged_plan"),
                            method<py_paged_write>("paged_write"),
                            method<py_paged_decode>("paged_decode"),
+                           method<py_paged_fork>("paged_fork"),
+                           method<py_paged_free>("paged_free"),
+                           method<py_paged_compact>("paged_compact"),
+                           method<py_paged_copy>("paged_copy"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -6,6 +6,11 @@ A serving step is ``paged_plan`` (which pages and slots the new tokens get),
 tensors and keep nothing; ``PagedKVCache`` holds a cache's tensors and passes
 them on. All of it runs on the GPU: a step needs no lengths on the host, so it
 can be captured into a CUDA graph and replayed.
+
+Requests may share pages: ``paged_fork`` lets rows begin as other rows' copies,
+``paged_free`` ends rows and gives back the pages that nobody holds any more,
+``paged_compact`` moves the used pages to the lower end of the cache, and
+``paged_copy`` carries out the copies that the first and the last list.
 """
 
 from __future__ import annotations
@@ -66,13 +71,82 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, softmax_scale=None, win
                                     out_dtype is torch.float32, workspace)
 
 
+class PagedFork(NamedTuple):
+    lens: torch.Tensor    # [n] i32, the new lengths
+    n_free: torch.Tensor  # [1] i32, free pages left
+    shares: torch.Tensor  # [num_pages] i32, owners of a page beyond the first
+    copies: torch.Tensor  # [n, 3] i32, (page, new page, tokens); tokens 0: none, -1: not a fork
+
+
+class PagedFreed(NamedTuple):
+    lens: torch.Tensor    # [n] i32, 0 for the rows that ended
+    n_free: torch.Tensor  # [1] i32
+    shares: torch.Tensor  # [num_pages] i32
+
+
+class PagedCompaction(NamedTuple):
+    block_table: torch.Tensor  # [n, max_pages] i32
+    shares: torch.Tensor       # [num_pages] i32
+    free_pages: torch.Tensor   # [F] i32, the lowest page on top, -1 behind the last
+    page_map: torch.Tensor     # [num_pages] i32, where each page went
+    copies: torch.Tensor       # [capacity, 3] i32, (page, new page, page_size) of every move, then -1
+
+
+def paged_fork(src, tokens, lens, block_table, shares, free_pages, n_free, page_size, out=None) -> PagedFork:
+    """Rows begin as copies of other rows, on their pages (all int32, on the GPU).
+
+    ``src`` [n]: the row that row r forks from, -1 for rows that take no part; row
+    r has to be free, and its source may not fork itself. ``tokens`` [n] (or None):
+    how many of the source's first tokens it takes, -1 for all. ``shares``
+    [num_pages] counts a page's owners beyond the first. Full pages are shared; a
+    page that a fork ends in is copied to one of its own (``copies``, for
+    ``paged_copy``). ``block_table`` is updated in place; ``lens``, ``n_free`` and
+    ``shares`` are not, unless ``out`` (a PagedFork) holds them as its own. A step
+    that cannot be done in full changes nothing and is reported by
+    ``device_status``."""
+    return PagedFork._make(_lib.bind().paged_fork(src, tokens, lens, block_table, shares, free_pages, n_free, page_size,
+                                                  *(out or (None,) * 4)))
+
+
+def paged_free(ends, lens, block_table, shares, free_pages, n_free, page_size, out=None) -> PagedFreed:
+    """Rows r with ``ends[r]`` < 0 end; their pages that no other row holds go on the
+    stack ``free_pages``, in place, in ascending order. For tables with shared
+    pages, before ``paged_plan``, whose ``new_lens`` can be passed as ``ends``.
+    ``lens``, ``n_free`` and ``shares`` are not changed, unless ``out`` (a
+    PagedFreed) holds them as its own."""
+    return PagedFreed._make(_lib.bind().paged_free(ends, lens, block_table, shares, free_pages, n_free, page_size,
+                                                   *(out or (None,) * 3)))
+
+
+def paged_compact(lens, block_table, shares, free_pages, n_free, page_size, capacity, out=None) -> PagedCompaction:
+    """Moves used pages into lower free ones, at most ``capacity`` of them: the
+    lowest free page takes the highest used one's place, and so on. Pages that are
+    not on the stack count as used. Nothing is changed in place, unless ``out`` (a
+    PagedCompaction) holds the tensors as its own. The contents follow by
+    ``paged_copy`` with ``copies``, before anything else writes the cache."""
+    return PagedCompaction._make(_lib.bind().paged_compact(lens, block_table, shares, free_pages, n_free, page_size,
+                                                           capacity, *(out or (None,) * 5)))
+
+
+def paged_copy(copies, caches):
+    """Copy pages within every one of ``caches`` (a list of [num_pages, page_size,
+    h_kv, d] tensors of one shape: keys and values of all layers), in place.
+    ``copies`` [m, 3] int32: (page, new page, how many of its first tokens), tokens
+    <= 0: no copy. Returns the caches."""
+    _lib.bind().paged_copy(copies, caches)
+    return caches
+
+
 class PagedKVCache:
     """The tensors of one paged cache and its requests.
 
     ``num_pages`` pages of ``page_size`` tokens, up to ``max_requests`` requests
-    (rows) of at most ``max_len`` tokens. A row is free while its length is 0."""
+    (rows) of at most ``max_len`` tokens. A row is free while its length is 0.
+    ``share_pages``: rows may share pages (``fork``, ``compact``); their owners are
+    counted in ``shares``, and requests end through ``paged_free``."""
 
-    def __init__(self, num_pages, page_size, h_kv, d, max_requests, max_len, dtype=torch.bfloat16, device="cuda"):
+    def __init__(self, num_pages, page_size, h_kv, d, max_requests, max_len, dtype=torch.bfloat16, device="cuda",
+                 share_pages=False):
         i32 = dict(dtype=torch.int32, device=device)
         self.page_size = page_size
         self.k = torch.empty(num_pages, page_size, h_kv, d, dtype=dtype, device=device)
@@ -81,14 +155,48 @@ class PagedKVCache:
         self.lens = torch.zeros(max_requests, **i32)
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)  # page 0 is handed out first
         self.n_free = torch.full((1,), num_pages, **i32)
+        self.shares = torch.zeros(num_pages, **i32) if share_pages else None
 
     def plan(self, new_lens, capacity) -> PagedPlan:
-        """``paged_plan`` on this cache, its lengths and stack updated in place."""
+        """``paged_plan`` on this cache, its lengths and stack updated in place.
+        Where pages are shared, the rows that end (-1) are freed first, also if the
+        plan then refuses the rest."""
+        if self.shares is not None:
+            self.free(new_lens)
         n, dev = self.lens.shape[0], self.lens.device
         slots, positions, cu_new, cu_pages = torch.empty(2 * (capacity + n + 1), dtype=torch.int32, device=dev).split(
             (capacity, capacity, n + 1, n + 1))
         return paged_plan(self.lens, new_lens, self.block_table, self.free_pages, self.n_free, self.page_size, capacity,
                           PagedPlan(slots, positions, cu_new, cu_pages, self.lens, self.n_free))
+
+    def _counted(self):
+        if self.shares is None:
+            raise ValueError("this cache does not count its pages' owners: PagedKVCache(..., share_pages=True)")
+
+    def free(self, ends):
+        """``paged_free`` on this cache, in place."""
+        self._counted()
+        return paged_free(ends, self.lens, self.block_table, self.shares, self.free_pages, self.n_free, self.page_size,
+                          PagedFreed(self.lens, self.n_free, self.shares))
+
+    def fork(self, src, tokens=None, caches=None):
+        """``paged_fork`` on this cache, in place, and its copies in ``caches`` (default: this cache's own two)."""
+        self._counted()
+        copies = torch.empty(len(self.lens), 3, dtype=torch.int32, device=self.lens.device)
+        step = paged_fork(src, tokens, self.lens, self.block_table, self.shares, self.free_pages, self.n_free,
+                          self.page_size, PagedFork(self.lens, self.n_free, self.shares, copies))
+        paged_copy(step.copies, [self.k, self.v] if caches is None else caches)
+        return step
+
+    def compact(self, capacity, caches=None) -> PagedCompaction:
+        """``paged_compact`` on this cache, in place, and its copies in ``caches`` (default: this cache's own two)."""
+        self._counted()
+        i32 = dict(dtype=torch.int32, device=self.lens.device)
+        step = paged_compact(self.lens, self.block_table, self.shares, self.free_pages, self.n_free, self.page_size, capacity,
+                             PagedCompaction(self.block_table, self.shares, self.free_pages,
+                                             torch.empty(len(self.shares), **i32), torch.empty(capacity, 3, **i32)))
+        paged_copy(step.copies, [self.k, self.v] if caches is None else caches)
+        return step
 
     def write(self, k, v, slot_map):
         paged_write(k, v, slot_map, self.k, self.v)

@@ -492,6 +492,97 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
                      size_t workspace_bytes, void* stream);
 
 /*
+ * Pages that several rows of a table hold. shares[p] is the number of rows that
+ * hold page p beyond the first: 0 for a page of one row, and for a free one.
+ * bea_paged_plan neither reads nor changes it (the pages that it hands out have
+ * 0), but it takes every page to be owned by one row: rows of a table with
+ * shared pages are ended by bea_paged_free, before the plan, which then meets
+ * them with length 0.
+ *
+ * Outputs may be their inputs (lens_out = lens, n_free_out = n_free, shares_out =
+ * shares); no arrays overlap otherwise.
+ *
+ * bea_paged_fork: rows begin as copies of other rows, sharing their pages.
+ *   src         [n] i32   -1: row r takes no part; else it becomes a fork of row
+ *               src[r], which does not fork itself. Row r has to be free (length 0).
+ *   tokens      NULL, or [n] i32: the row takes the source's first tokens[r]
+ *               tokens; -1 (and NULL): all of them
+ *   lens, block_table (read and written), free_pages, n_free   as for
+ *               bea_paged_plan; free_pages is only read
+ *   shares      [num_pages] i32
+ *   lens_out [n], n_free_out [1], shares_out [num_pages]   written
+ *   copies      [n, 3] i32, written: where a fork ends inside a page that page's
+ *               tokens are copied to a page of its own, popped in row order: (page,
+ *               new page, tokens); (-1, -1, 0) for a fork that needs none, (-1, -1,
+ *               -1) for other rows. For bea_paged_copy, in every layer.
+ * Full pages are shared. All or nothing: a row or a number out of range, a
+ * source that forks, a row that is not free, a length beyond the table, or a
+ * stack that runs empty leaves everything as it is (every copy -1) and the device
+ * status reads BEA_ERR_PAGES. A page outside [0, num_pages) in a source's row is
+ * handed on uncounted, and not copied; it is reported.
+ */
+int bea_paged_fork(const bea_tensor* src, const bea_tensor* tokens, const bea_tensor* lens,
+                   const bea_tensor* block_table, const bea_tensor* shares, const bea_tensor* free_pages,
+                   const bea_tensor* n_free, int64_t page_size, const bea_tensor* lens_out,
+                   const bea_tensor* n_free_out, const bea_tensor* shares_out, const bea_tensor* copies, void* stream);
+
+/*
+ * Rows end; pages that no row holds any more go back on the stack, in ascending
+ * order of their ids.
+ *   ends        [n] i32: row r ends where it is negative (the new_lens of
+ *               bea_paged_plan can be passed)
+ *   free_pages  read and written; the rest as for bea_paged_fork
+ *   lens_out    0 for the rows that end
+ * A height of the stack out of range leaves everything as it is; a row whose
+ * length is out of range stays; pages outside [0, num_pages) are passed over;
+ * pages that pass the stack's end are lost; a page given back more often than it
+ * was held goes on the stack once. Each is reported.
+ */
+int bea_paged_free(const bea_tensor* ends, const bea_tensor* lens, const bea_tensor* block_table,
+                   const bea_tensor* shares, const bea_tensor* free_pages, const bea_tensor* n_free, int64_t page_size,
+                   const bea_tensor* lens_out, const bea_tensor* n_free_out, const bea_tensor* shares_out,
+                   void* stream);
+
+/*
+ * Used pages move to the lower end of the cache: the lowest free page takes the
+ * highest used one's place, the next the next, as long as that is a move
+ * downwards and `copies` has room. All pages that are not on the stack count as
+ * used.
+ *   lens [n], block_table [n, max_pages], shares [num_pages], free_pages [F],
+ *   n_free [1]         read
+ *   block_table_out    the table with the new pages; entries behind a row's last
+ *                      page are those of the table
+ *   shares_out, free_pages_out (the lowest page on top, -1 behind the last; the
+ *                      height stays)
+ *   page_map           [num_pages] i32: where each page went, itself if nowhere
+ *   copies             [capacity, 3] i32: (page, new page, page_size) of every
+ *                      move, then -1
+ * block_table_out may be block_table, free_pages_out free_pages and shares_out
+ * shares. The moves' contents are copied by bea_paged_copy, before anything
+ * else writes the cache. num_pages <= 2^20. A stack with a page twice, a page
+ * outside [0, num_pages) or a height out of range: nothing moves; a table entry
+ * outside stays as it is, a length out of range counts as 0 or all of the table.
+ * Each is reported.
+ */
+int bea_paged_compact(const bea_tensor* lens, const bea_tensor* block_table, const bea_tensor* shares,
+                      const bea_tensor* free_pages, const bea_tensor* n_free, int64_t page_size,
+                      const bea_tensor* block_table_out, const bea_tensor* shares_out, const bea_tensor* free_pages_out,
+                      const bea_tensor* page_map, const bea_tensor* copies, void* stream);
+
+/*
+ * Copies the first tokens of pages to other pages, in every cache alike.
+ *   copies     [m, 3] i32, rows one behind the other: (page, new page, tokens);
+ *              tokens <= 0: no copy. No new page may be a page of another copy.
+ *   caches     HOST array of n_caches tensors [num_pages, page_size, h_kv, d]
+ *              (keys and values of every layer), bf16 or f32, one shape, own
+ *              strides, none overlapping; read during the call only
+ * d * element size must be a multiple of 16 bytes. A copy with a page outside the
+ * cache, from a page to itself, or of more than page_size tokens is left out and
+ * reported.
+ */
+int bea_paged_copy(const bea_tensor* copies, const bea_tensor* caches, int n_caches, void* stream);
+
+/*
  * Synchronises `stream`, reads the device status word of the current device
  * and clears it. Returns BEA_OK, BEA_ERR_TIMEOUT if any kernel since the last
  * read gave up a wait, BEA_ERR_UNSUPPORTED if a kernel met a configuration it
