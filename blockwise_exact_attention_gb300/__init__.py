@@ -21,7 +21,8 @@ Public API (all calls run in libbea.so's CUDA kernels on the current stream):
 * ``paged_plan / paged_write / paged_decode`` (and ``PagedKVCache``, which
   holds their state): a paged K/V cache, from request lengths to the attention
   of one new token per request.
-* ``paged_fork / paged_free / paged_compact / paged_copy``: rows that share pages.
+* ``paged_fork / paged_free / paged_compact / paged_copy``: rows that share pages;
+  ``paged_decode_shared``: their common first keys read once for a group.
 
 The seeded input generators live in ``workloads`` and import nothing else.
 """
@@ -59,6 +60,8 @@ from .paged import (  # noqa: F401
     paged_compact,
     paged_copy,
     paged_decode,
+    paged_decode_shared,
+    paged_decode_shared_workspace_bytes,
     paged_decode_workspace_bytes,
     paged_fork,
     paged_free,

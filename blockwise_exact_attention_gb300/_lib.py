@@ -60,6 +60,8 @@ EXPORTS = (
     "bea_paged_write",
     "bea_paged_decode_workspace_size",
     "bea_paged_decode",
+    "bea_paged_decode_shared_workspace_size",
+    "bea_paged_decode_shared",
     "bea_paged_fork",
     "bea_paged_free",
     "bea_paged_compact",
@@ -177,6 +179,10 @@ def load() -> ctypes.CDLL:
     lib.bea_paged_decode_workspace_size.restype = sz
     lib.bea_paged_decode.argtypes = [P, P, P, P, P, P, P, f, i, vp, sz, vp]
     lib.bea_paged_decode.restype = i
+    lib.bea_paged_decode_shared_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64]
+    lib.bea_paged_decode_shared_workspace_size.restype = sz
+    lib.bea_paged_decode_shared.argtypes = [P, P, P, P, P, P, P, P, P, f, vp, sz, vp]
+    lib.bea_paged_decode_shared.restype = i
     lib.bea_paged_fork.argtypes = [P, P, P, P, P, P, P, i64, P, P, P, P, vp]
     lib.bea_paged_fork.restype = i
     lib.bea_paged_free.argtypes = [P, P, P, P, P, P, i64, P, P, P, vp]

@@ -14,6 +14,7 @@
 #include "common.cuh"
 
 namespace bea {
+struct PagedDecodeParams;
 namespace abi {
 
 // Records the launch count of a successful call (bea_last_launch_count) and
@@ -36,6 +37,7 @@ int check_qkv(const bea_tensor* q, const bea_tensor* k, const bea_tensor* v, flo
 int check_lse(const bea_tensor* lse, const AttnDims& a);
 // TMA descriptor over a [n, l, h, d] bf16 tensor: 64-column boxes of 128 rows, 128-byte swizzle.
 int make_seq_map(const bea_tensor* t, CUtensorMap* map);
+int make_page_map(const bea_tensor* t, int rows, CUtensorMap* map);
 int make_acc_map(const bea_tensor* t, CUtensorMap* map);
 int make_grad_map(const bea_tensor* g, CUtensorMap* map);
 
@@ -46,6 +48,10 @@ bool broadcast(const bea_tensor* t);
 bool same_strides(const bea_tensor* a, const bea_tensor* b);
 // A [num_pages, page_size, h_kv, d] pair of caches.
 int check_caches(const bea_tensor* k, const bea_tensor* v);
+// What the single-token attention calls have in common, all but the workspace and the status word.
+int check_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_tensor* v_cache,
+                       const bea_tensor* block_table, const bea_tensor* lens, const bea_tensor* out,
+                       const bea_tensor* lse, float softmax_scale, int window_left, PagedDecodeParams* p);
 // An (input, output) pair of the rotary calls, of `like`'s dtype, batch, length and head dim.
 int check_rope_pair(const bea_tensor* x, const bea_tensor* y, const bea_tensor* like);
 // A frequency (radians per position) as the fraction of a turn per position, times 2^64.

@@ -191,7 +191,7 @@ int check_lse(const bea_tensor* lse, const AttnDims& a) {
 // [n, l, h, d] tensor -> TMA descriptor with boxes of 128 rows x 128 bytes
 // (box_cols elements of es bytes), 128-byte swizzled.
 static int make_map4(const bea_tensor* t, CUtensorMapDataType dt, int64_t es, cuuint32_t box_cols,
-                     CUtensorMap* map) {
+                     CUtensorMap* map, cuuint32_t box_rows = 128) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   int rc = get_encoder(&enc);
   if (rc) return rc;
@@ -202,7 +202,7 @@ static int make_map4(const bea_tensor* t, CUtensorMapDataType dt, int64_t es, cu
   const cuuint64_t s_n = (n > 1) ? t->stride[0] * es : s_l * l;
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)hh, (cuuint64_t)l, (cuuint64_t)n};
   cuuint64_t strides[3] = {s_h, s_l, s_n};
-  cuuint32_t box[4] = {box_cols, 1, 128, 1};
+  cuuint32_t box[4] = {box_cols, 1, box_rows, 1};
   cuuint32_t es1[4] = {1, 1, 1, 1};
   CUresult r = enc(map, dt, 4, t->data, dims, strides, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -212,6 +212,11 @@ static int make_map4(const bea_tensor* t, CUtensorMapDataType dt, int64_t es, cu
 // bf16 [n, l, h, d]: 64-column boxes (the layout the MMA descriptors expect; also the fused
 // ring step's bf16 final copy)
 int make_seq_map(const bea_tensor* t, CUtensorMap* map) { return make_map4(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, map); }
+
+// bf16 [num_pages, page_size, h_kv, d]: 64-column boxes of some tokens of a page
+int make_page_map(const bea_tensor* t, int rows, CUtensorMap* map) {
+  return make_map4(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, map, (cuuint32_t)rows);
+}
 
 // dK / dV of the backward: bf16 64-column or fp32 32-column boxes
 int make_grad_map(const bea_tensor* g, CUtensorMap* map) {

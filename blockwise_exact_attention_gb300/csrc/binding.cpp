@@ -564,6 +564,41 @@ PyObject* py_paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// paged_decode_shared(q, k_cache, v_cache, block_table, lens, group_rows, shared_lens, scale, out, lse, f32_out, workspace)
+// -> (out, lse)
+PyObject* py_paged_decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments("paged_decode_shared", n, 12);
+  Tensor t[7];
+  for (int i = 0; i < 7; ++i) t[i] = tensor(a[i]);
+  const Tensor &q = t[0], &kc = t[1], &table = t[3];
+  TORCH_CHECK_VALUE(q.dim() == 4 && kc.dim() == 4 && table.dim() == 2 && t[6].dim() == 1,
+                    "paged_decode_shared: q [n, 1, h, d], caches [pages, page_size, h_kv, d], block_table [n, max_pages], "
+                    "shared_lens [groups]");
+  const float scale = static_cast<float>(real(a[7]));
+  Tensor out = to_write(tensor(a[8], true)), lse = to_write(tensor(a[9], true)), ws = tensor(a[11], true);
+  if (!out.defined()) out = empty(q.sizes(), integer(a[10]) != 0 ? at::kFloat : q.scalar_type(), q);
+  if (!lse.defined()) lse = empty({q.size(0), q.size(2), 1}, at::kFloat, q);
+  if (!ws.defined()) {
+    const size_t need = bea_paged_decode_shared_workspace_size(q.size(0), q.size(2), kc.size(2), q.size(3),
+                                                               table.size(1) * kc.size(1), t[6].size(0));
+    if (need > 0) ws = empty({static_cast<int64_t>(need)}, at::kByte, q);
+  }
+  Call c;
+  const bea_tensor* r[9];
+  for (int i = 0; i < 7; ++i) r[i] = c.add(t[i]);
+  r[7] = c.add(out);
+  r[8] = c.add(lse);
+  TORCH_CHECK_VALUE(!ws.defined() || (ws.is_cuda() && ws.get_device() == q.get_device() && ws.is_contiguous()),
+                    "paged_decode_shared: the workspace has to be contiguous and on the tensors' device");
+  finish(counted(bea_paged_decode_shared(r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], scale,
+                                         ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, c.stream())),
+         "paged_decode_shared");
+  written({out, lse});
+  return tuple({out, lse});
+  END_HANDLE_TH_ERRORS
+}
+
 // ---- shared pages ------------------------------------------------------------------
 
 // The i-th of a call's outputs: given, or new.
@@ -701,6 +736,7 @@ PyMethodDef g_methods[] = {method<py_setup>("setup"),
                            method<py_paged_plan>("paged_plan"),
                            method<py_paged_write>("paged_write"),
                            method<py_paged_decode>("paged_decode"),
+                           method<py_paged_decode_shared>("paged_decode_shared"),
                            method<py_paged_fork>("paged_fork"),
                            method<py_paged_free>("paged_free"),
                            method<py_paged_compact>("paged_compact"),

@@ -86,6 +86,7 @@ struct PagedDecodeParams {
   const int32_t* table;
   int64_t table_stride;
   const int32_t* lens;
+  const int32_t* skip;  // null, or the number of first keys of each request that are left out (bf16; left unbounded)
   void* ws;
   uint32_t* status;
 };

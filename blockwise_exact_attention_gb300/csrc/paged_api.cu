@@ -55,6 +55,52 @@ int check_caches(const bea_tensor* k, const bea_tensor* v) {
   return BEA_OK;
 }
 
+int check_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_tensor* v_cache,
+                       const bea_tensor* block_table, const bea_tensor* lens, const bea_tensor* out,
+                       const bea_tensor* lse, float softmax_scale, int window_left, PagedDecodeParams* p) {
+  int rc;
+  if ((rc = check_tensor(q, 4)) || (rc = check_caches(k_cache, v_cache)) || (rc = check_ints(block_table, 2)) ||
+      (rc = check_ints(lens, 1)) || (rc = check_tensor(out, 4)) || (rc = check_tensor(lse, 3)))
+    return rc;
+  if (q->dtype != k_cache->dtype || lse->dtype != BEA_F32) return BEA_ERR_DTYPE;
+  if (out->dtype != q->dtype && out->dtype != BEA_F32) return BEA_ERR_DTYPE;
+  const int64_t n = q->shape[0], h = q->shape[2], d = q->shape[3], hkv = k_cache->shape[2];
+  if (q->shape[1] != 1 || !same_shape(out, q)) return BEA_ERR_SHAPE;
+  if (lse->shape[0] != n || lse->shape[1] != h || lse->shape[2] != 1) return BEA_ERR_SHAPE;
+  if (block_table->shape[0] != n || lens->shape[0] != n) return BEA_ERR_SHAPE;
+  if (k_cache->shape[3] != d || hkv <= 0 || h % hkv != 0) return BEA_ERR_SHAPE;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f) || window_left < -1) return BEA_ERR_ARG;
+  if (broadcast(out) || broadcast(lse)) return BEA_ERR_ARG;
+  if (q->dtype == BEA_BF16 ? (d != 64 && d != 128) : (d < 4 || d > 128 || d % 4 != 0)) return BEA_ERR_UNSUPPORTED;
+  if (n * h > (int64_t(1) << 31) - 1 || h * d > (int64_t(1) << 31) - 1) return BEA_ERR_SHAPE;
+  const int64_t page = k_cache->shape[1], max_pages = block_table->shape[1];
+  const int64_t max_keys = max_pages * page;
+  if (max_keys >= bea::kUnbounded) return BEA_ERR_SHAPE;
+  if (!bea::paged_decode_fits(hkv, d, q->dtype == BEA_F32, max_keys)) return BEA_ERR_SHAPE;
+  std::memset(p, 0, sizeof(*p));
+  p->n = (int)n;
+  p->h = (int)h;
+  p->hkv = (int)hkv;
+  p->d = (int)d;
+  p->num_pages = (int)k_cache->shape[0];
+  p->page = (int)page;
+  p->page_shift = (page & (page - 1)) == 0 ? __builtin_ctzll((unsigned long long)page) : -1;
+  p->max_pages = (int)max_pages;
+  p->left = window_left < 0 || window_left > bea::kUnbounded ? bea::kUnbounded : window_left;
+  p->is_f32 = q->dtype == BEA_F32;
+  p->out_is_f32 = out->dtype == BEA_F32;
+  p->scale = softmax_scale;
+  p->q = seq4(q);
+  p->out = seq4(out);
+  p->kc = seq4(k_cache);
+  p->vc = seq4(v_cache);
+  p->lse = lse3(lse);
+  p->table = static_cast<const int32_t*>(block_table->data);
+  p->table_stride = block_table->stride[0];
+  p->lens = static_cast<const int32_t*>(lens->data);
+  return BEA_OK;
+}
+
 // One of rope's (input, output) pairs.
 int check_rope_pair(const bea_tensor* x, const bea_tensor* y, const bea_tensor* like) {
   int rc;
@@ -219,52 +265,14 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
                      const bea_tensor* block_table, const bea_tensor* lens, const bea_tensor* out,
                      const bea_tensor* lse, float softmax_scale, int window_left, void* workspace,
                      size_t workspace_bytes, void* stream) {
-  int rc;
-  if ((rc = check_tensor(q, 4)) || (rc = check_caches(k_cache, v_cache)) || (rc = check_ints(block_table, 2)) ||
-      (rc = check_ints(lens, 1)) || (rc = check_tensor(out, 4)) || (rc = check_tensor(lse, 3)))
-    return rc;
-  if (q->dtype != k_cache->dtype || lse->dtype != BEA_F32) return BEA_ERR_DTYPE;
-  if (out->dtype != q->dtype && out->dtype != BEA_F32) return BEA_ERR_DTYPE;
-  const int64_t n = q->shape[0], h = q->shape[2], d = q->shape[3], hkv = k_cache->shape[2];
-  if (q->shape[1] != 1 || !same_shape(out, q)) return BEA_ERR_SHAPE;
-  if (lse->shape[0] != n || lse->shape[1] != h || lse->shape[2] != 1) return BEA_ERR_SHAPE;
-  if (block_table->shape[0] != n || lens->shape[0] != n) return BEA_ERR_SHAPE;
-  if (k_cache->shape[3] != d || hkv <= 0 || h % hkv != 0) return BEA_ERR_SHAPE;
-  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f) || window_left < -1) return BEA_ERR_ARG;
-  if (broadcast(out) || broadcast(lse)) return BEA_ERR_ARG;
-  if (q->dtype == BEA_BF16 ? (d != 64 && d != 128) : (d < 4 || d > 128 || d % 4 != 0)) return BEA_ERR_UNSUPPORTED;
-  if (n * h > (int64_t(1) << 31) - 1 || h * d > (int64_t(1) << 31) - 1) return BEA_ERR_SHAPE;
-  const int64_t page = k_cache->shape[1], max_pages = block_table->shape[1];
-  const int64_t max_keys = max_pages * page;
-  if (max_keys >= bea::kUnbounded) return BEA_ERR_SHAPE;
-  if (!bea::paged_decode_fits(hkv, d, q->dtype == BEA_F32, max_keys)) return BEA_ERR_SHAPE;
-  const size_t need = bea::paged_decode_workspace(h, hkv, d, max_keys);
+  bea::PagedDecodeParams p;
+  int rc = check_paged_decode(q, k_cache, v_cache, block_table, lens, out, lse, softmax_scale, window_left, &p);
+  if (rc) return rc;
+  const size_t need = bea::paged_decode_workspace(p.h, p.hkv, p.d, (int64_t)p.max_pages * p.page);
   if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < need))
     return BEA_ERR_WORKSPACE;
-  bea::PagedDecodeParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.n = (int)n;
-  p.h = (int)h;
-  p.hkv = (int)hkv;
-  p.d = (int)d;
-  p.num_pages = (int)k_cache->shape[0];
-  p.page = (int)page;
-  p.page_shift = (page & (page - 1)) == 0 ? __builtin_ctzll((unsigned long long)page) : -1;
-  p.max_pages = (int)max_pages;
-  p.left = window_left < 0 || window_left > bea::kUnbounded ? bea::kUnbounded : window_left;
-  p.is_f32 = q->dtype == BEA_F32;
-  p.out_is_f32 = out->dtype == BEA_F32;
-  p.scale = softmax_scale;
-  p.q = seq4(q);
-  p.out = seq4(out);
-  p.kc = seq4(k_cache);
-  p.vc = seq4(v_cache);
-  p.lse = lse3(lse);
-  p.table = ints(block_table);
-  p.table_stride = block_table->stride[0];
-  p.lens = ints(lens);
   p.ws = workspace;
-  if (n == 0 || h == 0) return finish(cudaSuccess, 0);
+  if (p.n == 0 || p.h == 0) return finish(cudaSuccess, 0);
   if ((rc = status_ptr_for_current_device(&p.status))) return rc;
   int launches = 0;
   return finish(bea::launch_paged_decode(p, static_cast<cudaStream_t>(stream), &launches), launches);

@@ -214,13 +214,14 @@ __device__ __forceinline__ int last_below(int n, int x, F key) {
   return lo;
 }
 
-template <bool kF32, int kD, int kHd>
+// kSkip: requests' first keys are left out (another kernel's), p.skip of each.
+template <bool kF32, int kD, int kHd, bool kSkip>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p, const __grid_constant__ Launch a) {
   using C = Cfg<kF32, kD, kHd>;
   extern __shared__ __align__(128) uint8_t smem[];
   // requests with a visible key, in order: tiles of a unit summed over those before, number, length
-  __shared__ int pre[kMaxRequests + 1], who[kMaxRequests], lens[kMaxRequests];
+  __shared__ int pre[kMaxRequests + 1], who[kMaxRequests], lens[kMaxRequests], skips[kSkip ? kMaxRequests : 1];
   __shared__ int4 warp_sums[kWarps];  // of a warp's requests: tiles, how many have some, the most
   __shared__ uint32_t masks[kWarps][C::kStages];
   __shared__ float2 ml[kWarps][2][16];  // of a warp's first and last part
@@ -243,7 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (blockIdx.x == 0) report_status(p.status, BEA_STATUS_PAGES);
       len = len < 0 ? 0 : most;
     }
-    const int tiles = len > 0 ? (len + C::kKeys - 1) / C::kKeys - first_key(len, p.left) / C::kKeys : 0;
+    const int skip = kSkip && r < a.n ? p.skip[a.r0 + r] : 0;
+    const int begin = kSkip ? skip : first_key(len, p.left);
+    const int tiles = len > begin ? (len + C::kKeys - 1) / C::kKeys - begin / C::kKeys : 0;
     const uint32_t some = __ballot_sync(~0u, tiles > 0);
     const int most_tiles = __reduce_max_sync(~0u, tiles);
     int inc = tiles;
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pre[at] = at_tiles;
       who[at] = a.r0 + r;
       lens[at] = len;
+      if constexpr (kSkip) skips[at] = skip;
     }
     if (r0 + kThreads < a.n) __syncthreads();  // before warp_sums is written again
   }
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (count < a.n) {
     for (int r = blockIdx.x; r < a.n; r += gridDim.x) {
       const int len = p.lens[a.r0 + r];
-      if (len > 0 && most > 0) continue;
+      if (min(len, most) > (kSkip ? p.skip[a.r0 + r] : 0)) continue;
       const int64_t b = a.r0 + r;
       for (int i = tid; i < p.h * p.d; i += kThreads) {
         const int hh = i / p.d;
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = w0 + i;
     const int k = last_below(count, t, tiles_before);
     const int cnt = pre[k + 1] - pre[k], in = t - pre[k] * units, unit = in / cnt;
-    const int len = lens[k], first = first_key(len, p.left);
+    const int len = lens[k], first = kSkip ? skips[k] : first_key(len, p.left);
     d_b = who[k];
     d_hk = unit;
     d_key = (first / C::kKeys + (in - unit * cnt)) * C::kKeys;
@@ -865,14 +869,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 // The most that one request's units can cost.
 int64_t request_cost(int64_t keys, int64_t units, int tile) { return ((keys + tile - 1) / tile + 1 + kUnitCost) * units; }
 
-template <bool kF32, int kD, int kHd>
+template <bool kF32, int kD, int kHd, bool kSkip = false>
 cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   using C = Cfg<kF32, kD, kHd>;
   static PerContext<int> cache;
   int ctas = 0;
   cudaError_t e = cache.get(
       [](int* v) {
-        cudaError_t r = cudaFuncSetAttribute(paged_decode_kernel<kF32, kD, kHd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t r = cudaFuncSetAttribute(paged_decode_kernel<kF32, kD, kHd, kSkip>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmem);
         if (r != cudaSuccess) return r;
         int sms = 0;
@@ -900,7 +904,7 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
     for (int64_t r0 = 0; r0 < p.n; r0 += at_once) {
       a.r0 = (int)r0;
       a.n = (int)(p.n - r0 < at_once ? p.n - r0 : at_once);
-      if ((e = launch_dependent(paged_decode_kernel<kF32, kD, kHd>, dim3(grid), kThreads, C::kSmem, s, p, a)) != cudaSuccess)
+      if ((e = launch_dependent(paged_decode_kernel<kF32, kD, kHd, kSkip>, dim3(grid), kThreads, C::kSmem, s, p, a)) != cudaSuccess)
         return e;
       *nlaunch += 1;
       if (!a.split) continue;
@@ -937,6 +941,8 @@ template <bool kF32, int kD>
 static cudaError_t launch_heads(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   const int group = p.h / p.hkv;
   if constexpr (!kF32) {
+    if (p.skip != nullptr)
+      return group <= 8 ? launch<false, kD, 8, true>(p, s, nlaunch) : launch<false, kD, 16, true>(p, s, nlaunch);
     return group <= 8 ? launch<false, kD, 8>(p, s, nlaunch) : launch<false, kD, 16>(p, s, nlaunch);
   } else {
     return group == 1   ? launch<true, kD, 1>(p, s, nlaunch)

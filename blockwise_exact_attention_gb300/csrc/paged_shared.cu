@@ -1,0 +1,787 @@
+// Attention of one new token per request, where groups of requests have their
+// first keys in common: those are read once for the whole group.
+//
+// The keys of request r are a prefix that its group shares and its own rest. The
+// prefix is a product of many queries with the same keys: the queries of all the
+// group's requests, and of the g = h / h_kv heads that read a K/V head, are the rows
+// of one matrix, so it runs like the forward, on the tensor cores:
+//   S = Q K^T, P = exp2(scale S - m) with a running maximum m, O += P V, l += sum P.
+// Its bytes are the prefix once, its flops 4 d a (query row, key): from 230 rows a K/V
+// head on the products are the bound, not HBM. The rest is paged_decode's kernel, told
+// where each request's own keys begin. A last kernel joins the two by their maxima and
+// sums, in a fixed order.
+//
+// Only whole tiles of 128 keys count as prefix, and only up to the shortest request of
+// the group and the first page that lies outside the cache: what is left over is the
+// requests' own. So the kernel has no masks, and what the shared path leaves out
+// the other one computes.
+//
+// The prefix kernel. A UNIT is up to 256 query rows of one (group, K/V head), its keys
+// a list of tiles; the units' tiles, one after another, are cut into equal runs, one
+// per CTA. Warps as in the forward: 0-3 and 4-7 softmax of 128 rows each (thread =
+// row), 8 and 10 load K and V tiles by TMA, a box per page, 9 issues the products.
+// With more than 128 rows both halves meet every tile; with up to 128 rows both have the
+// same rows and take the tiles in turn, which keeps the tensor core and the exponentials
+// overlapped, and each half writes its own part.
+//
+// P enters the second product as two bf16 terms, 16 bits of it (cut off, then the rest
+// rounded; the rest is kept above 0, by 2^-24 of P at most, so that an infinite value
+// stays infinite). That is half as many products again, which cost nothing while HBM is
+// the bound; one term alone would be off by up to 2^-9 of the output.
+#include <cuda_bf16.h>
+
+#include "launch_cache.cuh"
+#include "paged_shared.cuh"
+#include "ptx.cuh"
+
+namespace bea {
+namespace {
+
+constexpr int kTile = 128;      // keys of a tile, rows of a half
+constexpr int kUnitRows = 256;  // of a unit
+constexpr int kMaxCtas = 160;   // one per SM
+constexpr int kThreads = 384;
+// As in the forward: 256 threads at 200 registers and 128 at 104 are what 384 are launched with.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch, "register split");
+constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
+constexpr float kRescale = 8.f;  // log2: O is rescaled only when a maximum grows by more
+constexpr uint32_t kPReadyBar = 1, kPReadyThreads = 128 + 32, kEpiBar = 3, kBothBar = 5;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// Steps of a run at least, as long as there are fewer than the GPU has CTAs.
+constexpr int kMinSteps = 2;
+
+template <int D>
+struct Cfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kKOff = 2 * kTileBytes;
+  static constexpr int kVOff = kKOff + kStages * kTileBytes;
+  static constexpr int kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr int kNumBars = 1 + 4 * kStages + 2 + 2 + 1;
+  static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
+  static constexpr int kSmem = kTableOff + 3 * (kMaxGroups + 1) * 4 + 1024 /*alignment*/;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
+  static constexpr uint32_t kVLbo = 64 * 128 * 2;
+};
+
+// ---- schedule ----------------------------------------------------------------------
+
+// A group as the setup finds it: its rows, the first of them that has keys, the tiles that are shared.
+struct Group {
+  int row0, rows, owner, tiles;
+};
+
+// Of a group: units of two halves, rows of a last unit of one half (0: none), and steps, a step being a tile of a unit of
+// two halves or two tiles of the other.
+struct Shape {
+  int rows, twos, one, tiles, one_steps;
+  __host__ __device__ Shape(int q_rows, int t) : rows(q_rows), tiles(t) {
+    twos = q_rows / kUnitRows;
+    one = q_rows - twos * kUnitRows;
+    if (one > kTile) one = 0, ++twos;
+    if (t == 0) twos = one = 0;
+    one_steps = one > 0 ? (t + 1) / 2 : 0;
+  }
+  __host__ __device__ int steps() const { return twos * tiles + one_steps; }       // of a K/V head
+  __host__ __device__ int part_rows() const { return twos * kUnitRows + 2 * one; }  // rows of its parts
+};
+
+// Where the groups' steps and parts' rows begin, [groups + 1] each; and the runs.
+struct Schedule {
+  const int *steps, *rows;
+  int total, ctas, share, over;
+  __device__ int begin(int c) const { return share * c + min(c, over); }
+  __device__ int cta_of(int v) const { return v < over * (share + 1) ? v / (share + 1) : over + (v - over * (share + 1)) / share; }
+};
+
+// A run's piece in one unit: steps [a, b) of it.
+struct Seg {
+  Group g;
+  int hk, q0, rows, two, a, b, part;  // q0: first query row in the group; part: first row of the unit's parts
+  __device__ int first(int t) const { return two ? a : 2 * a + t; }  // half t's first tile
+  __device__ int count(int t) const {                                // and how many it has
+    if (two) return b - a;
+    const int last = min(2 * b, g.tiles);
+    return max(0, (last - 2 * a - t + 1) / 2);
+  }
+  __device__ int tile0() const { return two ? a : 2 * a; }
+  __device__ int tile1() const { return two ? b : min(2 * b, g.tiles); }
+};
+
+__device__ __forceinline__ Seg seg_at(const Schedule& s, const Group* groups, int n_groups, int heads, int v, int end) {
+  int lo = 0, hi = n_groups - 1;  // the last group whose steps begin at v or before
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.steps[mid] <= v)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  Seg r;
+  r.g = groups[lo];
+  const Shape sh(r.g.rows * heads, r.g.tiles);
+  const int each = sh.steps(), in_group = v - s.steps[lo];
+  r.hk = in_group / each;
+  const int in = in_group - r.hk * each, u = min(in / sh.tiles, sh.twos);
+  r.two = u < sh.twos;
+  r.q0 = u * kUnitRows;
+  r.rows = r.two ? min(kUnitRows, sh.rows - r.q0) : sh.one;
+  r.a = in - u * sh.tiles;
+  const int all = r.two ? sh.tiles : sh.one_steps;
+  r.b = min(all, r.a + (end - v));
+  r.part = s.rows[lo] + r.hk * sh.part_rows() + r.q0;
+  return r;
+}
+
+// Workspace.
+struct Layout {
+  size_t skip, groups, tables, suffix, suffix_lse, decode, ml, o, total;
+};
+__host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+inline Layout layout(int64_t n, int64_t h, int64_t d, int64_t groups, size_t decode_bytes) {
+  Layout w;
+  const size_t rows = 2 * (size_t)(n * h) + (size_t)kUnitRows * kMaxCtas;
+  w.skip = 0;
+  w.groups = w.skip + up256((size_t)n * 4);
+  w.tables = w.groups + up256((size_t)groups * sizeof(Group));
+  w.suffix = w.tables + up256(2 * (size_t)(groups + 1) * 4);
+  w.suffix_lse = w.suffix + up256((size_t)n * h * d * 4);
+  w.decode = w.suffix_lse + up256((size_t)n * h * 4);
+  w.ml = w.decode + up256(decode_bytes);
+  w.o = w.ml + up256(rows * 8);
+  w.total = w.o + up256(rows * d * 4);
+  return w;
+}
+
+struct Args {
+  int n, h, hkv, d, groups, max_keys, num_pages, page, box, max_ctas;
+  const int32_t *group_rows, *shared_lens, *lens, *table;
+  int64_t table_stride;
+  Seq4 q, out;
+  Lse3 lse;
+  int out_is_f32;
+  float sl2;
+  int* skip;
+  Group* group;
+  int* tables;  // [groups + 1] first steps, [groups + 1] first part rows
+  const float *suffix, *suffix_lse;
+  float2* ml;
+  float* o;
+  uint32_t* status;
+};
+
+// ---- setup -------------------------------------------------------------------------
+
+constexpr int kSetupThreads = 512;
+
+// The least of the block's values, to all threads.
+__device__ __forceinline__ int block_min(int x, int* words) {
+  x = __reduce_min_sync(~0u, x);
+  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = words[threadIdx.x & (kSetupThreads / 32 - 1)];
+  x = __reduce_min_sync(~0u, x);
+  __syncthreads();  // `words` is free
+  return x;
+}
+
+// A block per group: its shortest request, how much is shared, and where each request's own keys begin.
+__global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __grid_constant__ Args p) {
+  __shared__ int words[kSetupThreads / 32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int g = blockIdx.x, tid = threadIdx.x;
+  // rows that are not in ascending order make no groups at all
+  bool wrong = false;
+  for (int i = tid; i <= p.groups; i += kSetupThreads) {
+    const int x = p.group_rows[i];
+    wrong = wrong || x < 0 || x > p.n || (i > 0 && p.group_rows[i - 1] > x);
+  }
+  const bool bad = __syncthreads_or(wrong);
+  const int r0 = bad ? 0 : p.group_rows[g], r1 = bad ? 0 : p.group_rows[g + 1];
+  if (g == 0) {  // rows of no group
+    const int a = bad ? p.n : p.group_rows[0], b = bad ? p.n : p.group_rows[p.groups];
+    for (int r = tid; r < p.n; r += kSetupThreads)
+      if (r < a || r >= b) p.skip[r] = 0;
+    if (bad && tid == 0) report_status(p.status, BEA_STATUS_PAGES);
+  }
+  int shortest = INT32_MAX, owner = INT32_MAX, live = 0;
+  for (int r = r0 + tid; r < r1; r += kSetupThreads) {
+    const int len = p.lens[r];
+    if (len <= 0) continue;
+    shortest = min(shortest, len);
+    owner = min(owner, r);
+    ++live;
+  }
+  shortest = block_min(shortest, words);
+  owner = block_min(owner, words);
+  const bool several = __syncthreads_count(live > 1) > 0 || __syncthreads_count(live > 0) > 1;
+  int shared = p.shared_lens[g];
+  if (shared < 0) {
+    if (tid == 0) report_status(p.status, BEA_STATUS_PAGES);
+    shared = 0;
+  }
+  // nothing is shared by one request
+  int tiles = several ? min(min(shared, shortest), p.max_keys) / kTile : 0;
+  if (tiles > 0) {
+    const int32_t* entries = p.table + owner * p.table_stride;
+    const int pages = (int)(((int64_t)tiles * kTile + p.page - 1) / p.page);
+    int first_bad = INT32_MAX;
+    for (int i = tid; i < pages; i += kSetupThreads) {
+      const int id = entries[i];
+      if (id < 0 || id >= p.num_pages) first_bad = min(first_bad, i);
+    }
+    first_bad = block_min(first_bad, words);
+    if (first_bad < pages) tiles = (int)((int64_t)first_bad * p.page / kTile);
+  }
+  for (int r = r0 + tid; r < r1; r += kSetupThreads) p.skip[r] = p.lens[r] > 0 ? tiles * kTile : 0;
+  if (tid == 0) p.group[g] = Group{r0, r1 - r0, owner, tiles};
+}
+
+// ---- the prefix --------------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                         const __grid_constant__ Args p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t *q_full = bars, *k_full = bars + 1, *v_full = k_full + C::kStages, *k_empty = v_full + C::kStages,
+           *v_empty = k_empty + C::kStages, *s_full = v_empty + C::kStages, *o_full = s_full + 2, *mma_done = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* first_step = reinterpret_cast<int*>(smem + C::kTableOff);
+  int* first_row = first_step + kMaxGroups + 1;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int heads = p.h / p.hkv;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bars[i], i == 0 ? 256 : 1);
+    fence_mbar_init();
+  }
+  if (warp == kKWarp && lane == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (warp == kVWarp) {  // sums of steps and part rows over the groups
+    int steps = 0, rows = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      int s = 0, r = 0;
+      if (g0 + lane < p.groups) {
+        const Group g = p.group[g0 + lane];
+        const Shape sh(g.rows * heads, g.tiles);
+        s = sh.steps() * p.hkv;
+        r = sh.part_rows() * p.hkv;
+      }
+      int si = s, ri = r;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, si, o), y = __shfl_up_sync(~0u, ri, o);
+        if (lane >= o) si += x, ri += y;
+      }
+      if (g0 + lane < p.groups) {
+        first_step[g0 + lane] = steps + si - s;
+        first_row[g0 + lane] = rows + ri - r;
+      }
+      steps += __shfl_sync(~0u, si, 31);
+      rows += __shfl_sync(~0u, ri, 31);
+    }
+    if (lane == 0) first_step[p.groups] = steps, first_row[p.groups] = rows;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Schedule sc;
+  sc.steps = first_step;
+  sc.rows = first_row;
+  sc.total = first_step[p.groups];
+  sc.ctas = min((int)gridDim.x, max(1, sc.total / kMinSteps));
+  sc.share = sc.total / sc.ctas;
+  sc.over = sc.total - sc.share * sc.ctas;
+  const int cta = blockIdx.x;
+  const int run0 = cta < sc.ctas ? sc.begin(cta) : 0, run1 = cta < sc.ctas ? sc.begin(cta + 1) : 0;
+  if (cta == 0)  // for the kernel that joins
+    for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
+      p.tables[i] = first_step[i];
+      p.tables[p.groups + 1 + i] = first_row[i];
+    }
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kKWarp || warp == kVWarp) {
+      // ========================== loads: a box per page and 64 columns, dealt to the lanes ==========================
+      const bool is_k = warp == kKWarp;
+      const CUtensorMap* map = is_k ? &tk : &tv;
+      uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+      uint8_t* area = smem + (is_k ? C::kKOff : C::kVOff);
+      const int boxes = kTile / p.box;  // of 64 columns of a tile
+      constexpr int kMost = kTile / 32;
+      bool ok = true;
+      int it = 0;
+      for (int v = run0; ok && v < run1;) {
+        const Seg sg = seg_at(sc, p.group, p.groups, heads, v, run1);
+        v += sg.b - sg.a;
+        const int32_t* entries = p.table + sg.g.owner * p.table_stride;
+        int id[kMost], off[kMost];  // of this lane's boxes in the next tile
+        auto look_up = [&](int j) {
+#pragma unroll
+          for (int i = 0; i < kMost; ++i) {
+            const int b = lane + 32 * i;
+            if (b >= boxes || j >= sg.tile1()) continue;
+            const int key = j * kTile + b * p.box, pg = key / p.page;
+            off[i] = key - pg * p.page;
+            id[i] = entries[pg];
+          }
+        };
+        look_up(sg.tile0());
+        for (int j = sg.tile0(); j < sg.tile1(); ++j, ++it) {
+          const int s = it % C::kStages;
+          if (it >= C::kStages && !(ok = warp_wait_parity(&empty[s], ((it / C::kStages) & 1) ^ 1, abort_flag, p.status))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], C::kTileBytes);
+          __syncwarp();
+          uint8_t* dst = area + s * C::kTileBytes;
+#pragma unroll
+          for (int i = 0; i < kMost; ++i) {
+            const int b = lane + 32 * i;
+            if (b >= boxes) continue;
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_4d(dst + x * 16384 + b * p.box * 128, map, &full[s], x * 64, sg.hk, off[i], id[i]);
+          }
+          look_up(j + 1);
+        }
+      }
+      // loads in flight must land before the CTA's shared memory goes away
+      for (int k = max(0, it - C::kStages); k < it; ++k) {
+        volatile int no_abort = 0;
+        wait_parity(&full[k % C::kStages], (k / C::kStages) & 1, &no_abort, p.status, 200000000ull);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ========================== products ==========================
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::kVOff), C::kVLbo, 1024);
+      bool ok = true;
+      int base = 0, seg = 0;
+      for (int v = run0; v < run1; ++seg) {
+        const Seg sg = seg_at(sc, p.group, p.groups, heads, v, run1);
+        v += sg.b - sg.a;
+        const int most = sg.count(0);  // the second half has as many tiles or one less
+        // half t's x-th tile is the ring's slot(t, x)-th
+        auto slot = [&](int t, int x) { return base + (sg.two ? x : 2 * x + t); };
+        auto issue_s = [&](int t, int x) {
+          const int i = slot(t, x), s = i % C::kStages;
+          if (ok) ok = warp_wait_parity(&k_full[s], (i / C::kStages) & 1, abort_flag, p.status);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t qd = sdesc_add(q_desc, sg.two ? t * C::kTileBytes : 0), kd = sdesc_add(k_desc, s * C::kTileBytes);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = (k / 4) * 16384 + (k % 4) * 32;
+            umma_ss_warp(tmem + t * 128, sdesc_add(qd, at), sdesc_add(kd, at), C::kIdescS, k > 0 ? 1u : 0u);
+          }
+          umma_commit_warp(&s_full[t]);
+          if (!sg.two || t == 1) umma_commit_warp(&k_empty[s]);
+        };
+        auto issue_pv = [&](int t, int x, int n) {
+          const int i = slot(t, x), s = i % C::kStages;
+          if (ok) ok = warp_wait_parity(&v_full[s], (i / C::kStages) & 1, abort_flag, p.status);
+          named_bar_sync(kPReadyBar + t, kPReadyThreads);  // P of the tile is in TMEM; joined after an abort too
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t vd = sdesc_add(v_desc, s * C::kTileBytes);
+#pragma unroll
+          for (int term = 0; term < 2; ++term)  // the rest of P, then what was cut off it first: small terms first
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              umma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + (term == 0 ? 64 : 0) + k * 8, sdesc_add(vd, k * 2048),
+                           C::kIdescPV, term > 0 || k > 0 || x > 0 ? 1u : 0u);
+          if (!sg.two || t == 1) umma_commit_warp(&v_empty[s]);
+          if (x == n - 1) umma_commit_warp(&o_full[t]);
+        };
+        if (ok) ok = warp_wait_parity(q_full, seg & 1, abort_flag, p.status);
+        const int n1 = sg.count(1);
+        issue_s(0, 0);
+        if (n1 > 0) issue_s(1, 0);
+        for (int x = 0; x < most; ++x) {
+          issue_pv(0, x, most);
+          if (x + 1 < most) issue_s(0, x + 1);
+          if (x < n1) issue_pv(1, x, n1);
+          if (x + 1 < n1) issue_s(1, x + 1);
+        }
+        base += sg.tile1() - sg.tile0();
+      }
+      umma_commit_warp(mma_done);
+      volatile int no_abort = 0;
+      wait_parity(mma_done, 0, &no_abort, p.status, 200000000ull);
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ========================== softmax ==========================
+    const int t = warp / 4, r = threadIdx.x % 128;
+    const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_base + t * 128, o_tmem = tmem + lane_base + 256 + t * 128;
+    bool ok = true;
+    int met = 0, done = 0;  // tiles and segments of this half so far
+    for (int v = run0; v < run1;) {
+      const Seg sg = seg_at(sc, p.group, p.groups, heads, v, run1);
+      v += sg.b - sg.a;
+      // ---- the unit's queries, 128-byte swizzled like the forward's; rows behind the last are zeros ----
+      {
+        constexpr int kPieces = D / 8;
+        const int n = (sg.two ? 2 : 1) * kTile * kPieces;
+        for (int i = threadIdx.x; i < n; i += 256) {
+          const int row = i / kPieces, c = i - row * kPieces;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < sg.rows) {
+            const int qr = sg.q0 + row, b = qr / heads, hh = sg.hk * heads + (qr - b * heads);
+            x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q.ptr) + (int64_t)(sg.g.row0 + b) * p.q.sn +
+                                                (int64_t)hh * p.q.sh + c * 8);
+          }
+          const int in = row % kTile;
+          *reinterpret_cast<uint4*>(smem + (row / kTile) * C::kTileBytes + (c / 8) * 16384 + in * 128 + (((c & 7) ^ (in & 7)) << 4)) = x;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+      }
+      float m_ref = -INFINITY, l_sum = 0.f;
+      const int n = sg.count(t);
+      for (int x = 0; x < n; ++x, ++met) {
+        if (ok) ok = warp_wait_parity(&s_full[t], met & 1, abort_flag, p.status);
+        if (!ok) {
+          named_bar_sync(kPReadyBar + t, kPReadyThreads);  // aborted: the phases stay matched
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld32(s_tmem, sr);
+        tmem_ld32(s_tmem + 32, sr + 32);
+        tmem_ld32(s_tmem + 64, sr + 64);
+        tmem_ld32(s_tmem + 96, sr + 96);
+        tmem_wait_ld();
+        reg_fence<128>(sr);
+        float m8[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          float m = fmax3(__uint_as_float(sr[u]), __uint_as_float(sr[u + 8]), __uint_as_float(sr[u + 16]));
+#pragma unroll
+          for (int k = 3; k < 15; k += 2) m = fmax3(m, __uint_as_float(sr[u + 8 * k]), __uint_as_float(sr[u + 8 * k + 8]));
+          m8[u] = fmaxf(m, __uint_as_float(sr[u + 120]));
+        }
+        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * p.sl2;
+        const float m_new = fmaxf(m_ref, mx);
+        const bool grow = m_new > m_ref + kRescale;
+        float f = 1.f;
+        bool rescale = false;
+        if (x == 0) {
+          m_ref = m_new;  // the first product overwrites O
+        } else {
+          rescale = __any_sync(~0u, grow);
+          if (grow) {
+            f = ex2_approx(m_ref - m_new);
+            m_ref = m_new;
+            l_sum *= f;
+          }
+        }
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t sl2 = f2(p.sl2, p.sl2), nm2 = f2(neg_m, neg_m), least2 = f2(0x1p-24f, 0x1p-24f);
+        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t hi[32], lo[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int e = 64 * hf + 2 * c;
+            const uint64_t a = f2_fma(f2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2, nm2);
+            const float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
+            const uint64_t pp = f2(p0, p1);
+            ps[c & 3] = f2_add(ps[c & 3], pp);
+            hi[c] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+            // less the first term: its 8 bits, with the sign of a subtraction
+            const uint64_t rest = f2_add(pp, f2(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) | 0x80000000u),
+                                                __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) | 0x80000000u)));
+            const uint64_t least = f2_mul(pp, least2);
+            lo[c] = pack_bf16x2(fmaxf(f2_lo(rest), f2_lo(least)), fmaxf(f2_hi(rest), f2_hi(least)));
+          }
+          tmem_st32(s_tmem + 32 * hf, hi);
+          tmem_st32(s_tmem + 64 + 32 * hf, lo);
+        }
+        const uint64_t s2 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
+        l_sum += f2_lo(s2) + f2_hi(s2);
+        if (rescale) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t orow[32];
+            tmem_ld32(o_tmem + c0, orow);
+            tmem_wait_ld();
+            reg_fence<32>(orow);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) orow[c] = __float_as_uint(__uint_as_float(orow[c]) * f);
+            tmem_st32(o_tmem + c0, orow);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        named_bar_sync(kPReadyBar + t, kPReadyThreads);
+      }
+      // ---- this half's part: O through shared memory (its query tile, free once O is done: every S product came before
+      // the last P V) so that memory sees whole 128-byte pieces of rows ----
+      if (n > 0) {
+        if (ok) ok = warp_wait_parity(&o_full[t], done & 1, abort_flag, p.status);
+        ++done;
+        tc_fence_after();
+      }
+      const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
+      const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows);
+      if (ok && r < rows) p.ml[part + r] = make_float2(m_ref, l_sum);
+      if (n > 0) {
+        uint8_t* stage = smem + t * C::kTileBytes;
+        const int piece = r & 7;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          if (ok) {
+            uint32_t orow[32];
+            tmem_ld32(o_tmem + c0, orow);
+            tmem_wait_ld();
+            reg_fence<32>(orow);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(stage + r * 128 + ((k ^ (r & 7)) << 4)) =
+                  make_uint4(orow[4 * k], orow[4 * k + 1], orow[4 * k + 2], orow[4 * k + 3]);
+          }
+          named_bar_sync(kEpiBar + t, 128);
+          if (ok) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int row = (r >> 3) + 16 * k;
+              if (row < rows)
+                *reinterpret_cast<uint4*>(p.o + (part + row) * D + c0 + 4 * piece) =
+                    *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+            }
+          }
+          named_bar_sync(kEpiBar + t, 128);
+        }
+        tc_fence_before();
+      }
+      if (v < run1) named_bar_sync(kBothBar, 256);  // both halves are done with the queries
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- join --------------------------------------------------------------------------
+
+constexpr int kJoinWarps = 4;
+
+// A warp per (request, query head), a lane D / 32 columns: the parts of its prefix, then its own keys' result.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __grid_constant__ Args p) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  if (item >= (int64_t)p.n * p.h) return;
+  const int b = (int)(item / p.h), hh = (int)(item - (int64_t)b * p.h);
+  float top = p.suffix_lse[item] * kLog2e, sum = top == -INFINITY ? 0.f : 1.f;
+  float o[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) o[j] = 0.f;
+  if (sum > 0.f) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = p.suffix[item * D + lane * N + j];
+  }
+  if (p.skip[b] > 0) {
+    // the request's group: the last that begins at it or before (groups without rows begin where the next does)
+    int lo = 0, hi = p.groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.group_rows[mid] <= b)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const Group g = p.group[lo];
+    const int heads = p.h / p.hkv, hk = hh / heads, row = (b - g.row0) * heads + (hh - hk * heads);
+    const Shape sh(g.rows * heads, g.tiles);
+    Schedule sc;
+    sc.total = p.tables[p.groups];
+    sc.ctas = min(p.max_ctas, max(1, sc.total / kMinSteps));
+    sc.share = sc.total / sc.ctas;
+    sc.over = sc.total - sc.share * sc.ctas;
+    const int u = min(row / kUnitRows, sh.twos), two = u < sh.twos;
+    const int begin = p.tables[lo] + hk * sh.steps() + u * sh.tiles, steps = two ? sh.tiles : sh.one_steps;
+    const int c0 = sc.cta_of(begin), c1 = sc.cta_of(begin + steps - 1);
+    const int64_t first = p.tables[p.groups + 1 + lo] + hk * sh.part_rows() + u * kUnitRows + (row - u * kUnitRows);
+    // part i: CTA c0 + i, or two of them a CTA
+    const int parts = (c1 - c0 + 1) * (two ? 1 : 2);
+    auto place = [&](int i) {
+      return two ? first + (int64_t)kUnitRows * (c0 + i) : first + (int64_t)kUnitRows * (c0 + (i >> 1)) + (i & 1) * sh.one;
+    };
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const int64_t at = place(min(i0 + lane, parts - 1));
+      const float2 e = i0 + lane < parts ? p.ml[at] : make_float2(-INFINITY, 0.f);
+      float m = e.x;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+      m = fmaxf(m, top);
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float w = e.x == -INFINITY ? 0.f : ex2_approx(e.x - ref), old = top == -INFINITY ? 0.f : ex2_approx(top - ref);
+      float l = e.x == -INFINITY ? 0.f : w * e.y;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
+      sum = sum * old + l;
+      top = m;
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] *= old;
+      const int n = min(32, parts - i0);
+      const uint32_t some = __ballot_sync(~0u, e.x != -INFINITY);  // a part without keys has no O
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float g1 = __shfl_sync(~0u, w, i);
+        const int64_t from = __shfl_sync(~0u, at, i);
+        if (!((some >> i) & 1u)) continue;
+        const float* y = p.o + from * D + lane * N;
+        if constexpr (N == 4) {
+          const float4 z = __ldcs(reinterpret_cast<const float4*>(y));
+          o[0] = fmaf(g1, z.x, o[0]), o[1] = fmaf(g1, z.y, o[1]), o[2] = fmaf(g1, z.z, o[2]), o[3] = fmaf(g1, z.w, o[3]);
+        } else {
+          const float2 z = __ldcs(reinterpret_cast<const float2*>(y));
+          o[0] = fmaf(g1, z.x, o[0]), o[1] = fmaf(g1, z.y, o[1]);
+        }
+      }
+    }
+  }
+  if (lane == 0) p.lse.ptr[b * p.lse.sn + hh * p.lse.sh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t to = b * p.out.sn + hh * p.out.sh + lane * N;
+#pragma unroll
+  for (int j = 0; j < N; ++j) o[j] *= inv;
+  if (p.out_is_f32) {
+    float* y = static_cast<float*>(p.out.ptr) + to;
+    if constexpr (N == 4)
+      *reinterpret_cast<float4*>(y) = make_float4(o[0], o[1], o[2], o[3]);
+    else
+      *reinterpret_cast<float2*>(y) = make_float2(o[0], o[1]);
+  } else {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out.ptr) + to;
+    if constexpr (N == 4)
+      *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    else
+      *reinterpret_cast<uint32_t*>(y) = pack_bf16x2(o[0], o[1]);
+  }
+}
+
+template <int D>
+cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s, int* nlaunch) {
+  using C = Cfg<D>;
+  struct Facts {
+    int ctas, regs;
+  };
+  static PerContext<Facts> cache;
+  Facts f{};
+  cudaError_t e = cache.get(
+      [](Facts* v) {
+        cudaError_t r = cudaFuncSetAttribute(shared_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (r != cudaSuccess) return r;
+        cudaFuncAttributes fa;
+        if ((r = cudaFuncGetAttributes(&fa, shared_prefix_kernel<D>)) != cudaSuccess) return r;
+        v->regs = fa.numRegs;
+        if ((r = device_sm_count(&v->ctas)) != cudaSuccess) return r;
+        if (v->ctas > kMaxCtas) v->ctas = kMaxCtas;
+        return r;
+      },
+      &f);
+  if (e != cudaSuccess) return e;
+  if (f.regs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split holds for that number only
+  const PagedDecodeParams& d = p.d;
+  uint8_t* ws = static_cast<uint8_t*>(d.ws);
+  const size_t decode_bytes = paged_decode_workspace(d.h, d.hkv, d.d, (int64_t)d.max_pages * d.page);
+  const Layout w = layout(d.n, d.h, d.d, p.groups, decode_bytes);
+  Args a = {};
+  a.n = d.n, a.h = d.h, a.hkv = d.hkv, a.d = d.d, a.groups = p.groups;
+  a.max_keys = d.max_pages * d.page;
+  a.num_pages = d.num_pages;
+  a.page = d.page;
+  a.box = paged_shared_box(d.page);
+  a.max_ctas = f.ctas;
+  a.group_rows = p.group_rows, a.shared_lens = p.shared_lens, a.lens = d.lens, a.table = d.table;
+  a.table_stride = d.table_stride;
+  a.q = d.q, a.out = d.out, a.lse = d.lse;
+  a.out_is_f32 = d.out_is_f32;
+  a.sl2 = d.scale * kLog2e;
+  a.skip = reinterpret_cast<int*>(ws + w.skip);
+  a.group = reinterpret_cast<Group*>(ws + w.groups);
+  a.tables = reinterpret_cast<int*>(ws + w.tables);
+  a.suffix = reinterpret_cast<float*>(ws + w.suffix);
+  a.suffix_lse = reinterpret_cast<float*>(ws + w.suffix_lse);
+  a.ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.o = reinterpret_cast<float*>(ws + w.o);
+  a.status = d.status;
+  if ((e = launch_dependent(shared_setup_kernel, dim3(p.groups), kSetupThreads, 0, s, a)) != cudaSuccess) return e;
+  *nlaunch += 1;
+  if ((e = launch_dependent(shared_prefix_kernel<D>, dim3(f.ctas), kThreads, C::kSmem, s, tk, tv, a)) != cudaSuccess) return e;
+  *nlaunch += 1;
+  // the requests' own keys, in fp32, with their log-sum-exp
+  PagedDecodeParams own = d;
+  own.skip = a.skip;
+  own.out = Seq4{ws + w.suffix, (int64_t)d.h * d.d, 0, d.d};
+  own.out_is_f32 = 1;
+  own.lse = Lse3{reinterpret_cast<float*>(ws + w.suffix_lse), d.h, 1};
+  own.ws = ws + w.decode;
+  if ((e = launch_paged_decode(own, s, nlaunch)) != cudaSuccess) return e;
+  const int64_t items = (int64_t)d.n * d.h;
+  e = launch_dependent(shared_join_kernel<D>, dim3((unsigned)((items + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, a);
+  if (e == cudaSuccess) *nlaunch += 1;
+  return e;
+}
+
+}  // namespace
+
+bool paged_shared_is_plain(int64_t groups, int64_t num_pages, int64_t max_keys) {
+  return groups == 0 || num_pages == 0 || max_keys < kTile;
+}
+
+int paged_shared_box(int64_t page) {
+  int b = kTile;
+  while (page % b != 0) b /= 2;
+  return b;
+}
+
+size_t paged_shared_workspace(int64_t n, int64_t h, int64_t h_kv, int64_t d, int64_t max_keys, int64_t groups) {
+  return layout(n, h, d, groups, paged_decode_workspace(h, h_kv, d, max_keys)).total;
+}
+
+bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int64_t groups) {
+  const int64_t most = (int64_t(1) << 31) - 1;
+  if (2 * n * h + (int64_t)kUnitRows * kMaxCtas > most) return false;
+  const int64_t units = h_kv * (n * (h / h_kv) / kUnitRows + (groups < n ? groups : n));
+  return units <= most / (max_keys / kTile + 1);
+}
+
+cudaError_t launch_paged_shared(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s,
+                                int* nlaunch) {
+  return p.d.d == 64 ? launch<64>(p, tk, tv, s, nlaunch) : launch<128>(p, tk, tv, s, nlaunch);
+}
+
+}  // namespace bea

@@ -1,0 +1,32 @@
+// Parameter block and launcher of attention over a shared prefix, shared by its
+// host entry point (shared_api.cu) and kernels (paged_shared.cu).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "paged.cuh"
+
+namespace bea {
+
+constexpr int kMaxGroups = 1024;  // their schedule is scanned in shared memory
+
+struct PagedSharedParams {
+  PagedDecodeParams d;  // ws: the whole workspace
+  int groups;
+  const int32_t *group_rows, *shared_lens;
+};
+// Whether no request can have a whole tile of keys, so that nothing is shared.
+bool paged_shared_is_plain(int64_t groups, int64_t num_pages, int64_t max_keys);
+size_t paged_shared_workspace(int64_t n, int64_t h, int64_t h_kv, int64_t d, int64_t max_keys, int64_t groups);
+// Whether the counts of the schedule fit 31 bits.
+bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int64_t groups);
+// tk, tv: boxes of 64 columns and paged_shared_box(page) tokens of a page.
+int paged_shared_box(int64_t page);
+cudaError_t launch_paged_shared(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s,
+                                int* nlaunch);
+
+}  // namespace bea

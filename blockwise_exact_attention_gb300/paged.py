@@ -11,6 +11,7 @@ Requests may share pages: ``paged_fork`` lets rows begin as other rows' copies,
 ``paged_free`` ends rows and gives back the pages that nobody holds any more,
 ``paged_compact`` moves the used pages to the lower end of the cache, and
 ``paged_copy`` carries out the copies that the first and the last list.
+``paged_decode_shared`` reads the keys that a group of rows shares once for all.
 """
 
 from __future__ import annotations
@@ -69,6 +70,27 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, softmax_scale=None, win
         raise TypeError(f"out_dtype {out_dtype}: {q.dtype} or float32")
     return _lib.bind().paged_decode(q, k_cache, v_cache, block_table, lens, softmax_scale, window_left, out, lse,
                                     out_dtype is torch.float32, workspace)
+
+
+def paged_decode_shared_workspace_bytes(q, k_cache, block_table, shared_lens) -> int:
+    return int(_lib.load().bea_paged_decode_shared_workspace_size(q.shape[0], q.shape[2], k_cache.shape[2], q.shape[3],
+                                                                  block_table.shape[1] * k_cache.shape[1],
+                                                                  shared_lens.shape[0]))
+
+
+def paged_decode_shared(q, k_cache, v_cache, block_table, lens, group_rows, shared_lens, softmax_scale=None, out=None,
+                        lse=None, out_dtype=None, workspace=None):
+    """``paged_decode`` (bf16, no window) where groups of requests have their first
+    keys in common, which are then read once for the group. Group g is the rows
+    ``group_rows[g]`` .. ``group_rows[g + 1] - 1`` ([groups + 1] int32, ascending);
+    their tables name the same pages for the first ``shared_lens[g]`` keys
+    ([groups] int32), as those of forked rows do. Rows of length 0 take no part."""
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
+    if out_dtype is not None and out_dtype not in (q.dtype, torch.float32):
+        raise TypeError(f"out_dtype {out_dtype}: {q.dtype} or float32")
+    return _lib.bind().paged_decode_shared(q, k_cache, v_cache, block_table, lens, group_rows, shared_lens, softmax_scale,
+                                           out, lse, out_dtype is torch.float32, workspace)
 
 
 class PagedFork(NamedTuple):
@@ -204,3 +226,7 @@ class PagedKVCache:
     def decode(self, q, softmax_scale=None, window_left=-1, **kw):
         """``paged_decode`` of one new token per row: q [max_requests, 1, h, d]."""
         return paged_decode(q, self.k, self.v, self.block_table, self.lens, softmax_scale, window_left, **kw)
+
+    def decode_shared(self, q, group_rows, shared_lens, softmax_scale=None, **kw):
+        """``paged_decode_shared`` of one new token per row."""
+        return paged_decode_shared(q, self.k, self.v, self.block_table, self.lens, group_rows, shared_lens, softmax_scale, **kw)

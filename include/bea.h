@@ -492,6 +492,38 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
                      size_t workspace_bytes, void* stream);
 
 /*
+ * bea_paged_decode for groups of requests whose first keys are the same (a
+ * prompt that many requests start from): those are read once for the group.
+ *
+ *   q, k_cache, v_cache, block_table, lens, out, lse   as for bea_paged_decode,
+ *               bf16 (f32: BEA_ERR_UNSUPPORTED); no window
+ *   group_rows  [groups + 1] i32, ascending: group g is the rows group_rows[g] ..
+ *               group_rows[g + 1] - 1; rows of no group share nothing
+ *   shared_lens [groups] i32: the group's first shared_lens[g] keys are the same
+ *               for all its requests, that is, the rows of the table name the same
+ *               pages for them (bea_paged_fork makes such rows). The first row that
+ *               holds a request is read for all.
+ *   workspace   bea_paged_decode_shared_workspace_size() bytes, 256-byte aligned.
+ *               Contents on entry irrelevant; calls that may run concurrently need
+ *               separate workspaces.
+ * A request of length 0 takes no part in its group, and gets out = 0, lse =
+ * -inf. Shared is what is whole tiles of 128 keys of the shortest request's and
+ * in pages of the cache; what is left over is read for each request. groups <=
+ * 1024. Results are those of bea_paged_decode up to rounding: weights of the
+ * shared keys have 16 bits in the product with the values. group_rows out of
+ * order or range: nothing is shared, and reported; a negative shared_lens counts
+ * as 0 and is reported; the rest as bea_paged_decode reports it. (2 h n + 40960 <
+ * 2^31, and h_kv (n h / h_kv / 256 + min(groups, n)) (max_keys / 128 + 1) < 2^31, else
+ * BEA_ERR_SHAPE.)
+ */
+size_t bea_paged_decode_shared_workspace_size(int64_t n, int64_t h, int64_t h_kv, int64_t d, int64_t max_keys,
+                                              int64_t groups);
+int bea_paged_decode_shared(const bea_tensor* q, const bea_tensor* k_cache, const bea_tensor* v_cache,
+                            const bea_tensor* block_table, const bea_tensor* lens, const bea_tensor* group_rows,
+                            const bea_tensor* shared_lens, const bea_tensor* out, const bea_tensor* lse,
+                            float softmax_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Pages that several rows of a table hold. shares[p] is the number of rows that
  * hold page p beyond the first: 0 for a page of one row, and for a free one.
  * bea_paged_plan neither reads nor changes it (the pages that it hands out have

@@ -200,3 +200,31 @@ def test_python_refusals():
     for call in (lambda: cache.fork(i), lambda: cache.free(i), lambda: cache.compact(2)):
         with pytest.raises(ValueError, match="share_pages"):
             call()
+
+
+def test_refusals_of_shared_decoding(lib):
+    good = dict(q=t((5, 1, 8, 64), BF16), k=t((20, 16, 2, 64), BF16), v=t((20, 16, 2, 64), BF16), table=t((5, 9)), lens=t((5,)),
+                rows=t((4,)), shared=t((3,)), out=t((5, 1, 8, 64), BF16), lse=t((5, 8, 1), F32))
+
+    def call(scale=0.1, ws=FAKE, size=1 << 40, **over):
+        a = [ref(x) for x in (good | over).values()]
+        return lib.bea_paged_decode_shared(*a, scale, ws, size, None)
+
+    need = lib.bea_paged_decode_shared_workspace_size(5, 8, 2, 64, 9 * 16, 3)
+    assert need > 0 and call(size=need - 1) == -8 and call(ws=None) == -8 and call(ws=FAKE + 16) == -8
+    for name in good:
+        assert call(**{name: None}) == ARG
+    assert call(rows=t((3,))) == SHAPE and call(shared=t((4,))) == SHAPE and call(rows=t((4, 1))) == SHAPE
+    assert call(rows=t((4,), F32)) == DTYPE and call(shared=t((3,), ptr=FAKE + 1)) == ALIGN
+    assert call(rows=t((1026,)), shared=t((1025,))) == UNSUP and call(scale=0.0) == ARG
+    assert call(**{k: t((5, 1, 8, 64) if k in ("q", "out") else (20, 16, 2, 64), F32) for k in ("q", "k", "v", "out")}) == UNSUP
+    assert call(q=t((5, 2, 8, 64), BF16)) == SHAPE and call(k=t((20, 16, 3, 64), BF16)) == SHAPE
+    assert call(out=t((5, 1, 8, 64), BF16, strides=[0, 512, 64, 1])) == ARG
+    # counts past 31 bits: 2 h n, and units times tiles
+    assert call(q=t((2 ** 20, 1, 1024, 64), BF16), out=t((2 ** 20, 1, 1024, 64), BF16), lse=t((2 ** 20, 1024, 1), F32),
+                table=t((2 ** 20, 9)), lens=t((2 ** 20,))) == SHAPE
+    assert call(q=t((2 ** 14, 1, 2, 64), BF16), out=t((2 ** 14, 1, 2, 64), BF16), lse=t((2 ** 14, 2, 1), F32),
+                table=t((2 ** 14, 2 ** 25)), lens=t((2 ** 14,)), rows=t((1025,)), shared=t((1024,))) == SHAPE
+    for bad in [(-1, 8, 2, 64, 9, 3), (5, -8, 2, 64, 9, 3), (5, 8, 0, 64, 9, 3), (5, 8, 2, -64, 9, 3), (5, 8, 2, 64, -9, 3),
+                (5, 8, 2, 64, 9, -3), (2 ** 31, 8, 2, 64, 9, 3), (5, 8, 2, 2 ** 40, 9, 3), (5, 8, 2, 64, 9, 2 ** 40)]:
+        assert lib.bea_paged_decode_shared_workspace_size(*bad) == 0
