@@ -94,5 +94,11 @@ size_t paged_decode_workspace(int64_t h, int64_t hkv, int64_t d, int64_t max_key
 // Whether a request's tiles can be counted in 31 bits.
 bool paged_decode_fits(int64_t hkv, int64_t d, bool is_f32, int64_t max_keys);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch);
+// The same of requests whose first keys are left out (p.skip of each; bf16), in two parts, so that another kernel can be
+// launched between them: the attention, then the join of what was cut between CTAs. Where that takes several rounds on one
+// workspace the first call does all of them. The attention lets the next launch in early once all that stands before it is
+// over.
+enum class DecodePhase { kAll, kAttend, kJoin };
+cudaError_t launch_paged_decode_rest(const PagedDecodeParams& p, DecodePhase phase, cudaStream_t s, int* nlaunch);
 
 }  // namespace bea

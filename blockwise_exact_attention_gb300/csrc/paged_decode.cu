@@ -227,8 +227,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float2 ml[kWarps][2][16];  // of a warp's first and last part
   __shared__ int2 part_of[kWarps][2];   // (request, unit) of these parts, -1: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_launch_dependents();
-  grid_dependency_wait();
+  if constexpr (kSkip) {  // the kernel behind relies on what stands before this one being over (paged_shared.cu)
+    grid_dependency_wait();
+    grid_launch_dependents();
+  } else {
+    grid_launch_dependents();
+    grid_dependency_wait();
+  }
 
   // ---- tiles per request, their sums, and this CTA's run [t0, t1) -----------------
   // an empty cache has no page to read from: every length is past it
@@ -870,7 +875,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 int64_t request_cost(int64_t keys, int64_t units, int tile) { return ((keys + tile - 1) / tile + 1 + kUnitCost) * units; }
 
 template <bool kF32, int kD, int kHd, bool kSkip = false>
-cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
+cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch, DecodePhase phase = DecodePhase::kAll) {
   using C = Cfg<kF32, kD, kHd>;
   static PerContext<int> cache;
   int ctas = 0;
@@ -897,6 +902,9 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   // Of a launch, so that a plane keeps CTAs enough to cut its work among. 300 heads to a K/V head, 16 requests of 4k-8k
   // keys: 155 us; 8: 161, 4: 183, 32: 136 us.
   constexpr int kMaxPlanes = 16;
+  const bool once = group <= kMaxPlanes * C::kRows && p.n <= at_once;
+  const bool attend = phase != DecodePhase::kJoin, join_too = phase == DecodePhase::kAll || once == (phase == DecodePhase::kJoin);
+  if (phase == DecodePhase::kJoin && !once) return cudaSuccess;
   for (a.head0 = 0; a.head0 < group; a.head0 += kMaxPlanes * C::kRows) {
     const int left = (group - a.head0 + C::kRows - 1) / C::kRows;
     a.planes = left < kMaxPlanes ? left : kMaxPlanes;
@@ -904,10 +912,12 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
     for (int64_t r0 = 0; r0 < p.n; r0 += at_once) {
       a.r0 = (int)r0;
       a.n = (int)(p.n - r0 < at_once ? p.n - r0 : at_once);
-      if ((e = launch_dependent(paged_decode_kernel<kF32, kD, kHd, kSkip>, dim3(grid), kThreads, C::kSmem, s, p, a)) != cudaSuccess)
-        return e;
-      *nlaunch += 1;
-      if (!a.split) continue;
+      if (attend) {
+        e = launch_dependent(paged_decode_kernel<kF32, kD, kHd, kSkip>, dim3(grid), kThreads, C::kSmem, s, p, a);
+        if (e != cudaSuccess) return e;
+        *nlaunch += 1;
+      }
+      if (!a.split || !join_too) continue;
       const dim3 join(grid, (unsigned)(group < C::kRows ? group : C::kRows));
       if ((e = launch_dependent(paged_join_kernel<kF32, kD, kHd>, join, kJoinWarps * 32, 0, s, p, a)) != cudaSuccess)
         return e;
@@ -941,14 +951,21 @@ template <bool kF32, int kD>
 static cudaError_t launch_heads(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   const int group = p.h / p.hkv;
   if constexpr (!kF32) {
-    if (p.skip != nullptr)
-      return group <= 8 ? launch<false, kD, 8, true>(p, s, nlaunch) : launch<false, kD, 16, true>(p, s, nlaunch);
     return group <= 8 ? launch<false, kD, 8>(p, s, nlaunch) : launch<false, kD, 16>(p, s, nlaunch);
   } else {
     return group == 1   ? launch<true, kD, 1>(p, s, nlaunch)
            : group <= 4 ? launch<true, kD, 4>(p, s, nlaunch)
                         : launch<true, kD, 8>(p, s, nlaunch);
   }
+}
+
+template <int kD>
+static cudaError_t launch_rest(const PagedDecodeParams& p, DecodePhase phase, cudaStream_t s, int* nlaunch) {
+  return p.h / p.hkv <= 8 ? launch<false, kD, 8, true>(p, s, nlaunch, phase) : launch<false, kD, 16, true>(p, s, nlaunch, phase);
+}
+
+cudaError_t launch_paged_decode_rest(const PagedDecodeParams& p, DecodePhase phase, cudaStream_t s, int* nlaunch) {
+  return p.d == 64 ? launch_rest<64>(p, phase, s, nlaunch) : launch_rest<128>(p, phase, s, nlaunch);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {

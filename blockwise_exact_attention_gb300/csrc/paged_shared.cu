@@ -48,6 +48,9 @@ constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
 constexpr float kRescale = 8.f;  // log2: O is rescaled only when a maximum grows by more
 constexpr uint32_t kPReadyBar = 1, kPReadyThreads = 128 + 32, kEpiBar = 3, kBothBar = 5;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A run's cut is moved by up to so many steps (and a quarter of a run) to a unit's border: a run in two units costs about 5
+// steps more, as it fetches queries and writes parts twice.
+constexpr int kSnap = 3;
 // Steps of a run at least, as long as there are fewer than the GPU has CTAs.
 constexpr int kMinSteps = 2;
 
@@ -61,16 +64,22 @@ struct Cfg {
   static constexpr int kBarOff = kVOff + kStages * kTileBytes;
   static constexpr int kNumBars = 1 + 4 * kStages + 2 + 2 + 1;
   static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
-  static constexpr int kSmem = kTableOff + 3 * (kMaxGroups + 1) * 4 + 1024 /*alignment*/;
+  static constexpr int kGroupOff = (kTableOff + 2 * (kMaxGroups + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kSmem = kGroupOff + kMaxGroups * 16 + 1024 /*alignment*/;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
   static constexpr uint32_t kVLbo = 64 * 128 * 2;
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---- schedule ----------------------------------------------------------------------
 
 // A group as the setup finds it: its rows, the first of them that has keys, the tiles that are shared.
-struct Group {
+struct alignas(16) Group {
   int row0, rows, owner, tiles;
 };
 
@@ -92,15 +101,51 @@ struct Shape {
 // Where the groups' steps and parts' rows begin, [groups + 1] each; and the runs.
 struct Schedule {
   const int *steps, *rows;
-  int total, ctas, share, over;
-  __device__ int begin(int c) const { return share * c + min(c, over); }
-  __device__ int cta_of(int v) const { return v < over * (share + 1) ? v / (share + 1) : over + (v - over * (share + 1)) / share; }
+  const Group* groups;
+  int n_groups, heads;  // heads: query heads of a K/V head
+  int total, ctas, snap;
+
+  __device__ Schedule(const int* s, const int* r, const Group* g, int n, int query_heads, int most_ctas)
+      : steps(s), rows(r), groups(g), n_groups(n), heads(query_heads), total(s[n]) {
+    ctas = min(most_ctas, max(1, total / kMinSteps));
+    snap = min(kSnap, total / ctas / 4);
+  }
+  // The group that step v belongs to: the last whose steps begin at v or before.
+  __device__ int group_of(int v) const {
+    int lo = 0, hi = n_groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (steps[mid] <= v)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+  // Where CTA c's run begins: equal shares, but a unit's border that is near takes the cut's place.
+  __device__ int begin(int c) const {
+    const int v = (int)((int64_t)total * c / ctas);
+    if (snap == 0 || v == 0 || v >= total) return v;
+    const int g = group_of(v);
+    const Shape sh(groups[g].rows * heads, groups[g].tiles);
+    int in = (v - steps[g]) % sh.steps();
+    const int u = min(in / sh.tiles, sh.twos), all = u < sh.twos ? sh.tiles : sh.one_steps;
+    in -= u * sh.tiles;
+    return in <= snap ? v - in : all - in <= snap ? v + all - in : v;
+  }
+  __device__ int cta_of(int v) const {
+    int c = (int)((((int64_t)v + 1) * ctas - 1) / total);
+    while (begin(c) > v) --c;
+    while (begin(c + 1) <= v) ++c;
+    return c;
+  }
 };
 
 // A run's piece in one unit: steps [a, b) of it.
 struct Seg {
   Group g;
-  int hk, q0, rows, two, a, b, part;  // q0: first query row in the group; part: first row of the unit's parts
+  int hk, q0, rows, two, a, b, part, end;  // q0: first query row in the group; part: first row of the unit's parts; end: the
+                                           // step behind the unit's last, of all
   __device__ int first(int t) const { return two ? a : 2 * a + t; }  // half t's first tile
   __device__ int count(int t) const {                                // and how many it has
     if (two) return b - a;
@@ -111,18 +156,11 @@ struct Seg {
   __device__ int tile1() const { return two ? b : min(2 * b, g.tiles); }
 };
 
-__device__ __forceinline__ Seg seg_at(const Schedule& s, const Group* groups, int n_groups, int heads, int v, int end) {
-  int lo = 0, hi = n_groups - 1;  // the last group whose steps begin at v or before
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.steps[mid] <= v)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
+__device__ __forceinline__ Seg seg_at(const Schedule& s, int v, int end) {
+  const int lo = s.group_of(v);
   Seg r;
-  r.g = groups[lo];
-  const Shape sh(r.g.rows * heads, r.g.tiles);
+  r.g = s.groups[lo];
+  const Shape sh(r.g.rows * s.heads, r.g.tiles);
   const int each = sh.steps(), in_group = v - s.steps[lo];
   r.hk = in_group / each;
   const int in = in_group - r.hk * each, u = min(in / sh.tiles, sh.twos);
@@ -132,13 +170,14 @@ __device__ __forceinline__ Seg seg_at(const Schedule& s, const Group* groups, in
   r.a = in - u * sh.tiles;
   const int all = r.two ? sh.tiles : sh.one_steps;
   r.b = min(all, r.a + (end - v));
+  r.end = v - r.a + all;
   r.part = s.rows[lo] + r.hk * sh.part_rows() + r.q0;
   return r;
 }
 
 // Workspace.
 struct Layout {
-  size_t skip, groups, tables, suffix, suffix_lse, decode, ml, o, total;
+  size_t skip, groups, rows, suffix, suffix_lse, decode, ml, o, total;
 };
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 inline Layout layout(int64_t n, int64_t h, int64_t d, int64_t groups, size_t decode_bytes) {
@@ -146,8 +185,8 @@ inline Layout layout(int64_t n, int64_t h, int64_t d, int64_t groups, size_t dec
   const size_t rows = 2 * (size_t)(n * h) + (size_t)kUnitRows * kMaxCtas;
   w.skip = 0;
   w.groups = w.skip + up256((size_t)n * 4);
-  w.tables = w.groups + up256((size_t)groups * sizeof(Group));
-  w.suffix = w.tables + up256(2 * (size_t)(groups + 1) * 4);
+  w.rows = w.groups + up256((size_t)groups * sizeof(Group));
+  w.suffix = w.rows + up256((size_t)n * h * sizeof(int4));
   w.suffix_lse = w.suffix + up256((size_t)n * h * d * 4);
   w.decode = w.suffix_lse + up256((size_t)n * h * 4);
   w.ml = w.decode + up256(decode_bytes);
@@ -166,7 +205,7 @@ struct Args {
   float sl2;
   int* skip;
   Group* group;
-  int* tables;  // [groups + 1] first steps, [groups + 1] first part rows
+  int4* row;  // of every (request, head) with a shared prefix: where its parts are
   const float *suffix, *suffix_lse;
   float2* ml;
   float* o;
@@ -243,7 +282,8 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
 
 // ---- the prefix --------------------------------------------------------------------
 
-template <int D>
+// kTerms: bf16 terms of P in the second product.
+template <int D, int kTerms>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                          const __grid_constant__ Args p) {
@@ -257,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* first_step = reinterpret_cast<int*>(smem + C::kTableOff);
   int* first_row = first_step + kMaxGroups + 1;
+  Group* groups = reinterpret_cast<Group*>(smem + C::kGroupOff);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int heads = p.h / p.hkv;
 
@@ -274,13 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   grid_launch_dependents();
-  grid_dependency_wait();
   if (warp == kVWarp) {  // sums of steps and part rows over the groups
     int steps = 0, rows = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
       int s = 0, r = 0;
       if (g0 + lane < p.groups) {
         const Group g = p.group[g0 + lane];
+        groups[g0 + lane] = g;
         const Shape sh(g.rows * heads, g.tiles);
         s = sh.steps() * p.hkv;
         r = sh.part_rows() * p.hkv;
@@ -304,21 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Schedule sc;
-  sc.steps = first_step;
-  sc.rows = first_row;
-  sc.total = first_step[p.groups];
-  sc.ctas = min((int)gridDim.x, max(1, sc.total / kMinSteps));
-  sc.share = sc.total / sc.ctas;
-  sc.over = sc.total - sc.share * sc.ctas;
+  const Schedule sc(first_step, first_row, groups, p.groups, heads, gridDim.x);
   const int cta = blockIdx.x;
   const int run0 = cta < sc.ctas ? sc.begin(cta) : 0, run1 = cta < sc.ctas ? sc.begin(cta + 1) : 0;
-  if (cta == 0)  // for the kernel that joins
-    for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
-      p.tables[i] = first_step[i];
-      p.tables[p.groups + 1 + i] = first_row[i];
-    }
-
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kKWarp || warp == kVWarp) {
@@ -332,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int it = 0;
       for (int v = run0; ok && v < run1;) {
-        const Seg sg = seg_at(sc, p.group, p.groups, heads, v, run1);
+        const Seg sg = seg_at(sc, v, run1);
         v += sg.b - sg.a;
         const int32_t* entries = p.table + sg.g.owner * p.table_stride;
         int id[kMost], off[kMost];  // of this lane's boxes in the next tile
@@ -377,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int base = 0, seg = 0;
       for (int v = run0; v < run1; ++seg) {
-        const Seg sg = seg_at(sc, p.group, p.groups, heads, v, run1);
+        const Seg sg = seg_at(sc, v, run1);
         v += sg.b - sg.a;
         const int most = sg.count(0);  // the second half has as many tiles or one less
         // half t's x-th tile is the ring's slot(t, x)-th
@@ -404,11 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t vd = sdesc_add(v_desc, s * C::kTileBytes);
 #pragma unroll
-          for (int term = 0; term < 2; ++term)  // the rest of P, then what was cut off it first: small terms first
+          for (int term = kTerms - 1; term >= 0; --term)  // small terms first
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              umma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + (term == 0 ? 64 : 0) + k * 8, sdesc_add(vd, k * 2048),
-                           C::kIdescPV, term > 0 || k > 0 || x > 0 ? 1u : 0u);
+              umma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + term * 64 + k * 8, sdesc_add(vd, k * 2048), C::kIdescPV,
+                           term < kTerms - 1 || k > 0 || x > 0 ? 1u : 0u);
           if (!sg.two || t == 1) umma_commit_warp(&v_empty[s]);
           if (x == n - 1) umma_commit_warp(&o_full[t]);
         };
@@ -437,27 +466,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tmem = tmem + lane_base + t * 128, o_tmem = tmem + lane_base + 256 + t * 128;
     bool ok = true;
     int met = 0, done = 0;  // tiles and segments of this half so far
-    for (int v = run0; v < run1;) {
-      const Seg sg = seg_at(sc, p.group, p.groups, heads, v, run1);
-      v += sg.b - sg.a;
-      // ---- the unit's queries, 128-byte swizzled like the forward's; rows behind the last are zeros ----
-      {
-        constexpr int kPieces = D / 8;
-        const int n = (sg.two ? 2 : 1) * kTile * kPieces;
-        for (int i = threadIdx.x; i < n; i += 256) {
-          const int row = i / kPieces, c = i - row * kPieces;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < sg.rows) {
-            const int qr = sg.q0 + row, b = qr / heads, hh = sg.hk * heads + (qr - b * heads);
-            x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q.ptr) + (int64_t)(sg.g.row0 + b) * p.q.sn +
-                                                (int64_t)hh * p.q.sh + c * 8);
-          }
-          const int in = row % kTile;
-          *reinterpret_cast<uint4*>(smem + (row / kTile) * C::kTileBytes + (c / 8) * 16384 + in * 128 + (((c & 7) ^ (in & 7)) << 4)) = x;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full);
+    // A unit's queries, 16 bytes of a row at a time, copied without passing through registers (where the prefetched ones
+    // would be spilled); rows behind the last repeat it and go nowhere.
+    constexpr int kPieces = D / 8, kRows = 256 / kPieces, kTimes = kUnitRows / kRows;
+    const int q_piece = threadIdx.x % kPieces, q_row = threadIdx.x / kPieces;
+    auto each_row = [&](const Seg& sg, auto f) {
+      const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.q.ptr) + sg.g.row0 * p.q.sn +
+                                  (int64_t)sg.hk * heads * p.q.sh + q_piece * 8;
+      const int step_b = kRows / heads, step_h = kRows - step_b * heads, last = sg.q0 + sg.rows - 1;
+      const int last_b = last / heads, last_h = last - last_b * heads;
+      int b = (sg.q0 + q_row) / heads, hh = sg.q0 + q_row - b * heads;
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) {
+        const bool in = b < last_b || (b == last_b && hh <= last_h);
+        f(q_row + i * kRows, base + (in ? b : last_b) * p.q.sn + (in ? hh : last_h) * p.q.sh);
+        b += step_b, hh += step_h;
+        if (hh >= heads) hh -= heads, ++b;
       }
+    };
+    for (int v = run0; v < run1;) {
+      const Seg sg = seg_at(sc, v, run1);
+      v += sg.b - sg.a;
+      // into shared memory, 128-byte swizzled like the forward's
+      each_row(sg, [&](int row, const __nv_bfloat16* from) {
+        const int in = row % kTile;
+        if (row < kTile || sg.two) cp_async16(smem_u32(smem + (row / kTile) * C::kTileBytes + (q_piece / 8) * 16384 + in * 128 +
+                            (((q_piece & 7) ^ (in & 7)) << 4)),
+                   from);
+      });
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
       float m_ref = -INFINITY, l_sum = 0.f;
       const int n = sg.count(t);
       for (int x = 0; x < n; ++x, ++met) {
@@ -498,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t sl2 = f2(p.sl2, p.sl2), nm2 = f2(neg_m, neg_m), least2 = f2(0x1p-24f, 0x1p-24f);
+        const uint64_t sl2 = f2(p.sl2, p.sl2), nm2 = f2(neg_m, neg_m);
         uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -507,18 +546,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 32; ++c) {
             const int e = 64 * hf + 2 * c;
             const uint64_t a = f2_fma(f2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2, nm2);
-            const float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
-            const uint64_t pp = f2(p0, p1);
-            ps[c & 3] = f2_add(ps[c & 3], pp);
-            hi[c] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-            // less the first term: its 8 bits, with the sign of a subtraction
-            const uint64_t rest = f2_add(pp, f2(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) | 0x80000000u),
-                                                __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) | 0x80000000u)));
-            const uint64_t least = f2_mul(pp, least2);
-            lo[c] = pack_bf16x2(fmaxf(f2_lo(rest), f2_lo(least)), fmaxf(f2_hi(rest), f2_hi(least)));
+            float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
+            if constexpr (kTerms == 1) {
+              ps[c & 3] = f2_add(ps[c & 3], f2(p0, p1));
+              hi[c] = pack_bf16x2(p0, p1);
+            } else {
+              // the last bit set, so that something is left behind the first term
+              p0 = __uint_as_float(__float_as_uint(p0) | 1u), p1 = __uint_as_float(__float_as_uint(p1) | 1u);
+              ps[c & 3] = f2_add(ps[c & 3], f2(p0, p1));
+              hi[c] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+              // less the first term: its 8 bits, with the sign of a subtraction
+              const uint64_t rest = f2_add(f2(p0, p1), f2(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) | 0x80000000u),
+                                                          __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) | 0x80000000u)));
+              lo[c] = pack_bf16x2(f2_lo(rest), f2_hi(rest));
+            }
           }
           tmem_st32(s_tmem + 32 * hf, hi);
-          tmem_st32(s_tmem + 64 + 32 * hf, lo);
+          if constexpr (kTerms == 2) tmem_st32(s_tmem + 64 + 32 * hf, lo);
         }
         const uint64_t s2 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
         l_sum += f2_lo(s2) + f2_hi(s2);
@@ -538,6 +582,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         named_bar_sync(kPReadyBar + t, kPReadyThreads);
       }
+      const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
+      const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows);
+      if (v < run1)  // the next unit's queries into L2, while this one's part is written
+        each_row(seg_at(sc, v, run1), [&](int, const __nv_bfloat16* from) {
+          if (q_piece % 8 == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
+        });
+      if (sg.a == 0) {
+        // for the kernel that joins: each row's first part, the parts' number, and the second half's distance
+        const int parts = (sc.cta_of(sg.end - 1) - cta + 1) * (sg.two ? 1 : 2);
+        for (int i = threadIdx.x; i < sg.rows; i += 256) {
+          const int qr = sg.q0 + i, b = qr / heads, hh = sg.hk * heads + (qr - b * heads);
+          p.row[(int64_t)(sg.g.row0 + b) * p.h + hh] = make_int4(kUnitRows * cta + sg.part + i, parts, sg.two ? 0 : sg.rows, 0);
+        }
+      }
       // ---- this half's part: O through shared memory (its query tile, free once O is done: every S product came before
       // the last P V) so that memory sees whole 128-byte pieces of rows ----
       if (n > 0) {
@@ -545,14 +603,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++done;
         tc_fence_after();
       }
-      const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
-      const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows);
       if (ok && r < rows) p.ml[part + r] = make_float2(m_ref, l_sum);
       if (n > 0) {
         uint8_t* stage = smem + t * C::kTileBytes;
         const int piece = r & 7;
+        // two buffers where the tile has room for them: a chunk's reads are then over when the next but one is written
+        constexpr bool kTwoBufs = C::kTileBytes >= 2 * 16384;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
+          uint8_t* buf = stage + (kTwoBufs ? (c0 & 32) * 512 : 0);
           if (ok) {
             uint32_t orow[32];
             tmem_ld32(o_tmem + c0, orow);
@@ -560,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             reg_fence<32>(orow);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(stage + r * 128 + ((k ^ (r & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(buf + r * 128 + ((k ^ (r & 7)) << 4)) =
                   make_uint4(orow[4 * k], orow[4 * k + 1], orow[4 * k + 2], orow[4 * k + 3]);
           }
           named_bar_sync(kEpiBar + t, 128);
@@ -570,10 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int row = (r >> 3) + 16 * k;
               if (row < rows)
                 *reinterpret_cast<uint4*>(p.o + (part + row) * D + c0 + 4 * piece) =
-                    *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+                    *reinterpret_cast<const uint4*>(buf + row * 128 + ((piece ^ (row & 7)) << 4));
             }
           }
-          named_bar_sync(kEpiBar + t, 128);
+          if (!kTwoBufs) named_bar_sync(kEpiBar + t, 128);
         }
         tc_fence_before();
       }
@@ -581,6 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  // what ran beside this kernel has to be over when it is
+  grid_dependency_wait();
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -594,81 +655,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinWarps = 4;
 
-// A warp per (request, query head), a lane D / 32 columns: the parts of its prefix, then its own keys' result.
+// A warp per (request, query head), a lane D / 32 columns: the parts of its prefix, then its own keys' result. A chain of
+// two memory latencies: where the parts are, and all else.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __grid_constant__ Args p) {
-  constexpr int N = D / 32;
+  constexpr int N = D / 32, kBatch = 8;
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   grid_dependency_wait();
   if (item >= (int64_t)p.n * p.h) return;
   const int b = (int)(item / p.h), hh = (int)(item - (int64_t)b * p.h);
-  float top = p.suffix_lse[item] * kLog2e, sum = top == -INFINITY ? 0.f : 1.f;
+  const int skip = p.skip[b];
+  const int4 where = p.row[item];  // of no request that shares: anything
   float o[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) o[j] = 0.f;
-  if (sum > 0.f) {
+  for (int j = 0; j < N; ++j) o[j] = p.suffix[item * D + lane * N + j];
+  float top = p.suffix_lse[item] * kLog2e, sum = top == -INFINITY ? 0.f : 1.f;  // without keys o is zeros
+  const int parts = skip > 0 ? where.y : 0;
+  // part i: one a CTA, or two
+  auto place = [&](int i) {
+    return where.z == 0 ? where.x + (int64_t)kUnitRows * i : where.x + (int64_t)kUnitRows * (i >> 1) + (i & 1) * where.z;
+  };
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const int n = min(32, parts - i0);
+    const float2 e = lane < n ? p.ml[place(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    float m = 0.f, w = 0.f;
+    for (int i1 = 0; i1 < n; i1 += kBatch) {
+      float y[kBatch][N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) o[j] = p.suffix[item * D + lane * N + j];
-  }
-  if (p.skip[b] > 0) {
-    // the request's group: the last that begins at it or before (groups without rows begin where the next does)
-    int lo = 0, hi = p.groups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.group_rows[mid] <= b)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const Group g = p.group[lo];
-    const int heads = p.h / p.hkv, hk = hh / heads, row = (b - g.row0) * heads + (hh - hk * heads);
-    const Shape sh(g.rows * heads, g.tiles);
-    Schedule sc;
-    sc.total = p.tables[p.groups];
-    sc.ctas = min(p.max_ctas, max(1, sc.total / kMinSteps));
-    sc.share = sc.total / sc.ctas;
-    sc.over = sc.total - sc.share * sc.ctas;
-    const int u = min(row / kUnitRows, sh.twos), two = u < sh.twos;
-    const int begin = p.tables[lo] + hk * sh.steps() + u * sh.tiles, steps = two ? sh.tiles : sh.one_steps;
-    const int c0 = sc.cta_of(begin), c1 = sc.cta_of(begin + steps - 1);
-    const int64_t first = p.tables[p.groups + 1 + lo] + hk * sh.part_rows() + u * kUnitRows + (row - u * kUnitRows);
-    // part i: CTA c0 + i, or two of them a CTA
-    const int parts = (c1 - c0 + 1) * (two ? 1 : 2);
-    auto place = [&](int i) {
-      return two ? first + (int64_t)kUnitRows * (c0 + i) : first + (int64_t)kUnitRows * (c0 + (i >> 1)) + (i & 1) * sh.one;
-    };
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      const int64_t at = place(min(i0 + lane, parts - 1));
-      const float2 e = i0 + lane < parts ? p.ml[at] : make_float2(-INFINITY, 0.f);
-      float m = e.x;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-      m = fmaxf(m, top);
-      const float ref = m == -INFINITY ? 0.f : m;
-      const float w = e.x == -INFINITY ? 0.f : ex2_approx(e.x - ref), old = top == -INFINITY ? 0.f : ex2_approx(top - ref);
-      float l = e.x == -INFINITY ? 0.f : w * e.y;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
-      sum = sum * old + l;
-      top = m;
-#pragma unroll
-      for (int j = 0; j < N; ++j) o[j] *= old;
-      const int n = min(32, parts - i0);
-      const uint32_t some = __ballot_sync(~0u, e.x != -INFINITY);  // a part without keys has no O
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float g1 = __shfl_sync(~0u, w, i);
-        const int64_t from = __shfl_sync(~0u, at, i);
-        if (!((some >> i) & 1u)) continue;
-        const float* y = p.o + from * D + lane * N;
+      for (int z = 0; z < kBatch; ++z) {
+        const float* from = p.o + place(i0 + min(i1 + z, n - 1)) * D + lane * N;
         if constexpr (N == 4) {
-          const float4 z = __ldcs(reinterpret_cast<const float4*>(y));
-          o[0] = fmaf(g1, z.x, o[0]), o[1] = fmaf(g1, z.y, o[1]), o[2] = fmaf(g1, z.z, o[2]), o[3] = fmaf(g1, z.w, o[3]);
+          const float4 x = __ldcs(reinterpret_cast<const float4*>(from));
+          y[z][0] = x.x, y[z][1] = x.y, y[z][2] = x.z, y[z][3] = x.w;
         } else {
-          const float2 z = __ldcs(reinterpret_cast<const float2*>(y));
-          o[0] = fmaf(g1, z.x, o[0]), o[1] = fmaf(g1, z.y, o[1]);
+          const float2 x = __ldcs(reinterpret_cast<const float2*>(from));
+          y[z][0] = x.x, y[z][1] = x.y;
         }
+      }
+      if (i1 == 0) {  // the weights, while the first parts are under way
+        m = e.x;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+        m = fmaxf(m, top);
+        const float ref = m == -INFINITY ? 0.f : m, old = top == -INFINITY ? 0.f : ex2_approx(top - ref);
+        w = e.x == -INFINITY ? 0.f : ex2_approx(e.x - ref);
+        float l = e.x == -INFINITY ? 0.f : w * e.y;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
+        sum = sum * old + l;
+        top = m;
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] *= old;
+      }
+#pragma unroll
+      for (int z = 0; z < kBatch; ++z) {
+        const float g1 = __shfl_sync(~0u, w, (i1 + z) & 31);
+        const bool there = __shfl_sync(~0u, e.x, (i1 + z) & 31) != -INFINITY && i1 + z < n;  // a part without keys has no O
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] = there ? fmaf(g1, y[z][j], o[j]) : o[j];
       }
     }
   }
@@ -692,7 +737,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __gr
   }
 }
 
-template <int D>
+template <int D, int kTerms>
 cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s, int* nlaunch) {
   using C = Cfg<D>;
   struct Facts {
@@ -702,10 +747,10 @@ cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUte
   Facts f{};
   cudaError_t e = cache.get(
       [](Facts* v) {
-        cudaError_t r = cudaFuncSetAttribute(shared_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaError_t r = cudaFuncSetAttribute(shared_prefix_kernel<D, kTerms>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (r != cudaSuccess) return r;
         cudaFuncAttributes fa;
-        if ((r = cudaFuncGetAttributes(&fa, shared_prefix_kernel<D>)) != cudaSuccess) return r;
+        if ((r = cudaFuncGetAttributes(&fa, shared_prefix_kernel<D, kTerms>)) != cudaSuccess) return r;
         v->regs = fa.numRegs;
         if ((r = device_sm_count(&v->ctas)) != cudaSuccess) return r;
         if (v->ctas > kMaxCtas) v->ctas = kMaxCtas;
@@ -732,15 +777,13 @@ cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUte
   a.sl2 = d.scale * kLog2e;
   a.skip = reinterpret_cast<int*>(ws + w.skip);
   a.group = reinterpret_cast<Group*>(ws + w.groups);
-  a.tables = reinterpret_cast<int*>(ws + w.tables);
+  a.row = reinterpret_cast<int4*>(ws + w.rows);
   a.suffix = reinterpret_cast<float*>(ws + w.suffix);
   a.suffix_lse = reinterpret_cast<float*>(ws + w.suffix_lse);
   a.ml = reinterpret_cast<float2*>(ws + w.ml);
   a.o = reinterpret_cast<float*>(ws + w.o);
   a.status = d.status;
   if ((e = launch_dependent(shared_setup_kernel, dim3(p.groups), kSetupThreads, 0, s, a)) != cudaSuccess) return e;
-  *nlaunch += 1;
-  if ((e = launch_dependent(shared_prefix_kernel<D>, dim3(f.ctas), kThreads, C::kSmem, s, tk, tv, a)) != cudaSuccess) return e;
   *nlaunch += 1;
   // the requests' own keys, in fp32, with their log-sum-exp
   PagedDecodeParams own = d;
@@ -749,7 +792,10 @@ cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUte
   own.out_is_f32 = 1;
   own.lse = Lse3{reinterpret_cast<float*>(ws + w.suffix_lse), d.h, 1};
   own.ws = ws + w.decode;
-  if ((e = launch_paged_decode(own, s, nlaunch)) != cudaSuccess) return e;
+  if ((e = launch_paged_decode_rest(own, DecodePhase::kAttend, s, nlaunch)) != cudaSuccess) return e;
+  if ((e = launch_dependent(shared_prefix_kernel<D, kTerms>, dim3(f.ctas), kThreads, C::kSmem, s, tk, tv, a)) != cudaSuccess) return e;
+  *nlaunch += 1;
+  if ((e = launch_paged_decode_rest(own, DecodePhase::kJoin, s, nlaunch)) != cudaSuccess) return e;
   const int64_t items = (int64_t)d.n * d.h;
   e = launch_dependent(shared_join_kernel<D>, dim3((unsigned)((items + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, a);
   if (e == cudaSuccess) *nlaunch += 1;
@@ -781,7 +827,9 @@ bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int
 
 cudaError_t launch_paged_shared(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s,
                                 int* nlaunch) {
-  return p.d.d == 64 ? launch<64>(p, tk, tv, s, nlaunch) : launch<128>(p, tk, tv, s, nlaunch);
+  if (p.d.out_is_f32)
+    return p.d.d == 64 ? launch<64, 2>(p, tk, tv, s, nlaunch) : launch<128, 2>(p, tk, tv, s, nlaunch);
+  return p.d.d == 64 ? launch<64, 1>(p, tk, tv, s, nlaunch) : launch<128, 1>(p, tk, tv, s, nlaunch);
 }
 
 }  // namespace bea
