@@ -87,6 +87,7 @@ struct PagedDecodeParams {
   int64_t table_stride;
   const int32_t* lens;
   const int32_t* skip;  // null, or the number of first keys of each request that are left out (bf16; left unbounded)
+  int* cuts;            // with skip: see launch_paged_decode_rest
   void* ws;
   uint32_t* status;
 };
@@ -94,11 +95,21 @@ size_t paged_decode_workspace(int64_t h, int64_t hkv, int64_t d, int64_t max_key
 // Whether a request's tiles can be counted in 31 bits.
 bool paged_decode_fits(int64_t hkv, int64_t d, bool is_f32, int64_t max_keys);
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch);
-// The same of requests whose first keys are left out (p.skip of each; bf16), in two parts, so that another kernel can be
-// launched between them: the attention, then the join of what was cut between CTAs. Where that takes several rounds on one
-// workspace the first call does all of them. The attention lets the next launch in early once all that stands before it is
-// over.
-enum class DecodePhase { kAll, kAttend, kJoin };
-cudaError_t launch_paged_decode_rest(const PagedDecodeParams& p, DecodePhase phase, cudaStream_t s, int* nlaunch);
+// The same of requests whose first keys are left out (p.skip of each; bf16). Lets the next launch in early once all that
+// stands before it is over. A (request, query head) cut between CTAs is left to the caller to join: cuts[request * h +
+// head] then says where its parts are, and is 0 where out and lse have been written.
+cudaError_t launch_paged_decode_rest(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch);
+// A cut: part 0 is CTA c's second, part i the first one of CTA c + i * planes; part z of a CTA, head row r (of a block of
+// `rows` heads of a K/V head): (m, l) at ml[(2 c + z) * 16 + r] (m in log2), O at o[((2 c + z) * rows + r) * d].
+struct DecodeParts {
+  size_t ml, o;  // byte offsets in the workspace
+  int rows;
+};
+DecodeParts paged_decode_parts(int64_t h, int64_t hkv, int64_t d);
+__host__ __device__ constexpr int cut_record(int cta, int parts, int planes) { return cta | parts << 10 | planes << 20; }
+struct Cut {
+  int cta, parts, planes;
+  __device__ explicit Cut(int record) : cta(record & 1023), parts(record >> 10 & 1023), planes(record >> 20) {}
+};
 
 }  // namespace bea

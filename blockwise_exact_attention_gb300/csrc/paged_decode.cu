@@ -294,7 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           static_cast<__nv_bfloat16*>(p.out.ptr)[to] = __float2bfloat16(0.f);
       }
-      for (int i = tid; i < p.h; i += kThreads) p.lse.ptr[b * p.lse.sn + i * p.lse.sh] = -INFINITY;
+      for (int i = tid; i < p.h; i += kThreads) {
+        p.lse.ptr[b * p.lse.sn + i * p.lse.sh] = -INFINITY;
+        if constexpr (kSkip) p.cuts[b * p.h + i] = 0;
+      }
     }
   }
   __syncthreads();
@@ -725,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = row + 8 * x;
         if (i >= rows) continue;
         if (covered) {
+          if (kSkip && (lane & 3) == 0) p.cuts[b * p.h + h0 + i] = 0;
           const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
           const int64_t to = b * p.out.sn + (h0 + i) * p.out.sh + col;
 #pragma unroll
@@ -795,17 +799,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (begin >= t0 && end <= t1) {
       if (lane * 4 < p.d) write_out4(p, b, hh, lane * 4, o, sum);
       if (lane == 0) write_lse(p, b, hh, top, sum);
+      if (kSkip && lane == 0) p.cuts[b * p.h + hh] = 0;
       continue;
     }
     const int slot = blockIdx.x * 2 + (begin < t0 ? 0 : 1);
     if (lane * 4 < p.d)
       *reinterpret_cast<float4*>(reinterpret_cast<float*>(ws + wl.o) + ((int64_t)slot * C::kRows + row) * kD + lane * 4) = o;
     if (lane == 0) reinterpret_cast<float2*>(ws + wl.ml)[slot * 16 + row] = make_float2(top, sum);
-    if (begin >= t0 && row == 0 && lane == 0) {
+    if (begin >= t0 && (kSkip || row == 0) && lane == 0) {
       // the CTA whose run holds the unit's last tile, at cost v: runs up to the `over`-th are one longer
       const int v = begin_cost(k_of) + (unit_of + 1) * (cnt + kUnitCost) - 1;
       const int last = v < over * (share + 1) ? v / (share + 1) : over + (v - over * (share + 1)) / share;
-      reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{(int)b, unit_of, last * a.planes + plane, 0};
+      if (row == 0) reinterpret_cast<Split*>(ws)[blockIdx.x] = Split{(int)b, unit_of, last * a.planes + plane, 0};
+      if constexpr (kSkip) p.cuts[b * p.h + hh] = cut_record(blockIdx.x, last - cta + 1, a.planes);
     }
   }
 }
@@ -868,6 +874,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   for (int w = 1; w < min(kJoinWarps, parts); ++w) add(part_ml[w], part[w][lane]);
   const int hh = sp.hk * group + head;
   if (lane == 0) write_lse(p, sp.b, hh, top, sum);
+  if (p.cuts != nullptr && lane == 0) p.cuts[(int64_t)sp.b * p.h + hh] = 0;  // no longer
   if (mine) write_out4(p, sp.b, hh, lane * 4, o, sum);
 }
 
@@ -875,7 +882,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 int64_t request_cost(int64_t keys, int64_t units, int tile) { return ((keys + tile - 1) / tile + 1 + kUnitCost) * units; }
 
 template <bool kF32, int kD, int kHd, bool kSkip = false>
-cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch, DecodePhase phase = DecodePhase::kAll) {
+cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
   using C = Cfg<kF32, kD, kHd>;
   static PerContext<int> cache;
   int ctas = 0;
@@ -902,9 +909,8 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch, Dec
   // Of a launch, so that a plane keeps CTAs enough to cut its work among. 300 heads to a K/V head, 16 requests of 4k-8k
   // keys: 155 us; 8: 161, 4: 183, 32: 136 us.
   constexpr int kMaxPlanes = 16;
-  const bool once = group <= kMaxPlanes * C::kRows && p.n <= at_once;
-  const bool attend = phase != DecodePhase::kJoin, join_too = phase == DecodePhase::kAll || once == (phase == DecodePhase::kJoin);
-  if (phase == DecodePhase::kJoin && !once) return cudaSuccess;
+  // Of requests whose first keys are left out the caller joins what is cut, unless the rounds share the workspace.
+  const bool join_here = !kSkip || group > kMaxPlanes * C::kRows || p.n > at_once;
   for (a.head0 = 0; a.head0 < group; a.head0 += kMaxPlanes * C::kRows) {
     const int left = (group - a.head0 + C::kRows - 1) / C::kRows;
     a.planes = left < kMaxPlanes ? left : kMaxPlanes;
@@ -912,12 +918,10 @@ cudaError_t launch(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch, Dec
     for (int64_t r0 = 0; r0 < p.n; r0 += at_once) {
       a.r0 = (int)r0;
       a.n = (int)(p.n - r0 < at_once ? p.n - r0 : at_once);
-      if (attend) {
-        e = launch_dependent(paged_decode_kernel<kF32, kD, kHd, kSkip>, dim3(grid), kThreads, C::kSmem, s, p, a);
-        if (e != cudaSuccess) return e;
-        *nlaunch += 1;
-      }
-      if (!a.split || !join_too) continue;
+      e = launch_dependent(paged_decode_kernel<kF32, kD, kHd, kSkip>, dim3(grid), kThreads, C::kSmem, s, p, a);
+      if (e != cudaSuccess) return e;
+      *nlaunch += 1;
+      if (!a.split || !join_here) continue;
       const dim3 join(grid, (unsigned)(group < C::kRows ? group : C::kRows));
       if ((e = launch_dependent(paged_join_kernel<kF32, kD, kHd>, join, kJoinWarps * 32, 0, s, p, a)) != cudaSuccess)
         return e;
@@ -960,12 +964,18 @@ static cudaError_t launch_heads(const PagedDecodeParams& p, cudaStream_t s, int*
 }
 
 template <int kD>
-static cudaError_t launch_rest(const PagedDecodeParams& p, DecodePhase phase, cudaStream_t s, int* nlaunch) {
-  return p.h / p.hkv <= 8 ? launch<false, kD, 8, true>(p, s, nlaunch, phase) : launch<false, kD, 16, true>(p, s, nlaunch, phase);
+static cudaError_t launch_rest(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
+  return p.h / p.hkv <= 8 ? launch<false, kD, 8, true>(p, s, nlaunch) : launch<false, kD, 16, true>(p, s, nlaunch);
 }
 
-cudaError_t launch_paged_decode_rest(const PagedDecodeParams& p, DecodePhase phase, cudaStream_t s, int* nlaunch) {
-  return p.d == 64 ? launch_rest<64>(p, phase, s, nlaunch) : launch_rest<128>(p, phase, s, nlaunch);
+cudaError_t launch_paged_decode_rest(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {
+  return p.d == 64 ? launch_rest<64>(p, s, nlaunch) : launch_rest<128>(p, s, nlaunch);
+}
+
+DecodeParts paged_decode_parts(int64_t h, int64_t hkv, int64_t d) {
+  const int rows = h / hkv <= 8 ? 8 : 16;
+  const WsLayout w = ws_layout(rows, row_elements(d, false));
+  return DecodeParts{w.ml, w.o, rows};
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s, int* nlaunch) {

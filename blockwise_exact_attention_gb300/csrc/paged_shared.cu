@@ -52,7 +52,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // steps more, as it fetches queries and writes parts twice.
 constexpr int kSnap = 3;
 // Steps of a run at least, as long as there are fewer than the GPU has CTAs.
-constexpr int kMinSteps = 2;
+constexpr int kMinSteps = 1;
 
 template <int D>
 struct Cfg {
@@ -177,7 +177,7 @@ __device__ __forceinline__ Seg seg_at(const Schedule& s, int v, int end) {
 
 // Workspace.
 struct Layout {
-  size_t skip, groups, rows, suffix, suffix_lse, decode, ml, o, total;
+  size_t skip, groups, rows, cuts, suffix, suffix_lse, decode, ml, o, total;
 };
 __host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 inline Layout layout(int64_t n, int64_t h, int64_t d, int64_t groups, size_t decode_bytes) {
@@ -186,7 +186,8 @@ inline Layout layout(int64_t n, int64_t h, int64_t d, int64_t groups, size_t dec
   w.skip = 0;
   w.groups = w.skip + up256((size_t)n * 4);
   w.rows = w.groups + up256((size_t)groups * sizeof(Group));
-  w.suffix = w.rows + up256((size_t)n * h * sizeof(int4));
+  w.cuts = w.rows + up256((size_t)n * h * sizeof(int4));
+  w.suffix = w.cuts + up256((size_t)n * h * 4);
   w.suffix_lse = w.suffix + up256((size_t)n * h * d * 4);
   w.decode = w.suffix_lse + up256((size_t)n * h * 4);
   w.ml = w.decode + up256(decode_bytes);
@@ -206,7 +207,11 @@ struct Args {
   int* skip;
   Group* group;
   int4* row;  // of every (request, head) with a shared prefix: where its parts are
-  const float *suffix, *suffix_lse;
+  const int* cuts;
+  const float *suffix, *suffix_lse;  // of the requests' own keys, where these are not cut; else
+  const float2* rest_ml;             // their parts
+  const float* rest_o;
+  int rest_rows;
   float2* ml;
   float* o;
   uint32_t* status;
@@ -214,25 +219,16 @@ struct Args {
 
 // ---- setup -------------------------------------------------------------------------
 
-constexpr int kSetupThreads = 512;
-
-// The least of the block's values, to all threads.
-__device__ __forceinline__ int block_min(int x, int* words) {
-  x = __reduce_min_sync(~0u, x);
-  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = words[threadIdx.x & (kSetupThreads / 32 - 1)];
-  x = __reduce_min_sync(~0u, x);
-  __syncthreads();  // `words` is free
-  return x;
-}
+constexpr int kSetupThreads = 256, kSetupWarps = kSetupThreads / 32;
 
 // A block per group: its shortest request, how much is shared, and where each request's own keys begin.
 __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __grid_constant__ Args p) {
-  __shared__ int words[kSetupThreads / 32];
+  __shared__ int3 words[kSetupWarps];
+  __shared__ int first_bad;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int g = blockIdx.x, tid = threadIdx.x;
+  const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int shared = p.shared_lens[g], r0 = p.group_rows[g], r1 = p.group_rows[g + 1];
   // rows that are not in ascending order make no groups at all
   bool wrong = false;
   for (int i = tid; i <= p.groups; i += kSetupThreads) {
@@ -240,12 +236,16 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
     wrong = wrong || x < 0 || x > p.n || (i > 0 && p.group_rows[i - 1] > x);
   }
   const bool bad = __syncthreads_or(wrong);
-  const int r0 = bad ? 0 : p.group_rows[g], r1 = bad ? 0 : p.group_rows[g + 1];
+  if (bad) r0 = r1 = 0;
   if (g == 0) {  // rows of no group
     const int a = bad ? p.n : p.group_rows[0], b = bad ? p.n : p.group_rows[p.groups];
     for (int r = tid; r < p.n; r += kSetupThreads)
       if (r < a || r >= b) p.skip[r] = 0;
     if (bad && tid == 0) report_status(p.status, BEA_STATUS_PAGES);
+  }
+  if (tid == 0) {
+    first_bad = INT32_MAX;
+    if (shared < 0) report_status(p.status, BEA_STATUS_PAGES);
   }
   int shortest = INT32_MAX, owner = INT32_MAX, live = 0;
   for (int r = r0 + tid; r < r1; r += kSetupThreads) {
@@ -255,27 +255,30 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
     owner = min(owner, r);
     ++live;
   }
-  shortest = block_min(shortest, words);
-  owner = block_min(owner, words);
-  const bool several = __syncthreads_count(live > 1) > 0 || __syncthreads_count(live > 0) > 1;
-  int shared = p.shared_lens[g];
-  if (shared < 0) {
-    if (tid == 0) report_status(p.status, BEA_STATUS_PAGES);
-    shared = 0;
-  }
+  shortest = __reduce_min_sync(~0u, shortest);
+  owner = __reduce_min_sync(~0u, owner);
+  live = __reduce_add_sync(~0u, live);
+  if (lane == 0) words[warp] = make_int3(shortest, owner, live);
+  __syncthreads();
+  const int3 w = words[lane % kSetupWarps];
+  shortest = __reduce_min_sync(~0u, w.x);
+  owner = __reduce_min_sync(~0u, w.y);
+  live = __reduce_add_sync(~0u, lane < kSetupWarps ? w.z : 0);
   // nothing is shared by one request
-  int tiles = several ? min(min(shared, shortest), p.max_keys) / kTile : 0;
+  int tiles = live > 1 ? max(0, min(min(shared, shortest), p.max_keys)) / kTile : 0;
   if (tiles > 0) {
     const int32_t* entries = p.table + owner * p.table_stride;
     const int pages = (int)(((int64_t)tiles * kTile + p.page - 1) / p.page);
-    int first_bad = INT32_MAX;
+    int at = INT32_MAX;
+#pragma unroll 8
     for (int i = tid; i < pages; i += kSetupThreads) {
       const int id = entries[i];
-      if (id < 0 || id >= p.num_pages) first_bad = min(first_bad, i);
+      if (id < 0 || id >= p.num_pages) at = min(at, i);
     }
-    first_bad = block_min(first_bad, words);
-    if (first_bad < pages) tiles = (int)((int64_t)first_bad * p.page / kTile);
+    if (at != INT32_MAX) atomicMin(&first_bad, at);
   }
+  __syncthreads();
+  if (first_bad != INT32_MAX) tiles = (int)((int64_t)first_bad * p.page / kTile);
   for (int r = r0 + tid; r < r1; r += kSetupThreads) p.skip[r] = p.lens[r] > 0 ? tiles * kTile : 0;
   if (tid == 0) p.group[g] = Group{r0, r1 - r0, owner, tiles};
 }
@@ -655,46 +658,69 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kJoinWarps = 4;
 
-// A warp per (request, query head), a lane D / 32 columns: the parts of its prefix, then its own keys' result. A chain of
-// two memory latencies: where the parts are, and all else.
-template <int D>
+// kSplit warps of a block to a (request, query head), a lane D / 32 columns: the parts of its prefix and of its own keys,
+// dealt to the warps, or its own keys' result. A chain of two memory latencies (where the parts are, the parts) as long as a
+// warp has at most kBatch of them.
+template <int D, int kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __grid_constant__ Args p) {
   constexpr int N = D / 32, kBatch = 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = warp % kSplit;
+  const int64_t item = (int64_t)blockIdx.x * (kJoinWarps / kSplit) + warp / kSplit;
   grid_dependency_wait();
-  if (item >= (int64_t)p.n * p.h) return;
-  const int b = (int)(item / p.h), hh = (int)(item - (int64_t)b * p.h);
+  const bool live = item < (int64_t)p.n * p.h;
+  if (kSplit == 1 && !live) return;
+  const int b = live ? (int)(item / p.h) : 0, hh = live ? (int)(item - (int64_t)b * p.h) : 0;
+  const int64_t row = (int64_t)b * p.h + hh;
   const int skip = p.skip[b];
-  const int4 where = p.row[item];  // of no request that shares: anything
-  float o[N];
+  const int4 where = p.row[row];  // of no request that shares: anything
+  const Cut cut(p.cuts[row]);
+  float o[N], top = p.suffix_lse[row] * kLog2e;
 #pragma unroll
-  for (int j = 0; j < N; ++j) o[j] = p.suffix[item * D + lane * N + j];
-  float top = p.suffix_lse[item] * kLog2e, sum = top == -INFINITY ? 0.f : 1.f;  // without keys o is zeros
-  const int parts = skip > 0 ? where.y : 0;
-  // part i: one a CTA, or two
-  auto place = [&](int i) {
+  for (int j = 0; j < N; ++j) o[j] = p.suffix[row * D + lane * N + j];
+  if (cut.parts > 0 || turn > 0) {  // not written, or another warp's
+    top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = 0.f;
+  }
+  float sum = top == -INFINITY ? 0.f : 1.f;  // without keys o is zeros
+  // the prefix' parts, one a CTA or two, then those of the rest; this warp's: turn, turn + kSplit, ...
+  const int shared = skip > 0 ? where.y : 0, parts = shared + cut.parts;
+  const int rest_row = hh % (p.h / p.hkv) % p.rest_rows;
+  auto prefix_row = [&](int i) {
     return where.z == 0 ? where.x + (int64_t)kUnitRows * i : where.x + (int64_t)kUnitRows * (i >> 1) + (i & 1) * where.z;
   };
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    const int n = min(32, parts - i0);
-    const float2 e = lane < n ? p.ml[place(i0 + lane)] : make_float2(-INFINITY, 0.f);
-    float m = 0.f, w = 0.f;
+  auto rest_slot = [&](int i) { return i == 0 ? 2 * cut.cta + 1 : 2 * (cut.cta + i * cut.planes); };
+  auto ml_of = [&](int i) {
+    return i < shared ? p.ml + prefix_row(i) : p.rest_ml + rest_slot(i - shared) * 16 + rest_row;
+  };
+  auto o_of = [&](int i) {
+    return i < shared ? p.o + prefix_row(i) * D
+                      : p.rest_o + ((int64_t)rest_slot(i - shared) * p.rest_rows + rest_row) * D;
+  };
+  const int mine = (parts - turn + kSplit - 1) / kSplit;
+  for (int i0 = 0; i0 < mine; i0 += 32) {
+    const int n = min(32, mine - i0);
+    const float2 e = lane < n ? *ml_of((i0 + lane) * kSplit + turn) : make_float2(-INFINITY, 0.f);
+    float w = 0.f;
     for (int i1 = 0; i1 < n; i1 += kBatch) {
       float y[kBatch][N];
 #pragma unroll
       for (int z = 0; z < kBatch; ++z) {
-        const float* from = p.o + place(i0 + min(i1 + z, n - 1)) * D + lane * N;
-        if constexpr (N == 4) {
-          const float4 x = __ldcs(reinterpret_cast<const float4*>(from));
-          y[z][0] = x.x, y[z][1] = x.y, y[z][2] = x.z, y[z][3] = x.w;
-        } else {
-          const float2 x = __ldcs(reinterpret_cast<const float2*>(from));
-          y[z][0] = x.x, y[z][1] = x.y;
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[z][j] = 0.f;
+        if (i1 + z < n) {
+          const float* from = o_of((i0 + i1 + z) * kSplit + turn) + lane * N;
+          if constexpr (N == 4) {
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(from));
+            y[z][0] = x.x, y[z][1] = x.y, y[z][2] = x.z, y[z][3] = x.w;
+          } else {
+            const float2 x = __ldcs(reinterpret_cast<const float2*>(from));
+            y[z][0] = x.x, y[z][1] = x.y;
+          }
         }
       }
       if (i1 == 0) {  // the weights, while the first parts are under way
-        m = e.x;
+        float m = e.x;
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
         m = fmaxf(m, top);
@@ -715,6 +741,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] = there ? fmaf(g1, y[z][j], o[j]) : o[j];
       }
+    }
+  }
+  if constexpr (kSplit > 1) {  // the warps' results, in order
+    __shared__ float part[kJoinWarps][D];
+    __shared__ float2 part_ml[kJoinWarps];
+#pragma unroll
+    for (int j = 0; j < N; ++j) part[warp][lane * N + j] = o[j];
+    if (lane == 0) part_ml[warp] = make_float2(top, sum);
+    __syncthreads();
+    if (turn > 0 || !live) return;
+#pragma unroll
+    for (int x = 1; x < kSplit; ++x) {
+      const float2 e = part_ml[warp + x];
+      const float m = fmaxf(top, e.x), ref = m == -INFINITY ? 0.f : m;
+      const float f = top == -INFINITY ? 0.f : ex2_approx(top - ref), g = e.x == -INFINITY ? 0.f : ex2_approx(e.x - ref);
+      top = m;
+      sum = sum * f + e.y * g;
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = o[j] * f + part[warp + x][lane * N + j] * g;
     }
   }
   if (lane == 0) p.lse.ptr[b * p.lse.sn + hh * p.lse.sh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -778,7 +823,12 @@ cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUte
   a.skip = reinterpret_cast<int*>(ws + w.skip);
   a.group = reinterpret_cast<Group*>(ws + w.groups);
   a.row = reinterpret_cast<int4*>(ws + w.rows);
+  a.cuts = reinterpret_cast<int*>(ws + w.cuts);
   a.suffix = reinterpret_cast<float*>(ws + w.suffix);
+  const DecodeParts rest = paged_decode_parts(d.h, d.hkv, d.d);
+  a.rest_ml = reinterpret_cast<float2*>(ws + w.decode + rest.ml);
+  a.rest_o = reinterpret_cast<float*>(ws + w.decode + rest.o);
+  a.rest_rows = rest.rows;
   a.suffix_lse = reinterpret_cast<float*>(ws + w.suffix_lse);
   a.ml = reinterpret_cast<float2*>(ws + w.ml);
   a.o = reinterpret_cast<float*>(ws + w.o);
@@ -788,24 +838,37 @@ cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUte
   // the requests' own keys, in fp32, with their log-sum-exp
   PagedDecodeParams own = d;
   own.skip = a.skip;
+  own.cuts = reinterpret_cast<int*>(ws + w.cuts);
   own.out = Seq4{ws + w.suffix, (int64_t)d.h * d.d, 0, d.d};
   own.out_is_f32 = 1;
   own.lse = Lse3{reinterpret_cast<float*>(ws + w.suffix_lse), d.h, 1};
   own.ws = ws + w.decode;
-  if ((e = launch_paged_decode_rest(own, DecodePhase::kAttend, s, nlaunch)) != cudaSuccess) return e;
+  if ((e = launch_paged_decode_rest(own, s, nlaunch)) != cudaSuccess) return e;
   if ((e = launch_dependent(shared_prefix_kernel<D, kTerms>, dim3(f.ctas), kThreads, C::kSmem, s, tk, tv, a)) != cudaSuccess) return e;
   *nlaunch += 1;
-  if ((e = launch_paged_decode_rest(own, DecodePhase::kJoin, s, nlaunch)) != cudaSuccess) return e;
   const int64_t items = (int64_t)d.n * d.h;
-  e = launch_dependent(shared_join_kernel<D>, dim3((unsigned)((items + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, a);
+  // Rows that do not fill the GPU are cut into many parts each.
+  const bool few = items <= 152 * 8;
+  const int64_t warps = items * (few ? kJoinWarps : 1);
+  e = launch_dependent(few ? shared_join_kernel<D, kJoinWarps> : shared_join_kernel<D, 1>,
+                       dim3((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, a);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }
 
 }  // namespace
 
-bool paged_shared_is_plain(int64_t groups, int64_t num_pages, int64_t max_keys) {
-  return groups == 0 || num_pages == 0 || max_keys < kTile;
+// Up to so many bytes of keys and values that sharing saves the other kernels take longer than reading them again. 32 / 8
+// heads of 128, GPU time with and without sharing: 4 requests behind 4k keys (50 MB) 20.6, 15.5 us, 8 behind 4k (117 MB)
+// 22.7, 23.4 us, 4 behind 16k (201 MB) 34.0, 39.2 us; 16 / 16 heads of 64: 8 behind 4k (117 MB) 22.9, 26.9 us.
+constexpr int64_t kLeastSaved = 96000000;
+
+static bool saves_little(int64_t n, int64_t h_kv, int64_t d, int64_t max_keys, int64_t groups) {
+  return groups == 0 || max_keys < kTile || (n - 1) * max_keys <= kLeastSaved / (h_kv * d * 4);
+}
+
+bool paged_shared_is_plain(const PagedDecodeParams& d, int64_t groups) {
+  return d.num_pages == 0 || saves_little(d.n, d.hkv, d.d, (int64_t)d.max_pages * d.page, groups);
 }
 
 int paged_shared_box(int64_t page) {
@@ -815,7 +878,8 @@ int paged_shared_box(int64_t page) {
 }
 
 size_t paged_shared_workspace(int64_t n, int64_t h, int64_t h_kv, int64_t d, int64_t max_keys, int64_t groups) {
-  return layout(n, h, d, groups, paged_decode_workspace(h, h_kv, d, max_keys)).total;
+  const size_t rest = paged_decode_workspace(h, h_kv, d, max_keys);
+  return saves_little(n, h_kv, d, max_keys, groups) ? rest : layout(n, h, d, groups, rest).total;
 }
 
 bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int64_t groups) {

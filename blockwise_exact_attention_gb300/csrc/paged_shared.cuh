@@ -19,8 +19,8 @@ struct PagedSharedParams {
   int groups;
   const int32_t *group_rows, *shared_lens;
 };
-// Whether no request can have a whole tile of keys, so that nothing is shared.
-bool paged_shared_is_plain(int64_t groups, int64_t num_pages, int64_t max_keys);
+// Whether sharing could save so little, by the table's width, that paged_decode is faster for all.
+bool paged_shared_is_plain(const PagedDecodeParams& d, int64_t groups);
 size_t paged_shared_workspace(int64_t n, int64_t h, int64_t h_kv, int64_t d, int64_t max_keys, int64_t groups);
 // Whether the counts of the schedule fit 31 bits.
 bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int64_t groups);

@@ -14,7 +14,7 @@ size_t bea_paged_decode_shared_workspace_size(int64_t n, int64_t h, int64_t h_kv
                                               int64_t groups) {
   if (n < 0 || h < 0 || h_kv <= 0 || d < 0 || max_keys < 0 || groups < 0) return 0;
   // what bea_paged_decode_shared refuses anyway, and products past 64 bits
-  if (h > (int64_t(1) << 31) || d > 128 || n > (int64_t(1) << 31) || n * h > (int64_t(1) << 31) || groups > bea::kMaxGroups) return 0;
+  if (h > (int64_t(1) << 31) || d < 1 || d > 128 || max_keys > bea::kUnbounded || n > (int64_t(1) << 31) || n * h > (int64_t(1) << 31) || groups > bea::kMaxGroups) return 0;
   return bea::paged_shared_workspace(n, h, h_kv, d, max_keys, groups);
 }
 
@@ -33,7 +33,7 @@ int bea_paged_decode_shared(const bea_tensor* q, const bea_tensor* k_cache, cons
   if (groups > bea::kMaxGroups) return BEA_ERR_UNSUPPORTED;
   if (!bea::paged_shared_fits(p.d.n, p.d.h, p.d.hkv, max_keys, groups)) return BEA_ERR_SHAPE;
   const size_t need = bea::paged_shared_workspace(p.d.n, p.d.h, p.d.hkv, p.d.d, max_keys, groups);
-  if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < need)
+  if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < need))
     return BEA_ERR_WORKSPACE;
   p.d.ws = workspace;
   p.groups = (int)groups;
@@ -43,7 +43,7 @@ int bea_paged_decode_shared(const bea_tensor* q, const bea_tensor* k_cache, cons
   if ((rc = status_ptr_for_current_device(&p.d.status))) return rc;
   int launches = 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (bea::paged_shared_is_plain(groups, p.d.num_pages, max_keys))
+  if (bea::paged_shared_is_plain(p.d, groups))
     return finish(bea::launch_paged_decode(p.d, s, &launches), launches);
   CUtensorMap tk, tv;
   const int box = bea::paged_shared_box(p.d.page);

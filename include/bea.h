@@ -503,14 +503,17 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
  *               for all its requests, that is, the rows of the table name the same
  *               pages for them (bea_paged_fork makes such rows). The first row that
  *               holds a request is read for all.
- *   workspace   bea_paged_decode_shared_workspace_size() bytes, 256-byte aligned.
- *               Contents on entry irrelevant; calls that may run concurrently need
+ *   workspace   bea_paged_decode_shared_workspace_size() bytes, 256-byte aligned;
+ *               may be NULL when that is 0. Contents on entry irrelevant; calls that may run concurrently need
  *               separate workspaces.
  * A request of length 0 takes no part in its group, and gets out = 0, lse =
  * -inf. Shared is what is whole tiles of 128 keys of the shortest request's and
- * in pages of the cache; what is left over is read for each request. groups <=
- * 1024. Results are those of bea_paged_decode up to rounding: weights of the
- * shared keys have 16 bits in the product with the values. group_rows out of
+ * in pages of the cache; what is left over is read for each request. Where the
+ * table has no room for 96 MB of keys and values that sharing could save, the
+ * groups are not looked at: the call is bea_paged_decode, which is then faster.
+ * groups <= 1024. Results are those of bea_paged_decode up to rounding: in the
+ * product with the values weights of the shared keys are rounded to bf16 (as in
+ * the forward) for a bf16 out, and have 16 bits for an f32 out. group_rows out of
  * order or range: nothing is shared, and reported; a negative shared_lens counts
  * as 0 and is reported; the rest as bea_paged_decode reports it. (2 h n + 40960 <
  * 2^31, and h_kv (n h / h_kv / 256 + min(groups, n)) (max_keys / 128 + 1) < 2^31, else

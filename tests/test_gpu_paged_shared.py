@@ -48,9 +48,10 @@ def i32(x):
     return torch.tensor(x, dtype=I32, device="cuda")
 
 
-def make(groups, h, h_kv, d, page, seed=0, qscale=1.0, extra_cols=1):
+def make(groups, h, h_kv, d, page, seed=0, qscale=1.0, wide=True):
     """groups: (shared keys, own keys of each row; None: a row without a request). What nobody owns holds NaN and
-    infinity. -> (q, k, v, table, lens), (group_rows, shared_lens)"""
+    infinity. `wide`: the table has room for so many keys that sharing may be worth it, whatever the lengths. -> (q, k, v,
+    table, lens), (group_rows, shared_lens)"""
     rng = np.random.default_rng(seed)
     lens, rows, cuts, total = [], [], [0], 0
     for shared, own in groups:
@@ -66,7 +67,9 @@ def make(groups, h, h_kv, d, page, seed=0, qscale=1.0, extra_cols=1):
         cuts.append(len(lens))
     pages = total + 3
     perm = rng.permutation(pages)
-    n, width = len(lens), max((len(r) for r, _ in rows), default=0) + extra_cols
+    n, width = len(lens), max((len(r) for r, _ in rows), default=0) + 1
+    if wide and n > 1:
+        width = max(width, 97_000_000 // (h_kv * d * 4 * page * (n - 1)) + 2)
     table = np.full((n, width), -1, dtype=np.int32)
     own_slot = np.zeros((pages, page), dtype=bool)
     for r, (row, _) in enumerate(rows):
@@ -150,6 +153,14 @@ def test_shared_lengths(shared):
     check(out, lse, *x, 0.1)
 
 
+def test_small_tables_take_the_kernel_of_single_requests():
+    import blockwise_exact_attention_gb300 as bea
+    x, g = make([(400, [1, 17, 300])], 8, 2, 64, 16, seed=1, wide=False)
+    out, lse = run(x, g, 0.1)
+    want = bea.paged_decode(*x, 0.1)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_a_long_prefix_and_large_scores():
     x, g = make([(20000, [1, 700, 90])], 8, 2, 128, 64, seed=1, qscale=20.0)
     out, lse = run(x, g, 0.15)
@@ -189,7 +200,7 @@ def test_no_more_is_shared_than_all_have():
         y = (*x[:4], i32([512, 300, 0, 512]))
         check(*run(y, (cuts, i32([shared])), 0.1), *y, 0.1)
         assert bea.device_status() == 0
-    long = (*x[:4], i32([100000, 0, 0, 512]))            # past the table: counts as all of it, whose last page is none
+    long = (*x[:4], i32([10 ** 6, 0, 0, 512]))           # past the table: counts as all of it, whose last page is none
     got = run(long, (cuts, i32([512])), 0.1)
     want = bea.paged_decode(*long, 0.1)
     assert bea.device_status() == PAGES
@@ -315,19 +326,19 @@ def test_past_32_bit_offsets():
     ids = [39999, 5, 39000, 20000, 38000]
     k[ids], v[ids] = draw((5, page, h_kv, d), 1), draw((5, page, h_kv, d), 2)
     q = draw((3, 1, 16, d), 3)
-    table = i32([[39999, 5, 39000, 20000], [39999, 5, 39000, 20000], [39999, 5, 39000, 38000]])
+    table = i32([[39999, 5, 39000, 20000] + [-1] * 200, [39999, 5, 39000, 20000] + [-1] * 200, [39999, 5, 39000, 38000] + [-1] * 200])
     lens = i32([256, 200, 230])
     out, lse = run((q, k, v, table, lens), (i32([0, 3]), i32([192])), 0.1)
     small = torch.zeros(40000, dtype=torch.long, device="cuda")
     small[ids] = torch.arange(5, device="cuda")
-    check(out, lse, q, k[ids], v[ids], small[table.long()].to(I32), lens, 0.1)
+    check(out, lse, q, k[ids], v[ids], small[table[:, :4].long()].to(I32), lens, 0.1)
 
 
 def test_forked_rows_decode_together():
     """The calls as they are used: a prompt, forks of it, steps of their own, and attention over what they share."""
     import blockwise_exact_attention_gb300 as bea
     h, h_kv, d, page, n, prompt = 8, 2, 128, 16, 6, 1000
-    cache = bea.PagedKVCache(200, page, h_kv, d, n, 1200, share_pages=True)
+    cache = bea.PagedKVCache(200, page, h_kv, d, n, 20000, share_pages=True)
     cache.k.fill_(math.nan), cache.v.fill_(math.nan)
     weight = [1 + draw((d,), 20 + i, 0.1).float() for i in range(2)]
     seq = [[] for _ in range(n)]

@@ -203,14 +203,14 @@ def test_python_refusals():
 
 
 def test_refusals_of_shared_decoding(lib):
-    good = dict(q=t((5, 1, 8, 64), BF16), k=t((20, 16, 2, 64), BF16), v=t((20, 16, 2, 64), BF16), table=t((5, 9)), lens=t((5,)),
+    good = dict(q=t((5, 1, 8, 64), BF16), k=t((20, 16, 2, 64), BF16), v=t((20, 16, 2, 64), BF16), table=t((5, 9000)), lens=t((5,)),
                 rows=t((4,)), shared=t((3,)), out=t((5, 1, 8, 64), BF16), lse=t((5, 8, 1), F32))
 
     def call(scale=0.1, ws=FAKE, size=1 << 40, **over):
         a = [ref(x) for x in (good | over).values()]
         return lib.bea_paged_decode_shared(*a, scale, ws, size, None)
 
-    need = lib.bea_paged_decode_shared_workspace_size(5, 8, 2, 64, 9 * 16, 3)
+    need = lib.bea_paged_decode_shared_workspace_size(5, 8, 2, 64, 144000, 3)
     assert need > 0 and call(size=need - 1) == -8 and call(ws=None) == -8 and call(ws=FAKE + 16) == -8
     for name in good:
         assert call(**{name: None}) == ARG
@@ -225,6 +225,9 @@ def test_refusals_of_shared_decoding(lib):
                 table=t((2 ** 20, 9)), lens=t((2 ** 20,))) == SHAPE
     assert call(q=t((2 ** 14, 1, 2, 64), BF16), out=t((2 ** 14, 1, 2, 64), BF16), lse=t((2 ** 14, 2, 1), F32),
                 table=t((2 ** 14, 2 ** 25)), lens=t((2 ** 14,)), rows=t((1025,)), shared=t((1024,))) == SHAPE
+    # a table with little room: what single requests need
+    assert lib.bea_paged_decode_shared_workspace_size(5, 8, 2, 64, 1600, 3) == lib.bea_paged_decode_workspace_size(8, 2, 64, 1600) < need
+    assert lib.bea_paged_decode_shared_workspace_size(5, 8, 2, 64, 160, 3) == 0
     for bad in [(-1, 8, 2, 64, 9, 3), (5, -8, 2, 64, 9, 3), (5, 8, 0, 64, 9, 3), (5, 8, 2, -64, 9, 3), (5, 8, 2, 64, -9, 3),
                 (5, 8, 2, 64, 9, -3), (2 ** 31, 8, 2, 64, 9, 3), (5, 8, 2, 2 ** 40, 9, 3), (5, 8, 2, 64, 9, 2 ** 40)]:
         assert lib.bea_paged_decode_shared_workspace_size(*bad) == 0
