@@ -10,6 +10,7 @@
 // backward pass does not enter the interpreter.
 #include <Python.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <string>
@@ -479,6 +480,35 @@ PyObject* py_norm_rotary_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ---- paged cache -----------------------------------------------------------------
 
+// New int32 tensors of one call, as views of one allocation (0.3 us each instead of 1), each on a 16-byte boundary.
+class Outputs {
+ public:
+  int count() const { return n_; }
+  void want(Tensor* t, int64_t rows, int64_t cols = 0) {  // cols 0: of one dimension
+    t_[n_] = t, rows_[n_] = rows, cols_[n_] = cols;
+    ++n_;
+  }
+  void make(const Tensor& beside) {
+    if (n_ == 0) return;
+    int64_t total = 0, at = 0;
+    for (int i = 0; i < n_; ++i) total += size(i);
+    const Tensor all = empty({total}, at::kInt, beside);
+    for (int i = 0; i < n_; ++i) {
+      *t_[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+      const int64_t shape[2] = {rows_[i], cols_[i]}, stride[2] = {cols_[i] > 0 ? cols_[i] : 1, 1};
+      const size_t dims = cols_[i] > 0 ? 2 : 1;
+      t_[i]->unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(shape, dims), at::IntArrayRef(stride, dims), at);
+      at += size(i);
+    }
+  }
+
+ private:
+  int64_t size(int i) const { return (rows_[i] * std::max<int64_t>(cols_[i], 1) + 3) / 4 * 4; }
+  Tensor* t_[8];
+  int64_t rows_[8], cols_[8];
+  int n_ = 0;
+};
+
 // paged_plan(lens, new_lens, block_table, free_pages, n_free, page_size, capacity, out) -> out, a tuple of
 // (slot_map, positions, cu_new, cu_pages, lens, n_free); out None: allocated
 PyObject* py_paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -495,16 +525,11 @@ PyObject* py_paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } else {
     TORCH_CHECK_VALUE(capacity >= 0 && capacity <= INT32_MAX, "paged_plan: capacity ", capacity);
     const int64_t rows = in[0].dim() == 1 ? in[0].size(0) : 0;
-    const int64_t sizes[6] = {capacity, capacity, rows + 1, rows + 1, rows, 1};
-    const int64_t one = 1;
-    int64_t total = 0, at = 0;
-    for (int64_t s : sizes) total += (s + 3) / 4 * 4;  // each on a 16-byte boundary
-    const Tensor all = empty({total}, at::kInt, in[0]);
-    for (int i = 0; i < 6; ++i) {  // views of one allocation
-      out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
-      out[i].unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(&sizes[i], 1), at::IntArrayRef(&one, 1), at);
-      at += (sizes[i] + 3) / 4 * 4;
-    }
+    Outputs all;
+    for (int64_t size : {capacity, static_cast<long long>(capacity), static_cast<long long>(rows + 1),
+                         static_cast<long long>(rows + 1), static_cast<long long>(rows), 1ll})
+      all.want(&out[all.count()], size);
+    all.make(in[0]);
   }
   Call c;
   const bea_tensor* r[11];
@@ -601,10 +626,17 @@ PyObject* py_paged_decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ---- shared pages ------------------------------------------------------------------
 
-// The i-th of a call's outputs: given, or new.
-Tensor ints_like(PyObject* o, const Tensor& x) {
-  Tensor t = to_write(tensor(o, true));
-  return t.defined() ? t : like(x);
+// One of a call's outputs: given, or new and shaped like `x` (where that is a vector or a matrix; the library refuses it
+// otherwise).
+void output(PyObject* o, Tensor* t, const Tensor& x, Outputs* made) {
+  *t = to_write(tensor(o, true));
+  if (t->defined()) return;
+  if (x.dim() == 2 && x.size(1) > 0)
+    made->want(t, x.size(0), x.size(1));
+  else if (x.dim() == 1)
+    made->want(t, x.size(0));
+  else
+    *t = like(x);
 }
 
 // Records of several tensors, for the call that takes any number of them.
@@ -621,9 +653,13 @@ PyObject* py_paged_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor in[7];
   for (int i = 0; i < 7; ++i) in[i] = i == 3 ? to_write(tensor(a[i])) : tensor(a[i], i == 1);
   const long long page = integer(a[7]);
-  const Tensor lens = ints_like(a[8], in[2]), height = ints_like(a[9], in[6]), shares = ints_like(a[10], in[4]);
-  Tensor copies = to_write(tensor(a[11], true));
-  if (!copies.defined()) copies = empty({in[2].dim() == 1 ? in[2].size(0) : 0, 3}, at::kInt, in[2]);
+  Tensor lens, height, shares, copies = to_write(tensor(a[11], true));
+  Outputs made;
+  output(a[8], &lens, in[2], &made);
+  output(a[9], &height, in[6], &made);
+  output(a[10], &shares, in[4], &made);
+  if (!copies.defined()) made.want(&copies, in[2].dim() == 1 ? in[2].size(0) : 0, 3);
+  made.make(in[2]);
   Call c;
   const bea_tensor* r[11];
   for (int i = 0; i < 7; ++i) r[i] = c.add(in[i]);
@@ -643,7 +679,12 @@ PyObject* py_paged_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor in[6];
   for (int i = 0; i < 6; ++i) in[i] = i == 4 ? to_write(tensor(a[i])) : tensor(a[i]);
   const long long page = integer(a[6]);
-  const Tensor lens = ints_like(a[7], in[1]), height = ints_like(a[8], in[5]), shares = ints_like(a[9], in[3]);
+  Tensor lens, height, shares;
+  Outputs made;
+  output(a[7], &lens, in[1], &made);
+  output(a[8], &height, in[5], &made);
+  output(a[9], &shares, in[3], &made);
+  made.make(in[1]);
   Call c;
   const bea_tensor* r[9];
   for (int i = 0; i < 6; ++i) r[i] = c.add(in[i]);
@@ -663,10 +704,14 @@ PyObject* py_paged_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   for (int i = 0; i < 5; ++i) in[i] = tensor(a[i]);
   const long long page = integer(a[5]), capacity = integer(a[6]);
   TORCH_CHECK_VALUE(capacity >= 0 && capacity <= INT32_MAX, "paged_compact: capacity ", capacity);
-  const Tensor table = ints_like(a[7], in[1]), shares = ints_like(a[8], in[2]), pool = ints_like(a[9], in[3]),
-               map = ints_like(a[10], in[2]);
-  Tensor copies = to_write(tensor(a[11], true));
-  if (!copies.defined()) copies = empty({capacity, 3}, at::kInt, in[0]);
+  Tensor table, shares, pool, map, copies = to_write(tensor(a[11], true));
+  Outputs made;
+  output(a[7], &table, in[1], &made);
+  output(a[8], &shares, in[2], &made);
+  output(a[9], &pool, in[3], &made);
+  output(a[10], &map, in[2], &made);
+  if (!copies.defined()) made.want(&copies, capacity, 3);
+  made.make(in[0]);
   TORCH_CHECK_VALUE(copies.dim() != 2 || copies.size(0) == capacity, "paged_compact: copies has ", copies.size(0),
                     " places, capacity is ", capacity);
   Call c;

@@ -7,11 +7,13 @@
 // adjoint), the gradients are
 //   dw = sum over rows of g * x r,   dx = r (w g - x r^2 mean(w g x)).
 //
-// HBM-bound: forward 2 elements moved for one of x, backward 3. A row belongs to `lanes` neighbouring lanes of a warp, a
-// power of two; each holds two 16-byte pieces of it, both ends of its pairs (half layout: a piece of the first half and its
-// partner in the second; interleaved: 32 bytes in a row), so the rotation needs no exchange and the norm a shuffle tree
-// of log2(lanes) steps. A thread does kHeads heads of one token: it sends their loads, works out the cosines and sines
-// while they are under way, then reduces, turns and stores.
+// HBM-bound: forward 2 elements moved for one of x, backward 3; but only just, a bf16 row leaves the SMs some 130
+// instructions for a lane's 16 elements. So elements go by pairs (fma.f32x2), the weights are multiplied into the
+// cosines and sines, and these are worked out once for a thread's whole token. A row belongs to `lanes` neighbouring lanes
+// of a warp, a power of two; each holds two 16-byte pieces of it, both ends of its pairs (half layout: a piece of the first
+// half and its partner in the second; interleaved: 32 bytes in a row), so the rotation needs no exchange and the norm a
+// shuffle tree of log2(lanes) steps. A thread takes a token's heads kHeads at a time: it sends their loads, reduces, turns
+// and stores; tokens that do not fill the GPU are shared out between several threads.
 //
 // The weights' gradient is a sum over all rows. A thread keeps its columns' sums in fp32 over all the rows it meets
 // (the grid is one wave, each block only q or only k), a block adds up its threads in shared memory, and a second kernel
@@ -31,6 +33,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kSmThreads = 2048;  // that an SM holds
 constexpr int kMaxD = 2 * kRopeMaxPairs;
+constexpr int kFwdHeads = 4;
+constexpr int kBwdHeads = 2, kBwdStages = 2, kBwdBlocks = 4;
 
 __device__ __forceinline__ float weight_at(const void* w, int is_f32, int c) {
   if (w == nullptr) return 1.f;
@@ -61,47 +65,70 @@ struct Place {
   __device__ __forceinline__ int second(int j) const { return kInter ? a + 2 * j + 1 : b + j; }
 };
 
-// The pieces of a row as the first and second elements of its pairs, and back.
+// A lane's two pieces as the first (u) and second (v) elements of its pairs, two pairs to a packed value, and back.
 template <bool kF32, bool kInter>
-__device__ __forceinline__ void unpack(const uint4& ra, const uint4& rb, float* u, float* v) {
-  using P = Piece<kF32>;
-  if constexpr (!kInter) {
-    P::load(ra, u);
-    P::load(rb, v);
+__device__ __forceinline__ void unpack(const uint4& a, const uint4& b, uint64_t* u, uint64_t* v) {
+  auto f = [](uint32_t x) { return __uint_as_float(x); };
+  if constexpr (kF32) {
+    if constexpr (kInter) {
+      u[0] = f2(f(a.x), f(a.z)), u[1] = f2(f(b.x), f(b.z));
+      v[0] = f2(f(a.y), f(a.w)), v[1] = f2(f(b.y), f(b.w));
+    } else {
+      u[0] = f2(f(a.x), f(a.y)), u[1] = f2(f(a.z), f(a.w));
+      v[0] = f2(f(b.x), f(b.y)), v[1] = f2(f(b.z), f(b.w));
+    }
   } else {
-    float x[2 * P::kN];
-    P::load(ra, x);
-    P::load(rb, x + P::kN);
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int j = 0; j < P::kN; ++j) u[j] = x[2 * j], v[j] = x[2 * j + 1];
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kInter) {
+        u[i] = f2(f(x[2 * i] << 16), f(x[2 * i + 1] << 16));
+        v[i] = f2(f(x[2 * i] & 0xFFFF0000u), f(x[2 * i + 1] & 0xFFFF0000u));
+      } else {
+        u[i] = f2(f(x[i] << 16), f(x[i] & 0xFFFF0000u));
+        v[i] = f2(f(x[4 + i] << 16), f(x[4 + i] & 0xFFFF0000u));
+      }
+    }
   }
 }
 template <bool kF32, bool kInter>
-__device__ __forceinline__ void pack(const float* u, const float* v, uint4& ra, uint4& rb) {
-  using P = Piece<kF32>;
-  if constexpr (!kInter) {
-    ra = P::store(u);
-    rb = P::store(v);
+__device__ __forceinline__ void pack(const uint64_t* u, const uint64_t* v, uint4& a, uint4& b) {
+  if constexpr (kF32) {
+    auto w = [](float x) { return __float_as_uint(x); };
+    if constexpr (kInter) {
+      a = make_uint4(w(f2_lo(u[0])), w(f2_lo(v[0])), w(f2_hi(u[0])), w(f2_hi(v[0])));
+      b = make_uint4(w(f2_lo(u[1])), w(f2_lo(v[1])), w(f2_hi(u[1])), w(f2_hi(v[1])));
+    } else {
+      a = make_uint4(w(f2_lo(u[0])), w(f2_hi(u[0])), w(f2_lo(u[1])), w(f2_hi(u[1])));
+      b = make_uint4(w(f2_lo(v[0])), w(f2_hi(v[0])), w(f2_lo(v[1])), w(f2_hi(v[1])));
+    }
   } else {
-    float x[2 * P::kN];
+    uint32_t x[8];
 #pragma unroll
-    for (int j = 0; j < P::kN; ++j) x[2 * j] = u[j], x[2 * j + 1] = v[j];
-    ra = P::store(x);
-    rb = P::store(x + P::kN);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kInter) {
+        x[2 * i] = pack_bf16x2(f2_lo(u[i]), f2_lo(v[i]));
+        x[2 * i + 1] = pack_bf16x2(f2_hi(u[i]), f2_hi(v[i]));
+      } else {
+        x[i] = pack_bf16x2(f2_lo(u[i]), f2_hi(u[i]));
+        x[4 + i] = pack_bf16x2(f2_lo(v[i]), f2_hi(v[i]));
+      }
+    }
+    a = make_uint4(x[0], x[1], x[2], x[3]);
+    b = make_uint4(x[4], x[5], x[6], x[7]);
   }
 }
 
-// Turns the pairs that are turned; the others pass untouched, whatever they hold.
-template <int N>
-__device__ __forceinline__ void turn_pairs(float* u, float* v, const float* cs, const float* sn, int pair, int pairs) {
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float a = u[j], b = v[j];
-    if (pair + j < pairs) {
-      u[j] = a * cs[j] - b * sn[j];
-      v[j] = b * cs[j] + a * sn[j];
-    }
-  }
+__device__ __forceinline__ uint64_t f2_select(bool lo, bool hi, uint64_t a, uint64_t b) {
+  return f2(lo ? f2_lo(a) : f2_lo(b), hi ? f2_hi(a) : f2_hi(b));
+}
+__device__ __forceinline__ uint64_t f2_neg(uint64_t a) { return a ^ 0x8000000080000000ull; }
+
+// 1 / sqrt(x): for bf16 rows the instruction, good to 2 units in the last place.
+template <bool kF32>
+__device__ __forceinline__ float root_inverse(float x) {
+  if constexpr (kF32) return __frsqrt_rn(x);
+  return rsqrtf(x);
 }
 
 struct Tables {
@@ -126,18 +153,24 @@ __device__ __forceinline__ void load_tables(const NormRopeParams& p, Tables& t) 
   __syncthreads();
 }
 
+// Cosines and sines of a lane's pairs, times the amplitude; of those that pass 1 and 0.
 template <int N>
 __device__ __forceinline__ void angles(const NormRopeParams& p, const Tables& t, int64_t b, int i, int pair, int inverse,
-                                       float* cs, float* sn) {
+                                       uint64_t* c, uint64_t* s) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    cs[j] = 1.f, sn[j] = 0.f;
-    if (pair + j < p.pairs) {
-      const int64_t pos = p.pos[t.axis[pair + j] * p.pos_sa + b * p.pos_sn + i];
-      cos_sin(pos, t.turn[pair + j], inverse, &cs[j], &sn[j]);
-      cs[j] *= p.amplitude;
-      sn[j] *= p.amplitude;
+  for (int j = 0; j < N; j += 2) {
+    float cs[2] = {1.f, 1.f}, sn[2] = {0.f, 0.f};
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      if (pair + j + z < p.pairs) {
+        const int64_t pos = p.pos[t.axis[pair + j + z] * p.pos_sa + b * p.pos_sn + i];
+        cos_sin(pos, t.turn[pair + j + z], inverse, &cs[z], &sn[z]);
+        cs[z] *= p.amplitude;
+        sn[z] *= p.amplitude;
+      }
     }
+    c[j / 2] = f2(cs[0], cs[1]);
+    s[j / 2] = f2(sn[0], sn[1]);
   }
 }
 
@@ -151,71 +184,112 @@ int host_lane_shift(int d, int n) {
   return s;
 }
 
-// Index: of a lane's work item; 32 bits where they are enough.
-template <bool kF32, bool kNorm, bool kInter, int kHeads, typename Index>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  using P = Piece<kF32>;
-  constexpr int N = P::kN;
+// An item: lane, token and a slice of `per` of its chunks of kHeads heads (q's, then k's).
+struct Item {
+  int64_t b;
+  int i, chunk0, lane;
+  __device__ Item(const NormRopeParams& p, int64_t it, int shift, int slices, int per) {
+    lane = (int)it & ((1 << shift) - 1);
+    const int64_t ts = it >> shift;
+    int64_t t;
+    if (ts < (int64_t(1) << 32)) {  // divisions in 32 bits where they are enough
+      t = (uint32_t)ts / (uint32_t)slices;
+      b = (uint32_t)t / (uint32_t)p.l;
+    } else {
+      t = ts / slices;
+      b = t / p.l;
+    }
+    i = (int)(t - b * p.l);
+    chunk0 = (int)(ts - t * slices) * per;
+  }
+};
+
+// kPartial: only a part of the head is turned.
+template <bool kF32, bool kNorm, bool kInter, bool kPartial, int kHeads>
+__global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int slices, int per) {
+  constexpr int N = Piece<kF32>::kN, H = N / 2;
   __shared__ Tables tables;
   load_tables<kNorm>(p, tables);
   constexpr int es = kF32 ? 4 : 2;
-  const int shift = lane_shift(p.d, N), lane = threadIdx.x & ((1 << shift) - 1);
-  const Place<kInter, N> at(lane, p.d, p.pairs);
-  const unsigned gq = (p.hq + kHeads - 1) / kHeads, groups = gq + (p.hk + kHeads - 1) / kHeads;
-  const Index total = ((Index)p.n * p.l * groups) << shift;
+  const int shift = lane_shift(p.d, N);
+  const Place<kInter, N> at(threadIdx.x & ((1 << shift) - 1), p.d, p.pairs);
+  const int cq = (p.hq + kHeads - 1) / kHeads, chunks = cq + (p.hk + kHeads - 1) / kHeads;
+  const int64_t total = ((int64_t)p.n * p.l * slices) << shift;
   const float inv_d = 1.f / (float)p.d;
   // a warp goes on while any of its items is one, so that all its lanes meet in the shuffles
-  for (Index it = (Index)blockIdx.x * kThreads + threadIdx.x; (it & ~(Index)31) < total; it += (Index)gridDim.x * kThreads) {
+  for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; (it & ~int64_t(31)) < total; it += (int64_t)gridDim.x * kThreads) {
     const bool live = it < total && at.mine;
-    const Index tg = live ? it >> shift : 0, t = tg / groups;
-    const unsigned g = (unsigned)(tg - t * groups);
-    const bool is_k = g >= gq;
-    const int h0 = (int)(is_k ? g - gq : g) * kHeads, heads = is_k ? p.hk : p.hq;
-    const int64_t b = t / p.l;
-    const int i = (int)(t - (Index)b * p.l);
-    const Seq4 &from = is_k ? p.k : p.q, &to = is_k ? p.ko : p.qo;
-    uint4 ra[kHeads], rb[kHeads];
-    const char* src = static_cast<const char*>(from.ptr) + (b * from.sn + i * from.sl + h0 * from.sh) * es;
+    const Item m(p, it < total ? it : 0, shift, slices, per);
+    // What a row's elements are multiplied by, r apart: with the first and second element of each pair and its partner.
+    uint64_t c[H], s[H], fc[H], fs[H];  // cos, sin of the first element; of the second (with other weights)
+    bool is_k = false;
+    for (int x0 = 0; x0 < per; ++x0) {
+      const int chunk = m.chunk0 + x0;
+      const bool k_now = chunk >= cq;
+      const int h0 = (k_now ? chunk - cq : chunk) * kHeads, heads = chunk < chunks ? (k_now ? p.hk : p.hq) : 0;
+      const Seq4 &from = k_now ? p.k : p.q, &to = k_now ? p.ko : p.qo;
+      uint4 ra[kHeads], rb[kHeads];
+      const char* src = static_cast<const char*>(from.ptr) + (m.b * from.sn + m.i * from.sl + h0 * from.sh) * es;
 #pragma unroll
-    for (int x = 0; x < kHeads; ++x) {
-      ra[x] = rb[x] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && h0 + x < heads) {
-        ra[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.a) * es));
-        rb[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.b) * es));
-      }
-    }
-    float cs[N], sn[N];
-    angles<N>(p, tables, b, i, at.mine ? at.pair : p.pairs, p.inverse, cs, sn);
-    char* dst = static_cast<char*>(to.ptr) + (b * to.sn + i * to.sl + h0 * to.sh) * es;
-#pragma unroll
-    for (int x = 0; x < kHeads; ++x) {
-      float u[N], v[N];
-      unpack<kF32, kInter>(ra[x], rb[x], u, v);
-      if constexpr (kNorm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) ss = fmaf(u[j], u[j], fmaf(v[j], v[j], ss));
-        for (int o = 1; o < (1 << shift); o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-        const float r = __frsqrt_rn(fmaf(ss, inv_d, p.eps));
-        const float* w = tables.w[is_k];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          u[j] *= r * (at.mine ? w[at.first(j)] : 0.f);
-          v[j] *= r * (at.mine ? w[at.second(j)] : 0.f);
+      for (int x = 0; x < kHeads; ++x) {
+        ra[x] = rb[x] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && h0 + x < heads) {
+          ra[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.a) * es));
+          rb[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.b) * es));
         }
       }
-      turn_pairs<N>(u, v, cs, sn, at.pair, p.pairs);
-      if (live && h0 + x < heads) {
-        uint4 oa, ob;
-        pack<kF32, kInter>(u, v, oa, ob);
-        uint4 *pa = reinterpret_cast<uint4*>(dst + (x * to.sh + at.a) * es),
-              *pb = reinterpret_cast<uint4*>(dst + (x * to.sh + at.b) * es);
-        if constexpr (kHeads == 8) {
-          __stcs(pa, oa);
-          __stcs(pb, ob);
+      if (x0 == 0 || (kNorm && k_now != is_k)) {
+        is_k = k_now;
+        angles<N>(p, tables, m.b, m.i, at.mine ? at.pair : p.pairs, p.inverse, c, s);
+        if constexpr (kNorm) {
+          const float* w = tables.w[is_k];
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            const uint64_t wu = at.mine ? f2(w[at.first(2 * j)], w[at.first(2 * j + 1)]) : 0ull;
+            const uint64_t wv = at.mine ? f2(w[at.second(2 * j)], w[at.second(2 * j + 1)]) : 0ull;
+            fc[j] = f2_mul(wv, c[j]);
+            fs[j] = f2_mul(wu, s[j]);
+            c[j] = f2_mul(wu, c[j]);
+            s[j] = f2_neg(f2_mul(wv, s[j]));
+          }
         } else {
-          *pa = oa;
-          *pb = ob;
+#pragma unroll
+          for (int j = 0; j < H; ++j) fs[j] = s[j], s[j] = f2_neg(s[j]), fc[j] = c[j];
+        }
+      }
+      char* dst = static_cast<char*>(to.ptr) + (m.b * to.sn + m.i * to.sl + h0 * to.sh) * es;
+#pragma unroll
+      for (int x = 0; x < kHeads; ++x) {
+        uint64_t u[H], v[H];
+        unpack<kF32, kInter>(ra[x], rb[x], u, v);
+        if constexpr (kNorm) {
+          uint64_t sq = 0ull;
+#pragma unroll
+          for (int j = 0; j < H; ++j) sq = f2_fma(u[j], u[j], f2_fma(v[j], v[j], sq));
+          float ss = f2_lo(sq) + f2_hi(sq);
+          for (int o = 1; o < (1 << shift); o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
+          const float r = root_inverse<kF32>(fmaf(ss, inv_d, p.eps));
+          const uint64_t rr = f2(r, r);
+#pragma unroll
+          for (int j = 0; j < H; ++j) u[j] = f2_mul(u[j], rr), v[j] = f2_mul(v[j], rr);
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          const uint64_t pu = f2_mul(u[j], c[j]), pv = f2_mul(v[j], fc[j]);
+          const uint64_t tu = f2_fma(v[j], s[j], pu), tv = f2_fma(u[j], fs[j], pv);
+          if constexpr (kPartial) {  // an element that passes does so whatever its neighbour holds
+            const bool lo = at.pair + 2 * j < p.pairs, hi = at.pair + 2 * j + 1 < p.pairs;
+            u[j] = f2_select(lo, hi, tu, pu);
+            v[j] = f2_select(lo, hi, tv, pv);
+          } else {
+            u[j] = tu, v[j] = tv;
+          }
+        }
+        if (live && h0 + x < heads) {
+          uint4 oa, ob;
+          pack<kF32, kInter>(u, v, oa, ob);
+          __stcs(reinterpret_cast<uint4*>(dst + (x * to.sh + at.a) * es), oa);
+          __stcs(reinterpret_cast<uint4*>(dst + (x * to.sh + at.b) * es), ob);
         }
       }
     }
@@ -223,97 +297,149 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 }
 
 // The gradient under the norm. Blocks [0, bq) do q, the others k; a block's threads step over its part's items.
-template <bool kF32, bool kInter, int kHeads>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, int bq) {
-  using P = Piece<kF32>;
-  constexpr int N = P::kN;
+//
+// A chunk is the rows of kHeads heads, x and the gradient, which go through shared memory by asynchronous copies, kStages -
+// 1 chunks ahead: each thread copies and reads back what is its own, so nothing but its own copies is waited for, and the
+// loads under way need no registers (a 32k training step with loads into registers 301 us, with 2 heads a chunk).
+struct BwdPart {
+  int bq, slices_q, per_q, slices_k, per_k;
+};
+template <int kHeads, int kStages>
+__host__ __device__ constexpr int bwd_smem() {
+  return kStages * kHeads * 4 * kThreads * 16;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
+  const int n = read ? 16 : 0;  // 0: zeros, and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+template <bool kF32, bool kInter, bool kPartial, int kHeads, int kStages>
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, const __grid_constant__ BwdPart q) {
+  constexpr int N = Piece<kF32>::kN, H = N / 2;
   __shared__ Tables tables;
-  __shared__ float sums[kThreads * 2 * N];
+  extern __shared__ __align__(16) uint8_t staged[];  // [stage][head][x a, x b, g a, g b][thread] of 16 bytes
+  static_assert(bwd_smem<kHeads, kStages>() >= kThreads * 2 * N * 4, "the sums take its place");
   load_tables<true>(p, tables);
   constexpr int es = kF32 ? 4 : 2;
-  const int shift = lane_shift(p.d, N), lane = threadIdx.x & ((1 << shift) - 1);
-  const Place<kInter, N> at(lane, p.d, p.pairs);
-  const bool is_k = (int)blockIdx.x >= bq;
-  const int64_t block = is_k ? blockIdx.x - bq : blockIdx.x, blocks = is_k ? gridDim.x - bq : bq;
-  const int heads = is_k ? p.hk : p.hq;
+  const int shift = lane_shift(p.d, N);
+  const Place<kInter, N> at(threadIdx.x & ((1 << shift) - 1), p.d, p.pairs);
+  const bool is_k = (int)blockIdx.x >= q.bq;
+  const int64_t block = is_k ? blockIdx.x - q.bq : blockIdx.x, blocks = is_k ? gridDim.x - q.bq : q.bq;
+  const int heads = is_k ? p.hk : p.hq, slices = is_k ? q.slices_k : q.slices_q, per = is_k ? q.per_k : q.per_q;
   const Seq4 &from = is_k ? p.k : p.q, &grad = is_k ? p.gk : p.gq, &to = is_k ? p.ko : p.qo;
-  const unsigned groups = (heads + kHeads - 1) / kHeads;
-  const int64_t total = ((int64_t)p.n * p.l * groups) << shift;
+  const int64_t total = ((int64_t)p.n * p.l * slices) << shift, first = block * kThreads + threadIdx.x, step = blocks * kThreads;
   const float inv_d = 1.f / (float)p.d;
-  float wa[N], wb[N], da[N], db[N];  // weights and their gradients' sums, of this lane's pairs
+  uint64_t wu[H], wv[H], du[H], dv[H];  // weights and their gradients' sums, of this lane's pairs
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    wa[j] = at.mine ? tables.w[is_k][at.first(j)] : 0.f;
-    wb[j] = at.mine ? tables.w[is_k][at.second(j)] : 0.f;
-    da[j] = db[j] = 0.f;
+  for (int j = 0; j < H; ++j) {
+    const float* w = tables.w[is_k];
+    wu[j] = at.mine ? f2(w[at.first(2 * j)], w[at.first(2 * j + 1)]) : 0ull;
+    wv[j] = at.mine ? f2(w[at.second(2 * j)], w[at.second(2 * j + 1)]) : 0ull;
+    du[j] = dv[j] = 0ull;
   }
-  for (int64_t it = block * kThreads + threadIdx.x; (it & ~int64_t(31)) < total; it += blocks * kThreads) {
+  // what is copied next: chunk `ahead` of item `it_ahead`
+  const uint32_t mine = smem_u32(staged) + threadIdx.x * 16;
+  int64_t it_ahead = first;
+  int ahead = 0, stage_ahead = 0, h_ahead = 0;
+  const char *src = nullptr, *gsrc = nullptr;
+  auto copy_next = [&]() {
+    if ((it_ahead & ~int64_t(31)) < total) {
+      if (ahead == 0) {
+        const Item m(p, it_ahead < total ? it_ahead : 0, shift, slices, per);
+        h_ahead = m.chunk0 * kHeads;
+        src = static_cast<const char*>(from.ptr) + (m.b * from.sn + m.i * from.sl + h_ahead * from.sh) * es;
+        gsrc = static_cast<const char*>(grad.ptr) + (m.b * grad.sn + m.i * grad.sl + h_ahead * grad.sh) * es;
+      }
+      const uint32_t dst = mine + stage_ahead * (kHeads * 4 * kThreads * 16);
+#pragma unroll
+      for (int x = 0; x < kHeads; ++x) {
+        const bool read = it_ahead < total && at.mine && h_ahead + x < heads;
+        // an address that is one, where nothing is read
+        const char *xs = read ? src + x * from.sh * es : src, *gs = read ? gsrc + x * grad.sh * es : gsrc;
+        cp_async16(dst + (x * 4 + 0) * kThreads * 16, xs + (read ? at.a * es : 0), read);
+        cp_async16(dst + (x * 4 + 1) * kThreads * 16, xs + (read ? at.b * es : 0), read);
+        cp_async16(dst + (x * 4 + 2) * kThreads * 16, gs + (read ? at.a * es : 0), read);
+        cp_async16(dst + (x * 4 + 3) * kThreads * 16, gs + (read ? at.b * es : 0), read);
+      }
+      h_ahead += kHeads;
+      src += kHeads * from.sh * es;
+      gsrc += kHeads * grad.sh * es;
+      if (++ahead == per) ahead = 0, it_ahead += step;
+    }
+    stage_ahead = stage_ahead + 1 == kStages ? 0 : stage_ahead + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");  // empty where there is nothing, so that groups count chunks
+  };
+#pragma unroll
+  for (int z = 0; z < kStages - 1; ++z) copy_next();
+  int stage = 0;
+  for (int64_t it = first; (it & ~int64_t(31)) < total; it += step) {
     const bool live = it < total && at.mine;
-    const int64_t tg = live ? it >> shift : 0;
-    int64_t t, b;
-    if (total < (int64_t(1) << 31)) {
-      t = (uint32_t)tg / groups;
-      b = (uint32_t)t / (uint32_t)p.l;
-    } else {
-      t = tg / groups;
-      b = t / p.l;
-    }
-    const int h0 = (int)(tg - t * groups) * kHeads, i = (int)(t - b * p.l);
-    const char* src = static_cast<const char*>(from.ptr) + (b * from.sn + i * from.sl + h0 * from.sh) * es;
-    const char* gsrc = static_cast<const char*>(grad.ptr) + (b * grad.sn + i * grad.sl + h0 * grad.sh) * es;
-    uint4 ra[kHeads], rb[kHeads], ga[kHeads], gb[kHeads];
+    const Item m(p, it < total ? it : 0, shift, slices, per);
+    uint64_t c[H], s[H];
+    angles<N>(p, tables, m.b, m.i, at.mine ? at.pair : p.pairs, 0, c, s);
+    int h0 = m.chunk0 * kHeads;
+    char* dst = static_cast<char*>(to.ptr) + (m.b * to.sn + m.i * to.sl + h0 * to.sh) * es;
+    for (int x0 = 0; x0 < per; ++x0, h0 += kHeads, dst += kHeads * to.sh * es) {
+      copy_next();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const uint4* here = reinterpret_cast<const uint4*>(staged) + stage * (kHeads * 4 * kThreads) + threadIdx.x;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
-    for (int x = 0; x < kHeads; ++x) {
-      ra[x] = rb[x] = ga[x] = gb[x] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && h0 + x < heads) {
-        ra[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.a) * es));
-        rb[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.b) * es));
-        ga[x] = __ldcs(reinterpret_cast<const uint4*>(gsrc + (x * grad.sh + at.a) * es));
-        gb[x] = __ldcs(reinterpret_cast<const uint4*>(gsrc + (x * grad.sh + at.b) * es));
-      }
-    }
-    float cs[N], sn[N];
-    angles<N>(p, tables, b, i, at.mine ? at.pair : p.pairs, 1, cs, sn);
-    char* dst = static_cast<char*>(to.ptr) + (b * to.sn + i * to.sl + h0 * to.sh) * es;
+      for (int x = 0; x < kHeads; ++x) {
+        uint64_t u[H], v[H], gu[H], gv[H];
+        unpack<kF32, kInter>(here[(x * 4 + 0) * kThreads], here[(x * 4 + 1) * kThreads], u, v);
+        unpack<kF32, kInter>(here[(x * 4 + 2) * kThreads], here[(x * 4 + 3) * kThreads], gu, gv);
+        uint64_t sq = 0ull, dot2 = 0ull, yu[H], yv[H];
 #pragma unroll
-    for (int x = 0; x < kHeads; ++x) {
-      float u[N], v[N], gu[N], gv[N];
-      unpack<kF32, kInter>(ra[x], rb[x], u, v);
-      unpack<kF32, kInter>(ga[x], gb[x], gu, gv);
-      turn_pairs<N>(gu, gv, cs, sn, at.pair, p.pairs);
-      float ss = 0.f, dot = 0.f;
+        for (int j = 0; j < H; ++j) {
+          // turned back: (g_u c + g_v s, g_v c - g_u s)
+          const uint64_t pu = f2_mul(gu[j], c[j]), pv = f2_mul(gv[j], c[j]);
+          const uint64_t tu = f2_fma(gv[j], s[j], pu), tv = f2_fma(gu[j], f2_neg(s[j]), pv);
+          if constexpr (kPartial) {
+            const bool lo = at.pair + 2 * j < p.pairs, hi = at.pair + 2 * j + 1 < p.pairs;
+            gu[j] = f2_select(lo, hi, tu, pu);
+            gv[j] = f2_select(lo, hi, tv, pv);
+          } else {
+            gu[j] = tu, gv[j] = tv;
+          }
+          yu[j] = f2_mul(gu[j], wu[j]);
+          yv[j] = f2_mul(gv[j], wv[j]);
+          sq = f2_fma(u[j], u[j], f2_fma(v[j], v[j], sq));
+          dot2 = f2_fma(yu[j], u[j], f2_fma(yv[j], v[j], dot2));
+        }
+        float ss = f2_lo(sq) + f2_hi(sq), dot = f2_lo(dot2) + f2_hi(dot2);
+        for (int o = 1; o < (1 << shift); o <<= 1) {
+          ss += __shfl_xor_sync(~0u, ss, o);
+          dot += __shfl_xor_sync(~0u, dot, o);
+        }
+        if (!(live && h0 + x < heads)) continue;
+        const float r = root_inverse<kF32>(fmaf(ss, inv_d, p.eps)), k = -dot * inv_d * r * r * r;
+        const uint64_t rr = f2(r, r), kk = f2(k, k);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        ss = fmaf(u[j], u[j], fmaf(v[j], v[j], ss));
-        dot = fmaf(gu[j] * wa[j], u[j], fmaf(gv[j] * wb[j], v[j], dot));
+        for (int j = 0; j < H; ++j) {
+          du[j] = f2_fma(gu[j], f2_mul(u[j], rr), du[j]);
+          dv[j] = f2_fma(gv[j], f2_mul(v[j], rr), dv[j]);
+          u[j] = f2_fma(u[j], kk, f2_mul(yu[j], rr));
+          v[j] = f2_fma(v[j], kk, f2_mul(yv[j], rr));
+        }
+        uint4 oa, ob;
+        pack<kF32, kInter>(u, v, oa, ob);
+        __stcs(reinterpret_cast<uint4*>(dst + (x * to.sh + at.a) * es), oa);
+        __stcs(reinterpret_cast<uint4*>(dst + (x * to.sh + at.b) * es), ob);
       }
-      for (int o = 1; o < (1 << shift); o <<= 1) {
-        ss += __shfl_xor_sync(~0u, ss, o);
-        dot += __shfl_xor_sync(~0u, dot, o);
-      }
-      if (!(live && h0 + x < heads)) continue;
-      const float r = __frsqrt_rn(fmaf(ss, inv_d, p.eps)), c = dot * inv_d * r * r;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        da[j] = fmaf(gu[j], u[j] * r, da[j]);
-        db[j] = fmaf(gv[j], v[j] * r, db[j]);
-        u[j] = r * (gu[j] * wa[j] - u[j] * c);
-        v[j] = r * (gv[j] * wb[j] - v[j] * c);
-      }
-      uint4 oa, ob;
-      pack<kF32, kInter>(u, v, oa, ob);
-      __stcs(reinterpret_cast<uint4*>(dst + (x * to.sh + at.a) * es), oa);
-      __stcs(reinterpret_cast<uint4*>(dst + (x * to.sh + at.b) * es), ob);
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if ((is_k ? p.dwk : p.dwq) == nullptr) return;
+  __syncthreads();
   // rows of d: one of every group of lanes
+  float* sums = reinterpret_cast<float*>(staged);
   if (at.mine) {
     float* row = sums + (threadIdx.x >> shift) * p.d;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      row[at.first(j)] = da[j];
-      row[at.second(j)] = db[j];
+      row[at.first(j)] = j & 1 ? f2_hi(du[j / 2]) : f2_lo(du[j / 2]);
+      row[at.second(j)] = j & 1 ? f2_hi(dv[j / 2]) : f2_lo(dv[j / 2]);
     }
   }
   __syncthreads();
@@ -358,55 +484,62 @@ auto with(bool x, F f) {
   return x ? f(std::true_type{}) : f(std::false_type{});
 }
 
-template <bool kF32, bool kNorm, bool kInter>
+// Into how many slices the chunks of a token go, so that `threads` threads have work, and how many chunks that is each.
+struct Slices {
+  int slices, per;
+  Slices(int64_t lanes_of_tokens, int chunks, int64_t threads) {
+    int64_t want = lanes_of_tokens > 0 ? (threads + lanes_of_tokens - 1) / lanes_of_tokens : 1;
+    if (want > chunks) want = chunks;
+    if (want < 1) want = 1;
+    per = (int)((chunks + want - 1) / want);
+    slices = per > 0 ? (chunks + per - 1) / per : 0;
+  }
+};
+
+constexpr int kBwdMaxBlocks = 2048;
+
+template <bool kF32, bool kNorm, bool kInter, bool kPartial>
 cudaError_t launch_fwd(const NormRopeParams& p, cudaStream_t s) {
   constexpr int N = kF32 ? 4 : 8;
   const int shift = host_lane_shift(p.d, N);
-  auto items = [&](int heads) {
-    return ((int64_t)p.n * p.l * ((p.hq + heads - 1) / heads + (p.hk + heads - 1) / heads)) << shift;
-  };
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const bool wide = items(8) >= (int64_t)sms * kSmThreads;  // enough to fill the GPU
-  int64_t blocks = (items(wide ? 8 : 4) + kThreads - 1) / kThreads;
+  const int chunks = (p.hq + kFwdHeads - 1) / kFwdHeads + (p.hk + kFwdHeads - 1) / kFwdHeads;
+  const Slices c(((int64_t)p.n * p.l) << shift, chunks, (int64_t)sms * kSmThreads);
+  int64_t blocks = ((((int64_t)p.n * p.l * c.slices) << shift) + kThreads - 1) / kThreads;
   if (blocks > (int64_t(1) << 30)) blocks = int64_t(1) << 30;  // the kernel strides over the rest
-  const bool narrow = blocks * kThreads * 2 < (int64_t(1) << 32);
-  auto kern = wide ? (narrow ? norm_rope_kernel<kF32, kNorm, kInter, 8, uint32_t> : norm_rope_kernel<kF32, kNorm, kInter, 8, uint64_t>)
-                   : norm_rope_kernel<kF32, kNorm, kInter, 4, uint32_t>;  // not wide: few items
-  return launch_dependent(kern, dim3((unsigned)blocks), kThreads, 0, s, p);
+  return launch_dependent(norm_rope_kernel<kF32, kNorm, kInter, kPartial, kFwdHeads>, dim3((unsigned)blocks), kThreads, 0, s, p,
+                          c.slices, c.per);
 }
 
-constexpr int kBwdHeads = 4;
-constexpr int kBwdMaxBlocks = 2048;
-
-template <bool kF32, bool kInter>
+template <bool kF32, bool kInter, bool kPartial>
 cudaError_t launch_bwd(const NormRopeParams& p, cudaStream_t s, int* bq, int* blocks) {
   constexpr int N = kF32 ? 4 : 8;
   static PerContext<int> cache;
   int cap = 0;
-  cudaError_t e = wave_cap(cache, norm_rope_bwd_kernel<kF32, kInter, kBwdHeads>, kThreads, 0, &cap);
+  auto kern = norm_rope_bwd_kernel<kF32, kInter, kPartial, kBwdHeads, kBwdStages>;
+  constexpr int smem = bwd_smem<kBwdHeads, kBwdStages>();
+  cudaError_t e = wave_cap(cache, kern, kThreads, smem, &cap);
   if (e != cudaSuccess) return e;
   if (cap > kBwdMaxBlocks) cap = kBwdMaxBlocks;
   const int shift = host_lane_shift(p.d, N);
-  auto need = [&](int heads) {
-    return ((((int64_t)p.n * p.l * ((heads + kBwdHeads - 1) / kBwdHeads)) << shift) + kThreads - 1) / kThreads;
-  };
-  const int64_t q = need(p.hq), k = need(p.hk);
+  const int64_t lanes = ((int64_t)p.n * p.l) << shift;
+  const int cq = (p.hq + kBwdHeads - 1) / kBwdHeads, ck = (p.hk + kBwdHeads - 1) / kBwdHeads;
   // a wave shared out by work, at least a block for each that has some
-  int64_t nq = q, nk = k;
-  if (q + k > cap) {
-    nq = k == 0 ? cap : (int64_t)((double)cap * q / (double)(q + k) + 0.5);
-    if (nq < 1) nq = 1;
-    if (k > 0 && nq > cap - 1) nq = cap - 1;
-    nk = cap - nq;
-    if (nk > k) nk = k;
-    if (nq > q) nq = q;
-  }
+  int64_t nq = cq + ck > 0 ? (int64_t)((double)cap * cq / (cq + ck) + 0.5) : 0;
+  if (cq > 0 && nq < 1) nq = 1;
+  if (ck > 0 && nq > cap - 1) nq = cap - 1;
+  int64_t nk = ck > 0 ? cap - nq : 0;
+  const Slices sq(lanes, cq, nq * kThreads), sk(lanes, ck, nk * kThreads);
+  auto most = [&](const Slices& c) { return (lanes * c.slices + kThreads - 1) / kThreads; };
+  if (nq > most(sq)) nq = most(sq);
+  if (nk > most(sk)) nk = most(sk);
   *bq = (int)nq;
   *blocks = (int)(nq + nk);
   if (*blocks == 0) return cudaSuccess;
-  return launch_dependent(norm_rope_bwd_kernel<kF32, kInter, kBwdHeads>, dim3((unsigned)*blocks), kThreads, 0, s, p, *bq);
+  const BwdPart part{*bq, sq.slices, sq.per, sk.slices, sk.per};
+  return launch_dependent(kern, dim3((unsigned)*blocks), kThreads, smem, s, p, part);
 }
 
 }  // namespace
@@ -415,7 +548,9 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s, int* nlaun
   const cudaError_t e = with(p.is_f32, [&](auto f32) {
     return with(p.norm, [&](auto norm) {
       return with(p.interleaved, [&](auto inter) {
-        return launch_fwd<decltype(f32)::value, decltype(norm)::value, decltype(inter)::value>(p, s);
+        return with(2 * p.pairs != p.d, [&](auto partial) {
+          return launch_fwd<decltype(f32)::value, decltype(norm)::value, decltype(inter)::value, decltype(partial)::value>(p, s);
+        });
       });
     });
   });
@@ -429,7 +564,9 @@ cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, cudaStream_t s, int* n
   int bq = 0, blocks = 0;
   cudaError_t e = with(p.is_f32, [&](auto f32) {
     return with(p.interleaved, [&](auto inter) {
-      return launch_bwd<decltype(f32)::value, decltype(inter)::value>(p, s, &bq, &blocks);
+      return with(2 * p.pairs != p.d, [&](auto partial) {
+        return launch_bwd<decltype(f32)::value, decltype(inter)::value, decltype(partial)::value>(p, s, &bq, &blocks);
+      });
     });
   });
   if (e != cudaSuccess) return e;
