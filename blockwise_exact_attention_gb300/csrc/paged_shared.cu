@@ -46,13 +46,12 @@ constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch, "register split");
 constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
 constexpr float kRescale = 8.f;  // log2: O is rescaled only when a maximum grows by more
-constexpr uint32_t kPReadyBar = 1, kPReadyThreads = 128 + 32, kEpiBar = 3, kBothBar = 5;
+constexpr uint32_t kPReadyBar = 1, kPReadyThreads = 128 + 32, kBothBar = 3;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// A run's cut is moved by up to so many steps (and a quarter of a run) to a unit's border: a run in two units costs about 5
-// steps more, as it fetches queries and writes parts twice.
-constexpr int kSnap = 3;
-// Steps of a run at least, as long as there are fewer than the GPU has CTAs.
-constexpr int kMinSteps = 1;
+// Of a unit besides its steps, in steps: a run in two units fetches queries and writes parts twice.
+constexpr int kUnitCost = 2;
+// A run's cut is moved by up to so many steps (and a quarter of a run) to a unit's border.
+constexpr int kSnap = 2;
 
 template <int D>
 struct Cfg {
@@ -76,6 +75,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// 32 bytes, a sector of memory, by one thread.
+__device__ __forceinline__ void store_sector(float* to, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // ---- schedule ----------------------------------------------------------------------
 
 // A group as the setup finds it: its rows, the first of them that has keys, the tiles that are shared.
@@ -84,7 +90,7 @@ struct alignas(16) Group {
 };
 
 // Of a group: units of two halves, rows of a last unit of one half (0: none), and steps, a step being a tile of a unit of
-// two halves or two tiles of the other.
+// two halves or two tiles of the other. A unit costs its steps, and kUnitCost behind them.
 struct Shape {
   int rows, twos, one, tiles, one_steps;
   __host__ __device__ Shape(int q_rows, int t) : rows(q_rows), tiles(t) {
@@ -94,44 +100,45 @@ struct Shape {
     if (t == 0) twos = one = 0;
     one_steps = one > 0 ? (t + 1) / 2 : 0;
   }
-  __host__ __device__ int steps() const { return twos * tiles + one_steps; }       // of a K/V head
+  // what a K/V head's units cost
+  __host__ __device__ int cost() const { return twos * (tiles + kUnitCost) + (one > 0 ? one_steps + kUnitCost : 0); }
   __host__ __device__ int part_rows() const { return twos * kUnitRows + 2 * one; }  // rows of its parts
 };
 
-// Where the groups' steps and parts' rows begin, [groups + 1] each; and the runs.
+// Where the groups' costs and parts' rows begin, [groups + 1] each; and the runs.
 struct Schedule {
-  const int *steps, *rows;
+  const int *costs, *rows;
   const Group* groups;
   int n_groups, heads;  // heads: query heads of a K/V head
   int total, ctas, snap;
 
-  __device__ Schedule(const int* s, const int* r, const Group* g, int n, int query_heads, int most_ctas)
-      : steps(s), rows(r), groups(g), n_groups(n), heads(query_heads), total(s[n]) {
-    ctas = min(most_ctas, max(1, total / kMinSteps));
+  __device__ Schedule(const int* c, const int* r, const Group* g, int n, int query_heads, int most_ctas)
+      : costs(c), rows(r), groups(g), n_groups(n), heads(query_heads), total(c[n]) {
+    ctas = min(most_ctas, max(1, total));  // a step each at least
     snap = min(kSnap, total / ctas / 4);
   }
-  // The group that step v belongs to: the last whose steps begin at v or before.
+  // The group that cost v belongs to: the last that begins at it or before.
   __device__ int group_of(int v) const {
     int lo = 0, hi = n_groups - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (steps[mid] <= v)
+      if (costs[mid] <= v)
         lo = mid;
       else
         hi = mid - 1;
     }
     return lo;
   }
-  // Where CTA c's run begins: equal shares, but a unit's border that is near takes the cut's place.
+  // Where CTA c's run begins: equal shares of the cost, but a unit's border that is near takes the cut's place.
   __device__ int begin(int c) const {
     const int v = (int)((int64_t)total * c / ctas);
-    if (snap == 0 || v == 0 || v >= total) return v;
+    if (v == 0 || v >= total) return v;
     const int g = group_of(v);
     const Shape sh(groups[g].rows * heads, groups[g].tiles);
-    int in = (v - steps[g]) % sh.steps();
-    const int u = min(in / sh.tiles, sh.twos), all = u < sh.twos ? sh.tiles : sh.one_steps;
-    in -= u * sh.tiles;
-    return in <= snap ? v - in : all - in <= snap ? v + all - in : v;
+    int in = (v - costs[g]) % sh.cost();
+    const int each = sh.tiles + kUnitCost, u = min(in / each, sh.twos), steps = u < sh.twos ? sh.tiles : sh.one_steps;
+    in -= u * each;
+    return in <= snap ? v - in : in >= steps - snap ? v + steps + kUnitCost - in : v;
   }
   __device__ int cta_of(int v) const {
     int c = (int)((((int64_t)v + 1) * ctas - 1) / total);
@@ -144,33 +151,35 @@ struct Schedule {
 // A run's piece in one unit: steps [a, b) of it.
 struct Seg {
   Group g;
-  int hk, q0, rows, two, a, b, part, end;  // q0: first query row in the group; part: first row of the unit's parts; end: the
-                                           // step behind the unit's last, of all
+  int hk, q0, rows, two, a, b, part;  // q0: first query row in the group; part: first row of the unit's parts
+  int last, next;                     // costs: of the unit's last step; where the run goes on
   __device__ int first(int t) const { return two ? a : 2 * a + t; }  // half t's first tile
   __device__ int count(int t) const {                                // and how many it has
     if (two) return b - a;
-    const int last = min(2 * b, g.tiles);
-    return max(0, (last - 2 * a - t + 1) / 2);
+    const int end = min(2 * b, g.tiles);
+    return max(0, (end - 2 * a - t + 1) / 2);
   }
   __device__ int tile0() const { return two ? a : 2 * a; }
   __device__ int tile1() const { return two ? b : min(2 * b, g.tiles); }
 };
 
+// The piece that begins at cost v, which is that of a step, of a run that ends at `end`.
 __device__ __forceinline__ Seg seg_at(const Schedule& s, int v, int end) {
   const int lo = s.group_of(v);
   Seg r;
   r.g = s.groups[lo];
   const Shape sh(r.g.rows * s.heads, r.g.tiles);
-  const int each = sh.steps(), in_group = v - s.steps[lo];
-  r.hk = in_group / each;
-  const int in = in_group - r.hk * each, u = min(in / sh.tiles, sh.twos);
+  const int in_group = v - s.costs[lo], unit = sh.tiles + kUnitCost;
+  r.hk = in_group / sh.cost();
+  const int in = in_group - r.hk * sh.cost(), u = min(in / unit, sh.twos);
   r.two = u < sh.twos;
   r.q0 = u * kUnitRows;
   r.rows = r.two ? min(kUnitRows, sh.rows - r.q0) : sh.one;
-  r.a = in - u * sh.tiles;
+  r.a = in - u * unit;
   const int all = r.two ? sh.tiles : sh.one_steps;
   r.b = min(all, r.a + (end - v));
-  r.end = v - r.a + all;
+  r.last = v - r.a + all - 1;
+  r.next = min(end, r.last + 1 + kUnitCost);
   r.part = s.rows[lo] + r.hk * sh.part_rows() + r.q0;
   return r;
 }
@@ -298,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
            *v_empty = k_empty + C::kStages, *s_full = v_empty + C::kStages, *o_full = s_full + 2, *mma_done = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* first_step = reinterpret_cast<int*>(smem + C::kTableOff);
-  int* first_row = first_step + kMaxGroups + 1;
+  int* first_cost = reinterpret_cast<int*>(smem + C::kTableOff);
+  int* first_row = first_cost + kMaxGroups + 1;
   Group* groups = reinterpret_cast<Group*>(smem + C::kGroupOff);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int heads = p.h / p.hkv;
@@ -318,15 +327,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   grid_launch_dependents();
-  if (warp == kVWarp) {  // sums of steps and part rows over the groups
-    int steps = 0, rows = 0;
+  if (warp == kVWarp) {  // sums of costs and part rows over the groups
+    int costs = 0, rows = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
       int s = 0, r = 0;
       if (g0 + lane < p.groups) {
-        const Group g = p.group[g0 + lane];
+        // past L1, like all that this kernel reads before it has waited for the launch before it
+        const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.group + g0 + lane));
+        const Group g{raw.x, raw.y, raw.z, raw.w};
         groups[g0 + lane] = g;
         const Shape sh(g.rows * heads, g.tiles);
-        s = sh.steps() * p.hkv;
+        s = sh.cost() * p.hkv;
         r = sh.part_rows() * p.hkv;
       }
       int si = s, ri = r;
@@ -336,19 +347,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane >= o) si += x, ri += y;
       }
       if (g0 + lane < p.groups) {
-        first_step[g0 + lane] = steps + si - s;
+        first_cost[g0 + lane] = costs + si - s;
         first_row[g0 + lane] = rows + ri - r;
       }
-      steps += __shfl_sync(~0u, si, 31);
+      costs += __shfl_sync(~0u, si, 31);
       rows += __shfl_sync(~0u, ri, 31);
     }
-    if (lane == 0) first_step[p.groups] = steps, first_row[p.groups] = rows;
+    if (lane == 0) first_cost[p.groups] = costs, first_row[p.groups] = rows;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Schedule sc(first_step, first_row, groups, p.groups, heads, gridDim.x);
+  const Schedule sc(first_cost, first_row, groups, p.groups, heads, gridDim.x);
   const int cta = blockIdx.x;
   const int run0 = cta < sc.ctas ? sc.begin(cta) : 0, run1 = cta < sc.ctas ? sc.begin(cta + 1) : 0;
   if (warp >= 8) {
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0;
       for (int v = run0; ok && v < run1;) {
         const Seg sg = seg_at(sc, v, run1);
-        v += sg.b - sg.a;
+        v = sg.next;
         const int32_t* entries = p.table + sg.g.owner * p.table_stride;
         int id[kMost], off[kMost];  // of this lane's boxes in the next tile
         auto look_up = [&](int j) {
@@ -375,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (b >= boxes || j >= sg.tile1()) continue;
             const int key = j * kTile + b * p.box, pg = key / p.page;
             off[i] = key - pg * p.page;
-            id[i] = entries[pg];
+            id[i] = __ldcg(entries + pg);
           }
         };
         look_up(sg.tile0());
@@ -410,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int base = 0, seg = 0;
       for (int v = run0; v < run1; ++seg) {
         const Seg sg = seg_at(sc, v, run1);
-        v += sg.b - sg.a;
+        v = sg.next;
         const int most = sg.count(0);  // the second half has as many tiles or one less
         // half t's x-th tile is the ring's slot(t, x)-th
         auto slot = [&](int t, int x) { return base + (sg.two ? x : 2 * x + t); };
@@ -487,19 +498,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (hh >= heads) hh -= heads, ++b;
       }
     };
-    for (int v = run0; v < run1;) {
-      const Seg sg = seg_at(sc, v, run1);
-      v += sg.b - sg.a;
-      // into shared memory, 128-byte swizzled like the forward's
+    // into shared memory, 128-byte swizzled like the forward's
+    auto copy_queries = [&](const Seg& sg) {
       each_row(sg, [&](int row, const __nv_bfloat16* from) {
         const int in = row % kTile;
         if (row < kTile || sg.two) cp_async16(smem_u32(smem + (row / kTile) * C::kTileBytes + (q_piece / 8) * 16384 + in * 128 +
-                            (((q_piece & 7) ^ (in & 7)) << 4)),
-                   from);
+                                                       (((q_piece & 7) ^ (in & 7)) << 4)),
+                                              from);
       });
+    };
+    auto queries_there = [&]() {
       cp_async_wait_all();
       fence_proxy_async_smem();
       mbar_arrive(q_full);
+    };
+    if (run0 < run1) {
+      copy_queries(seg_at(sc, run0, run1));
+      queries_there();
+    }
+    for (int v = run0; v < run1;) {
+      const Seg sg = seg_at(sc, v, run1);
+      v = sg.next;
       float m_ref = -INFINITY, l_sum = 0.f;
       const int n = sg.count(t);
       for (int x = 0; x < n; ++x, ++met) {
@@ -585,61 +604,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         named_bar_sync(kPReadyBar + t, kPReadyThreads);
       }
-      const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
-      const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows);
-      if (v < run1)  // the next unit's queries into L2, while this one's part is written
-        each_row(seg_at(sc, v, run1), [&](int, const __nv_bfloat16* from) {
-          if (q_piece % 8 == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
-        });
+      // Both halves have met the unit's last S: the next one's queries may take the place of its queries, and their S
+      // products run while this unit's parts are written.
+      const bool more = v < run1;
+      if (more) {
+        named_bar_sync(kBothBar, 256);
+        copy_queries(seg_at(sc, v, run1));
+      }
       if (sg.a == 0) {
         // for the kernel that joins: each row's first part, the parts' number, and the second half's distance
-        const int parts = (sc.cta_of(sg.end - 1) - cta + 1) * (sg.two ? 1 : 2);
+        const int parts = (sc.cta_of(sg.last) - cta + 1) * (sg.two ? 1 : 2);
         for (int i = threadIdx.x; i < sg.rows; i += 256) {
           const int qr = sg.q0 + i, b = qr / heads, hh = sg.hk * heads + (qr - b * heads);
           p.row[(int64_t)(sg.g.row0 + b) * p.h + hh] = make_int4(kUnitRows * cta + sg.part + i, parts, sg.two ? 0 : sg.rows, 0);
         }
       }
-      // ---- this half's part: O through shared memory (its query tile, free once O is done: every S product came before
-      // the last P V) so that memory sees whole 128-byte pieces of rows ----
+      if (more) queries_there();
+      // ---- this half's part, each thread its row, whole 32-byte sectors of it at a time ----
+      const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
+      const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows) + r;
+      if (ok && r < rows) p.ml[part] = make_float2(m_ref, l_sum);
       if (n > 0) {
         if (ok) ok = warp_wait_parity(&o_full[t], done & 1, abort_flag, p.status);
         ++done;
         tc_fence_after();
-      }
-      if (ok && r < rows) p.ml[part + r] = make_float2(m_ref, l_sum);
-      if (n > 0) {
-        uint8_t* stage = smem + t * C::kTileBytes;
-        const int piece = r & 7;
-        // two buffers where the tile has room for them: a chunk's reads are then over when the next but one is written
-        constexpr bool kTwoBufs = C::kTileBytes >= 2 * 16384;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint8_t* buf = stage + (kTwoBufs ? (c0 & 32) * 512 : 0);
-          if (ok) {
-            uint32_t orow[32];
+        if (ok) {
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 64) {
+            uint32_t orow[64];
             tmem_ld32(o_tmem + c0, orow);
+            tmem_ld32(o_tmem + c0 + 32, orow + 32);
             tmem_wait_ld();
-            reg_fence<32>(orow);
+            reg_fence<64>(orow);
+            if (r < rows) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(buf + r * 128 + ((k ^ (r & 7)) << 4)) =
-                  make_uint4(orow[4 * k], orow[4 * k + 1], orow[4 * k + 2], orow[4 * k + 3]);
-          }
-          named_bar_sync(kEpiBar + t, 128);
-          if (ok) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int row = (r >> 3) + 16 * k;
-              if (row < rows)
-                *reinterpret_cast<uint4*>(p.o + (part + row) * D + c0 + 4 * piece) =
-                    *reinterpret_cast<const uint4*>(buf + row * 128 + ((piece ^ (row & 7)) << 4));
+              for (int k = 0; k < 8; ++k) store_sector(p.o + part * D + c0 + 8 * k, orow + 8 * k);
             }
           }
-          if (!kTwoBufs) named_bar_sync(kEpiBar + t, 128);
         }
         tc_fence_before();
       }
-      if (v < run1) named_bar_sync(kBothBar, 256);  // both halves are done with the queries
     }
   }
 
@@ -661,9 +665,9 @@ constexpr int kJoinWarps = 4;
 // kSplit warps of a block to a (request, query head), a lane D / 32 columns: the parts of its prefix and of its own keys,
 // dealt to the warps, or its own keys' result. A chain of two memory latencies (where the parts are, the parts) as long as a
 // warp has at most kBatch of them.
-template <int D, int kSplit>
-__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __grid_constant__ Args p) {
-  constexpr int N = D / 32, kBatch = 8;
+template <int D, int kSplit, int kBatch>
+__global__ void __launch_bounds__(kJoinWarps * 32, kBatch == 4 ? 8 : 1) shared_join_kernel(const __grid_constant__ Args p) {
+  constexpr int N = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = warp % kSplit;
   const int64_t item = (int64_t)blockIdx.x * (kJoinWarps / kSplit) + warp / kSplit;
   grid_dependency_wait();
@@ -847,11 +851,13 @@ cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUte
   if ((e = launch_dependent(shared_prefix_kernel<D, kTerms>, dim3(f.ctas), kThreads, C::kSmem, s, tk, tv, a)) != cudaSuccess) return e;
   *nlaunch += 1;
   const int64_t items = (int64_t)d.n * d.h;
-  // Rows that do not fill the GPU are cut into many parts each.
-  const bool few = items <= 152 * 8;
+  // Rows that do not fill the GPU have many parts each, four warps a row then; where there are warps enough to hide the
+  // latency fewer loads at a time leave room for more of them. (256 requests of 32 heads: 95.9 us with 4 at a time, 97.9 with
+  // 8; 64 requests 62.8, 61.3 us; 16 requests 36.2 us, with one warp a row 42.0.)
+  const bool few = items <= 152 * 8, many = items > 152 * 32;
   const int64_t warps = items * (few ? kJoinWarps : 1);
-  e = launch_dependent(few ? shared_join_kernel<D, kJoinWarps> : shared_join_kernel<D, 1>,
-                       dim3((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, a);
+  auto join = few ? shared_join_kernel<D, kJoinWarps, 8> : many ? shared_join_kernel<D, 1, 4> : shared_join_kernel<D, 1, 8>;
+  e = launch_dependent(join, dim3((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, a);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }
@@ -886,7 +892,7 @@ bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int
   const int64_t most = (int64_t(1) << 31) - 1;
   if (2 * n * h + (int64_t)kUnitRows * kMaxCtas > most) return false;
   const int64_t units = h_kv * (n * (h / h_kv) / kUnitRows + (groups < n ? groups : n));
-  return units <= most / (max_keys / kTile + 1);
+  return units <= most / (max_keys / kTile + 1 + kUnitCost);
 }
 
 cudaError_t launch_paged_shared(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s,

@@ -43,7 +43,8 @@ int bea_paged_decode_shared(const bea_tensor* q, const bea_tensor* k_cache, cons
   if ((rc = status_ptr_for_current_device(&p.d.status))) return rc;
   int launches = 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (bea::paged_shared_is_plain(p.d, groups))
+  // (no copies by box from a cache whose pages, tokens or heads lie on one another)
+  if (bea::paged_shared_is_plain(p.d, groups) || broadcast(k_cache) || broadcast(v_cache))
     return finish(bea::launch_paged_decode(p.d, s, &launches), launches);
   CUtensorMap tk, tv;
   const int box = bea::paged_shared_box(p.d.page);

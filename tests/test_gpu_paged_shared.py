@@ -153,6 +153,29 @@ def test_shared_lengths(shared):
     check(out, lse, *x, 0.1)
 
 
+@pytest.mark.parametrize("n,h,h_kv", [(1100, 2, 1), (5, 300, 1)])
+def test_more_than_one_round_of_the_rest(n, h, h_kv):
+    """More requests, or more heads to a K/V head, than the kernel of the requests' own keys takes at once, some of them cut
+    between CTAs."""
+    rng = random.Random(n)
+    own = [rng.choice([0, 1, 9, 700]) for _ in range(n)] if n < 100 else [1500 if i % 300 == 7 else i % 5 for i in range(n)]
+    x, g = make([(256, own)], h, h_kv, 64, 16, seed=n)
+    out, lse = run(x, g, 0.1)
+    check(out, lse, *x, 0.1)
+    out, lse = run(x, g, 0.1, out_dtype=F32)
+    check(out, lse, *x, 0.1)
+
+
+def test_a_cache_of_one_page_many_times():
+    """An expanded cache, which cannot be copied by box: nothing is shared."""
+    import blockwise_exact_attention_gb300 as bea
+    k, v, q = draw((1, 16, 2, 64), 1), draw((1, 16, 2, 64), 2), draw((3, 1, 4, 64), 3)
+    table, lens = torch.arange(60000, dtype=I32, device="cuda").repeat(3, 1) % 40, i32([600, 620, 630])
+    x = (q, k.expand(40, 16, 2, 64), v.expand(40, 16, 2, 64), table, lens)
+    got, want = run(x, (i32([0, 3]), i32([600])), 0.1), bea.paged_decode(*x, 0.1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_small_tables_take_the_kernel_of_single_requests():
     import blockwise_exact_attention_gb300 as bea
     x, g = make([(400, [1, 17, 300])], 8, 2, 64, 16, seed=1, wide=False)
