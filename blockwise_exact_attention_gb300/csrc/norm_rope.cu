@@ -18,6 +18,10 @@
 // The weights' gradient is a sum over all rows. A thread keeps its columns' sums in fp32 over all the rows it meets
 // (the grid is one wave, each block only q or only k), a block adds up its threads in shared memory, and a second kernel
 // the blocks, all in a fixed order: the same call gives the same bits.
+//
+// Measured (GPU time, inputs larger than L2): [1, 32768, 32 + 8, 128] bf16 forward 113 us (5.9 TB/s), with its gradient
+// 290 us (5.8 TB/s; a copy reaches 6.7); without the norm, half of the head turned, 101 us (6.6 TB/s). [1, 16384, 16 + 16,
+// 128] f32 84 and 216 us (6.4, 6.2 TB/s). 256 tokens of 32 + 8 heads: 5.2 us, the host takes 7.5
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -31,8 +35,13 @@ namespace bea {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSmThreads = 2048;  // that an SM holds
+// Threads of an SM that a forward's tokens are shared out between, at least: two waves of them. Fewer slices of a token compute
+// its angles less often, more of them end together ([8, 4096, 16 + 16, 64] bf16: 640 threads 55.0 us, 1280 49.9, 2048 58.0;
+// [1, 4096, 32 + 8, 128]: 23.2, 18.5, 22.5 us).
+constexpr int kSmThreads = 1280;
 constexpr int kMaxD = 2 * kRopeMaxPairs;
+// Heads of a chunk. Forward: 2 and 8 heads 131 and 127 us for [1, 32768, 32 + 8, 128] bf16 (now 113). Backward: 1 head three
+// stages deep 2-4% slower; 3 or 5 blocks to an SM 318 and 350 us for the training step (now 290).
 constexpr int kFwdHeads = 4;
 constexpr int kBwdHeads = 2, kBwdStages = 2, kBwdBlocks = 4;
 
