@@ -13,7 +13,8 @@
 namespace bea {
 
 // Launch with programmatic stream serialisation: the kernel may be set up while the one before it on the stream still
-// runs, so it has to call grid_dependency_wait() in every thread before it touches anything in memory. (The attention
+// runs, so it has to call grid_dependency_wait() in every thread before it touches anything in memory. (One kernel waits at
+// its end instead: paged_shared.cu says what it relies on. The attention
 // kernels, whose last writes are bulk copies, let in only the next step of a ring.) A chain of short
 // kernels gains 0.4-1 us a launch in a graph, and 1.2 us where the host launches them one by one. Which kernels let the
 // next one in early (grid_launch_dependents) is measured: those of one CTA per SM or fewer do, as it hides the next

@@ -112,7 +112,7 @@ struct alignas(16) Group {
 // two halves or two tiles of the other. A unit costs its steps, and kUnitCost behind them.
 struct Shape {
   int rows, twos, one, tiles, one_steps;
-  __host__ __device__ Shape(int q_rows, int t) : rows(q_rows), tiles(t) {
+  __device__ Shape(int q_rows, int t) : rows(q_rows), tiles(t) {
     twos = q_rows / kUnitRows;
     one = q_rows - twos * kUnitRows;
     if (one > kTile) one = 0, ++twos;
@@ -120,8 +120,8 @@ struct Shape {
     one_steps = one > 0 ? (t + 1) / 2 : 0;
   }
   // what a K/V head's units cost
-  __host__ __device__ int cost() const { return twos * (tiles + kUnitCost) + (one > 0 ? one_steps + kUnitCost : 0); }
-  __host__ __device__ int part_rows() const { return twos * kUnitRows + 2 * one; }  // rows of its parts
+  __device__ int cost() const { return twos * (tiles + kUnitCost) + (one > 0 ? one_steps + kUnitCost : 0); }
+  __device__ int part_rows() const { return twos * kUnitRows + 2 * one; }  // rows of its parts
 };
 
 // Where the groups' costs and parts' rows begin, [groups + 1] each; and the runs.
@@ -172,8 +172,7 @@ struct Seg {
   Group g;
   int hk, q0, rows, two, a, b, part;  // q0: first query row in the group; part: first row of the unit's parts
   int last, next;                     // costs: of the unit's last step; where the run goes on
-  __device__ int first(int t) const { return two ? a : 2 * a + t; }  // half t's first tile
-  __device__ int count(int t) const {                                // and how many it has
+  __device__ int count(int t) const {  // half t's tiles
     if (two) return b - a;
     const int end = min(2 * b, g.tiles);
     return max(0, (end - 2 * a - t + 1) / 2);
@@ -207,7 +206,7 @@ __device__ __forceinline__ Seg seg_at(const Schedule& s, int v, int end) {
 struct Layout {
   size_t skip, groups, rows, cuts, suffix, suffix_lse, decode, ml, o, total;
 };
-__host__ __device__ inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 inline Layout layout(int64_t n, int64_t h, int64_t d, int64_t groups, size_t decode_bytes) {
   Layout w;
   const size_t rows = 2 * (size_t)(n * h) + (size_t)kUnitRows * kMaxCtas;
@@ -873,7 +872,7 @@ cudaError_t launch(const PagedSharedParams& p, const CUtensorMap& tk, const CUte
   // Rows that do not fill the GPU have many parts each, four warps a row then; where there are warps enough to hide the
   // latency fewer loads at a time leave room for more of them. (256 requests of 32 heads: 95.9 us with 4 at a time, 97.9 with
   // 8; 64 requests 62.8, 61.3 us; 16 requests 36.2 us, with one warp a row 42.0.)
-  const bool few = items <= 152 * 8, many = items > 152 * 32;
+  const bool few = items <= f.ctas * 8, many = items > f.ctas * 32;
   const int64_t warps = items * (few ? kJoinWarps : 1);
   auto join = few ? shared_join_kernel<D, kJoinWarps, 8> : many ? shared_join_kernel<D, 1, 4> : shared_join_kernel<D, 1, 8>;
   e = launch_dependent(join, dim3((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, a);

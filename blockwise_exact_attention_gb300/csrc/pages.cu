@@ -542,7 +542,13 @@ unsigned grid_of(int64_t items, int64_t per, int most) {
   return (unsigned)(b < 1 ? 1 : b < most ? b : most);
 }
 
-constexpr int kMostRowBlocks = 152 * 8;  // of kRowThreads: a wave
+// Blocks of kRowThreads: a wave of them, or one to an SM.
+cudaError_t most_blocks(int* wave, int* each) {
+  int sms = 0;
+  const cudaError_t e = device_sm_count(&sms);
+  *wave = sms * 8, *each = sms;
+  return e;
+}
 
 }  // namespace
 
@@ -562,10 +568,12 @@ cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t s, int* nlaunch)
     if (e == cudaSuccess) *nlaunch += 1;
     return e;
   }
-  const unsigned more = p.s.shares_out != p.s.shares ? grid_of(p.s.num_pages, 4096, 64) : 0;
+  int wave = 0, each = 0;
+  if ((e = most_blocks(&wave, &each)) != cudaSuccess) return e;
+  const unsigned more = p.s.shares_out != p.s.shares ? grid_of(p.s.num_pages, 4096, each) : 0;
   if ((e = launch_dependent(fork_plan_kernel, dim3(1 + more), kClusterThreads, 0, s, p)) != cudaSuccess) return e;
   *nlaunch += 1;
-  e = launch_dependent(fork_rows_kernel, dim3(grid_of(p.s.n, 1, kMostRowBlocks)), kRowThreads, 0, s, p);
+  e = launch_dependent(fork_rows_kernel, dim3(grid_of(p.s.n, 1, wave)), kRowThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }
@@ -577,12 +585,14 @@ cudaError_t launch_paged_free(const FreeParams& p, cudaStream_t s, int* nlaunch)
     if (e == cudaSuccess) *nlaunch += 1;
     return e;
   }
+  int wave = 0, each = 0;
+  if ((e = most_blocks(&wave, &each)) != cudaSuccess) return e;
   if (p.s.shares_out != p.s.shares) {
-    e = launch_dependent(copy_shares_kernel, dim3(grid_of(p.s.num_pages, 1024, 152)), kRowThreads, 0, s, p.s);
+    e = launch_dependent(copy_shares_kernel, dim3(grid_of(p.s.num_pages, 1024, each)), kRowThreads, 0, s, p.s);
     if (e != cudaSuccess) return e;
     *nlaunch += 1;
   }
-  e = launch_dependent(free_rows_kernel, dim3(grid_of(p.s.n, 1, kMostRowBlocks)), kRowThreads, 0, s, p);
+  e = launch_dependent(free_rows_kernel, dim3(grid_of(p.s.n, 1, wave)), kRowThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
   e = launch_dependent(free_push_kernel<false>, dim3(kCtas), kClusterThreads, 0, s, p);
@@ -607,17 +617,19 @@ cudaError_t launch_paged_compact(const CompactParams& p, cudaStream_t s, int* nl
     if (e == cudaSuccess) *nlaunch += 1;
     return e;
   }
+  int wave = 0, each = 0;
+  if ((e = most_blocks(&wave, &each)) != cudaSuccess) return e;
   const int64_t most = p.s.num_pages > 3 * (int64_t)p.capacity ? p.s.num_pages : 3 * (int64_t)p.capacity;
-  e = launch_dependent(compact_init_kernel, dim3(grid_of(most, 1024, 152)), kRowThreads, 0, s, p);
+  e = launch_dependent(compact_init_kernel, dim3(grid_of(most, 1024, each)), kRowThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
   e = launch_dependent(compact_plan_kernel, dim3(1), kClusterThreads, smem, s, p);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
-  e = launch_dependent(compact_moves_kernel, dim3(grid_of(p.capacity, 512, 152)), kRowThreads, 0, s, p);
+  e = launch_dependent(compact_moves_kernel, dim3(grid_of(p.capacity, 512, each)), kRowThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
-  e = launch_dependent(compact_table_kernel, dim3(grid_of(p.s.n, 1, kMostRowBlocks)), kRowThreads, 0, s, p);
+  e = launch_dependent(compact_table_kernel, dim3(grid_of(p.s.n, 1, wave)), kRowThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }

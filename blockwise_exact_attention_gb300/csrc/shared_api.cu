@@ -14,7 +14,8 @@ size_t bea_paged_decode_shared_workspace_size(int64_t n, int64_t h, int64_t h_kv
                                               int64_t groups) {
   if (n < 0 || h < 0 || h_kv <= 0 || d < 0 || max_keys < 0 || groups < 0) return 0;
   // what bea_paged_decode_shared refuses anyway, and products past 64 bits
-  if (h > (int64_t(1) << 31) || d < 1 || d > 128 || max_keys > bea::kUnbounded || n > (int64_t(1) << 31) || n * h > (int64_t(1) << 31) || groups > bea::kMaxGroups) return 0;
+  constexpr int64_t most = int64_t(1) << 31;
+  if (n > most || h > most || n * h > most || d < 1 || d > 128 || max_keys > bea::kUnbounded || groups > bea::kMaxGroups) return 0;
   return bea::paged_shared_workspace(n, h, h_kv, d, max_keys, groups);
 }
 
