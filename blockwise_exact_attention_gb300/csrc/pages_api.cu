@@ -157,13 +157,14 @@ int bea_paged_copy(const bea_tensor* copies, const bea_tensor* caches, int n_cac
     if (!same_shape(&caches[i], &caches[0])) return BEA_ERR_SHAPE;
     if (broadcast(&caches[i])) return BEA_ERR_ARG;
   }
-  if (n_caches == 0 || copies->shape[0] == 0) return finish(cudaSuccess, 0);
+  if (n_caches == 0) return finish(cudaSuccess, 0);
   const int64_t *shape = caches[0].shape, es = caches[0].dtype == BEA_F32 ? 4 : 2, row = shape[3] * es;
   if (row % 16 != 0) return BEA_ERR_UNSUPPORTED;
   if (shape[1] > kMost || shape[2] > kMost || row > kMost || shape[1] * shape[2] > kMost ||
       shape[1] * shape[2] * (row / 16) > kMost)
     return BEA_ERR_SHAPE;
-  if (shape[0] == 0 || shape[1] == 0 || shape[2] == 0 || shape[3] == 0) return finish(cudaSuccess, 0);
+  if (copies->shape[0] == 0 || shape[0] == 0 || shape[1] == 0 || shape[2] == 0 || shape[3] == 0)
+    return finish(cudaSuccess, 0);
   bea::CopyParams p;
   std::memset(&p, 0, sizeof(p));
   p.m = (int)copies->shape[0];

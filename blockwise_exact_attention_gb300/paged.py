@@ -195,6 +195,16 @@ class PagedKVCache:
         if self.shares is None:
             raise ValueError("this cache does not count its pages' owners: PagedKVCache(..., share_pages=True)")
 
+    def _caches(self, caches, copies):
+        """What a step copies in, refused before the step where ``paged_copy`` would refuse it behind it."""
+        if caches is None:
+            return [self.k, self.v]
+        for c in caches:
+            if c.shape[:2] != self.k.shape[:2]:
+                raise ValueError(f"a cache of shape {tuple(c.shape)} beside one of {self.k.shape[0]} pages of {self.page_size} "
+                                 "tokens")
+        return paged_copy(copies[:0], caches)
+
     def free(self, ends):
         """``paged_free`` on this cache, in place."""
         self._counted()
@@ -205,19 +215,22 @@ class PagedKVCache:
         """``paged_fork`` on this cache, in place, and its copies in ``caches`` (default: this cache's own two)."""
         self._counted()
         copies = torch.empty(len(self.lens), 3, dtype=torch.int32, device=self.lens.device)
+        caches = self._caches(caches, copies)
         step = paged_fork(src, tokens, self.lens, self.block_table, self.shares, self.free_pages, self.n_free,
                           self.page_size, PagedFork(self.lens, self.n_free, self.shares, copies))
-        paged_copy(step.copies, [self.k, self.v] if caches is None else caches)
+        paged_copy(step.copies, caches)
         return step
 
     def compact(self, capacity, caches=None) -> PagedCompaction:
         """``paged_compact`` on this cache, in place, and its copies in ``caches`` (default: this cache's own two)."""
         self._counted()
         i32 = dict(dtype=torch.int32, device=self.lens.device)
+        copies = torch.empty(capacity, 3, **i32)
+        caches = self._caches(caches, copies)
         step = paged_compact(self.lens, self.block_table, self.shares, self.free_pages, self.n_free, self.page_size, capacity,
                              PagedCompaction(self.block_table, self.shares, self.free_pages,
-                                             torch.empty(len(self.shares), **i32), torch.empty(capacity, 3, **i32)))
-        paged_copy(step.copies, [self.k, self.v] if caches is None else caches)
+                                             torch.empty(len(self.shares), **i32), copies))
+        paged_copy(step.copies, caches)
         return step
 
     def write(self, k, v, slot_map):

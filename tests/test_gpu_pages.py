@@ -245,6 +245,24 @@ def test_copy_of_many_caches_and_of_nothing():
     assert all(torch.equal(a, b) for a, b in zip(caches, want)) and bea.device_status() == 0
 
 
+def test_a_step_is_refused_before_it_changes_the_cache_when_its_copies_would_be():
+    import blockwise_exact_attention_gb300 as bea
+    cache = bea.PagedKVCache(8, 16, 2, 64, 3, 64, share_pages=True)
+    cache.plan(i32([20, 0, 0]), 20)
+    names = "block_table", "lens", "shares", "free_pages", "n_free"
+    before = [getattr(cache, x).clone() for x in names]
+    other_pages = torch.empty(8, 8, 2, 64, dtype=torch.bfloat16, device="cuda")
+    short_rows = torch.empty(8, 16, 2, 4, dtype=torch.float16, device="cuda")
+    for bad, error in (([cache.k, other_pages], ValueError), ([cache.k, cache.k.float()], bea._lib.BeaError), ([short_rows], TypeError),
+                       ([cache.k[..., 4:]], bea._lib.BeaError), ([cache.k, cache.k.cpu()], ValueError)):
+        for step in (lambda: cache.fork(i32([-1, 0, -1]), caches=bad), lambda: cache.compact(4, caches=bad)):
+            with pytest.raises(error):
+                step()
+            assert all(torch.equal(getattr(cache, x), b) for x, b in zip(names, before))
+    step = cache.fork(i32([-1, 0, -1]), caches=(cache.v, cache.k))
+    assert step.lens.tolist() == [20, 20, 0] and bea.device_status() == 0
+
+
 def test_copy_leaves_out_what_does_not_fit():
     import blockwise_exact_attention_gb300 as bea
     big = 2 ** 31 - 1

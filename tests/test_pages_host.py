@@ -182,6 +182,8 @@ def test_refusals_of_copy(lib):
     assert copy(caches=(t((7, 16, 2, 64), BF16, strides=[2048, 0, 64, 1]),)) == ARG
     assert copy(caches=(t((7, 16, 2, 64), BF16, ptr=FAKE + 8),)) == ALIGN
     assert copy(caches=()) == 0 and copy(copies=t((0, 3))) == 0
+    # nothing to copy: the caches are looked at all the same
+    assert copy(copies=t((0, 3)), caches=(t((7, 16, 1, 4), BF16, strides=[128, 8, 8, 1]),)) == UNSUP
 
 
 def test_python_refusals():
