@@ -204,34 +204,37 @@ __device__ __forceinline__ bool length_fits(const PagesState& s, int len) {
   return len >= 0 && len <= (int64_t)s.max_pages * s.page;
 }
 
-// The pages of row r counted down if it ends, by `step` threads of which this is the `first`-th.
+// The pages of row r counted down if it ends, by `step` threads of which this is the `first`-th. (This thread's first entry is
+// read beside the length and not behind it: an entry of a row that stays costs less than another latency.)
 __device__ __forceinline__ void free_entries(const FreeParams& p, int r, int first, int step) {
-  const int ends = p.ends[r], len = p.s.lens[r];
+  const int32_t* entries = p.table + r * p.table_stride;
+  const int ends = p.ends[r], len = p.s.lens[r], entry = first < p.s.max_pages ? entries[first] : 0;
   if (ends >= 0 || !length_fits(p.s, len)) return;
   const int held = pages_held(len, p.s.page);
-  const int32_t* entries = p.table + r * p.table_stride;
-#pragma unroll 4
-  for (int c = first; c < held; c += step) {
-    const int id = entries[c];
+  auto give = [&](int id) {
     if (id >= 0 && id < p.s.num_pages)
       atomicSub(p.s.shares_out + id, 1);
     else
       report_status(p.s.status, BEA_STATUS_PAGES);
-  }
+  };
+  if (first < held) give(entry);
+#pragma unroll 4
+  for (int c = first + step; c < held; c += step) give(entries[c]);
 }
 
 __global__ void __launch_bounds__(kRowThreads) free_rows_kernel(const __grid_constant__ FreeParams p) {
   grid_dependency_wait();
-  if (!height_fits(p.s, p.s.n_free[0])) return;
-  for (int r = blockIdx.x; r < p.s.n; r += gridDim.x) free_entries(p, r, threadIdx.x, kRowThreads);
+  const bool ok = height_fits(p.s, p.s.n_free[0]);
+  for (int r = blockIdx.x; ok && r < p.s.n; r += gridDim.x) free_entries(p, r, threadIdx.x, kRowThreads);
 }
 
-// One cluster, each CTA a run of the pages. kAll: the copy of the shares and the rows that end before it.
+// One cluster, kTile pages at a time, read once: a warp takes kWords times 32 in a row, and lane j keeps a bit for each of the
+// j-th 32 that nobody holds. kAll: the copy of the shares and the rows that end before it.
 template <bool kAll>
 __global__ void __cluster_dims__(kCtas) __launch_bounds__(kClusterThreads) free_push_kernel(const __grid_constant__ FreeParams p) {
-  constexpr int kRun = 4;  // consecutive pages of a thread
+  constexpr int kWords = 16, kTile = kCtas * kClusterThreads * kWords;
   __shared__ int sums[kClusterThreads / 32];
-  __shared__ int counts[kCtas];  // of every CTA's run
+  __shared__ int counts[2][kCtas];  // of every CTA's run, of this tile and the next
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   grid_dependency_wait();
@@ -247,47 +250,50 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kClusterThreads) free_
         free_entries(p, r, threadIdx.x & 31, 32);
     cluster.sync();
   }
-  constexpr int kTile = kClusterThreads * kRun;
-  // runs of whole tiles
-  const int tiles = (p.s.num_pages + kTile - 1) / kTile, each = (tiles + kCtas - 1) / kCtas;
-  const int64_t first = (int64_t)rank * each * kTile, last = min((int64_t)p.s.num_pages, first + (int64_t)each * kTile);
-  int mine = 0;
-  for (int64_t i = first + threadIdx.x; i < last; i += kClusterThreads) mine += __ldcg(p.s.shares_out + i) < 0;
-  const int total = block_scan<kClusterThreads>(mine, sums).y;
-  if (threadIdx.x < kCtas) *cluster.map_shared_rank(&counts[rank], threadIdx.x) = total;
-  cluster.sync();  // the counts are there, and the height and lengths below have not been written
-  int at = have, all = 0;
-  for (int c = 0; c < kCtas; ++c) {
-    if (c < rank) at += counts[c];
-    all += counts[c];
-  }
+  int at = have;
   bool lost = !ok;
-  if (ok && total > 0) {
-    for (int64_t t0 = first; t0 < last; t0 += kTile) {
-      const int64_t i0 = t0 + (int64_t)threadIdx.x * kRun;
-      int v[kRun], n = 0;
+  // of a small cache fewer, so that all warps have some
+  const int words = min(kWords, (p.s.num_pages + kCtas * kClusterThreads - 1) / (kCtas * kClusterThreads));
+  const int lane = threadIdx.x & 31, warp = rank * (kClusterThreads / 32) + (threadIdx.x >> 5);
+  int turn = 0;
+  for (int64_t t0 = 0; t0 < p.s.num_pages; t0 += kTile, turn ^= 1) {
+    const int64_t i0 = t0 + (int64_t)warp * words * 32;
+    int v[kWords];
 #pragma unroll
-      for (int z = 0; z < kRun; ++z) {
-        v[z] = i0 + z < last ? __ldcg(p.s.shares_out + i0 + z) : 0;
-        n += v[z] < 0;
-      }
-      __syncthreads();  // `sums` is free
-      const int2 s = block_scan<kClusterThreads>(n, sums);
-      int to = at + s.x;
+    for (int j = 0; j < kWords; ++j) {
+      const int64_t id = i0 + j * 32 + lane;
+      v[j] = j < words && id < p.s.num_pages ? __ldcg(p.s.shares_out + id) : 0;
+    }
+    uint32_t mine = 0;
 #pragma unroll
-      for (int z = 0; z < kRun; ++z) {
-        if (v[z] >= 0) continue;
-        if (to < p.s.n_pool)
-          p.pool[to] = (int)(i0 + z);
-        else
-          lost = true;
-        ++to;
-        if (v[z] < -1) lost = true;  // more rows gave it back than held it
-        p.s.shares_out[i0 + z] = 0;
-      }
-      at += s.y;
+    for (int j = 0; j < kWords; ++j) {
+      const uint32_t b = __ballot_sync(~0u, v[j] < 0);
+      if (lane == j) mine = b;
+      if (v[j] < -1) lost = true;  // more rows gave it back than held it
+    }
+    const int2 s = block_scan<kClusterThreads>(__popc(mine), sums);
+    if (threadIdx.x < kCtas) *cluster.map_shared_rank(&counts[turn][rank], threadIdx.x) = s.y;
+    cluster.sync();  // the counts are there, and what is written below has been read
+    int to = at + s.x;
+    for (int c = 0; c < kCtas; ++c) {
+      if (c < rank) to += counts[turn][c];
+      at += counts[turn][c];
+    }
+    if (!ok) continue;
+    for (uint32_t some = __ballot_sync(~0u, mine != 0); some != 0; some &= some - 1) {
+      const int j = __ffs(some) - 1;
+      const uint32_t b = __shfl_sync(~0u, mine, j), bit = 1u << lane;
+      const int where = __shfl_sync(~0u, to, j) + __popc(b & (bit - 1u));
+      if (!(b & bit)) continue;
+      const int64_t id = i0 + j * 32 + lane;
+      if (where < p.s.n_pool)
+        p.pool[where] = (int)id;
+      else
+        lost = true;
+      p.s.shares_out[id] = 0;
     }
   }
+  if (p.s.num_pages == 0) cluster.sync();  // the height and lengths have been read by all
   if (rank == 0) {
     for (int r = threadIdx.x; r < p.s.n; r += kClusterThreads) {
       const int len = p.s.lens[r];
@@ -295,7 +301,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kClusterThreads) free_
       if (ends && !length_fits(p.s, len)) lost = true;
       p.s.lens_out[r] = ok && ends && length_fits(p.s, len) ? 0 : len;
     }
-    if (threadIdx.x == 0) p.s.n_free_out[0] = ok ? min(have + all, p.s.n_pool) : have;
+    if (threadIdx.x == 0) p.s.n_free_out[0] = ok ? min(at, p.s.n_pool) : have;
   }
   if (lost) report_status(p.s.status, BEA_STATUS_PAGES);
   cluster.sync();  // no CTA ends while another may still write its counts
@@ -312,11 +318,19 @@ __device__ __forceinline__ void compact_init(const CompactParams& p, int64_t fir
   for (int64_t i = first; i < 3 * (int64_t)p.capacity; i += step) p.copies[i] = -1;
 }
 
+// 32 pages.
+struct Word {
+  int w;
+  uint32_t taken, filled, left, free;  // bits of its pages: used before, holes to be filled, used ones that leave, free after
+  int holes_at, taken_at, free_at;     // how many of these stand before it (taken: used before)
+};
+
 // The moves and the new stack, by one block, but for what compact_moves does. `wait` stands between what only reads and the
 // first write to what compact_init writes. holes: a bit per page, zeros.
 template <typename F>
 __device__ void compact_plan(const CompactParams& p, uint32_t* holes, int* sums, F wait) {
   constexpr int kThreads = kClusterThreads;
+  __shared__ Word todo[kThreads];
   const int pages = p.s.num_pages, words = (pages + 31) / 32, tid = threadIdx.x, lane = tid & 31;
   const int have = p.s.n_free[0];
   bool wrong = have < 0 || have > p.s.n_pool || have > pages;
@@ -346,7 +360,7 @@ __device__ void compact_plan(const CompactParams& p, uint32_t* holes, int* sums,
   }
   const int moves = min(block_scan<kThreads>(below, sums).y, p.capacity);
   wait();
-  // Words in the order of the pages, a word per thread and 32 words to a warp, whose lanes take a word's pages one each.
+  // Words in the order of the pages, a word per thread.
   int holes_before = 0, free_before = 0;  // in the words of earlier turns: holes, pages that are free in the end
   for (int w0 = 0; w0 < words; w0 += kThreads) {
     const int w = w0 + tid;
@@ -376,20 +390,23 @@ __device__ void compact_plan(const CompactParams& p, uint32_t* holes, int* sums,
     const int free_at = free_before + f.x;
     holes_before += h.y;
     free_before += f.y;
-    const int base = (w & ~31) * 32;  // the first page of the warp's words
-    for (uint32_t some = __ballot_sync(~0u, (filled | free) != 0u); some != 0; some &= some - 1) {
-      const int z = __ffs(some) - 1;
-      const uint32_t f_bits = __shfl_sync(~0u, filled, z), l_bits = __shfl_sync(~0u, left, z), e_bits = __shfl_sync(~0u, free, z);
-      const int h_at = __shfl_sync(~0u, holes_at, z), t_at = __shfl_sync(~0u, taken_at, z), e_at = __shfl_sync(~0u, free_at, z);
-      const uint32_t taken_bits = __shfl_sync(~0u, taken, z), mine = 1u << lane, lower = mine - 1u;
-      const int page = base + z * 32 + lane;
-      if (f_bits & mine) {
-        const int64_t k = 3 * (int64_t)(h_at + __popc(f_bits & lower));  // all holes below a filled one are filled
+    __syncthreads();
+    // The words that have something to be written are dealt to the warps, whose lanes take a word's pages one each.
+    const bool some = (filled | free) != 0u;
+    const int2 q = block_scan<kThreads>(some, sums);
+    if (some) todo[q.x] = Word{w, taken, filled, left, free, holes_at, taken_at, free_at};
+    __syncthreads();
+    for (int z = tid >> 5; z < q.y; z += kThreads / 32) {
+      const Word d = todo[z];
+      const int page = d.w * 32 + lane;
+      const uint32_t mine = 1u << lane, lower = mine - 1u;
+      if (d.filled & mine) {
+        const int64_t k = 3 * (int64_t)(d.holes_at + __popc(d.filled & lower));  // all holes below a filled one are filled
         p.copies[k + 1] = page;
         p.copies[k + 2] = p.s.page;
       }
-      if (l_bits & mine) p.copies[3 * (int64_t)(used - 1 - (t_at + __popc(taken_bits & lower)))] = page;
-      if (e_bits & mine) p.pool_out[have - 1 - (e_at + __popc(e_bits & lower))] = page;
+      if (d.left & mine) p.copies[3 * (int64_t)(used - 1 - (d.taken_at + __popc(d.taken & lower)))] = page;
+      if (d.free & mine) p.pool_out[have - 1 - (d.free_at + __popc(d.free & lower))] = page;
     }
   }
   for (int i = have + tid; i < p.s.n_pool; i += kThreads) p.pool_out[i] = -1;
@@ -553,9 +570,9 @@ cudaError_t most_blocks(int* wave, int* each) {
 }  // namespace
 
 // Up to `entries` entries of a table and pages of a cache one cluster does all of a call, in one launch instead of two to four,
-// each of which costs the host 2 us. GPU time, cluster and launches: 8 rows of 46 entries forked 4.4, 4.4 us, freed 6.3, 6.0, a
-// cache of 242 pages compacted 7.1, 8.0 us; 64 rows of 128 entries 5.4, 4.6, 7.6, 8.1, 11.5, 13.7 us (4210 pages); 256 rows of
-// 258 entries 6.1, 4.8, 10.7, 9.8, 23.7, 22.4 us (33330 pages); 512 rows of 512 entries 10.3, 5.5, 18.7, 14.3, 65.6, 55.2 us.
+// each of which costs the host 2 us. GPU time, cluster and launches: 8 rows of 46 entries forked 4.3, 4.4 us, freed 6.4, 6.1, a
+// cache of 242 pages compacted 7.2, 7.5 us; 64 rows of 128 entries 5.3, 4.7, 7.4, 7.8, 10.1, 9.8 us (4210 pages); 256 rows of
+// 258 entries 5.9, 4.8, 9.3, 8.5, 21.7, 18.7 us (33330 pages).
 static bool fits_cluster(const PagesState& s, int64_t entries) {
   return (int64_t)s.n * s.max_pages <= entries && s.num_pages <= entries;
 }
