@@ -42,7 +42,7 @@ constexpr int kSmThreads = 1280;
 constexpr int kMaxD = 2 * kRopeMaxPairs;
 // Heads of a chunk. Forward: 2 and 8 heads 131 and 127 us for [1, 32768, 32 + 8, 128] bf16 (now 113). Backward: 1 head three
 // stages deep 2-4% slower; 3 or 5 blocks to an SM 318 and 350 us for the training step (now 290).
-constexpr int kFwdHeads = 4;
+constexpr int kFwdHeads = 4, kFwdStages = 2;
 constexpr int kBwdHeads = 2, kBwdStages = 2, kBwdBlocks = 4;
 
 __device__ __forceinline__ float weight_at(const void* w, int is_f32, int c) {
@@ -213,10 +213,71 @@ struct Item {
   }
 };
 
-// kPartial: only a part of the head is turned.
-template <bool kF32, bool kNorm, bool kInter, bool kPartial, int kHeads>
+// Rows on their way through shared memory, by asynchronous copies that need no registers: a slot of 16 bytes for every piece,
+// 2 * lanes of them to a row. kOwn: each thread copies and reads back what is its own, so nothing but its own copies is waited
+// for. Else a row's lanes copy its pieces in memory's order, whichever they need, so that every copy fills whole sectors
+// where a lane's two pieces lie side by side (a 32k training step, interleaved, 371 us with kOwn, 288 without; with half of
+// the head turned, 8k, 116 and 104 us); the last bit is turned so that eight lanes that read every other piece meet
+// different banks.
+template <bool kF32, bool kOwn>
+struct Staged {
+  static constexpr int kN = Piece<kF32>::kN;
+  static constexpr int kBytes = kThreads * 2 * 16;  // of a row for each group of lanes
+  int first, second;                                // the pieces this lane copies, -1: none
+  uint32_t to0, to1, from0, from1;
+  __device__ Staged(int shift, int d, int a, int b, bool mine) {
+    if constexpr (kOwn) {
+      first = mine ? a / kN : -1;
+      second = mine ? b / kN : -1;
+      to0 = from0 = threadIdx.x * 16;
+      to1 = from1 = (kThreads + threadIdx.x) * 16;
+    } else {
+      const int lanes = 1 << shift, row = (threadIdx.x >> shift) << (shift + 1), pieces = d / kN;
+      const int i = threadIdx.x & (lanes - 1);
+      auto slot = [](int x) { return (uint32_t)(x ^ ((x >> 3) & 1)) * 16; };
+      first = i < pieces ? i : -1;
+      second = i + lanes < pieces ? i + lanes : -1;
+      to0 = slot(row + i);
+      to1 = slot(row + i + lanes);
+      from0 = slot(row + a / kN);
+      from1 = slot(row + b / kN);
+    }
+  }
+  // src: the row, or any address where nothing is read and the slots become zeros.
+  __device__ __forceinline__ void copy(uint32_t area, const char* src, bool read) const {
+    one(area + to0, src, first, read);
+    one(area + to1, src, second, read);
+  }
+  __device__ __forceinline__ void one(uint32_t dst, const char* src, int piece, bool read) const {
+    read = read && piece >= 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src + (read ? piece * 16 : 0)), "r"(read ? 16 : 0)
+                 : "memory");
+  }
+  // Ends a chunk's copies; of chunks without any too, so that groups count chunks.
+  __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Before copies go where something has been read.
+  __device__ __forceinline__ void been_read() const {
+    if constexpr (!kOwn) __syncwarp();
+  }
+  // All chunks but the last kLeft are there.
+  template <int kLeft>
+  __device__ __forceinline__ void there() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+    if constexpr (!kOwn) __syncwarp();
+  }
+  __device__ __forceinline__ void read(const uint8_t* area, uint4& a, uint4& b) const {
+    a = *reinterpret_cast<const uint4*>(area + from0);
+    b = *reinterpret_cast<const uint4*>(area + from1);
+  }
+};
+
+// kPartial: only a part of the head is turned. kStages: chunks in shared memory, kStages - 1 of them ahead; 0: loads into
+// registers.
+template <bool kF32, bool kNorm, bool kInter, bool kPartial, int kHeads, int kStages>
 __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int slices, int per) {
   constexpr int N = Piece<kF32>::kN, H = N / 2;
+  using S = Staged<kF32, !kInter && !kPartial>;
+  extern __shared__ __align__(16) uint8_t rows[];  // [stage][head] of S::kBytes
   __shared__ Tables tables;
   load_tables<kNorm>(p, tables);
   constexpr int es = kF32 ? 4 : 2;
@@ -225,8 +286,36 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_con
   const int cq = (p.hq + kHeads - 1) / kHeads, chunks = cq + (p.hk + kHeads - 1) / kHeads;
   const int64_t total = ((int64_t)p.n * p.l * slices) << shift;
   const float inv_d = 1.f / (float)p.d;
+  const S st(shift, p.d, at.a, at.b, at.mine);
+  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+  // what is copied next: chunk c_ahead, the `ahead`-th of item it_ahead
+  int64_t it_ahead = first, b_ahead = 0;
+  int i_ahead = 0, c_ahead = 0, ahead = 0, stage_ahead = 0, stage = 0;
+  auto copy_next = [&]() {
+    if ((it_ahead & ~int64_t(31)) < total) {
+      if (ahead == 0) {
+        const Item m(p, it_ahead < total ? it_ahead : 0, shift, slices, per);
+        b_ahead = m.b, i_ahead = m.i, c_ahead = m.chunk0;
+      }
+      const bool k_now = c_ahead >= cq;
+      const int h0 = (k_now ? c_ahead - cq : c_ahead) * kHeads, heads = c_ahead < chunks ? (k_now ? p.hk : p.hq) : 0;
+      const Seq4& from = k_now && p.hk > 0 ? p.k : p.q;
+      const char* src = static_cast<const char*>(from.ptr) + (b_ahead * from.sn + i_ahead * from.sl) * es;
+#pragma unroll
+      for (int x = 0; x < kHeads; ++x) {
+        const bool read = it_ahead < total && h0 + x < heads;
+        st.copy(smem_u32(rows) + (stage_ahead * kHeads + x) * S::kBytes, read ? src + (h0 + x) * from.sh * es : src, read);
+      }
+      ++c_ahead;
+      if (++ahead == per) ahead = 0, it_ahead += step;
+    }
+    stage_ahead = stage_ahead + 1 == kStages ? 0 : stage_ahead + 1;
+    st.commit();
+  };
+#pragma unroll
+  for (int z = 0; z + 1 < kStages; ++z) copy_next();
   // a warp goes on while any of its items is one, so that all its lanes meet in the shuffles
-  for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; (it & ~int64_t(31)) < total; it += (int64_t)gridDim.x * kThreads) {
+  for (int64_t it = first; (it & ~int64_t(31)) < total; it += step) {
     const bool live = it < total && at.mine;
     const Item m(p, it < total ? it : 0, shift, slices, per);
     // What a row's elements are multiplied by, r apart: with the first and second element of each pair and its partner.
@@ -238,13 +327,21 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_con
       const int h0 = (k_now ? chunk - cq : chunk) * kHeads, heads = chunk < chunks ? (k_now ? p.hk : p.hq) : 0;
       const Seq4 &from = k_now ? p.k : p.q, &to = k_now ? p.ko : p.qo;
       uint4 ra[kHeads], rb[kHeads];
-      const char* src = static_cast<const char*>(from.ptr) + (m.b * from.sn + m.i * from.sl + h0 * from.sh) * es;
+      const uint8_t* here = rows + stage * kHeads * S::kBytes;
+      if constexpr (kStages > 0) {
+        st.been_read();
+        copy_next();
+        st.template there<kStages - 1>();
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+      } else {
+        const char* src = static_cast<const char*>(from.ptr) + (m.b * from.sn + m.i * from.sl + h0 * from.sh) * es;
 #pragma unroll
-      for (int x = 0; x < kHeads; ++x) {
-        ra[x] = rb[x] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h0 + x < heads) {
-          ra[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.a) * es));
-          rb[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.b) * es));
+        for (int x = 0; x < kHeads; ++x) {
+          ra[x] = rb[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (live && h0 + x < heads) {
+            ra[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.a) * es));
+            rb[x] = __ldcs(reinterpret_cast<const uint4*>(src + (x * from.sh + at.b) * es));
+          }
         }
       }
       if (x0 == 0 || (kNorm && k_now != is_k)) {
@@ -270,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_con
 #pragma unroll
       for (int x = 0; x < kHeads; ++x) {
         uint64_t u[H], v[H];
+        if constexpr (kStages > 0) st.read(here + x * S::kBytes, ra[x], rb[x]);
         unpack<kF32, kInter>(ra[x], rb[x], u, v);
         if constexpr (kNorm) {
           uint64_t sq = 0ull;
@@ -308,25 +406,21 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_con
 // The gradient under the norm. Blocks [0, bq) do q, the others k; a block's threads step over its part's items.
 //
 // A chunk is the rows of kHeads heads, x and the gradient, which go through shared memory by asynchronous copies, kStages -
-// 1 chunks ahead: each thread copies and reads back what is its own, so nothing but its own copies is waited for, and the
-// loads under way need no registers (a 32k training step with loads into registers 301 us, with 2 heads a chunk).
+// 1 chunks ahead (a 32k training step with loads into registers 301 us, with 2 heads a chunk).
 struct BwdPart {
   int bq, slices_q, per_q, slices_k, per_k;
 };
 template <int kHeads, int kStages>
 __host__ __device__ constexpr int bwd_smem() {
-  return kStages * kHeads * 4 * kThreads * 16;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
-  const int n = read ? 16 : 0;  // 0: zeros, and nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  return kStages * kHeads * 2 * kThreads * 2 * 16;
 }
 
 template <bool kF32, bool kInter, bool kPartial, int kHeads, int kStages>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, const __grid_constant__ BwdPart q) {
   constexpr int N = Piece<kF32>::kN, H = N / 2;
   __shared__ Tables tables;
-  extern __shared__ __align__(16) uint8_t staged[];  // [stage][head][x a, x b, g a, g b][thread] of 16 bytes
+  using S = Staged<kF32, !kInter && !kPartial>;
+  extern __shared__ __align__(16) uint8_t staged[];  // [stage][head][x, gradient] of S::kBytes
   static_assert(bwd_smem<kHeads, kStages>() >= kThreads * 2 * N * 4, "the sums take its place");
   load_tables<true>(p, tables);
   constexpr int es = kF32 ? 4 : 2;
@@ -347,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     du[j] = dv[j] = 0ull;
   }
   // what is copied next: chunk `ahead` of item `it_ahead`
-  const uint32_t mine = smem_u32(staged) + threadIdx.x * 16;
+  const S st(shift, p.d, at.a, at.b, at.mine);
   int64_t it_ahead = first;
   int ahead = 0, stage_ahead = 0, h_ahead = 0;
   const char *src = nullptr, *gsrc = nullptr;
@@ -359,16 +453,12 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
         src = static_cast<const char*>(from.ptr) + (m.b * from.sn + m.i * from.sl + h_ahead * from.sh) * es;
         gsrc = static_cast<const char*>(grad.ptr) + (m.b * grad.sn + m.i * grad.sl + h_ahead * grad.sh) * es;
       }
-      const uint32_t dst = mine + stage_ahead * (kHeads * 4 * kThreads * 16);
 #pragma unroll
       for (int x = 0; x < kHeads; ++x) {
-        const bool read = it_ahead < total && at.mine && h_ahead + x < heads;
-        // an address that is one, where nothing is read
-        const char *xs = read ? src + x * from.sh * es : src, *gs = read ? gsrc + x * grad.sh * es : gsrc;
-        cp_async16(dst + (x * 4 + 0) * kThreads * 16, xs + (read ? at.a * es : 0), read);
-        cp_async16(dst + (x * 4 + 1) * kThreads * 16, xs + (read ? at.b * es : 0), read);
-        cp_async16(dst + (x * 4 + 2) * kThreads * 16, gs + (read ? at.a * es : 0), read);
-        cp_async16(dst + (x * 4 + 3) * kThreads * 16, gs + (read ? at.b * es : 0), read);
+        const bool read = it_ahead < total && h_ahead + x < heads;
+        const uint32_t area = smem_u32(staged) + (stage_ahead * kHeads + x) * 2 * S::kBytes;
+        st.copy(area, read ? src + x * from.sh * es : src, read);  // src: an address that is one
+        st.copy(area + S::kBytes, read ? gsrc + x * grad.sh * es : gsrc, read);
       }
       h_ahead += kHeads;
       src += kHeads * from.sh * es;
@@ -376,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
       if (++ahead == per) ahead = 0, it_ahead += step;
     }
     stage_ahead = stage_ahead + 1 == kStages ? 0 : stage_ahead + 1;
-    asm volatile("cp.async.commit_group;" ::: "memory");  // empty where there is nothing, so that groups count chunks
+    st.commit();
   };
 #pragma unroll
   for (int z = 0; z < kStages - 1; ++z) copy_next();
@@ -389,15 +479,19 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     int h0 = m.chunk0 * kHeads;
     char* dst = static_cast<char*>(to.ptr) + (m.b * to.sn + m.i * to.sl + h0 * to.sh) * es;
     for (int x0 = 0; x0 < per; ++x0, h0 += kHeads, dst += kHeads * to.sh * es) {
+      st.been_read();
       copy_next();
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      const uint4* here = reinterpret_cast<const uint4*>(staged) + stage * (kHeads * 4 * kThreads) + threadIdx.x;
+      st.template there<kStages - 1>();
+      const uint8_t* here = staged + stage * kHeads * 2 * S::kBytes;
       stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
       for (int x = 0; x < kHeads; ++x) {
         uint64_t u[H], v[H], gu[H], gv[H];
-        unpack<kF32, kInter>(here[(x * 4 + 0) * kThreads], here[(x * 4 + 1) * kThreads], u, v);
-        unpack<kF32, kInter>(here[(x * 4 + 2) * kThreads], here[(x * 4 + 3) * kThreads], gu, gv);
+        uint4 ia, ib;
+        st.read(here + x * 2 * S::kBytes, ia, ib);
+        unpack<kF32, kInter>(ia, ib, u, v);
+        st.read(here + (x * 2 + 1) * S::kBytes, ia, ib);
+        unpack<kF32, kInter>(ia, ib, gu, gv);
         uint64_t sq = 0ull, dot2 = 0ull, yu[H], yv[H];
 #pragma unroll
         for (int j = 0; j < H; ++j) {
@@ -518,8 +612,14 @@ cudaError_t launch_fwd(const NormRopeParams& p, cudaStream_t s) {
   const Slices c(((int64_t)p.n * p.l) << shift, chunks, (int64_t)sms * kSmThreads);
   int64_t blocks = ((((int64_t)p.n * p.l * c.slices) << shift) + kThreads - 1) / kThreads;
   if (blocks > (int64_t(1) << 30)) blocks = int64_t(1) << 30;  // the kernel strides over the rest
-  return launch_dependent(norm_rope_kernel<kF32, kNorm, kInter, kPartial, kFwdHeads>, dim3((unsigned)blocks), kThreads, 0, s, p,
-                          c.slices, c.per);
+  auto launch = [&](auto kern, int smem) {
+    return launch_dependent(kern, dim3((unsigned)blocks), kThreads, smem, s, p, c.slices, c.per);
+  };
+  if constexpr (kNorm && !kF32) {
+    constexpr int smem = kFwdStages * kFwdHeads * Staged<kF32, true>::kBytes;
+    if (c.per > 1) return launch(norm_rope_kernel<kF32, kNorm, kInter, kPartial, kFwdHeads, kFwdStages>, smem);
+  }
+  return launch(norm_rope_kernel<kF32, kNorm, kInter, kPartial, kFwdHeads, 0>, 0);
 }
 
 template <bool kF32, bool kInter, bool kPartial>
