@@ -83,7 +83,8 @@ struct Cfg {
   static constexpr int kNumBars = 1 + 4 * kStages + 2 + 2 + 1;
   static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
   static constexpr int kGroupOff = (kTableOff + 2 * (kMaxGroups + 1) * 4 + 15) / 16 * 16;
-  static constexpr int kSmem = kGroupOff + kMaxGroups * 16 + 1024 /*alignment*/;
+  static constexpr int kFirstOff = kGroupOff + kMaxGroups * 16;
+  static constexpr int kSmem = kFirstOff + 128 + 1024 /*alignment*/;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
   static constexpr uint32_t kVLbo = 64 * 128 * 2;
@@ -125,6 +126,7 @@ struct Shape {
 };
 
 // Where the groups' costs and parts' rows begin, [groups + 1] each; and the runs.
+struct First;
 struct Schedule {
   const int *costs, *rows;
   const Group* groups;
@@ -136,6 +138,7 @@ struct Schedule {
     ctas = min(most_ctas, max(1, total));  // a step each at least
     snap = min(kSnap, total / ctas / 4);
   }
+  __device__ Schedule(const int* c, const int* r, const Group* g, int n, int query_heads, const First& f);
   // The group that cost v belongs to: the last that begins at it or before.
   __device__ int group_of(int v) const {
     int lo = 0, hi = n_groups - 1;
@@ -201,6 +204,16 @@ __device__ __forceinline__ Seg seg_at(const Schedule& s, int v, int end) {
   r.part = s.rows[lo] + r.hk * sh.part_rows() + r.q0;
   return r;
 }
+
+// What a CTA's warps find of the schedule when they begin.
+struct First {
+  int total, ctas, snap, run0, run1;
+  Seg seg;  // of the run's first unit
+};
+static_assert(sizeof(First) <= 128, "its place");
+
+__device__ __forceinline__ Schedule::Schedule(const int* c, const int* r, const Group* g, int n, int query_heads, const First& f)
+    : costs(c), rows(r), groups(g), n_groups(n), heads(query_heads), total(f.total), ctas(f.ctas), snap(f.snap) {}
 
 // Workspace.
 struct Layout {
@@ -328,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* first_cost = reinterpret_cast<int*>(smem + C::kTableOff);
   int* first_row = first_cost + kMaxGroups + 1;
   Group* groups = reinterpret_cast<Group*>(smem + C::kGroupOff);
+  First& first = *reinterpret_cast<First*>(smem + C::kFirstOff);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int heads = p.h / p.hkv;
 
@@ -372,14 +386,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       rows += __shfl_sync(~0u, ri, 31);
     }
     if (lane == 0) first_cost[p.groups] = costs, first_row[p.groups] = rows;
+    __syncwarp();
+    // The run and its first unit, once for all warps: what each of them does not run when it begins it does not wait for, and
+    // cold instructions are most of what passes until a CTA's first load.
+    const Schedule sc(first_cost, first_row, groups, p.groups, heads, gridDim.x);
+    const int cta = blockIdx.x, at = cta < sc.ctas ? sc.begin(cta + (lane & 1)) : 0;
+    const int run0 = __shfl_sync(~0u, at, 0), run1 = __shfl_sync(~0u, at, 1);
+    if (lane == 0) {
+      first.total = sc.total, first.ctas = sc.ctas, first.snap = sc.snap;
+      first.run0 = run0, first.run1 = run1;
+      if (run0 < run1) first.seg = seg_at(sc, run0, run1);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Schedule sc(first_cost, first_row, groups, p.groups, heads, gridDim.x);
-  const int cta = blockIdx.x;
-  const int run0 = cta < sc.ctas ? sc.begin(cta) : 0, run1 = cta < sc.ctas ? sc.begin(cta + 1) : 0;
+  const Schedule sc(first_cost, first_row, groups, p.groups, heads, first);
+  const int cta = blockIdx.x, run0 = first.run0, run1 = first.run1;
+  auto unit_at = [&](int v) { return v == run0 ? first.seg : seg_at(sc, v, run1); };
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kKWarp || warp == kVWarp) {
@@ -393,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int it = 0;
       for (int v = run0; ok && v < run1;) {
-        const Seg sg = seg_at(sc, v, run1);
+        const Seg sg = unit_at(v);
         v = sg.next;
         const int32_t* entries = p.table + sg.g.owner * p.table_stride;
         int id[kMost], off[kMost];  // of this lane's boxes in the next tile
@@ -438,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int base = 0, seg = 0;
       for (int v = run0; v < run1; ++seg) {
-        const Seg sg = seg_at(sc, v, run1);
+        const Seg sg = unit_at(v);
         v = sg.next;
         const int most = sg.count(0);  // the second half has as many tiles or one less
         // half t's x-th tile is the ring's slot(t, x)-th
@@ -531,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(q_full);
     };
     if (run0 < run1) {
-      copy_queries(seg_at(sc, run0, run1));
+      copy_queries(first.seg);
       queries_there();
     }
     for (int v = run0; v < run1;) {
-      const Seg sg = seg_at(sc, v, run1);
+      const Seg sg = unit_at(v);
       v = sg.next;
       float m_ref = -INFINITY, l_sum = 0.f;
       const int n = sg.count(t);
