@@ -12,16 +12,19 @@
 // cosines and sines, and these are worked out once for a thread's whole token. A row belongs to `lanes` neighbouring lanes
 // of a warp, a power of two; each holds two 16-byte pieces of it, both ends of its pairs (half layout: a piece of the first
 // half and its partner in the second; interleaved: 32 bytes in a row), so the rotation needs no exchange and the norm a
-// shuffle tree of log2(lanes) steps. A thread takes a token's heads kHeads at a time: it sends their loads, reduces, turns
-// and stores; tokens that do not fill the GPU are shared out between several threads.
+// shuffle tree of log2(lanes) steps. A thread takes a token's heads kHeads at a time, a CHUNK: it reduces, turns and stores
+// one while the next is on its way into shared memory, where the norm leaves bf16 rows little time to send loads and wait
+// (forward 113 us with loads into registers, 110 so; of a thread with one chunk there is no next, and f32 rows and those without
+// a norm gain nothing or lose 3-8%: loads into registers there). Tokens that do not fill the GPU are shared out between
+// several threads.
 //
 // The weights' gradient is a sum over all rows. A thread keeps its columns' sums in fp32 over all the rows it meets
 // (the grid is one wave, each block only q or only k), a block adds up its threads in shared memory, and a second kernel
 // the blocks, all in a fixed order: the same call gives the same bits.
 //
-// Measured (GPU time, inputs larger than L2): [1, 32768, 32 + 8, 128] bf16 forward 113 us (5.9 TB/s), with its gradient
-// 290 us (5.8 TB/s; a copy reaches 6.7); without the norm, half of the head turned, 101 us (6.6 TB/s). [1, 16384, 16 + 16,
-// 128] f32 84 and 216 us (6.4, 6.2 TB/s). 256 tokens of 32 + 8 heads: 5.2 us, the host takes 7.5
+// Measured (GPU time, inputs larger than L2): [1, 32768, 32 + 8, 128] bf16 forward 110 us (6.1 TB/s), with its gradient
+// 288 us (5.8 TB/s; a copy reaches 6.7), 290 interleaved; interleaved without the norm 103 us (6.5 TB/s). [1, 16384, 16 + 16,
+// 128] f32 85 and 216 us (6.3, 6.2 TB/s). 256 tokens of 32 + 8 heads: 4.9 us, the host takes 7.5
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -36,12 +39,13 @@ namespace {
 
 constexpr int kThreads = 128;
 // Threads of an SM that a forward's tokens are shared out between, at least: two waves of them. Fewer slices of a token compute
-// its angles less often, more of them end together ([8, 4096, 16 + 16, 64] bf16: 640 threads 55.0 us, 1280 49.9, 2048 58.0;
-// [1, 4096, 32 + 8, 128]: 23.2, 18.5, 22.5 us).
+// its angles less often, more of them end together ([8, 4096, 16 + 16, 64] bf16: 640 threads 50.6 us, 1280 46.2; [1, 4096,
+// 32 + 8, 128]: 20.8, 17.4 us; 2048 16-20% slower than 1280, with loads into registers).
 constexpr int kSmThreads = 1280;
 constexpr int kMaxD = 2 * kRopeMaxPairs;
-// Heads of a chunk. Forward: 2 and 8 heads 131 and 127 us for [1, 32768, 32 + 8, 128] bf16 (now 113). Backward: 1 head three
-// stages deep 2-4% slower; 3 or 5 blocks to an SM 318 and 350 us for the training step (now 290).
+// Heads of a chunk. Forward: 2 heads three stages deep 111.5 us for [1, 32768, 32 + 8, 128] bf16 (now 110), 2 and 8 with loads
+// into registers 131 and 127 us; 6 blocks to an SM 123 us. Backward: 1 head three or four stages deep 2-4% slower; 3 or 5
+// blocks to an SM 318 and 350 us for the training step (now 288).
 constexpr int kFwdHeads = 4, kFwdStages = 2;
 constexpr int kBwdHeads = 2, kBwdStages = 2, kBwdBlocks = 4;
 

@@ -39,14 +39,18 @@
 // kernel before it ends, so that the join finds both done.
 //
 // Measured (GPU time, three sets of inputs in turn; h / h_kv 32 / 8, d = 128): 64
-// requests behind 32k shared keys, up to 1k own ones each, 61 us, where 188 MB take 28
-// and the products 18 (behind 16k 46 us, 493 without sharing); 256 behind 16k, up to 600 own, 96 us (27,
-// 36). Of the latter 3 go to the setup, 29 to the rest (its bytes at 5 TB/s), 58 to
-// the prefix and 9 to the join. A step of a unit takes 1.47 us, the tensor core busy
-// 70% of it (the chain S, maximum, exponentials, P V of two halves in turn); before a
-// CTA's first step 8 us pass (schedule, queries, keys, cold instructions), and its
-// part takes 3-4 to write, all CTAs' 20 MB at once. Two threads to a row (640 threads
-// at 96 registers) meet to exchange maxima: no faster.
+// requests behind 32k shared keys, up to 1k own ones each, 59.5 us, where 188 MB take
+// 28 and the products 18 (behind 16k 46 us, 493 without sharing); 256 behind 16k, up
+// to 600 own, 93 us (27, 36). Of the latter 3 go to the setup, 29 to the rest (its
+// bytes at 5 TB/s), 54 to the prefix and 8 to the join. A step of a unit takes 1.47
+// us, the tensor core busy 70% of it (the chain S, maximum, exponentials, P V of two
+// halves in turn); before a CTA's first scores 4.5 us pass (schedule, queries, keys,
+// cold instructions), its first two steps take 2 each, and its part 3 to write, all
+// CTAs' 20 MB at once. Tried without gain: two threads to a row (640 threads at 96
+// registers), which meet to exchange maxima; runs that get shorter from CTA to CTA, as
+// these start up to 10 us apart (most of them at the end of that); the rest's kernel on
+// 64-112 SMs and the prefix beside it (both take longer); tiles called into L2 a step
+// ahead (66 us).
 #include <cuda_bf16.h>
 
 #include "launch_cache.cuh"
@@ -67,8 +71,10 @@ constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
 constexpr float kRescale = 8.f;  // log2: O is rescaled only when a maximum grows by more
 constexpr uint32_t kPReadyBar = 1, kPReadyThreads = 128 + 32, kBothBar = 3;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// Of a unit besides its steps, in steps: a run in two units fetches queries and writes parts twice.
-constexpr int kUnitCost = 2;
+// Of a unit besides its steps, in steps: a run in two units fetches queries and writes parts twice. A fifth of a run, within these
+// bounds. (2 and 5 everywhere, runs of 27 steps, 256 requests behind 16k keys: 96.9, 93.8 us; of 13, 64 behind 32k: the same;
+// of 5, 96 in three groups: 68.5, 71.6 us, 16 behind 4k: 24.7, 26.4 us.)
+constexpr int kLeastUnitCost = 2, kMostUnitCost = 5;
 // A run's cut is moved by up to so many steps (and a quarter of a run) to a unit's border.
 constexpr int kSnap = 2;
 
@@ -84,7 +90,8 @@ struct Cfg {
   static constexpr int kTableOff = kBarOff + kNumBars * 8 + 16;
   static constexpr int kGroupOff = (kTableOff + 2 * (kMaxGroups + 1) * 4 + 15) / 16 * 16;
   static constexpr int kFirstOff = kGroupOff + kMaxGroups * 16;
-  static constexpr int kSmem = kFirstOff + 128 + 1024 /*alignment*/;
+  static constexpr int kUnitOff = kFirstOff + 128;  // each softmax warp's unit, 64 bytes
+  static constexpr int kSmem = kUnitOff + 8 * 64 + 1024 /*alignment*/;
   static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
   static constexpr uint32_t kVLbo = 64 * 128 * 2;
@@ -110,7 +117,7 @@ struct alignas(16) Group {
 };
 
 // Of a group: units of two halves, rows of a last unit of one half (0: none), and steps, a step being a tile of a unit of
-// two halves or two tiles of the other. A unit costs its steps, and kUnitCost behind them.
+// two halves or two tiles of the other.
 struct Shape {
   int rows, twos, one, tiles, one_steps;
   __device__ Shape(int q_rows, int t) : rows(q_rows), tiles(t) {
@@ -120,8 +127,8 @@ struct Shape {
     if (t == 0) twos = one = 0;
     one_steps = one > 0 ? (t + 1) / 2 : 0;
   }
-  // what a K/V head's units cost
-  __device__ int cost() const { return twos * (tiles + kUnitCost) + (one > 0 ? one_steps + kUnitCost : 0); }
+  // what a K/V head's units cost: their steps, and behind them unit_cost each
+  __device__ int cost(int unit_cost) const { return twos * (tiles + unit_cost) + (one > 0 ? one_steps + unit_cost : 0); }
   __device__ int part_rows() const { return twos * kUnitRows + 2 * one; }  // rows of its parts
 };
 
@@ -131,10 +138,10 @@ struct Schedule {
   const int *costs, *rows;
   const Group* groups;
   int n_groups, heads;  // heads: query heads of a K/V head
-  int total, ctas, snap;
+  int total, ctas, snap, unit;  // unit: a unit's cost besides its steps
 
-  __device__ Schedule(const int* c, const int* r, const Group* g, int n, int query_heads, int most_ctas)
-      : costs(c), rows(r), groups(g), n_groups(n), heads(query_heads), total(c[n]) {
+  __device__ Schedule(const int* c, const int* r, const Group* g, int n, int query_heads, int most_ctas, int unit_cost)
+      : costs(c), rows(r), groups(g), n_groups(n), heads(query_heads), total(c[n]), unit(unit_cost) {
     ctas = min(most_ctas, max(1, total));  // a step each at least
     snap = min(kSnap, total / ctas / 4);
   }
@@ -157,10 +164,10 @@ struct Schedule {
     if (v == 0 || v >= total) return v;
     const int g = group_of(v);
     const Shape sh(groups[g].rows * heads, groups[g].tiles);
-    int in = (v - costs[g]) % sh.cost();
-    const int each = sh.tiles + kUnitCost, u = min(in / each, sh.twos), steps = u < sh.twos ? sh.tiles : sh.one_steps;
+    int in = (v - costs[g]) % sh.cost(unit);
+    const int each = sh.tiles + unit, u = min(in / each, sh.twos), steps = u < sh.twos ? sh.tiles : sh.one_steps;
     in -= u * each;
-    return in <= snap ? v - in : in >= steps - snap ? v + steps + kUnitCost - in : v;
+    return in <= snap ? v - in : in >= steps - snap ? v + steps + unit - in : v;
   }
   __device__ int cta_of(int v) const {
     int c = (int)((((int64_t)v + 1) * ctas - 1) / total);
@@ -190,30 +197,30 @@ __device__ __forceinline__ Seg seg_at(const Schedule& s, int v, int end) {
   Seg r;
   r.g = s.groups[lo];
   const Shape sh(r.g.rows * s.heads, r.g.tiles);
-  const int in_group = v - s.costs[lo], unit = sh.tiles + kUnitCost;
-  r.hk = in_group / sh.cost();
-  const int in = in_group - r.hk * sh.cost(), u = min(in / unit, sh.twos);
+  const int in_group = v - s.costs[lo], each = sh.tiles + s.unit, head = sh.cost(s.unit);
+  r.hk = in_group / head;
+  const int in = in_group - r.hk * head, u = min(in / each, sh.twos);
   r.two = u < sh.twos;
   r.q0 = u * kUnitRows;
   r.rows = r.two ? min(kUnitRows, sh.rows - r.q0) : sh.one;
-  r.a = in - u * unit;
+  r.a = in - u * each;
   const int all = r.two ? sh.tiles : sh.one_steps;
   r.b = min(all, r.a + (end - v));
   r.last = v - r.a + all - 1;
-  r.next = min(end, r.last + 1 + kUnitCost);
+  r.next = min(end, r.last + 1 + s.unit);
   r.part = s.rows[lo] + r.hk * sh.part_rows() + r.q0;
   return r;
 }
 
 // What a CTA's warps find of the schedule when they begin.
 struct First {
-  int total, ctas, snap, run0, run1;
+  int total, ctas, snap, unit, run0, run1;
   Seg seg;  // of the run's first unit
 };
-static_assert(sizeof(First) <= 128, "its place");
+static_assert(sizeof(First) <= 128 && sizeof(Seg) <= 64, "their places");
 
 __device__ __forceinline__ Schedule::Schedule(const int* c, const int* r, const Group* g, int n, int query_heads, const First& f)
-    : costs(c), rows(r), groups(g), n_groups(n), heads(query_heads), total(f.total), ctas(f.ctas), snap(f.snap) {}
+    : costs(c), rows(r), groups(g), n_groups(n), heads(query_heads), total(f.total), ctas(f.ctas), snap(f.snap), unit(f.unit) {}
 
 // Workspace.
 struct Layout {
@@ -360,16 +367,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_launch_dependents();
   if (warp == kVWarp) {  // sums of costs and part rows over the groups
-    int costs = 0, rows = 0;
+    int costs = 0, rows = 0, steps = 0;
+    for (int i = lane; i < p.groups; i += 32) {
+      // past L1, like all that this kernel reads before it has waited for the launch before it
+      const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.group + i));
+      groups[i] = Group{raw.x, raw.y, raw.z, raw.w};
+      steps += Shape(raw.y * heads, raw.w).cost(0) * p.hkv;
+    }
+    steps = __reduce_add_sync(~0u, steps);
+    const int unit_cost = min(max(steps / (5 * (int)gridDim.x), kLeastUnitCost), kMostUnitCost);
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
       int s = 0, r = 0;
       if (g0 + lane < p.groups) {
-        // past L1, like all that this kernel reads before it has waited for the launch before it
-        const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.group + g0 + lane));
-        const Group g{raw.x, raw.y, raw.z, raw.w};
-        groups[g0 + lane] = g;
+        const Group g = groups[g0 + lane];
         const Shape sh(g.rows * heads, g.tiles);
-        s = sh.cost() * p.hkv;
+        s = sh.cost(unit_cost) * p.hkv;
         r = sh.part_rows() * p.hkv;
       }
       int si = s, ri = r;
@@ -389,11 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     // The run and its first unit, once for all warps: what each of them does not run when it begins it does not wait for, and
     // cold instructions are most of what passes until a CTA's first load.
-    const Schedule sc(first_cost, first_row, groups, p.groups, heads, gridDim.x);
+    const Schedule sc(first_cost, first_row, groups, p.groups, heads, gridDim.x, unit_cost);
     const int cta = blockIdx.x, at = cta < sc.ctas ? sc.begin(cta + (lane & 1)) : 0;
     const int run0 = __shfl_sync(~0u, at, 0), run1 = __shfl_sync(~0u, at, 1);
     if (lane == 0) {
-      first.total = sc.total, first.ctas = sc.ctas, first.snap = sc.snap;
+      first.total = sc.total, first.ctas = sc.ctas, first.snap = sc.snap, first.unit = sc.unit;
       first.run0 = run0, first.run1 = run1;
       if (run0 < run1) first.seg = seg_at(sc, run0, run1);
     }
@@ -402,9 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Schedule sc(first_cost, first_row, groups, p.groups, heads, first);
-  const int cta = blockIdx.x, run0 = first.run0, run1 = first.run1;
-  auto unit_at = [&](int v) { return v == run0 ? first.seg : seg_at(sc, v, run1); };
+  // (read again from shared memory where it is needed: few registers are free in between)
+  auto schedule = [&]() { return Schedule(first_cost, first_row, groups, p.groups, heads, first); };
+  const int cta = blockIdx.x, run0 = first.run0;
+  auto unit_at = [&](int v) { return v == run0 ? first.seg : seg_at(schedule(), v, first.run1); };
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kKWarp || warp == kVWarp) {
@@ -417,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kMost = kTile / 32;
       bool ok = true;
       int it = 0;
-      for (int v = run0; ok && v < run1;) {
+      for (int v = run0; ok && v < first.run1;) {
         const Seg sg = unit_at(v);
         v = sg.next;
         const int32_t* entries = p.table + sg.g.owner * p.table_stride;
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v_desc = sdesc_sw128(smem_u32(smem + C::kVOff), C::kVLbo, 1024);
       bool ok = true;
       int base = 0, seg = 0;
-      for (int v = run0; v < run1; ++seg) {
+      for (int v = run0; v < first.run1; ++seg) {
         const Seg sg = unit_at(v);
         v = sg.next;
         const int most = sg.count(0);  // the second half has as many tiles or one less
@@ -523,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tmem = tmem + lane_base + t * 128, o_tmem = tmem + lane_base + 256 + t * 128;
     bool ok = true;
     int met = 0, done = 0;  // tiles and segments of this half so far
+    Seg& unit = *reinterpret_cast<Seg*>(smem + C::kUnitOff + warp * 64);  // the tiles' loop has no registers for it
     // A unit's queries, 16 bytes of a row at a time, copied without passing through registers (where the prefetched ones
     // would be spilled); rows behind the last repeat it and go nowhere.
     constexpr int kPieces = D / 8, kRows = 256 / kPieces, kTimes = kUnitRows / kRows;
@@ -555,15 +569,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     };
-    if (run0 < run1) {
+    if (run0 < first.run1) {
       copy_queries(first.seg);
       queries_there();
     }
-    for (int v = run0; v < run1;) {
-      const Seg sg = unit_at(v);
-      v = sg.next;
+    for (int v = run0; v < first.run1;) {
+      int n;
+      {
+        const Seg begun = unit_at(v);
+        v = begun.next;
+        n = begun.count(t);
+        if (lane == 0) unit = begun;
+        __syncwarp();
+      }
       float m_ref = -INFINITY, l_sum = 0.f;
-      const int n = sg.count(t);
       for (int x = 0; x < n; ++x, ++met) {
         if (ok) ok = warp_wait_parity(&s_full[t], met & 1, abort_flag, p.status);
         if (!ok) {
@@ -647,16 +666,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         named_bar_sync(kPReadyBar + t, kPReadyThreads);
       }
+      const Seg sg = unit;
       // Both halves have met the unit's last S: the next one's queries may take the place of its queries, and their S
       // products run while this unit's parts are written.
-      const bool more = v < run1;
+      const bool more = v < first.run1;
       if (more) {
         named_bar_sync(kBothBar, 256);
-        copy_queries(seg_at(sc, v, run1));
+        copy_queries(unit_at(v));
       }
       if (sg.a == 0) {
         // for the kernel that joins: each row's first part, the parts' number, and the second half's distance
-        const int parts = (sc.cta_of(sg.last) - cta + 1) * (sg.two ? 1 : 2);
+        const int parts = (schedule().cta_of(sg.last) - cta + 1) * (sg.two ? 1 : 2);
         for (int i = threadIdx.x; i < sg.rows; i += 256) {
           const int qr = sg.q0 + i, b = qr / heads, hh = sg.hk * heads + (qr - b * heads);
           p.row[(int64_t)(sg.g.row0 + b) * p.h + hh] = make_int4(kUnitRows * cta + sg.part + i, parts, sg.two ? 0 : sg.rows, 0);
@@ -935,7 +955,7 @@ bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int
   const int64_t most = (int64_t(1) << 31) - 1;
   if (2 * n * h + (int64_t)kUnitRows * kMaxCtas > most) return false;
   const int64_t units = h_kv * (n * (h / h_kv) / kUnitRows + (groups < n ? groups : n));
-  return units <= most / (max_keys / kTile + 1 + kUnitCost);
+  return units <= most / (max_keys / kTile + 1 + kMostUnitCost);
 }
 
 cudaError_t launch_paged_shared(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s,

@@ -516,7 +516,7 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
  * the forward) for a bf16 out, and have 16 bits for an f32 out. group_rows out of
  * order or range: nothing is shared, and reported; a negative shared_lens counts
  * as 0 and is reported; the rest as bea_paged_decode reports it. (2 h n + 40960 <
- * 2^31, and h_kv (n h / h_kv / 256 + min(groups, n)) (max_keys / 128 + 4) < 2^31, else
+ * 2^31, and h_kv (n h / h_kv / 256 + min(groups, n)) (max_keys / 128 + 6) < 2^31, else
  * BEA_ERR_SHAPE.)
  */
 size_t bea_paged_decode_shared_workspace_size(int64_t n, int64_t h, int64_t h_kv, int64_t d, int64_t max_keys,
