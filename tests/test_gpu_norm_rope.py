@@ -179,6 +179,39 @@ def test_many_rows_take_the_wide_kernel_and_the_same_values():
     check_bwd(None, twice[0][2], q, w, g[0], pos, (64,), BF16)
 
 
+@pytest.mark.parametrize("d,how", [(64, dict(rotary_dim=32, layout="interleaved")), (80, dict(rotary_dim=48)),
+                                   (256, dict(layout="interleaved")), (128, dict(rotary_dim=64)), (96, dict()),
+                                   (48, dict(rotary_dim=2, layout="interleaved")), (16, dict(rotary_dim=0))])
+def test_many_rows_in_every_layout(d, how):
+    """Threads with several chunks, whose rows run ahead through shared memory: the bits of threads with one, in place too,
+    and the gradients of rows anywhere."""
+    import blockwise_exact_attention_gb300 as bea
+    n, l, hq, hk = (2, 11000, 13, 6) if d < 256 else (1, 4001, 13, 6)
+    sections = (how.get("rotary_dim", d) // 2,)
+    pos, p = positions(n, l, 1, top=200000)
+    q, k, w = draw((n, l, hq, d), BF16, 1, 2.0), draw((n, l, hk, d), BF16, 2, 0.3), draw((d,), F32, 3)
+    qo, ko = bea.norm_rope_axes(q, k, p, sections, w, None, EPS, **how)
+    rows = [0, 1, 2, l // 2, l - 2, l - 1]
+    check_fwd(qo[:, rows], q[:, rows], w, pos[:, :, rows], sections, BF16, **how)
+    check_fwd(ko[:, rows], k[:, rows], None, pos[:, :, rows], sections, BF16, **how)
+    for at in range(0, l, 1000):                         # few enough for threads with one chunk
+        part = slice(at, at + 1000)
+        few = bea.norm_rope_axes(q[:1, part], k[:1, part], p[:, :1, part], sections, w, None, EPS, **how)
+        assert torch.equal(few[0], qo[:1, part]) and torch.equal(few[1], ko[:1, part])
+    g = [draw(q.shape, BF16, 4), draw(k.shape, BF16, 5)]
+    leaves = [t.clone().requires_grad_() for t in (q, k, w)]
+    grads = torch.autograd.grad(bea.norm_rotary_axes(*leaves[:2], p, sections, leaves[2], None, EPS, **how), leaves, g)
+    check_bwd(grads[0][:, rows], None, q[:, rows], w, g[0][:, rows], pos[:, :, rows], sections, BF16, **how)
+    check_bwd(grads[1][:, rows], None, k[:, rows], None, g[1][:, rows], pos[:, :, rows], sections, BF16, **how)
+    small = slice(0, 50)
+    dq, dk = (t.detach().clone().requires_grad_() for t in (q[:, small], k[:, small]))
+    again = torch.autograd.grad(bea.norm_rotary_axes(dq, dk, p[:, :, small].contiguous(), sections, w, None, EPS, **how), (dq, dk),
+                                [t[:, small] for t in g])
+    assert torch.equal(again[0], grads[0][:, small]) and torch.equal(again[1], grads[1][:, small])
+    bea.norm_rope_axes(q, k, p, sections, w, None, EPS, q_out=q, k_out=k, **how)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+
+
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_strides_and_in_place(layout):
     import blockwise_exact_attention_gb300 as bea

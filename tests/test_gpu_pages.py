@@ -120,6 +120,31 @@ def test_free(n, width, page, rate, alias):
     assert bea.device_status() == 0
 
 
+@pytest.mark.parametrize("n,width,pages", [(3, 5000, 14000), (70, 2000, 131072), (150, 2100, 300000)])
+def test_free_of_many_pages(n, width, pages):
+    """Caches of which a warp takes several words, and of more than one turn."""
+    import blockwise_exact_attention_gb300 as bea
+    rng = random.Random(pages)
+    ids = rng.sample(range(pages), pages)
+    held, rest = ids[:pages * 2 // 3], ids[pages * 2 // 3:]
+    counts, table, lens = [0] * pages, [], []
+    for _ in range(n):
+        m = rng.randint(0, width)
+        row = rng.sample(held, m)
+        for p in row:
+            counts[p] += 1
+        table.append(row + [-1] * (width - m))
+        lens.append(2 * m - (rng.random() < 0.5 and m > 0))
+    shares = [max(c - 1, 0) for c in counts]
+    pool = rest + [-1] * (pages - len(rest))
+    ends = [rng.choice([-1, 0]) for _ in range(n)]
+    want = og.free(ends, lens, table, shares, pool, len(rest), 2)
+    P = i32(pool)
+    got = bea.paged_free(i32(ends), i32(lens), i32(table, width), i32(shares), P, i32([len(rest)]), 2)
+    assert want[4] and got.lens.tolist() == want[0] and got.shares.tolist() == want[1] and P.tolist() == want[2]
+    assert got.n_free.tolist() == [want[3]] and bea.device_status() == 0
+
+
 def test_free_of_wrong_states():
     import blockwise_exact_attention_gb300 as bea
     table = [[1, 2], [1, 9], [-1, 3], [0, 5]]
