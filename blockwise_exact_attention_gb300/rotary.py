@@ -95,29 +95,29 @@ class RopeScaling(NamedTuple):
 def _laid_out(sections, base, spectrum, rotary_dim, layout, scaling, d):
     """The table of a rotation with a layout: (axis, frequency) of every turned pair, the number of axes, the amplitude
     and whether pairs are interleaved."""
+    if scaling is not None and not isinstance(scaling, RopeScaling):
+        raise TypeError(f"scaling {scaling!r} is not a RopeScaling")
+    return _built_layout(sections, (*map(type, sections),), base, spectrum, rotary_dim, layout, scaling, d)
+
+
+@functools.lru_cache(maxsize=128, typed=True)
+def _built_layout(sections, types, base, spectrum, rotary_dim, layout, scaling, d):
     rotary_dim = d if rotary_dim is None else rotary_dim
     if not isinstance(rotary_dim, int) or rotary_dim < 0 or rotary_dim > d or rotary_dim % 2 != 0:
         raise ValueError(f"rotary_dim {rotary_dim} is not an even number of elements of a head of {d}")
     if layout not in ("half", "interleaved"):
         raise ValueError(f"layout {layout!r}: 'half' or 'interleaved'")
-    if scaling is not None and not isinstance(scaling, RopeScaling):
-        raise TypeError(f"scaling {scaling!r} is not a RopeScaling")
-    table = _scaled_table(sections, (*map(type, sections),), base, spectrum, rotary_dim, scaling)
-    return (*table, int(layout == "interleaved"))
-
-
-@functools.lru_cache(maxsize=128, typed=True)
-def _scaled_table(sections, types, base, spectrum, rotary_dim, scaling):
+    axis, freq, axes = _built_table(sections, types, base, spectrum, rotary_dim)
+    interleaved = int(layout == "interleaved")
     if scaling is None:
-        return (*_built_table(sections, types, base, spectrum, rotary_dim), 1.0)
+        return axis, freq, axes, 1.0, interleaved
     scaling.checked()
-    axis, _, axes = _built_table(sections, types, base, spectrum, rotary_dim)
     half = rotary_dim // 2
     freq = []
     for pairs in sections:
         for j in range(pairs):
             freq.append(scaling.frequency(base, len(freq), half) if spectrum == "joint" else scaling.frequency(base, j, pairs))
-    return axis, struct.pack(f"={half}d", *freq), axes, scaling.size()
+    return axis, struct.pack(f"={half}d", *freq), axes, scaling.size(), interleaved
 
 
 def _plainly(q, rotary_dim, layout, scaling) -> bool:
