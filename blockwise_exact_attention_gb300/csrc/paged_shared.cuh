@@ -24,9 +24,13 @@ bool paged_shared_is_plain(const PagedDecodeParams& d, int64_t groups);
 size_t paged_shared_workspace(int64_t n, int64_t h, int64_t h_kv, int64_t d, int64_t max_keys, int64_t groups);
 // Whether the counts of the schedule fit 31 bits.
 bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int64_t groups);
-// tk, tv: boxes of 64 columns and paged_shared_box(page) tokens of a page.
+// Of a page's rows tiles of 128 take any multiple of the largest power of two, up to 128, that divides a page.
 int paged_shared_box(int64_t page);
-cudaError_t launch_paged_shared(const PagedSharedParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s,
-                                int* nlaunch);
+// Boxes of 64 columns and paged_shared_box(page) << i tokens, those of no more than a page and a tile.
+constexpr int kPageMaps = 8;
+struct PageMaps {
+  CUtensorMap k[kPageMaps], v[kPageMaps];
+};
+cudaError_t launch_paged_shared(const PagedSharedParams& p, const PageMaps& maps, cudaStream_t s, int* nlaunch);
 
 }  // namespace bea

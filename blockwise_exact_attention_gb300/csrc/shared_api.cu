@@ -47,10 +47,12 @@ int bea_paged_decode_shared(const bea_tensor* q, const bea_tensor* k_cache, cons
   // (no copies by box from a cache whose pages, tokens or heads lie on one another)
   if (bea::paged_shared_is_plain(p.d, groups) || broadcast(k_cache) || broadcast(v_cache))
     return finish(bea::launch_paged_decode(p.d, s, &launches), launches);
-  CUtensorMap tk, tv;
-  const int box = bea::paged_shared_box(p.d.page);
-  if ((rc = make_page_map(k_cache, box, &tk)) || (rc = make_page_map(v_cache, box, &tv))) return rc;
-  return finish(bea::launch_paged_shared(p, tk, tv, s, &launches), launches);
+  bea::PageMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  int box = bea::paged_shared_box(p.d.page);
+  for (int i = 0; i < bea::kPageMaps && box <= 128 && box <= p.d.page; ++i, box *= 2)
+    if ((rc = make_page_map(k_cache, box, &maps.k[i])) || (rc = make_page_map(v_cache, box, &maps.v[i]))) return rc;
+  return finish(bea::launch_paged_shared(p, maps, s, &launches), launches);
 }
 
 }  // extern "C"

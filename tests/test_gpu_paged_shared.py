@@ -145,6 +145,14 @@ def test_pages(page, d):
     check(out, lse, *x, 0.2)
 
 
+@pytest.mark.parametrize("page", [2, 5, 7, 12, 30, 31, 50, 63, 65, 96, 126, 127, 129, 160, 192, 200, 513])
+def test_pages_in_boxes_of_several_sizes(page):
+    """Pages that end inside a tile, their rows in boxes of every power of two."""
+    x, g = make([(1300 // page * page + page, [0, 9, 130]), (900 // page * page + page, [1, 70])], 6, 3, 64, page, seed=page)
+    out, lse = run(x, g, 0.2)
+    check(out, lse, *x, 0.2)
+
+
 @pytest.mark.parametrize("shared", [0, 1, 127, 128, 129, 255, 256, 384, 385, 512, 1152, 5000])
 def test_shared_lengths(shared):
     """None, less than a tile, odd and even numbers of tiles, cut over the CTAs and not."""
