@@ -72,6 +72,29 @@ constexpr int kRowThreads = 256;
 // Of the kernels that one cluster runs.
 constexpr int kClusterThreads = 1024, kCtas = 8;
 
+// The rows' entries dealt to a cluster's warps, several to a row where there are fewer rows than warps, as long as each has 64
+// entries of a row's `width` (two rows of 8000 entries compacted by a warp each 87 us, so 8.5; a power of two: divisions took 0.5 us of a small fork's 6.5).
+template <typename F>
+__device__ __forceinline__ void rows_of_cluster(int n, int width, int rank, F f) {
+  constexpr int kBits = 8;  // of a warp's number
+  static_assert(kCtas * kClusterThreads / 32 == 1 << kBits, "the cluster's warps");
+  const int warp = rank + kCtas * (threadIdx.x >> 5);
+  const int row_bits = n > 1 ? 32 - __clz(n - 1) : 0, most = 31 - __clz(max((width + 63) / 64, 1));
+  const int bits = max(0, min(kBits - row_bits, most));  // 2^bits warps to a row
+  const int first = (warp & ((1 << bits) - 1)) * 32 + (threadIdx.x & 31);
+  for (int r = warp >> bits; r < n; r += 1 << (kBits - bits)) f(r, first, 32 << bits);
+}
+// To a grid's blocks of kRowThreads, several to a row where there are fewer rows than blocks, as long as each has 1024 entries
+// of a row's `width`.
+template <typename F>
+__device__ __forceinline__ void rows_of_grid(int n, int width, F f) {
+  const int slices = max(1, min((int)gridDim.x / max(n, 1), (width + 1023) / 1024));
+  for (int64_t i = blockIdx.x; i < (int64_t)n * slices; i += gridDim.x) {
+    const int r = (int)(i / slices), slice = (int)(i - (int64_t)r * slices);
+    f(r, slice * kRowThreads + (int)threadIdx.x, slices * kRowThreads);
+  }
+}
+
 // One row of the step: how many tokens it takes (-1: it takes no part), and whether it is wrong.
 struct ForkRow {
   int src, took;
@@ -171,7 +194,7 @@ __global__ void __launch_bounds__(kClusterThreads) fork_plan_kernel(const __grid
 }
 __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const __grid_constant__ ForkParams p) {
   grid_dependency_wait();
-  for (int r = blockIdx.x; r < p.s.n; r += gridDim.x) fork_entries(p, r, threadIdx.x, kRowThreads);
+  rows_of_grid(p.s.n, p.s.max_pages, [&](int r, int first, int step) { fork_entries(p, r, first, step); });
 }
 
 // All of it by one cluster: its first block the step, then its warps the rows.
@@ -187,8 +210,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kClusterThreads)
     copy_ints(p.s.shares_out, p.s.shares, p.s.num_pages, (rank - 1) * kClusterThreads + (int)threadIdx.x,
               (kCtas - 1) * kClusterThreads);
   cluster.sync();
-  for (int r = rank + kCtas * (threadIdx.x >> 5); r < p.s.n; r += kCtas * kClusterThreads / 32)
-    fork_entries(p, r, threadIdx.x & 31, 32);
+  rows_of_cluster(p.s.n, p.s.max_pages, rank, [&](int r, int first, int step) { fork_entries(p, r, first, step); });
 }
 
 // ---- free ------------------------------------------------------------------------
@@ -224,8 +246,8 @@ __device__ __forceinline__ void free_entries(const FreeParams& p, int r, int fir
 
 __global__ void __launch_bounds__(kRowThreads) free_rows_kernel(const __grid_constant__ FreeParams p) {
   grid_dependency_wait();
-  const bool ok = height_fits(p.s, p.s.n_free[0]);
-  for (int r = blockIdx.x; ok && r < p.s.n; r += gridDim.x) free_entries(p, r, threadIdx.x, kRowThreads);
+  if (!height_fits(p.s, p.s.n_free[0])) return;
+  rows_of_grid(p.s.n, p.s.max_pages, [&](int r, int first, int step) { free_entries(p, r, first, step); });
 }
 
 // One cluster, kTile pages at a time, read once: a warp takes kWords times 32 in a row, and lane j keeps a bit for each of the
@@ -246,8 +268,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kClusterThreads) free_
       cluster.sync();
     }
     if (ok)
-      for (int r = rank + kCtas * (threadIdx.x >> 5); r < p.s.n; r += kCtas * kClusterThreads / 32)
-        free_entries(p, r, threadIdx.x & 31, 32);
+      rows_of_cluster(p.s.n, p.s.max_pages, rank, [&](int r, int first, int step) { free_entries(p, r, first, step); });
     cluster.sync();
   }
   int at = have;
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(kRowThreads) compact_moves_kernel(const __grid
 }
 __global__ void __launch_bounds__(kRowThreads) compact_table_kernel(const __grid_constant__ CompactParams p) {
   grid_dependency_wait();
-  for (int r = blockIdx.x; r < p.s.n; r += gridDim.x) compact_entries(p, r, threadIdx.x, kRowThreads);
+  rows_of_grid(p.s.n, p.s.max_pages, [&](int r, int first, int step) { compact_entries(p, r, first, step); });
 }
 
 // One block, between the kernels above; or one cluster for everything, its first block for the plan.
@@ -490,8 +511,7 @@ __global__ void __cluster_dims__(kCtas) __launch_bounds__(kClusterThreads)
   cluster.sync();  // the list of moves is there
   compact_moves(p, rank * kClusterThreads + (int)threadIdx.x, kCtas * kClusterThreads);
   cluster.sync();
-  for (int r = rank + kCtas * (threadIdx.x >> 5); r < p.s.n; r += kCtas * kClusterThreads / 32)
-    compact_entries(p, r, threadIdx.x & 31, 32);
+  rows_of_cluster(p.s.n, p.s.max_pages, rank, [&](int r, int first, int step) { compact_entries(p, r, first, step); });
 }
 
 // ---- copy ------------------------------------------------------------------------
@@ -559,6 +579,9 @@ unsigned grid_of(int64_t items, int64_t per, int most) {
   return (unsigned)(b < 1 ? 1 : b < most ? b : most);
 }
 
+// Blocks for the rows' entries.
+unsigned row_blocks(const PagesState& s, int wave) { return grid_of(s.n * (((int64_t)s.max_pages + 1023) / 1024), 1, wave); }
+
 // Blocks of kRowThreads: a wave of them, or one to an SM.
 cudaError_t most_blocks(int* wave, int* each) {
   int sms = 0;
@@ -590,7 +613,7 @@ cudaError_t launch_paged_fork(const ForkParams& p, cudaStream_t s, int* nlaunch)
   const unsigned more = p.s.shares_out != p.s.shares ? grid_of(p.s.num_pages, 4096, each) : 0;
   if ((e = launch_dependent(fork_plan_kernel, dim3(1 + more), kClusterThreads, 0, s, p)) != cudaSuccess) return e;
   *nlaunch += 1;
-  e = launch_dependent(fork_rows_kernel, dim3(grid_of(p.s.n, 1, wave)), kRowThreads, 0, s, p);
+  e = launch_dependent(fork_rows_kernel, dim3(row_blocks(p.s, wave)), kRowThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }
@@ -609,7 +632,7 @@ cudaError_t launch_paged_free(const FreeParams& p, cudaStream_t s, int* nlaunch)
     if (e != cudaSuccess) return e;
     *nlaunch += 1;
   }
-  e = launch_dependent(free_rows_kernel, dim3(grid_of(p.s.n, 1, wave)), kRowThreads, 0, s, p);
+  e = launch_dependent(free_rows_kernel, dim3(row_blocks(p.s, wave)), kRowThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
   e = launch_dependent(free_push_kernel<false>, dim3(kCtas), kClusterThreads, 0, s, p);
@@ -646,7 +669,7 @@ cudaError_t launch_paged_compact(const CompactParams& p, cudaStream_t s, int* nl
   e = launch_dependent(compact_moves_kernel, dim3(grid_of(p.capacity, 512, each)), kRowThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   *nlaunch += 1;
-  e = launch_dependent(compact_table_kernel, dim3(grid_of(p.s.n, 1, wave)), kRowThreads, 0, s, p);
+  e = launch_dependent(compact_table_kernel, dim3(row_blocks(p.s, wave)), kRowThreads, 0, s, p);
   if (e == cudaSuccess) *nlaunch += 1;
   return e;
 }

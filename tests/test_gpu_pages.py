@@ -163,6 +163,29 @@ def test_free_of_wrong_states():
         assert got.n_free.tolist() == [want[3]] and bea.device_status() == PAGES
 
 
+@pytest.mark.parametrize("n,width,page", [(1, 3000, 8), (2, 8000, 3), (3, 30000, 2), (100, 129, 16), (5, 65, 1)])
+def test_few_long_rows(n, width, page):
+    """Rows whose entries several warps, or several blocks, take."""
+    import blockwise_exact_attention_gb300 as bea
+    lens, table, shares, pool, height = state(n, width, page, 2 * n + 9, n, live=0.9, shared=width // 3)
+    lens, table = lens + [0] * n, table + [[-1] * width] * n
+    src = [-1] * n + [r if lens[r] else -1 for r in range(n)]
+    T, S, P, H = i32(table, width), i32(shares), i32(pool), i32([height])
+    want = og.fork(src, [-1] * 2 * n, lens, table, shares, pool, height, page)
+    got = bea.paged_fork(i32(src), None, i32(lens), T, S, P, H, page)
+    assert got.lens.tolist() == want[0] and T.tolist() == want[1] and got.shares.tolist() == want[2]
+    assert got.n_free.tolist() == [want[3]] and got.copies.tolist() == want[4]
+    lens, table, shares, height = want[0], want[1], want[2], want[3]
+    want = og.compact(lens, table, shares, pool, height, page, 50)
+    moved = bea.paged_compact(got.lens, T, got.shares, P, got.n_free, page, 50)
+    assert all(a.tolist() == b for a, b in zip(moved, want))
+    ends = [-1 if r % 3 != 1 else 0 for r in range(2 * n)]
+    want = og.free(ends, lens, want[0], want[1], want[2], height, page)
+    freed = bea.paged_free(i32(ends), got.lens, moved.block_table, moved.shares, moved.free_pages, got.n_free, page)
+    assert freed.lens.tolist() == want[0] and freed.shares.tolist() == want[1] and moved.free_pages.tolist() == want[2]
+    assert freed.n_free.tolist() == [want[3]] and bea.device_status() == 0
+
+
 @pytest.mark.parametrize("most", [0, 3, 10 ** 4])
 @pytest.mark.parametrize("alias", [False, True])
 @pytest.mark.parametrize("n,width,page", SIZES)
