@@ -283,6 +283,9 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_con
   using S = Staged<kF32, !kInter && !kPartial>;
   extern __shared__ __align__(16) uint8_t rows[];  // [stage][head] of S::kBytes
   __shared__ Tables tables;
+  // A thread's cosines and sines, without the weights of q or k: worked out again for k, and with a chunk's missing heads
+  // computed along, 6 + 3 heads of [14, 6507] took 97 us, not 80.
+  __shared__ uint64_t kept[kNorm ? 2 * H : 1][kThreads];
   load_tables<kNorm>(p, tables);
   constexpr int es = kF32 ? 4 : 2;
   const int shift = lane_shift(p.d, N);
@@ -350,7 +353,16 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_con
       }
       if (x0 == 0 || (kNorm && k_now != is_k)) {
         is_k = k_now;
-        angles<N>(p, tables, m.b, m.i, at.mine ? at.pair : p.pairs, p.inverse, c, s);
+        if (x0 == 0) {
+          angles<N>(p, tables, m.b, m.i, at.mine ? at.pair : p.pairs, p.inverse, c, s);
+          if constexpr (kNorm) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) kept[2 * j][threadIdx.x] = c[j], kept[2 * j + 1][threadIdx.x] = s[j];
+          }
+        } else if constexpr (kNorm) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) c[j] = kept[2 * j][threadIdx.x], s[j] = kept[2 * j + 1][threadIdx.x];
+        }
         if constexpr (kNorm) {
           const float* w = tables.w[is_k];
 #pragma unroll
@@ -368,8 +380,10 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rope_kernel(const __grid_con
         }
       }
       char* dst = static_cast<char*>(to.ptr) + (m.b * to.sn + m.i * to.sl + h0 * to.sh) * es;
+      const int most = __reduce_max_sync(~0u, heads - h0);  // heads that some lane of the warp has
 #pragma unroll
       for (int x = 0; x < kHeads; ++x) {
+        if (x >= most) break;
         uint64_t u[H], v[H];
         if constexpr (kStages > 0) st.read(here + x * S::kBytes, ra[x], rb[x]);
         unpack<kF32, kInter>(ra[x], rb[x], u, v);
@@ -488,8 +502,10 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
       st.template there<kStages - 1>();
       const uint8_t* here = staged + stage * kHeads * 2 * S::kBytes;
       stage = stage + 1 == kStages ? 0 : stage + 1;
+      const int most = __reduce_max_sync(~0u, heads - h0);
 #pragma unroll
       for (int x = 0; x < kHeads; ++x) {
+        if (x >= most) break;
         uint64_t u[H], v[H], gu[H], gv[H];
         uint4 ia, ib;
         st.read(here + x * 2 * S::kBytes, ia, ib);
