@@ -23,7 +23,7 @@
 // the blocks, all in a fixed order: the same call gives the same bits.
 //
 // Measured (GPU time, inputs larger than L2): [1, 32768, 32 + 8, 128] bf16 forward 110 us (6.1 TB/s), with its gradient
-// 288 us (5.8 TB/s; a copy reaches 6.7), 290 interleaved; interleaved without the norm 103 us (6.5 TB/s). [1, 16384, 16 + 16,
+// 286 us (5.9 TB/s; a copy reaches 6.7), interleaved too; interleaved without the norm 103 us (6.5 TB/s). [1, 16384, 16 + 16,
 // 128] f32 85 and 216 us (6.3, 6.2 TB/s). 256 tokens of 32 + 8 heads: 4.9 us, the host takes 7.5
 #include <type_traits>
 
@@ -45,7 +45,7 @@ constexpr int kSmThreads = 1280;
 constexpr int kMaxD = 2 * kRopeMaxPairs;
 // Heads of a chunk. Forward: 2 heads three stages deep 111.5 us for [1, 32768, 32 + 8, 128] bf16 (now 110), 2 and 8 with loads
 // into registers 131 and 127 us; 6 blocks to an SM 123 us. Backward: 1 head three or four stages deep 2-4% slower; 3 or 5
-// blocks to an SM 318 and 350 us for the training step (now 288).
+// blocks to an SM 318 and 350 us for the training step (now 286).
 constexpr int kFwdHeads = 4, kFwdStages = 2;
 constexpr int kBwdHeads = 2, kBwdStages = 2, kBwdBlocks = 4;
 
