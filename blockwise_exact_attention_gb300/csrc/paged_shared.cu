@@ -68,6 +68,9 @@ constexpr int kThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch, "register split");
 constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
+// The sum of weights of a part without keys, whose O is not written. (Of keys without a maximum it is 0 or NaN, and NaN belongs
+// to the result.)
+constexpr float kNoKeys = -1.f;
 constexpr float kRescale = 8.f;  // log2: O is rescaled only when a maximum grows by more
 constexpr uint32_t kPReadyBar = 1, kPReadyThreads = 128 + 32, kBothBar = 3;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -692,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- this half's part, each thread its row, whole 32-byte sectors of it at a time ----
       const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
       const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows) + r;
-      if (ok && r < rows) p.ml[part] = make_float2(m_ref, l_sum);
+      if (ok && r < rows) p.ml[part] = make_float2(m_ref, n > 0 ? l_sum : kNoKeys);
       if (n > 0) {
         if (ok) ok = warp_wait_parity(&o_full[t], done & 1, abort_flag, p.status);
         ++done;
@@ -773,7 +776,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kBatch == 4 ? 8 : 1) shared_j
   const int mine = (parts - turn + kSplit - 1) / kSplit;
   for (int i0 = 0; i0 < mine; i0 += 32) {
     const int n = min(32, mine - i0);
-    const float2 e = lane < n ? *ml_of((i0 + lane) * kSplit + turn) : make_float2(-INFINITY, 0.f);
+    const float2 e = lane < n ? *ml_of((i0 + lane) * kSplit + turn) : make_float2(-INFINITY, kNoKeys);
+    const bool keys = e.y != kNoKeys;
     float w = 0.f;
     for (int i1 = 0; i1 < n; i1 += kBatch) {
       float y[kBatch][N];
@@ -798,8 +802,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kBatch == 4 ? 8 : 1) shared_j
         for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
         m = fmaxf(m, top);
         const float ref = m == -INFINITY ? 0.f : m, old = top == -INFINITY ? 0.f : ex2_approx(top - ref);
-        w = e.x == -INFINITY ? 0.f : ex2_approx(e.x - ref);
-        float l = e.x == -INFINITY ? 0.f : w * e.y;
+        w = ex2_approx(e.x - ref);  // 0 where there is no maximum
+        float l = keys ? w * e.y : 0.f;
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
         sum = sum * old + l;
@@ -810,7 +814,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kBatch == 4 ? 8 : 1) shared_j
 #pragma unroll
       for (int z = 0; z < kBatch; ++z) {
         const float g1 = __shfl_sync(~0u, w, (i1 + z) & 31);
-        const bool there = __shfl_sync(~0u, e.x, (i1 + z) & 31) != -INFINITY && i1 + z < n;  // a part without keys has no O
+        const bool there = __shfl_sync(~0u, keys, (i1 + z) & 31) && i1 + z < n;
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] = there ? fmaf(g1, y[z][j], o[j]) : o[j];
       }
