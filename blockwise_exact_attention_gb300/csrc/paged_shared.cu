@@ -24,13 +24,14 @@
 // both have the same rows and take the tiles in turn, which keeps the tensor core and
 // the exponentials overlapped, and each half writes its own part.
 //
-// P enters the second product rounded to bf16 for a bf16 output, as in the forward:
-// off by up to 2^-9 of each weight, on average as much as the output's own rounding.
-// For an f32 output it goes in as two bf16 terms, 16 bits of it (cut off, then the
-// rest rounded; P's last bit is set, so that something is left of it and an infinite
-// value stays infinite). Twice the products of P V and half as many instructions again:
-// 64 requests behind 32k keys 61.3 and 75.2 us, 256 behind 16k 97 and 119 us, 96 in
-// three groups 69.7 and 73.2 us. The sums of weights are in fp32 either way.
+// P enters the second product as two bf16 terms, 16 bits of it (cut off, then the rest
+// rounded; P's last bit is set, so that something is left of it and an infinite value
+// stays infinite). One rounded term, as in the forward, is off by up to 2^-8 of each
+// weight, on average as much as a bf16 output's own rounding (0.0024 of its size against
+// fp64, 0.0017 with two), and takes 64 requests behind 32k keys from 75.2 to 61.3 us, 256
+// behind 16k from 119 to 97, 96 in three groups from 73.2 to 69.7: paged_decode's weights
+// have all their bits, and a call that takes its place gives the same. The sums of weights
+// are in fp32.
 //
 // Order of the launches: the setup, which finds what each group shares; the rest's
 // kernel; the prefix; the join. The prefix kernel waits for nothing when it starts: it
@@ -335,8 +336,7 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
 
 // ---- the prefix --------------------------------------------------------------------
 
-// kTerms: bf16 terms of P in the second product.
-template <int D, int kTerms>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_prefix_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__ Args p) {
   using C = Cfg<D>;
@@ -512,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t vd = sdesc_add(v_desc, s * C::kTileBytes);
 #pragma unroll
-          for (int term = kTerms - 1; term >= 0; --term)  // small terms first
+          for (int term = 1; term >= 0; --term)  // small terms first
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
               umma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + term * 64 + k * 8, sdesc_add(vd, k * 2048), C::kIdescPV,
-                           term < kTerms - 1 || k > 0 || x > 0 ? 1u : 0u);
+                           term == 0 || k > 0 || x > 0 ? 1u : 0u);
           if (!sg.two || t == 1) umma_commit_warp(&v_empty[s]);
           if (x == n - 1) umma_commit_warp(&o_full[t]);
         };
@@ -640,22 +640,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = 64 * hf + 2 * c;
             const uint64_t a = f2_fma(f2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2, nm2);
             float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
-            if constexpr (kTerms == 1) {
-              ps[c & 3] = f2_add(ps[c & 3], f2(p0, p1));
-              hi[c] = pack_bf16x2(p0, p1);
-            } else {
-              // the last bit set, so that something is left behind the first term
-              p0 = __uint_as_float(__float_as_uint(p0) | 1u), p1 = __uint_as_float(__float_as_uint(p1) | 1u);
-              ps[c & 3] = f2_add(ps[c & 3], f2(p0, p1));
-              hi[c] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-              // less the first term: its 8 bits, with the sign of a subtraction
-              const uint64_t rest = f2_add(f2(p0, p1), f2(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) | 0x80000000u),
-                                                          __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) | 0x80000000u)));
-              lo[c] = pack_bf16x2(f2_lo(rest), f2_hi(rest));
-            }
+            // the last bit set, so that something is left behind the first term
+            p0 = __uint_as_float(__float_as_uint(p0) | 1u), p1 = __uint_as_float(__float_as_uint(p1) | 1u);
+            ps[c & 3] = f2_add(ps[c & 3], f2(p0, p1));
+            hi[c] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+            // less the first term: its 8 bits, with the sign of a subtraction
+            const uint64_t rest = f2_add(f2(p0, p1), f2(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) | 0x80000000u),
+                                                        __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) | 0x80000000u)));
+            lo[c] = pack_bf16x2(f2_lo(rest), f2_hi(rest));
           }
           tmem_st32(s_tmem + 32 * hf, hi);
-          if constexpr (kTerms == 2) tmem_st32(s_tmem + 64 + 32 * hf, lo);
+          tmem_st32(s_tmem + 64 + 32 * hf, lo);
         }
         const uint64_t s2 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
         l_sum += f2_lo(s2) + f2_hi(s2);
@@ -859,7 +854,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kBatch == 4 ? 8 : 1) shared_j
   }
 }
 
-template <int D, int kTerms>
+template <int D>
 cudaError_t launch(const PagedSharedParams& p, const PageMaps& maps, cudaStream_t s, int* nlaunch) {
   using C = Cfg<D>;
   struct Facts {
@@ -869,10 +864,10 @@ cudaError_t launch(const PagedSharedParams& p, const PageMaps& maps, cudaStream_
   Facts f{};
   cudaError_t e = cache.get(
       [](Facts* v) {
-        cudaError_t r = cudaFuncSetAttribute(shared_prefix_kernel<D, kTerms>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaError_t r = cudaFuncSetAttribute(shared_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (r != cudaSuccess) return r;
         cudaFuncAttributes fa;
-        if ((r = cudaFuncGetAttributes(&fa, shared_prefix_kernel<D, kTerms>)) != cudaSuccess) return r;
+        if ((r = cudaFuncGetAttributes(&fa, shared_prefix_kernel<D>)) != cudaSuccess) return r;
         v->regs = fa.numRegs;
         if ((r = device_sm_count(&v->ctas)) != cudaSuccess) return r;
         if (v->ctas > kMaxCtas) v->ctas = kMaxCtas;
@@ -921,7 +916,7 @@ cudaError_t launch(const PagedSharedParams& p, const PageMaps& maps, cudaStream_
   own.lse = Lse3{reinterpret_cast<float*>(ws + w.suffix_lse), d.h, 1};
   own.ws = ws + w.decode;
   if ((e = launch_paged_decode_rest(own, s, nlaunch)) != cudaSuccess) return e;
-  if ((e = launch_dependent(shared_prefix_kernel<D, kTerms>, dim3(f.ctas), kThreads, C::kSmem, s, maps, a)) != cudaSuccess) return e;
+  if ((e = launch_dependent(shared_prefix_kernel<D>, dim3(f.ctas), kThreads, C::kSmem, s, maps, a)) != cudaSuccess) return e;
   *nlaunch += 1;
   const int64_t items = (int64_t)d.n * d.h;
   // Rows that do not fill the GPU have many parts each, four warps a row then; where there are warps enough to hide the
@@ -969,9 +964,7 @@ bool paged_shared_fits(int64_t n, int64_t h, int64_t h_kv, int64_t max_keys, int
 }
 
 cudaError_t launch_paged_shared(const PagedSharedParams& p, const PageMaps& maps, cudaStream_t s, int* nlaunch) {
-  if (p.d.out_is_f32)
-    return p.d.d == 64 ? launch<64, 2>(p, maps, s, nlaunch) : launch<128, 2>(p, maps, s, nlaunch);
-  return p.d.d == 64 ? launch<64, 1>(p, maps, s, nlaunch) : launch<128, 1>(p, maps, s, nlaunch);
+  return p.d.d == 64 ? launch<64>(p, maps, s, nlaunch) : launch<128>(p, maps, s, nlaunch);
 }
 
 }  // namespace bea

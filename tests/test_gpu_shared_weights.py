@@ -1,0 +1,69 @@
+"""The softmax weights of shared keys in paged_decode_shared, and their sums.
+
+One weight: of the shared keys the first has score 0 and value 0, the last score -x and value 1, x another one for
+each request, and all others weight 0. So the output is w = p / (1 + p), p = exp(-x), and what is lost of one weight
+shows in full. u = 2^-23. The weight enters the matrix product as two bf16 terms: the first is cut off to 8 bits, the
+rest, below 2^-7 of p, is rounded to 8 bits: off by 2^-15 of p at most; the last bit that is set adds u. The exponent's
+two roundings are u x in p at most, the exponential 2 u, the sum 1 + p, its bits that are set, its reciprocal, the last
+product and joining the parts a few u more:
+  |out - w| <= w (2^-15 + u (x + 20)).
+A bf16 output is that rounded once more, half a step of it, 2^-8."""
+
+import math
+
+import numpy as np
+import pytest
+
+from test_gpu_paged_shared import BF16, F32, i32, make, run
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -23
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__ as g
+    g.build()
+
+
+@pytest.mark.parametrize("apart", [100, 3000])
+@pytest.mark.parametrize("n,h,d", [(9, 3, 64), (200, 1, 128), (70, 8, 128)])
+def test_one_weight(n, h, d, apart):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n + d)
+    x = (4 * torch.rand((n, h), device="cuda", generator=g)).to(BF16)
+    page, length = 128, -(-(apart + 2) // 128) * 128
+    k = torch.zeros((length // page + 1, page, 1, d), dtype=BF16, device="cuda")
+    v = torch.zeros_like(k)
+    k[..., 1] = -2.0 ** 30                              # weight 0
+    flat = k.view(-1, d)
+    flat[0, 1] = flat[apart + 1, 1] = 0
+    flat[apart + 1, 0] = -1
+    v.view(-1, d)[apart + 1] = 1
+    q = torch.zeros((n, 1, h, d), dtype=BF16, device="cuda")
+    q[:, 0, :, 0], q[..., 1] = x, 1
+    width = 97_000_000 // (d * 4 * page * (n - 1)) + length // page + 2
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    table[:, :length // page + 1] = torch.arange(length // page + 1, device="cuda")
+    args = (q, k, v, table, i32([length + 1] * n)), (i32([0, n]), i32([length]))
+    x = x.double().cpu().numpy()[:, None, :, None]
+    w = np.exp(-x) / (1 + np.exp(-x))
+    tol = w * (2.0 ** -15 + U * (x + 20))
+    out32, lse = run(*args, 1.0, out_dtype=F32)
+    err = np.abs(out32.double().cpu().numpy() - w)
+    assert (err <= tol).all(), (err / tol).max()
+    out, lse16 = run(*args, 1.0)
+    err = np.abs(out.double().cpu().numpy() - w)
+    assert (err <= tol + 2.0 ** -8 * (w + tol)).all(), (err / w).max()
+    assert torch.equal(out, out32.to(BF16)) and torch.equal(lse16, lse)
+
+
+@pytest.mark.parametrize("h,h_kv,d", [(8, 2, 64), (7, 1, 128), (40, 2, 128)])
+def test_a_bf16_output_is_the_rounded_f32_one(h, h_kv, d):
+    """Up to eight tiles of a run, that is; behind them the two are summed in other pieces."""
+    x, g = make([(700, [1, 0, 17, None, 300, 31, 2]), (256, [4] * 40)], h, h_kv, d, 16, seed=h + d, qscale=4.0)
+    out, lse = run(x, g, 0.1)
+    out32, lse32 = run(x, g, 0.1, out_dtype=F32)
+    assert torch.equal(out, out32.to(BF16)) and torch.equal(lse, lse32)
