@@ -31,7 +31,7 @@
 // fp64, 0.0017 with two), and takes 64 requests behind 32k keys from 75.2 to 61.3 us, 256
 // behind 16k from 119 to 97, 96 in three groups from 73.2 to 69.7: paged_decode's weights
 // have all their bits, and a call that takes its place gives the same. The sums of weights
-// are in fp32.
+// are in fp32, those of P V in the tensor core's accumulator for some tiles and in fp32 above.
 //
 // Order of the launches: the setup, which finds what each group shares; the rest's
 // kernel; the prefix; the join. The prefix kernel waits for nothing when it starts: it
@@ -81,6 +81,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kLeastUnitCost = 2, kMostUnitCost = 5;
 // A run's cut is moved by up to so many steps (and a quarter of a run) to a unit's border.
 constexpr int kSnap = 2;
+// Tiles that are summed in one accumulator before it joins the part in memory, in fp32: the tensor core cuts off what it adds up.
+// (Values of 1, runs of 216 tiles: one accumulator 1.5e-4 low, 612 us; 64 tiles 4.1e-5, 614 us; 32 1.8e-5, 636 us; 16 7e-6, 695
+// us; 8 2.3e-6, 779 us; one 4e-8, 2262 us. A weight is off by up to 3e-5, a bf16 output by 4e-3.)
+constexpr int kFlushF32 = 16, kFlushBf16 = 64;
 
 template <int D>
 struct Cfg {
@@ -254,6 +258,7 @@ struct Args {
   Seq4 q, out;
   Lse3 lse;
   int out_is_f32;
+  int flush;  // tiles that are summed in one accumulator, less 1; a power of two of them
   float sl2;
   int* skip;
   Group* group;
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
               umma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + term * 64 + k * 8, sdesc_add(vd, k * 2048), C::kIdescPV,
-                           term == 0 || k > 0 || x > 0 ? 1u : 0u);
+                           term == 0 || k > 0 || (x & p.flush) != 0 ? 1u : 0u);
           if (!sg.two || t == 1) umma_commit_warp(&v_empty[s]);
           if (x == n - 1) umma_commit_warp(&o_full[t]);
         };
@@ -578,6 +583,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     };
+    // This half's part, each thread its row, whole 32-byte sectors of it at a time: what the accumulator holds, and f times what
+    // has been written of it.
+    auto write_part = [&](bool more, float f) {
+      const int rows = unit.two ? min(kTile, unit.rows - t * kTile) : unit.rows;  // of this half
+      float* to = p.o + ((int64_t)kUnitRows * cta + unit.part + t * (unit.two ? kTile : unit.rows) + r) * D;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 64) {
+        uint32_t orow[64];
+        tmem_ld32(o_tmem + c0, orow);
+        tmem_ld32(o_tmem + c0 + 32, orow + 32);
+        tmem_wait_ld();
+        reg_fence<64>(orow);
+        if (r < rows) {
+          if (more) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float4 y = *reinterpret_cast<const float4*>(to + c0 + 4 * k);
+              uint32_t* x = orow + 4 * k;
+              x[0] = __float_as_uint(fmaf(y.x, f, __uint_as_float(x[0])));
+              x[1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(x[1])));
+              x[2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(x[2])));
+              x[3] = __float_as_uint(fmaf(y.w, f, __uint_as_float(x[3])));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) store_sector(to + c0 + 8 * k, orow + 8 * k);
+        }
+        __syncwarp();
+      }
+    };
     if (run0 < first.run1) {
       copy_queries(first.seg);
       queries_there();
@@ -591,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) unit = begun;
         __syncwarp();
       }
-      float m_ref = -INFINITY, l_sum = 0.f;
+      float m_ref = -INFINITY, l_sum = 0.f, m_kept = 0.f;  // m_kept: the maximum that the part written so far goes by
+      auto kept = [&]() { return m_kept == m_ref ? 1.f : ex2_approx(m_kept - m_ref); };
       for (int x = 0; x < n; ++x, ++met) {
         if (ok) ok = warp_wait_parity(&s_full[t], met & 1, abort_flag, p.status);
         if (!ok) {
@@ -599,6 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
+        if (x > 0 && (x & p.flush) == 0) {  // S of this tile came behind the products before it
+          write_part(x > p.flush + 1, kept());
+          m_kept = m_ref;
+        }
         uint32_t sr[128];
         tmem_ld32(s_tmem, sr);
         tmem_ld32(s_tmem + 32, sr + 32);
@@ -622,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x == 0) {
           m_ref = m_new;  // the first product overwrites O
         } else {
-          rescale = __any_sync(~0u, grow);
+          rescale = __any_sync(~0u, grow) && (x & p.flush) != 0;  // else the next product overwrites O too
           if (grow) {
             f = ex2_approx(m_ref - m_new);
             m_ref = m_new;
@@ -687,7 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (more) queries_there();
-      // ---- this half's part, each thread its row, whole 32-byte sectors of it at a time ----
       const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
       const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows) + r;
       if (ok && r < rows) p.ml[part] = make_float2(m_ref, n > 0 ? l_sum : kNoKeys);
@@ -695,20 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = warp_wait_parity(&o_full[t], done & 1, abort_flag, p.status);
         ++done;
         tc_fence_after();
-        if (ok) {
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 64) {
-            uint32_t orow[64];
-            tmem_ld32(o_tmem + c0, orow);
-            tmem_ld32(o_tmem + c0 + 32, orow + 32);
-            tmem_wait_ld();
-            reg_fence<64>(orow);
-            if (r < rows) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) store_sector(p.o + part * D + c0 + 8 * k, orow + 8 * k);
-            }
-          }
-        }
+        if (ok) write_part(n > p.flush + 1, kept());
         tc_fence_before();
       }
     }
@@ -891,6 +917,7 @@ cudaError_t launch(const PagedSharedParams& p, const PageMaps& maps, cudaStream_
   a.table_stride = d.table_stride;
   a.q = d.q, a.out = d.out, a.lse = d.lse;
   a.out_is_f32 = d.out_is_f32;
+  a.flush = (d.out_is_f32 ? kFlushF32 : kFlushBf16) - 1;
   a.sl2 = d.scale * kLog2e;
   a.skip = reinterpret_cast<int*>(ws + w.skip);
   a.group = reinterpret_cast<Group*>(ws + w.groups);

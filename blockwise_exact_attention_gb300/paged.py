@@ -88,7 +88,7 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, lens, group_rows, shar
 
     In the product with the values weights of shared keys have 16 bits, where
     ``paged_decode``'s have 24: a bf16 output is as exact, a float32 one is within
-    2**-15 of sum(p |v|)."""
+    2**-14 of sum(p |v|)."""
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(q.shape[-1])
     if out_dtype is not None and out_dtype not in (q.dtype, torch.float32):

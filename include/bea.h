@@ -512,9 +512,10 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
  * table has no room for 96 MB of keys and values that sharing could save, the
  * groups are not looked at: the call is bea_paged_decode, which is then faster.
  * groups <= 1024. Results are those of bea_paged_decode up to rounding: in the
- * product with the values weights of the shared keys have 16 bits. group_rows out
- * of order or range: nothing is shared, and reported; a negative shared_lens counts
- * as 0 and is reported; the rest as bea_paged_decode reports it. (2 h n + 40960 <
+ * product with the values weights of the shared keys have 16 bits, and an f32 out is
+ * within 2^-14 of sum(p |v|), however many they are. group_rows out of order or
+ * range: nothing is shared, and reported; a negative shared_lens counts as 0 and is
+ * reported; the rest as bea_paged_decode reports it. (2 h n + 40960 <
  * 2^31, and h_kv (n h / h_kv / 256 + min(groups, n)) (max_keys / 128 + 6) < 2^31, else
  * BEA_ERR_SHAPE.)
  */

@@ -67,3 +67,27 @@ def test_a_bf16_output_is_the_rounded_f32_one(h, h_kv, d):
     out, lse = run(x, g, 0.1)
     out32, lse32 = run(x, g, 0.1, out_dtype=F32)
     assert torch.equal(out, out32.to(BF16)) and torch.equal(lse, lse32)
+
+
+@pytest.mark.parametrize("n,h,h_kv,d,keys", [(256, 64, 2, 128, 65536), (256, 64, 2, 64, 65536), (64, 32, 8, 128, 16384)])
+def test_long_sums(n, h, h_kv, d, keys):
+    """Values of 1, whose output is 1, in units that a CTA follows over up to 216 tiles. 16 tiles of 2 * 8 products are
+    added up by the tensor core, which may cut off a unit of 2^-23 of its sum in each: of a sum that grows evenly half
+    of 256 units, 2^-16. What the weights lose is as often up as down, of 16384 keys and more together 6 * 2^-15 / sqrt(3) *
+    1.2 / 128 at most (six standard deviations; scores of a standard deviation of 0.6), below 2^-19; so are the sums of
+    weights, up to 216 roundings to nearest, and the parts' pieces and merges."""
+    import blockwise_exact_attention_gb300 as bea
+    g = torch.Generator(device="cuda")
+    g.manual_seed(h + d)
+    page = 128
+    k = torch.randn((keys // page, page, h_kv, d), device="cuda", generator=g).to(BF16)
+    q = (0.57 / (0.1 * math.sqrt(d)) * torch.randn((n, 1, h, d), device="cuda", generator=g)).to(BF16)
+    table = torch.arange(keys // page, dtype=torch.int32, device="cuda").repeat(n, 1)
+    x = (q, k, torch.ones_like(k), table, i32([keys] * n))
+    out, lse = run(x, (i32([0, n]), i32([keys])), 0.1, out_dtype=F32)
+    assert (out.double() - 1).abs().max() <= 2.0 ** -16 + 3 * 2.0 ** -19
+    # lse, about 11: its sum as above, itself rounded three times
+    want = bea.paged_decode(*(t[:2] if t.shape[0] == n else t for t in x), 0.1, out_dtype=F32)
+    assert (lse[:2] - want[1]).abs().max() <= 2.0 ** -18
+    out16, lse16 = run(x, (i32([0, n]), i32([keys])), 0.1)
+    assert (out16 == 1).all() and torch.equal(lse16, lse)
