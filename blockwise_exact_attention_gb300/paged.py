@@ -202,7 +202,7 @@ class PagedKVCache:
     def _caches(self, caches, copies):
         """What a step copies in, refused before the step where ``paged_copy`` would refuse it behind it."""
         if caches is None:
-            return [self.k, self.v]
+            return paged_copy(copies[:0], [self.k, self.v])
         for c in caches:
             if c.shape[:2] != self.k.shape[:2]:
                 raise ValueError(f"a cache of shape {tuple(c.shape)} beside one of {self.k.shape[0]} pages of {self.page_size} "
