@@ -187,11 +187,13 @@ class PagedKVCache:
         """``paged_plan`` on this cache, its lengths and stack updated in place.
         Where pages are shared, the rows that end (-1) are freed first, also if the
         plan then refuses the rest."""
-        if self.shares is not None:
-            self.free(new_lens)
+        if not 0 <= capacity < 2**31:
+            raise ValueError(f"capacity {capacity}")
         n, dev = self.lens.shape[0], self.lens.device
         slots, positions, cu_new, cu_pages = torch.empty(2 * (capacity + n + 1), dtype=torch.int32, device=dev).split(
             (capacity, capacity, n + 1, n + 1))
+        if self.shares is not None:
+            self.free(new_lens)
         return paged_plan(self.lens, new_lens, self.block_table, self.free_pages, self.n_free, self.page_size, capacity,
                           PagedPlan(slots, positions, cu_new, cu_pages, self.lens, self.n_free))
 

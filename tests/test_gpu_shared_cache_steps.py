@@ -45,3 +45,17 @@ def test_pages_that_cannot_be_copied():
         with pytest.raises(bea._lib.BeaError, match="ARG"):
             step()
         assert unchanged(cache, before)
+
+
+def test_a_capacity_that_is_none():
+    """The rows that end are not freed by a plan that raises."""
+    import blockwise_exact_attention_gb300 as bea
+    cache = bea.PagedKVCache(12, 4, 1, 64, 4, 16, share_pages=True)
+    cache.plan(i32([5, 9, 0, 0]), 14)
+    before = state(cache)
+    for capacity in (-1, -100, 2.5, None, "many", 2 ** 62):
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            cache.plan(i32([-1, 1, 0, 0]), capacity)
+        assert unchanged(cache, before), capacity
+    plan = cache.plan(i32([-1, 1, 0, 0]), 1)
+    assert plan.lens.tolist() == [0, 10, 0, 0] and cache.n_free.item() == 9
