@@ -82,8 +82,8 @@ constexpr int kLeastUnitCost = 2, kMostUnitCost = 5;
 // A run's cut is moved by up to so many steps (and a quarter of a run) to a unit's border.
 constexpr int kSnap = 2;
 // Tiles that are summed in one accumulator before it joins the part in memory, in fp32: the tensor core cuts off what it adds up.
-// (Values of 1, runs of 216 tiles: one accumulator 1.5e-4 low, 612 us; 64 tiles 4.1e-5, 614 us; 32 1.8e-5, 636 us; 16 7e-6, 695
-// us; 8 2.3e-6, 779 us; one 4e-8, 2262 us. A weight is off by up to 3e-5, a bf16 output by 4e-3.)
+// Values of 1, runs of 216 tiles: one accumulator 1.5e-4 low, 526 us; 64 tiles 4.1e-5, 554 us; 16 7e-6, 640 us. A weight is off by
+// up to 3e-5, a bf16 output by 4e-3.
 constexpr int kFlushF32 = 16, kFlushBf16 = 64;
 
 template <int D>
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + term * 64 + k * 8, sdesc_add(vd, k * 2048), C::kIdescPV,
                            term == 0 || k > 0 || (x & p.flush) != 0 ? 1u : 0u);
           if (!sg.two || t == 1) umma_commit_warp(&v_empty[s]);
-          if (x == n - 1) umma_commit_warp(&o_full[t]);
+          if (x == n - 1 || (x & p.flush) == p.flush) umma_commit_warp(&o_full[t]);
         };
         if (ok) ok = warp_wait_parity(q_full, seg & 1, abort_flag, p.status);
         const int n1 = sg.count(1);
@@ -583,36 +583,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(q_full);
     };
-    // This half's part, each thread its row, whole 32-byte sectors of it at a time: what the accumulator holds, and f times what
-    // has been written of it.
-    auto write_part = [&](bool more, float f) {
-      const int rows = unit.two ? min(kTile, unit.rows - t * kTile) : unit.rows;  // of this half
-      float* to = p.o + ((int64_t)kUnitRows * cta + unit.part + t * (unit.two ? kTile : unit.rows) + r) * D;
-#pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 64) {
-        uint32_t orow[64];
-        tmem_ld32(o_tmem + c0, orow);
-        tmem_ld32(o_tmem + c0 + 32, orow + 32);
-        tmem_wait_ld();
-        reg_fence<64>(orow);
-        if (r < rows) {
-          if (more) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float4 y = *reinterpret_cast<const float4*>(to + c0 + 4 * k);
-              uint32_t* x = orow + 4 * k;
-              x[0] = __float_as_uint(fmaf(y.x, f, __uint_as_float(x[0])));
-              x[1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(x[1])));
-              x[2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(x[2])));
-              x[3] = __float_as_uint(fmaf(y.w, f, __uint_as_float(x[3])));
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) store_sector(to + c0 + 8 * k, orow + 8 * k);
-        }
-        __syncwarp();
-      }
-    };
     if (run0 < first.run1) {
       copy_queries(first.seg);
       queries_there();
@@ -626,117 +596,152 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) unit = begun;
         __syncwarp();
       }
-      float m_ref = -INFINITY, l_sum = 0.f, m_kept = 0.f;  // m_kept: the maximum that the part written so far goes by
-      auto kept = [&]() { return m_kept == m_ref ? 1.f : ex2_approx(m_kept - m_ref); };
-      for (int x = 0; x < n; ++x, ++met) {
-        if (ok) ok = warp_wait_parity(&s_full[t], met & 1, abort_flag, p.status);
-        if (!ok) {
-          named_bar_sync(kPReadyBar + t, kPReadyThreads);  // aborted: the phases stay matched
-          continue;
-        }
-        tc_fence_after();
-        if (x > 0 && (x & p.flush) == 0) {  // S of this tile came behind the products before it
-          write_part(x > p.flush + 1, kept());
-          m_kept = m_ref;
-        }
-        uint32_t sr[128];
-        tmem_ld32(s_tmem, sr);
-        tmem_ld32(s_tmem + 32, sr + 32);
-        tmem_ld32(s_tmem + 64, sr + 64);
-        tmem_ld32(s_tmem + 96, sr + 96);
-        tmem_wait_ld();
-        reg_fence<128>(sr);
-        float m8[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          float m = fmax3(__uint_as_float(sr[u]), __uint_as_float(sr[u + 8]), __uint_as_float(sr[u + 16]));
-#pragma unroll
-          for (int k = 3; k < 15; k += 2) m = fmax3(m, __uint_as_float(sr[u + 8 * k]), __uint_as_float(sr[u + 8 * k + 8]));
-          m8[u] = fmaxf(m, __uint_as_float(sr[u + 120]));
-        }
-        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * p.sl2;
-        const float m_new = fmaxf(m_ref, mx);
-        const bool grow = m_new > m_ref + kRescale;
-        float f = 1.f;
-        bool rescale = false;
-        if (x == 0) {
-          m_ref = m_new;  // the first product overwrites O
-        } else {
-          rescale = __any_sync(~0u, grow) && (x & p.flush) != 0;  // else the next product overwrites O too
-          if (grow) {
-            f = ex2_approx(m_ref - m_new);
-            m_ref = m_new;
-            l_sum *= f;
+      float m_ref = -INFINITY, l_sum = 0.f;
+      int x = 0;
+      do {
+        const int end = min(n, x + p.flush + 1);
+        for (; x < end; ++x, ++met) {
+          if (ok) ok = warp_wait_parity(&s_full[t], met & 1, abort_flag, p.status);
+          if (!ok) {
+            named_bar_sync(kPReadyBar + t, kPReadyThreads);  // aborted: the phases stay matched
+            continue;
           }
-        }
-        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t sl2 = f2(p.sl2, p.sl2), nm2 = f2(neg_m, neg_m);
-        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+          tc_fence_after();
+          uint32_t sr[128];
+          tmem_ld32(s_tmem, sr);
+          tmem_ld32(s_tmem + 32, sr + 32);
+          tmem_ld32(s_tmem + 64, sr + 64);
+          tmem_ld32(s_tmem + 96, sr + 96);
+          tmem_wait_ld();
+          reg_fence<128>(sr);
+          float m8[8];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t hi[32], lo[32];
+          for (int u = 0; u < 8; ++u) {
+            float m = fmax3(__uint_as_float(sr[u]), __uint_as_float(sr[u + 8]), __uint_as_float(sr[u + 16]));
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int e = 64 * hf + 2 * c;
-            const uint64_t a = f2_fma(f2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2, nm2);
-            float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
-            // the last bit set, so that something is left behind the first term
-            p0 = __uint_as_float(__float_as_uint(p0) | 1u), p1 = __uint_as_float(__float_as_uint(p1) | 1u);
-            ps[c & 3] = f2_add(ps[c & 3], f2(p0, p1));
-            hi[c] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-            // less the first term: its 8 bits, with the sign of a subtraction
-            const uint64_t rest = f2_add(f2(p0, p1), f2(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) | 0x80000000u),
-                                                        __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) | 0x80000000u)));
-            lo[c] = pack_bf16x2(f2_lo(rest), f2_hi(rest));
+            for (int k = 3; k < 15; k += 2) m = fmax3(m, __uint_as_float(sr[u + 8 * k]), __uint_as_float(sr[u + 8 * k + 8]));
+            m8[u] = fmaxf(m, __uint_as_float(sr[u + 120]));
           }
-          tmem_st32(s_tmem + 32 * hf, hi);
-          tmem_st32(s_tmem + 64 + 32 * hf, lo);
-        }
-        const uint64_t s2 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
-        l_sum += f2_lo(s2) + f2_hi(s2);
-        if (rescale) {
+          const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * p.sl2;
+          const float m_new = fmaxf(m_ref, mx);
+          const bool grow = m_new > m_ref + kRescale;
+          float f = 1.f;
+          bool rescale = false;
+          if (x == 0) {
+            m_ref = m_new;  // the first product overwrites O
+          } else {
+            rescale = __any_sync(~0u, grow) && (x & p.flush) != 0;  // else the next product overwrites O too
+            if (grow) {
+              f = ex2_approx(m_ref - m_new);
+              m_ref = m_new;
+              l_sum *= f;
+            }
+          }
+          const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+          const uint64_t sl2 = f2(p.sl2, p.sl2), nm2 = f2(neg_m, neg_m);
+          uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t hi[32], lo[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int e = 64 * hf + 2 * c;
+              const uint64_t a = f2_fma(f2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2, nm2);
+              float p0 = ex2_approx(f2_lo(a)), p1 = ex2_approx(f2_hi(a));
+              // the last bit set, so that something is left behind the first term
+              p0 = __uint_as_float(__float_as_uint(p0) | 1u), p1 = __uint_as_float(__float_as_uint(p1) | 1u);
+              ps[c & 3] = f2_add(ps[c & 3], f2(p0, p1));
+              hi[c] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+              // less the first term: its 8 bits, with the sign of a subtraction
+              const uint64_t rest = f2_add(f2(p0, p1), f2(__uint_as_float((__float_as_uint(p0) & 0xFFFF0000u) | 0x80000000u),
+                                                          __uint_as_float((__float_as_uint(p1) & 0xFFFF0000u) | 0x80000000u)));
+              lo[c] = pack_bf16x2(f2_lo(rest), f2_hi(rest));
+            }
+            tmem_st32(s_tmem + 32 * hf, hi);
+            tmem_st32(s_tmem + 64 + 32 * hf, lo);
+          }
+          const uint64_t s2 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
+          l_sum += f2_lo(s2) + f2_hi(s2);
+          if (rescale) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t orow[32];
-            tmem_ld32(o_tmem + c0, orow);
-            tmem_wait_ld();
-            reg_fence<32>(orow);
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t orow[32];
+              tmem_ld32(o_tmem + c0, orow);
+              tmem_wait_ld();
+              reg_fence<32>(orow);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) orow[c] = __float_as_uint(__uint_as_float(orow[c]) * f);
-            tmem_st32(o_tmem + c0, orow);
+              for (int c = 0; c < 32; ++c) orow[c] = __float_as_uint(__uint_as_float(orow[c]) * f);
+              tmem_st32(o_tmem + c0, orow);
+            }
           }
+          tmem_wait_st();
+          tc_fence_before();
+          named_bar_sync(kPReadyBar + t, kPReadyThreads);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        named_bar_sync(kPReadyBar + t, kPReadyThreads);
-      }
-      const Seg sg = unit;
-      // Both halves have met the unit's last S: the next one's queries may take the place of its queries, and their S
-      // products run while this unit's parts are written.
-      const bool more = v < first.run1;
-      if (more) {
-        named_bar_sync(kBothBar, 256);
-        copy_queries(unit_at(v));
-      }
-      if (sg.a == 0) {
-        // for the kernel that joins: each row's first part, the parts' number, and the second half's distance
-        const int parts = (schedule().cta_of(sg.last) - cta + 1) * (sg.two ? 1 : 2);
-        for (int i = threadIdx.x; i < sg.rows; i += 256) {
-          const int qr = sg.q0 + i, b = qr / heads, hh = sg.hk * heads + (qr - b * heads);
-          p.row[(int64_t)(sg.g.row0 + b) * p.h + hh] = make_int4(kUnitRows * cta + sg.part + i, parts, sg.two ? 0 : sg.rows, 0);
+        const Seg sg = unit;
+        const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
+        const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows) + r;
+        if (x == n) {
+          // Both halves have met the unit's last S: the next one's queries may take the place of its queries, and their S
+          // products run while this unit's parts are written.
+          const bool more = v < first.run1;
+          if (more) {
+            named_bar_sync(kBothBar, 256);
+            copy_queries(unit_at(v));
+          }
+          if (sg.a == 0) {
+            // for the kernel that joins: each row's first part, the parts' number, and the second half's distance
+            const int parts = (schedule().cta_of(sg.last) - cta + 1) * (sg.two ? 1 : 2);
+            for (int i = threadIdx.x; i < sg.rows; i += 256) {
+              const int qr = sg.q0 + i, b = qr / heads, hh = sg.hk * heads + (qr - b * heads);
+              p.row[(int64_t)(sg.g.row0 + b) * p.h + hh] = make_int4(kUnitRows * cta + sg.part + i, parts, sg.two ? 0 : sg.rows, 0);
+            }
+          }
+          if (more) queries_there();
+          if (n == 0 && r < rows) p.ml[part] = make_float2(-INFINITY, kNoKeys);
         }
-      }
-      if (more) queries_there();
-      const int rows = sg.two ? min(kTile, sg.rows - t * kTile) : sg.rows;  // of this half
-      const int64_t part = (int64_t)kUnitRows * cta + sg.part + t * (sg.two ? kTile : sg.rows) + r;
-      if (ok && r < rows) p.ml[part] = make_float2(m_ref, n > 0 ? l_sum : kNoKeys);
-      if (n > 0) {
-        if (ok) ok = warp_wait_parity(&o_full[t], done & 1, abort_flag, p.status);
-        ++done;
-        tc_fence_after();
-        if (ok) write_part(n > p.flush + 1, kept());
-        tc_fence_before();
-      }
+        if (n > 0) {
+          // ---- what the accumulator holds joins this half's part, each thread its row, whole 32-byte sectors of it at a time ----
+          if (ok) ok = warp_wait_parity(&o_full[t], done & 1, abort_flag, p.status);
+          ++done;
+          tc_fence_after();
+          if (ok) {
+            const bool some = x > p.flush + 1;  // of it has been written, by the maximum that stands beside it
+            float f = 1.f;
+            if (r < rows) {
+              const float m = some ? p.ml[part].x : m_ref;
+              if (m != m_ref) f = ex2_approx(m - m_ref);
+              p.ml[part] = make_float2(m_ref, l_sum);
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 64) {
+              uint32_t orow[64];
+              tmem_ld32(o_tmem + c0, orow);
+              tmem_ld32(o_tmem + c0 + 32, orow + 32);
+              tmem_wait_ld();
+              reg_fence<64>(orow);
+              float* to = p.o + part * D + c0;
+              if (r < rows) {
+                if (some) {
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) {
+                    const float4 y = *reinterpret_cast<const float4*>(to + 4 * k);
+                    uint32_t* z = orow + 4 * k;
+                    z[0] = __float_as_uint(fmaf(y.x, f, __uint_as_float(z[0])));
+                    z[1] = __float_as_uint(fmaf(y.y, f, __uint_as_float(z[1])));
+                    z[2] = __float_as_uint(fmaf(y.z, f, __uint_as_float(z[2])));
+                    z[3] = __float_as_uint(fmaf(y.w, f, __uint_as_float(z[3])));
+                  }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) store_sector(to + 8 * k, orow + 8 * k);
+              }
+              __syncwarp();
+            }
+          }
+          tc_fence_before();
+        }
+      } while (x < n);
     }
   }
 

@@ -91,3 +91,37 @@ def test_long_sums(n, h, h_kv, d, keys):
     assert (lse[:2] - want[1]).abs().max() <= 2.0 ** -18
     out16, lse16 = run(x, (i32([0, n]), i32([keys])), 0.1)
     assert (out16 == 1).all() and torch.equal(lse16, lse)
+
+
+@pytest.mark.parametrize("falls", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_runs_whose_maximum_grows(d, falls):
+    """Scores that climb (or fall) by 60 along 16384 keys which a CTA follows over some 54 tiles, so that what has been
+    summed is rescaled again and again. A score is within (d + 2) u S in either call, twice of it in a weight and in their sum,
+    and 2^-14 of A = sum p |v| is the products'; the log-sum-exps (below 64) differ by the scores' error and what four
+    roundings of 2^-18 leave."""
+    import blockwise_exact_attention_gb300 as bea
+    n, h, keys, page = 256, 64, 16384, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    k = (0.1 * torch.randn((keys, 1, d), device="cuda", generator=g)).to(BF16)
+    ramp = torch.arange(keys, device="cuda") * (60 / keys)
+    k[:, 0, 0] = ramp.flip(0) if falls else ramp
+    k = k.view(keys // page, page, 1, d)
+    v = (1 + torch.randn(k.shape, device="cuda", generator=g)).to(BF16)
+    q = torch.randn((n, 1, h, d), device="cuda", generator=g).to(BF16)
+    q[..., 0] = 1
+    table = torch.arange(keys // page, dtype=torch.int32, device="cuda").repeat(n, 1)
+    lens = i32([keys] * n)
+    out, lse = run((q, k, v, table, lens), (i32([0, n]), i32([keys])), 1.0, out_dtype=F32)
+    some = [0, 1, 100, 255]
+    few = (q[some], k, v, table[some], lens[some])
+    want, want_lse = bea.paged_decode(*few, 1.0, out_dtype=F32)
+    size, _ = bea.paged_decode(few[0], k, v.abs(), *few[3:], 1.0, out_dtype=F32)
+    s = 60 + 0.1 * d * 4                                  # no score's sum of sizes is above it
+    e = 2 * (d + 2) * U * s
+    assert ((out[some] - want).abs() <= (2 * e + 2.0 ** -14) * size).all()
+    assert (lse[some] - want_lse).abs().max() <= e + 2.0 ** -16
+    out16, _ = run((q, k, v, table, lens), (i32([0, n]), i32([keys])), 1.0)
+    assert ((out16[some] - want).abs() <= (2 * e + 2.0 ** -13) * size + 2.0 ** -8 * (want.abs() + 2.0 ** -8 * size)).all()
+    assert bea.device_status() == 0
