@@ -13,8 +13,8 @@
 //
 // Only whole tiles of 128 keys count as prefix, and only up to the shortest request of
 // the group and the first page that lies outside the cache: what is left over is the
-// requests' own. So the kernel has no masks, and what the shared path leaves out
-// the other one computes.
+// requests' own, as are all keys of a request whose table names other pages there. So
+// the kernel has no masks, and what the shared path leaves out the other one computes.
 //
 // The prefix kernel. A UNIT is up to 256 query rows of one (group, K/V head), its keys
 // a list of tiles; the units' tiles, one after another, are cut into runs of equal
@@ -275,15 +275,20 @@ struct Args {
 
 // ---- setup -------------------------------------------------------------------------
 
-constexpr int kSetupThreads = 256, kSetupWarps = kSetupThreads / 32;
+constexpr int kSetupThreads = 512, kSetupWarps = kSetupThreads / 32;
+constexpr int kSetupRows = 4;  // compared at a time
 
-// A block per group: its shortest request, how much is shared, and where each request's own keys begin.
+// gridDim.y blocks to a group, which take its rows in turn: its shortest request, how much is shared, and where each
+// request's own keys begin. A row whose table names another page than the owner's among the shared ones shares nothing: the
+// join passes over its prefix' parts. That comparison takes up to 2 us (64 requests behind 32k keys in pages of 16 88.8 -> 90.4, 256
+// behind 16k 118.6 -> 120.5; by one block to a group 89 -> 218).
 __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __grid_constant__ Args p) {
   __shared__ int3 words[kSetupWarps];
-  __shared__ int first_bad;
+  __shared__ int first_bad, first_other[kSetupRows];
   grid_launch_dependents();
   grid_dependency_wait();
   const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int turn = blockIdx.y, turns = gridDim.y;
   int shared = p.shared_lens[g], r0 = p.group_rows[g], r1 = p.group_rows[g + 1];
   // rows that are not in ascending order make no groups at all
   bool wrong = false;
@@ -293,15 +298,16 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
   }
   const bool bad = __syncthreads_or(wrong);
   if (bad) r0 = r1 = 0;
-  if (g == 0) {  // rows of no group
+  if (g == 0 && turn == 0) {  // rows of no group
     const int a = bad ? p.n : p.group_rows[0], b = bad ? p.n : p.group_rows[p.groups];
     for (int r = tid; r < p.n; r += kSetupThreads)
       if (r < a || r >= b) p.skip[r] = 0;
     if (bad && tid == 0) report_status(p.status, BEA_STATUS_PAGES);
   }
+  if (turn > 0 && turn >= r1 - r0) return;
   if (tid == 0) {
     first_bad = INT32_MAX;
-    if (shared < 0) report_status(p.status, BEA_STATUS_PAGES);
+    if (shared < 0 && turn == 0) report_status(p.status, BEA_STATUS_PAGES);
   }
   int shortest = INT32_MAX, owner = INT32_MAX, live = 0;
   for (int r = r0 + tid; r < r1; r += kSetupThreads) {
@@ -321,22 +327,42 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
   owner = __reduce_min_sync(~0u, w.y);
   live = __reduce_add_sync(~0u, lane < kSetupWarps ? w.z : 0);
   // nothing is shared by one request
-  int tiles = live > 1 ? max(0, min(min(shared, shortest), p.max_keys)) / kTile : 0;
-  if (tiles > 0) {
-    const int32_t* entries = p.table + owner * p.table_stride;
-    const int pages = (int)(((int64_t)tiles * kTile + p.page - 1) / p.page);
-    int at = INT32_MAX;
-#pragma unroll 8
+  const int most = live > 1 ? max(0, min(min(shared, shortest), p.max_keys)) / kTile : 0;
+  const int pages = (int)(((int64_t)most * kTile + p.page - 1) / p.page);
+  const int32_t* entries = p.table + owner * p.table_stride;  // read where there is one
+  for (int64_t row = r0 + turn; row < r1 || row == r0; row += (int64_t)turns * kSetupRows) {
+    if (tid < kSetupRows) first_other[tid] = INT32_MAX;
+    __syncthreads();
+    const int32_t* others[kSetupRows];
+#pragma unroll
+    for (int z = 0; z < kSetupRows; ++z) {  // of a row without a request, or behind the last: the owner's again
+      const int64_t r = row + z * turns;
+      others[z] = most > 0 && r < r1 && p.lens[r] > 0 ? p.table + r * p.table_stride : entries;
+    }
+    int at = INT32_MAX, other[kSetupRows];
+#pragma unroll
+    for (int z = 0; z < kSetupRows; ++z) other[z] = INT32_MAX;
+#pragma unroll 4
     for (int i = tid; i < pages; i += kSetupThreads) {
       const int id = entries[i];
       if (id < 0 || id >= p.num_pages) at = min(at, i);
+#pragma unroll
+      for (int z = 0; z < kSetupRows; ++z)
+        if (others[z][i] != id) other[z] = min(other[z], i);
     }
     if (at != INT32_MAX) atomicMin(&first_bad, at);
+#pragma unroll
+    for (int z = 0; z < kSetupRows; ++z)
+      if (other[z] != INT32_MAX) atomicMin(&first_other[z], other[z]);
+    __syncthreads();
+    const int tiles = first_bad != INT32_MAX ? (int)((int64_t)first_bad * p.page / kTile) : most;
+    if (tid < kSetupRows) {
+      const int64_t r = row + tid * turns;
+      if (r < r1) p.skip[r] = p.lens[r] > 0 && (int64_t)first_other[tid] * p.page >= (int64_t)tiles * kTile ? tiles * kTile : 0;
+    }
+    if (turn == 0 && row == r0 && tid == 0) p.group[g] = Group{r0, r1 - r0, owner, tiles};
+    __syncthreads();
   }
-  __syncthreads();
-  if (first_bad != INT32_MAX) tiles = (int)((int64_t)first_bad * p.page / kTile);
-  for (int r = r0 + tid; r < r1; r += kSetupThreads) p.skip[r] = p.lens[r] > 0 ? tiles * kTile : 0;
-  if (tid == 0) p.group[g] = Group{r0, r1 - r0, owner, tiles};
 }
 
 // ---- the prefix --------------------------------------------------------------------
@@ -937,7 +963,8 @@ cudaError_t launch(const PagedSharedParams& p, const PageMaps& maps, cudaStream_
   a.ml = reinterpret_cast<float2*>(ws + w.ml);
   a.o = reinterpret_cast<float*>(ws + w.o);
   a.status = d.status;
-  if ((e = launch_dependent(shared_setup_kernel, dim3(p.groups), kSetupThreads, 0, s, a)) != cudaSuccess) return e;
+  const int turns = f.ctas / p.groups < 1 ? 1 : f.ctas / p.groups < d.n ? f.ctas / p.groups : d.n;
+  if ((e = launch_dependent(shared_setup_kernel, dim3(p.groups, turns), kSetupThreads, 0, s, a)) != cudaSuccess) return e;
   *nlaunch += 1;
   // the requests' own keys, in fp32, with their log-sum-exp
   PagedDecodeParams own = d;

@@ -84,7 +84,8 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, lens, group_rows, shar
     keys in common, which are then read once for the group. Group g is the rows
     ``group_rows[g]`` .. ``group_rows[g + 1] - 1`` ([groups + 1] int32, ascending);
     their tables name the same pages for the first ``shared_lens[g]`` keys
-    ([groups] int32), as those of forked rows do. Rows of length 0 take no part.
+    ([groups] int32), as those of forked rows do. Rows of length 0 take no part, and a
+    row that names other pages than the group's first reads its keys for itself.
 
     In the product with the values weights of shared keys have 16 bits, where
     ``paged_decode``'s have 24: a bf16 output is as exact, a float32 one is within
