@@ -24,7 +24,7 @@
 //
 // Measured (GPU time, inputs larger than L2): [1, 32768, 32 + 8, 128] bf16 forward 110 us (6.1 TB/s), with its gradient
 // 286 us (5.9 TB/s; a copy reaches 6.7), interleaved too; interleaved without the norm 103 us (6.5 TB/s). [1, 16384, 16 + 16,
-// 128] f32 85 and 216 us (6.3, 6.2 TB/s). 256 tokens of 32 + 8 heads: 4.9 us, the host takes 7.5
+// 128] f32 85 and 216 us (6.3, 6.2 TB/s). 256 tokens of 32 + 8 heads: 5.1 us, the host takes 7.1-8.6
 #include <type_traits>
 
 #include <cuda_bf16.h>

@@ -6,8 +6,8 @@
 // group's requests, and of the g = h / h_kv heads that read a K/V head, are the rows
 // of one matrix, so it runs like the forward, on the tensor cores:
 //   S = Q K^T, P = exp2(scale S - m) with a running maximum m, O += P V, l += sum P.
-// Its bytes are the prefix once, its flops 4 d a (query row, key): from 230 rows a K/V
-// head on the products are the bound, not HBM. The rest is paged_decode's kernel, told
+// Its bytes are the prefix once, its flops 6 d a (query row, key), P being two terms: from
+// 190 rows a K/V head on the products are the bound, not HBM. The rest is paged_decode's kernel, told
 // where each request's own keys begin. A last kernel joins the two by their maxima and
 // sums, in a fixed order.
 //
@@ -40,18 +40,18 @@
 // kernel before it ends, so that the join finds both done.
 //
 // Measured (GPU time, three sets of inputs in turn; h / h_kv 32 / 8, d = 128): 64
-// requests behind 32k shared keys, up to 1k own ones each, 59.5 us, where 188 MB take
-// 28 and the products 18 (behind 16k 46 us, 493 without sharing); 256 behind 16k, up
-// to 600 own, 93 us (27, 36). Of the latter 3 go to the setup, 29 to the rest (its
-// bytes at 5 TB/s), 54 to the prefix and 8 to the join. A step of a unit takes 1.47
-// us, the tensor core busy 70% of it (the chain S, maximum, exponentials, P V of two
-// halves in turn); before a CTA's first scores 4.5 us pass (schedule, queries, keys,
-// cold instructions), its first two steps take 2 each, and its part 3 to write, all
-// CTAs' 20 MB at once. Tried without gain: two threads to a row (640 threads at 96
-// registers), which meet to exchange maxima; runs that get shorter from CTA to CTA, as
-// these start up to 10 us apart (most of them at the end of that); the rest's kernel on
-// 64-112 SMs and the prefix beside it (both take longer); tiles called into L2 a step
-// ahead (66 us).
+// requests behind 32k shared keys, up to 1k own ones each, 75 us, where 188 MB take
+// 28 and the products 27 (behind 16k 67 us, 490 without sharing); 256 behind 16k, up
+// to 600 own, 120 us (27, 54). Of the latter 5 go to the setup, 29 to the rest (its
+// bytes at 5 TB/s), 78 to the prefix and 8 to the join. A step of a unit takes 2.4
+// us, 1.5 of them (3072 cycles) the tensor core's: the chain S, maximum, exponentials
+// and their terms, P V of two halves in turn. Before a CTA's first scores 4.5 us pass
+// (schedule, queries, keys, cold instructions), and its part takes 3 to write, all
+// CTAs' 20 MB at once. Tried without gain, with one term: two threads to a row (640
+// threads at 96 registers), which meet to exchange maxima; runs that get shorter from
+// CTA to CTA, as these start up to 10 us apart (most of them at the end of that); the
+// rest's kernel on 64-112 SMs and the prefix beside it (both take longer); tiles called
+// into L2 a step ahead.
 #include <cuda_bf16.h>
 
 #include "launch_cache.cuh"
@@ -76,8 +76,8 @@ constexpr float kRescale = 8.f;  // log2: O is rescaled only when a maximum grow
 constexpr uint32_t kPReadyBar = 1, kPReadyThreads = 128 + 32, kBothBar = 3;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // Of a unit besides its steps, in steps: a run in two units fetches queries and writes parts twice. A fifth of a run, within these
-// bounds. (2 and 5 everywhere, runs of 27 steps, 256 requests behind 16k keys: 96.9, 93.8 us; of 13, 64 behind 32k: the same;
-// of 5, 96 in three groups: 68.5, 71.6 us, 16 behind 4k: 24.7, 26.4 us.)
+// bounds. (2 and 5 everywhere, runs of 27 steps, 256 requests behind 16k keys: 123.0, 119.5 us; of 13, 64 behind 32k: the same;
+// of 5, 96 in three groups: 72.2, 75.3 us, 16 behind 4k: 25.4, 27.2 us.)
 constexpr int kLeastUnitCost = 2, kMostUnitCost = 5;
 // A run's cut is moved by up to so many steps (and a quarter of a run) to a unit's border.
 constexpr int kSnap = 2;
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kMost; ++i) {
             // A page's rows in this tile, the largest box that fits first. (Boxes of one size, that which divides the page, for 20
-            // requests of 16 heads behind 32k keys: pages of 50 tokens 169 us, now 83, of 20 115, 86, of 7 284, 158; of 32 78,
-            // 80: more boxes than one in 30 ns are what bounds a tile.)
+            // requests of 16 heads behind 32k keys and P in one term: pages of 50 tokens 169 us, so 83, of 20 115, 86, of 7 284,
+            // 158; of 32 78, 80: more boxes than one in 30 ns are what bounds a tile. In two terms 95, 100, 166, 93.)
             const int64_t from = (first_page + lane + 32 * i) * (int64_t)p.page - j * kTile;
             int row = (int)max(from, (int64_t)0);
             const int end = (int)min(from + p.page, (int64_t)kTile);
@@ -979,8 +979,8 @@ cudaError_t launch(const PagedSharedParams& p, const PageMaps& maps, cudaStream_
   *nlaunch += 1;
   const int64_t items = (int64_t)d.n * d.h;
   // Rows that do not fill the GPU have many parts each, four warps a row then; where there are warps enough to hide the
-  // latency fewer loads at a time leave room for more of them. (256 requests of 32 heads: 95.9 us with 4 at a time, 97.9 with
-  // 8; 64 requests 62.8, 61.3 us; 16 requests 36.2 us, with one warp a row 42.0.)
+  // latency fewer loads at a time leave room for more of them. (256 requests of 32 heads: 118.7 us with 4 at a time, 122.3 with
+  // 8; 64 requests 76.5, 74.7 us; 8 requests 23.6 us, with one warp a row 27.0.)
   const bool few = items <= f.ctas * 8, many = items > f.ctas * 32;
   const int64_t warps = items * (few ? kJoinWarps : 1);
   auto join = few ? shared_join_kernel<D, kJoinWarps, 8> : many ? shared_join_kernel<D, 1, 4> : shared_join_kernel<D, 1, 8>;
@@ -992,8 +992,8 @@ cudaError_t launch(const PagedSharedParams& p, const PageMaps& maps, cudaStream_
 }  // namespace
 
 // Up to so many bytes of keys and values that sharing saves the other kernels take longer than reading them again. 32 / 8
-// heads of 128, GPU time with and without sharing: 4 requests behind 4k keys (50 MB) 20.6, 15.5 us, 8 behind 4k (117 MB)
-// 22.7, 23.4 us, 4 behind 16k (201 MB) 34.0, 39.2 us; 16 / 16 heads of 64: 8 behind 4k (117 MB) 22.9, 26.9 us.
+// heads of 128, GPU time with and without sharing: 4 requests behind 4k keys (50 MB) 22.5, 16.3 us, 8 behind 4k (117 MB)
+// 23.6, 23.8 us, 4 behind 16k (201 MB) 34.6, 40.7 us; 16 / 16 heads of 64: 8 behind 4k (117 MB) 24.0, 27.7 us.
 constexpr int64_t kLeastSaved = 96000000;
 
 static bool saves_little(int64_t n, int64_t h_kv, int64_t d, int64_t max_keys, int64_t groups) {

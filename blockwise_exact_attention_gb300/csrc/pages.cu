@@ -593,9 +593,11 @@ cudaError_t most_blocks(int* wave, int* each) {
 }  // namespace
 
 // Up to `entries` entries of a table and pages of a cache one cluster does all of a call, in one launch instead of two to four,
-// each of which costs the host 2 us. GPU time, cluster and launches: 8 rows of 46 entries forked 4.3, 4.4 us, freed 6.4, 6.1, a
-// cache of 242 pages compacted 7.2, 7.5 us; 64 rows of 128 entries 5.3, 4.7, 7.4, 7.8, 10.1, 9.8 us (4210 pages); 256 rows of
-// 258 entries 5.9, 4.8, 9.3, 8.5, 21.7, 18.7 us (33330 pages).
+// each of which costs the host 1-2 us. In a graph, cluster and launches: 8 rows of 46 entries forked 4.4, 4.9 us, freed 5.8, 6.1, a
+// cache of 242 pages compacted 7.3, 7.9 us; 64 rows of 128 entries 4.5, 4.9, 7.2, 8.0, 9.2, 10.5 us (4210 pages); 128 rows of 128
+// (16384 entries) 4.6, 5.0, 7.2, 7.9, 10.5, 11.3 us; 256 rows of 128 (32768) 5.2, 5.1, 7.8, 8.0, 14.1, 13.7 us; 128 rows of 512
+// 6.0, 5.2, 9.3, 8.7, 21.4, 19.1 us. Called one by one, 16384 entries: 6.0, 7.9, 7.5, 9.3, 10.4, 13.0 us; 32768: 5.9, 7.9, 7.9, 9.6,
+// 14.2, 14.4 us.
 static bool fits_cluster(const PagesState& s, int64_t entries) {
   return (int64_t)s.n * s.max_pages <= entries && s.num_pages <= entries;
 }

@@ -87,6 +87,11 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, lens, group_rows, shar
     ([groups] int32), as those of forked rows do. Rows of length 0 take no part, and a
     row that names other pages than the group's first reads its keys for itself.
 
+    The table's width decides whether groups are looked at: only where (n - 1) rows of
+    it have room for 96 MB of keys and values, which sharing could save. A table much
+    wider than its lengths takes the slower way for few requests; narrow it
+    (``block_table[:, :pages]``) where the longest length is known.
+
     In the product with the values weights of shared keys have 16 bits, where
     ``paged_decode``'s have 24: a bf16 output is as exact, a float32 one is within
     2**-14 of sum(p |v|)."""
@@ -248,5 +253,6 @@ class PagedKVCache:
         return paged_decode(q, self.k, self.v, self.block_table, self.lens, softmax_scale, window_left, **kw)
 
     def decode_shared(self, q, group_rows, shared_lens, softmax_scale=None, **kw):
-        """``paged_decode_shared`` of one new token per row."""
+        """``paged_decode_shared`` of one new token per row. The table is ``max_len`` wide: few rows that are much shorter are
+        decoded faster by ``decode``."""
         return paged_decode_shared(q, self.k, self.v, self.block_table, self.lens, group_rows, shared_lens, softmax_scale, **kw)

@@ -46,14 +46,19 @@ class RopeScaling(NamedTuple):
     """Frequencies for sequences ``factor`` times as long as the trained ones.
 
     ``kind`` "linear": every frequency divided by the factor (positions
-    interpolated). "ntk": base ** (P / (P - 1) * log factor) more, P the number of
+    interpolated). "ntk": the base times factor ** (P / (P - 1)), P the number of
     pairs of the spectrum, so that the first pair keeps its frequency and the last
     has a factor'th of it. "yarn": by parts (Peng et al., "YaRN", 2023): a pair
     that turns more than ``beta_fast`` times within ``original_max`` positions
     keeps its frequency, one that turns less than ``beta_slow`` times has a
-    factor'th of it, with a ramp linear in the turns between; and the turned pairs
-    are multiplied by ``amplitude`` (default 0.1 log(factor) + 1; 1 for the other
-    kinds)."""
+    factor'th of it, with a ramp linear in the turns between, as the paper's formula
+    has it; and the turned pairs are multiplied by ``amplitude`` (default
+    0.1 log(factor) + 1, the natural logarithm; 1 for the other kinds).
+
+    Models were also trained under the name "yarn" with a ramp linear in the pair's
+    index between two rounded borders. Between the borders their frequencies are
+    others, in places by more than a factor of two: this kind is not for their
+    weights."""
     kind: str
     factor: float
     original_max: int | None = None
