@@ -280,8 +280,8 @@ constexpr int kSetupRows = 4;  // compared at a time
 
 // gridDim.y blocks to a group, which take its rows in turn: its shortest request, how much is shared, and where each
 // request's own keys begin. A row whose table names another page than the owner's among the shared ones shares nothing: the
-// join passes over its prefix' parts. That comparison takes up to 2 us (64 requests behind 32k keys in pages of 16 88.8 -> 90.4, 256
-// behind 16k 118.6 -> 120.5; by one block to a group 89 -> 218).
+// join passes over its prefix' parts. That comparison takes 1-2 us (64 requests behind 32k keys in pages of 16 88.8 -> 91.0, 256
+// behind 16k 118.6 -> 120.3; by one block to a group 89 -> 218).
 __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __grid_constant__ Args p) {
   __shared__ int3 words[kSetupWarps];
   __shared__ int first_bad, first_other[kSetupRows];
@@ -330,6 +330,13 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
   const int most = live > 1 ? max(0, min(min(shared, shortest), p.max_keys)) / kTile : 0;
   const int pages = (int)(((int64_t)most * kTile + p.page - 1) / p.page);
   const int32_t* entries = p.table + owner * p.table_stride;  // read where there is one
+  // Forks of a prompt have the page that it ends in as copies of their own: where a row goes along up to the last page and
+  // names another one there, that page is left out for all.
+  bool other_end = false;
+  for (int r = r0 + tid; pages > 1 && r < r1; r += kSetupThreads) {
+    const int32_t* end = p.table + r * p.table_stride + pages - 2;
+    other_end = other_end || (p.lens[r] > 0 && end[0] == entries[pages - 2] && end[1] != entries[pages - 1]);
+  }
   for (int64_t row = r0 + turn; row < r1 || row == r0; row += (int64_t)turns * kSetupRows) {
     if (tid < kSetupRows) first_other[tid] = INT32_MAX;
     __syncthreads();
@@ -354,8 +361,8 @@ __global__ void __launch_bounds__(kSetupThreads) shared_setup_kernel(const __gri
 #pragma unroll
     for (int z = 0; z < kSetupRows; ++z)
       if (other[z] != INT32_MAX) atomicMin(&first_other[z], other[z]);
-    __syncthreads();
-    const int tiles = first_bad != INT32_MAX ? (int)((int64_t)first_bad * p.page / kTile) : most;
+    const int last = __syncthreads_or(other_end) ? pages - 1 : INT32_MAX, end = min(first_bad, last);
+    const int tiles = end != INT32_MAX ? (int)((int64_t)end * p.page / kTile) : most;
     if (tid < kSetupRows) {
       const int64_t r = row + tid * turns;
       if (r < r1) p.skip[r] = p.lens[r] > 0 && (int64_t)first_other[tid] * p.page >= (int64_t)tiles * kTile ? tiles * kTile : 0;

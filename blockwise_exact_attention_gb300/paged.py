@@ -85,7 +85,8 @@ def paged_decode_shared(q, k_cache, v_cache, block_table, lens, group_rows, shar
     ``group_rows[g]`` .. ``group_rows[g + 1] - 1`` ([groups + 1] int32, ascending);
     their tables name the same pages for the first ``shared_lens[g]`` keys
     ([groups] int32), as those of forked rows do. Rows of length 0 take no part, and a
-    row that names other pages than the group's first reads its keys for itself.
+    row that names other pages than the group's first reads its keys for itself. The
+    page that a forked prompt ends in may be counted in or not: it is not shared.
 
     The table's width decides whether groups are looked at: only where (n - 1) rows of
     it have room for 96 MB of keys and values, which sharing could save. A table much

@@ -503,7 +503,9 @@ int bea_paged_decode(const bea_tensor* q, const bea_tensor* k_cache, const bea_t
  *               for all its requests, that is, the rows of the table name the same
  *               pages for them (bea_paged_fork makes such rows). The first row that
  *               holds a request is read for all whose tables name its pages; a row
- *               that names another one among them is read for itself.
+ *               that names another one among them is read for itself. (Where that is
+ *               the last of them only, as in forks of a prompt that ends inside a
+ *               page, that page is not shared.)
  *   workspace   bea_paged_decode_shared_workspace_size() bytes, 256-byte aligned;
  *               may be NULL when that is 0. Contents on entry irrelevant; calls that may run concurrently need
  *               separate workspaces.

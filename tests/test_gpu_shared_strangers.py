@@ -87,3 +87,25 @@ def test_a_row_that_took_the_place_of_one_that_ended():
     out, lse = cache.decode_shared(q, i32([0, 6]), i32([1500]), 0.1)
     check(out, lse, q, cache.k, cache.v, cache.block_table, cache.lens, 0.1)
     assert bea.device_status() == 0
+
+
+@pytest.mark.parametrize("page,prompt,shared", [(16, 1541, 1536), (100, 1540, 1408), (100, 1500, 1408), (256, 1000, 768), (7, 1540, 1536),
+                                                (300, 1537, 1408), (1000, 1999, 896)])
+def test_forks_that_name_the_prompt_as_shared(page, prompt, shared):
+    """The page that a prompt ends in is a copy in each fork: what stands before it stays shared. (A workspace begins with
+    the number of shared keys that each row leaves to its group.)"""
+    import blockwise_exact_attention_gb300 as bea
+    n, h, h_kv, d = 9, 4, 2, 64
+    cache = bea.PagedKVCache(12 * (prompt // page + 3), page, h_kv, d, n, 40000, share_pages=True)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(page)
+    cache.k.normal_(generator=gen), cache.v.normal_(generator=gen)
+    cache.plan(i32([prompt] + [0] * (n - 1)), prompt)
+    cache.fork(i32([-1] + [0] * (n - 2) + [-1]))
+    cache.plan(i32([1] * (n - 1) + [prompt]), n - 1 + prompt)       # and one row of another prompt
+    q = torch.randn((n, 1, h, d), device="cuda", generator=gen).to(BF16)
+    g = i32([0, n]), i32([prompt])
+    ws = torch.zeros(bea.paged_decode_shared_workspace_bytes(q, cache.k, cache.block_table, g[1]), dtype=torch.uint8, device="cuda")
+    out, lse = cache.decode_shared(q, *g, 0.1, workspace=ws)
+    check(out, lse, q, cache.k, cache.v, cache.block_table, cache.lens, 0.1)
+    assert ws[:4 * n].view(torch.int32).tolist() == [shared] * (n - 1) + [0] and bea.device_status() == 0
